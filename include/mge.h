@@ -15,6 +15,9 @@
  *   grouped_mlp_bwd     dy permute (+quantize), dh GEMM with fused SwiGLU backward and
  *                       d_prob, dW_down, dX and dW_gate_up grouped GEMMs
  *   unpermute_combine   out[t] = sum over the k slots of in[perm_pos[t][i]]
+ * the router's other scores (moe_route_topk, moe_route_topk_bwd: softmax or sigmoid, balance
+ * bias, groups), MXFP4 weights (mxfp4_quantize, mxfp4_dequantize, mxfp4_grouped_gemm,
+ * grouped_mlp_fwd_mxfp4)
  * and the router backward (moe_router_bwd: d_logits from d_prob), the forward without
  * the fusion (grouped_mlp_fwd_unfused, the baseline the fusion is measured against) and
  * the one scale of FP8 with one scale per tensor (mge_tensor_scale; the quantizers then
@@ -294,6 +297,18 @@ size_t mge_fwd_workspace_bytes(const mge_fwd_args* args);
 mge_status grouped_mlp_fwd(const mge_fwd_args* args, void* stream);
 
 /* ------------------------------------------------------------------------------
+ * grouped_mlp_fwd_mxfp4 — grouped_mlp_fwd for serving on MXFP4 weights: the same arguments
+ * with prec = MGE_PREC_MXFP8 (x_perm, h: MXFP8 as there) and w_gate_up / w_down the MXFP4
+ * codes ([2F][H/2], [H][F/2]; mxfp4_quantize ROW) with their scales ([2F][H/32],
+ * [H][F/32]).  h is quantized to MXFP8 in the gate-up product's epilogue.
+ * Workspace: mge_fwd_mxfp4_workspace_bytes(args).
+ * Errors: as grouped_mlp_fwd; MGE_ERR_UNSUPPORTED for training (saved_gu, h_col or
+ * h_col_scale given) or prec BF16.
+ * ---------------------------------------------------------------------------- */
+size_t mge_fwd_mxfp4_workspace_bytes(const mge_fwd_args* args);
+mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
  * mge_fwd_saved_bytes — sizes of the activations a training forward saves for the
  * backward.  The fused forward keeps the SwiGLU input and output out of HBM only in
  * part ("some" intermediates are not materialised: the ai4snews report, paragraph on
@@ -495,6 +510,169 @@ typedef struct mge_router_bwd_args {
 } mge_router_bwd_args;
 
 mge_status moe_router_bwd(const mge_router_bwd_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * moe_route_topk — the router's choice in its other forms: softmax or sigmoid scores, a
+ * balance bias, groups of experts, weights renormalised or not.  Its topk_idx / topk_prob
+ * go into moe_route_permute with MGE_ROUTE_PROB_GIVEN.  Per token with logits l:
+ *   scores   s_e = softmax(l)_e, or 1 / (1 + exp(-l_e)); a logit of -inf or NaN masks its
+ *            expert: s_e = 0
+ *   choice   by key_e = l_e, or with a bias key_e = s_e + bias_e: the k largest keys, ties
+ *            to the lower index, masked experts (and those whose bias is -inf or NaN) after
+ *            all others.  num_groups > 1: the E experts are num_groups consecutive groups
+ *            of equal size; a group's score is the sum of its group_topn (1 or 2) largest
+ *            keys (without a bias: scores) over its unmasked experts; the choice is among
+ *            the experts of the topk_groups groups of largest score (ties to the lower
+ *            group, groups without an unmasked expert last).
+ *   weights  topk_prob[t][i] = scale * s_i / (sum of the k chosen s), or scale * s_i
+ *            (renormalize = 0); 0 where the sum is 0 (every chosen expert masked).
+ * The bias takes part in the choice only.  A choice that goes by computed scores (a bias,
+ * or group_topn 2) compares them in 64 bits, so near-equal experts rank as the formula
+ * ranks them; weights are fp32.  A logit of +inf counts as equal to every other +inf and
+ * above all finite ones.
+ * logits: fp32 or bf16 [T][E], row stride logits_row_stride elements (>= E).
+ * Errors: MGE_ERR_INVALID_ARG for T < 0, E outside [1, 256], k outside [1, min(E, 8)], an
+ * unknown score or dtype, num_groups < 1 or not dividing E, topk_groups outside
+ * [1, num_groups], k > topk_groups * E / num_groups, group_topn other than 1 or 2, a scale
+ * that is not finite, a row stride below E, NULL logits / topk_idx / topk_prob (T > 0).
+ * T = 0 is a no-op.  No workspace.
+ * ---------------------------------------------------------------------------- */
+enum { MGE_SCORE_SOFTMAX = 0, MGE_SCORE_SIGMOID = 1 };
+
+typedef struct mge_route_topk_args {
+  uint32_t struct_size;
+  int32_t T, E, k;
+  int32_t score;                         /* MGE_SCORE_* */
+  int32_t num_groups, topk_groups, group_topn;
+  int32_t renormalize;
+  float scale;
+  int32_t logits_dtype;                  /* MGE_DTYPE_* */
+  int64_t logits_row_stride;             /* elements */
+  const void* logits;                    /* [T][E] */
+  const float* bias;                     /* [E] or NULL */
+  int32_t* topk_idx;                     /* [T][k] */
+  float* topk_prob;                      /* [T][k] */
+} mge_route_topk_args;
+
+mge_status moe_route_topk(const mge_route_topk_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * moe_route_topk_bwd — gradient of moe_route_topk's weights with respect to the logits
+ * (the choice itself, and with it the bias, has none).  With the scores s of the logits,
+ * d_i = scale * d_prob[t][i] and, over the chosen slots, w_i = s_i / sum_j s_j:
+ *   sigmoid, renormalised   d_logits[idx_i] += (d_i - sum_j w_j d_j) w_i (1 - s_i)
+ *   sigmoid                 d_logits[idx_i] += d_i s_i (1 - s_i)
+ *   softmax, renormalised   d_logits[idx_i] += (d_i - sum_j w_j d_j) w_i
+ *   softmax                 d_logits[e] = s_e ([e chosen] d_e - sum_j s_j d_j), every e
+ * and 0 elsewhere.  Slots with an index outside [0, E) take no part; slots that share an
+ * expert add up in slot order.  d_logits has the logits' type, [T][E] contiguous, every
+ * element written (sums in fp32, one rounding for bf16).
+ * Errors: as moe_route_topk, and MGE_ERR_INVALID_ARG for a NULL d_prob / d_logits (T > 0).
+ * ---------------------------------------------------------------------------- */
+typedef struct mge_route_topk_bwd_args {
+  uint32_t struct_size;
+  int32_t T, E, k;
+  int32_t score;                         /* MGE_SCORE_* */
+  int32_t renormalize;
+  float scale;
+  int32_t logits_dtype;                  /* MGE_DTYPE_*, of logits and d_logits */
+  int64_t logits_row_stride;             /* elements */
+  const void* logits;                    /* [T][E] */
+  const int32_t* topk_idx;               /* [T][k] */
+  const float* d_prob;                   /* [T][k] */
+  void* d_logits;                        /* [T][E] */
+} mge_route_topk_bwd_args;
+
+mge_status moe_route_topk_bwd(const mge_route_topk_bwd_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * mxfp4_quantize — BF16 -> MXFP4 (E2M1 + E8M0 per 32), the 4-bit form beside
+ * mxfp8_quantize: magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign.  Per block of 32 values
+ * e = floor(log2(amax)) - 2 clamped to [-127, 127] (all-zero block: -127), scale byte
+ * e + 127, element = v / 2^e to the nearest E2M1 value (ties to even), saturating at 6
+ * (OCP MX v1.0).  Two elements share a byte, the even one in the low half.
+ * in, batch, R, C, strides, orient: as mxfp8_quantize.
+ * ROW: row_codes [b][R][C/2], row_scales [b][R][C/32].
+ * COL: col_codes [b][C][Rp/2], col_scales [b][C][Rp/32], Rp = R rounded up to 32 (zero
+ * padded) — the ROW quantization of the transpose (the operand of an input gradient:
+ * dX = dY W is mxfp4_grouped_gemm with W's column form).
+ * Errors: as mxfp8_quantize (without segments and tensor scale); batch <= 65535.
+ * ---------------------------------------------------------------------------- */
+typedef struct mge_quant4_args {
+  uint32_t struct_size;
+  int32_t batch, R, C;
+  int64_t in_batch_stride, in_row_stride;
+  const uint16_t* in;
+  uint32_t orient;           /* MGE_ORIENT_ROW | MGE_ORIENT_COL */
+  uint8_t* row_codes;
+  uint8_t* row_scales;
+  uint8_t* col_codes;
+  uint8_t* col_scales;
+} mge_quant4_args;
+
+mge_status mxfp4_quantize(const mge_quant4_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * mxfp4_dequantize — the values of `rows` contiguous rows of C MXFP4 elements: codes
+ * [rows][C/2], scales [rows][C/32] -> out [rows][C] bf16 or fp32 (exact in both, apart
+ * from bf16's and fp32's largest values; a scale byte of 255, the format's NaN, gives NaN).
+ * Errors: MGE_ERR_INVALID_ARG for rows < 0, C not a multiple of 32 or negative, an unknown
+ * dtype, NULL or misaligned (16-byte) codes / out, NULL scales.
+ * ---------------------------------------------------------------------------- */
+typedef struct mge_dequant4_args {
+  uint32_t struct_size;
+  int64_t rows;
+  int32_t C;
+  int32_t out_dtype;         /* MGE_DTYPE_* */
+  const uint8_t* codes;
+  const uint8_t* scales;
+  void* out;
+} mge_dequant4_args;
+
+mge_status mxfp4_dequantize(const mge_dequant4_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * mxfp4_grouped_gemm — the grouped product on MXFP4 weights: for every expert e and row r
+ * of its group, out[r][n] = sum_k a[r][k] w_e[n][k] (K = the blocks' axis of both), fp32
+ * accumulation on block-scaled MFMA, out bf16 or fp32.  a: MXFP8 codes [rows][K] or MXFP4
+ * codes [rows][K/2], with scales [rows][K/32].  w, w_scale: [host] arrays of E device
+ * pointers, codes [N][K/2] and scales [N][K/32].
+ * Groups: split_sizes / group_offsets as moe_route_permute writes them (any alignment); both
+ * NULL (E = 1): one group of all rows.  total_rows: an upper bound of the groups' row count
+ * the caller knows (T*k), or 0 for `rows`; it only sizes the launch and more rows than that
+ * in the groups are an error of the caller (some groups may then stay unwritten).  Rows
+ * outside the groups are untouched.
+ * The matrix unit adds the 128 products of one instruction with less than fp32's precision
+ * when the operands are MXFP8 (about 1e-5 relative to the sum's magnitude); MXFP4 products
+ * add exactly to fp32 rounding.
+ * Workspace: mge_gemm4_workspace_bytes(args).
+ * Errors: MGE_ERR_INVALID_ARG for E outside [1, 256], N or K not a positive multiple of 32,
+ * rows < 0 or >= 2^31 / K, an expert's weight of 2^31 bytes or more, unknown formats, NULL or
+ * misaligned (16-byte) a / out / weights, NULL scales, one of split_sizes / group_offsets
+ * without the other or E > 1 without both; MGE_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------------- */
+enum { MGE_FORMAT_MXFP8 = 0, MGE_FORMAT_MXFP4 = 1 };
+
+typedef struct mge_gemm4_args {
+  uint32_t struct_size;
+  int32_t a_format;                      /* MGE_FORMAT_* */
+  int32_t E, N, K;
+  int64_t rows;                          /* rows of a and out */
+  int64_t total_rows;
+  const int32_t* split_sizes;            /* [E] or NULL */
+  const int32_t* group_offsets;          /* [E] (or [E+1]) or NULL */
+  const uint8_t* a;
+  const uint8_t* a_scale;
+  const uint8_t* const* w;               /* [host] E pointers */
+  const uint8_t* const* w_scale;         /* [host] E pointers */
+  int32_t out_dtype;                     /* MGE_DTYPE_* */
+  void* out;                             /* [rows][N] */
+  void* workspace;
+  size_t workspace_bytes;
+} mge_gemm4_args;
+
+size_t mge_gemm4_workspace_bytes(const mge_gemm4_args* args);
+mge_status mxfp4_grouped_gemm(const mge_gemm4_args* args, void* stream);
 
 /* ------------------------------------------------------------------------------ helpers */
 const char* mge_status_string(mge_status s);

@@ -8,8 +8,9 @@ moe_grouped_expert_amd.build``); without it every call raises.
 """
 from ._binding import (  # noqa: F401
     BwdOut, FwdOut, MgeError, RouteOut, check_device_errors, fwd_saved_bytes, grouped_mlp_bwd, grouped_mlp_fwd,
-    grouped_mlp_fwd_unfused,
+    grouped_mlp_fwd_mxfp4, grouped_mlp_fwd_unfused,
     lib,
+    moe_route_topk, moe_route_topk_bwd, mxfp4_dequantize, mxfp4_grouped_gemm, mxfp4_quantize,
     moe_route_permute, moe_router_bwd, mxfp8_quantize, perm_rows, profile_start, profile_stop, tensor_scale,
     unpermute_combine,
 )

@@ -19,6 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libmge.so")
 MGE_OK, MGE_ERR_INVALID_ARG, MGE_ERR_UNSUPPORTED, MGE_ERR_WORKSPACE, MGE_ERR_HIP, MGE_ERR_DEVICE_CHECK = range(6)
 PREC = {"bf16": 0, "mxfp8": 1}
 DTYPE = {"bf16": 0, "f32": 1}
+SCORE = {"softmax": 0, "sigmoid": 1}
+FORMAT = {"mxfp8": 0, "mxfp4": 1}
 ORIENT_ROW, ORIENT_COL = 1, 2
 ROUTE_WANT_COL, ROUTE_PROB_GIVEN = 1, 2
 
@@ -92,8 +94,40 @@ class RouterBwdArgs(C.Structure):
                 ("d_prob", vp), ("d_logits", vp)]
 
 
+class RouteTopkArgs(C.Structure):
+    _fields_ = [("struct_size", u32), ("T", i32), ("E", i32), ("k", i32), ("score", i32), ("num_groups", i32),
+                ("topk_groups", i32), ("group_topn", i32), ("renormalize", i32), ("scale", C.c_float),
+                ("logits_dtype", i32), ("logits_row_stride", i64), ("logits", vp), ("bias", vp), ("topk_idx", vp),
+                ("topk_prob", vp)]
+
+
+class RouteTopkBwdArgs(C.Structure):
+    _fields_ = [("struct_size", u32), ("T", i32), ("E", i32), ("k", i32), ("score", i32), ("renormalize", i32),
+                ("scale", C.c_float), ("logits_dtype", i32), ("logits_row_stride", i64), ("logits", vp),
+                ("topk_idx", vp), ("d_prob", vp), ("d_logits", vp)]
+
+
+class Quant4Args(C.Structure):
+    _fields_ = [("struct_size", u32), ("batch", i32), ("R", i32), ("C", i32), ("in_batch_stride", i64),
+                ("in_row_stride", i64), ("in_", vp), ("orient", u32), ("row_codes", vp), ("row_scales", vp),
+                ("col_codes", vp), ("col_scales", vp)]
+
+
+class Dequant4Args(C.Structure):
+    _fields_ = [("struct_size", u32), ("rows", i64), ("C", i32), ("out_dtype", i32), ("codes", vp), ("scales", vp),
+                ("out", vp)]
+
+
+class Gemm4Args(C.Structure):
+    _fields_ = [("struct_size", u32), ("a_format", i32), ("E", i32), ("N", i32), ("K", i32), ("rows", i64),
+                ("total_rows", i64), ("split_sizes", vp), ("group_offsets", vp), ("a", vp), ("a_scale", vp), ("w", vp),
+                ("w_scale", vp), ("out_dtype", i32), ("out", vp), ("workspace", vp), ("workspace_bytes", C.c_size_t)]
+
+
 _LIB = None
-EXPORTS = ["mge_perm_rows", "mge_route_workspace_bytes", "moe_route_permute", "moe_route_permute_noalloc",
+EXPORTS = ["moe_route_topk", "moe_route_topk_bwd", "mxfp4_quantize", "mxfp4_dequantize", "mge_gemm4_workspace_bytes",
+           "mxfp4_grouped_gemm", "mge_fwd_mxfp4_workspace_bytes", "grouped_mlp_fwd_mxfp4",
+           "mge_perm_rows", "mge_route_workspace_bytes", "moe_route_permute", "moe_route_permute_noalloc",
            "mxfp8_quantize",
            "mge_fwd_workspace_bytes", "grouped_mlp_fwd", "mge_fwd_saved_bytes", "mge_fwd_unfused_workspace_bytes", "grouped_mlp_fwd_unfused",
            "mge_tensor_scale_workspace_bytes", "mge_tensor_scale", "mge_quant_workspace_bytes",
@@ -129,7 +163,14 @@ def lib():
         L.mge_tensor_scale_workspace_bytes.argtypes = [i32, i64]
         L.mge_bwd_workspace_bytes.restype = C.c_size_t
         L.mge_bwd_workspace_bytes.argtypes = [C.POINTER(BwdArgs)]
-        for name, st in (("moe_route_permute", RouteArgs), ("moe_route_permute_noalloc", RouteArgs),
+        L.mge_gemm4_workspace_bytes.restype = C.c_size_t
+        L.mge_gemm4_workspace_bytes.argtypes = [C.POINTER(Gemm4Args)]
+        L.mge_fwd_mxfp4_workspace_bytes.restype = C.c_size_t
+        L.mge_fwd_mxfp4_workspace_bytes.argtypes = [C.POINTER(FwdArgs)]
+        for name, st in (("moe_route_topk", RouteTopkArgs), ("moe_route_topk_bwd", RouteTopkBwdArgs),
+                         ("mxfp4_quantize", Quant4Args), ("mxfp4_dequantize", Dequant4Args),
+                         ("mxfp4_grouped_gemm", Gemm4Args), ("grouped_mlp_fwd_mxfp4", FwdArgs),
+                         ("moe_route_permute", RouteArgs), ("moe_route_permute_noalloc", RouteArgs),
                          ("mxfp8_quantize", QuantArgs),
                          ("mge_tensor_scale", TensorScaleArgs),
                          ("grouped_mlp_fwd", FwdArgs), ("grouped_mlp_fwd_unfused", FwdUnfusedArgs),
@@ -629,4 +670,236 @@ def moe_router_bwd(topk_idx: torch.Tensor, topk_prob: torch.Tensor, d_prob: torc
     a.T, a.E, a.k = T, E, k
     a.topk_idx, a.topk_prob, a.d_prob, a.d_logits = _ptr(topk_idx), _ptr(topk_prob), _ptr(d_prob), _ptr(out)
     _check(lib().moe_router_bwd(C.byref(a), _stream(dev)), "moe_router_bwd")
+    return out
+
+
+# ------------------------------------------------------------------------------ router choice
+
+_TORCH_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _call(fn: str, a, dev) -> None:
+    """One library call on the current stream of `dev`, with `dev` current while it launches."""
+    f = getattr(lib(), fn)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(f(C.byref(a), _stream(dev)), fn)
+    else:
+        with torch.cuda.device(dev):
+            _check(f(C.byref(a), _stream(dev)), fn)
+
+
+def _on(dev, *ts) -> None:
+    _need(dev.type == "cuda", f"tensors must be on a GPU (got {dev})")
+    for t in ts:
+        _need(t is None or t.device == dev, "tensors on different devices")
+
+
+def _check_logits(logits, score: str):
+    _need(score in SCORE, f"score must be 'softmax' or 'sigmoid', not {score!r}")
+    _need(logits.dim() == 2 and logits.dtype in _TORCH_DTYPE, "logits must be [T, E], float32 or bfloat16")
+    _need(logits.shape[1] <= 1 or logits.stride(1) == 1, "the experts of a row of logits must be contiguous")
+
+
+def _row_stride(t) -> int:
+    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def moe_route_topk(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                   num_groups: int = 1, topk_groups: int = 1, group_topn: int = 2, renormalize: bool = True,
+                   scale: float = 1.0, out=None):
+    """The k experts of each token and their weights -> (topk_idx int32 [T, k], topk_prob fp32 [T, k]), the pair that
+    moe_route_permute takes.  logits: [T, E] fp32 or bf16 (rows may be strided); -inf or NaN masks an expert.
+    score "softmax" or "sigmoid"; bias: fp32 [E], added to the scores for the choice only; num_groups / topk_groups:
+    choose among the topk_groups best of num_groups equal groups, ranked by the sum of their group_topn (1 or 2)
+    best; renormalize: weights divided by their sum; all weights times scale.  out: the pair to write into."""
+    _check_logits(logits, score)
+    T, E = logits.shape
+    dev = logits.device
+    idx, prob = out if out is not None else (torch.empty((T, k), device=dev, dtype=torch.int32),
+                                             torch.empty((T, k), device=dev, dtype=torch.float32))
+    _on(dev, bias, idx, prob)
+    _need(bias is None or (bias.dtype == torch.float32 and bias.is_contiguous() and bias.numel() == E),
+          "bias must be contiguous float32 [E]")
+    _need(idx.dtype == torch.int32 and prob.dtype == torch.float32 and idx.shape == (T, k) and prob.shape == (T, k)
+          and idx.is_contiguous() and prob.is_contiguous(), "out must be contiguous (int32 [T, k], float32 [T, k])")
+    a = RouteTopkArgs(C.sizeof(RouteTopkArgs), T, E, k, SCORE[score], num_groups, topk_groups, group_topn,
+                      1 if renormalize else 0, scale, _TORCH_DTYPE[logits.dtype], _row_stride(logits), _ptr(logits),
+                      _ptr(bias), _ptr(idx), _ptr(prob))
+    _call("moe_route_topk", a, dev)
+    return idx, prob
+
+
+def moe_route_topk_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, d_prob: torch.Tensor, score: str = "softmax",
+                       renormalize: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """d_logits [T, E] (the logits' dtype, contiguous) from the forward's logits and choice and d_prob fp32 [T, k];
+    score, renormalize and scale as the forward had them (the choice and its bias have no gradient)."""
+    _check_logits(logits, score)
+    T, E = logits.shape
+    dev = logits.device
+    if out is None:
+        out = torch.empty((T, E), device=dev, dtype=logits.dtype)
+    _on(dev, topk_idx, d_prob, out)
+    _need(topk_idx.dim() == 2 and topk_idx.shape[0] == T and topk_idx.dtype == torch.int32 and topk_idx.is_contiguous(),
+          "topk_idx must be contiguous int32 [T, k]")
+    _need(d_prob.shape == topk_idx.shape and d_prob.dtype == torch.float32 and d_prob.is_contiguous(),
+          "d_prob must be contiguous float32 [T, k]")
+    _need(out.shape == (T, E) and out.dtype == logits.dtype and out.is_contiguous(),
+          "out must be contiguous [T, E] of the logits' dtype")
+    a = RouteTopkBwdArgs(C.sizeof(RouteTopkBwdArgs), T, E, topk_idx.shape[1], SCORE[score], 1 if renormalize else 0,
+                         scale, _TORCH_DTYPE[logits.dtype], _row_stride(logits), _ptr(logits), _ptr(topk_idx),
+                         _ptr(d_prob), _ptr(out))
+    _call("moe_route_topk_bwd", a, dev)
+    return out
+
+
+# ------------------------------------------------------------------------------ MXFP4
+
+def _is_u8(t) -> bool:
+    return t.dtype == torch.uint8 and t.is_contiguous()
+
+
+def mxfp4_quantize(w: torch.Tensor, orient: str = "row", out=None):
+    """BF16 [..., R, C] -> (row_codes, row_scales, col_codes, col_scales) in MXFP4 (absent ones None): codes uint8
+    [..., R, C/2] (two elements a byte, the even one in the low half) and scales uint8 [..., R, C/32]; the column
+    form is that of the transpose, R padded to 32: [..., C, Rp/2] and [..., C, Rp/32].  orient "row", "col" or
+    "both".  w: contiguous, or a 2-D matrix with a row stride that is a multiple of 8."""
+    _need(w.dtype == torch.bfloat16 and w.dim() >= 2, "w must be bfloat16 [..., R, C]")
+    _need(orient in ("row", "col", "both"), f"orient must be 'row', 'col' or 'both', not {orient!r}")
+    strided = w.dim() == 2 and (w.shape[1] <= 1 or w.stride(1) == 1) and w.stride(0) >= w.shape[1]
+    _need(w.is_contiguous() or strided, "w must be contiguous, or a matrix of contiguous rows")
+    R, Cc = w.shape[-2], w.shape[-1]
+    lead = tuple(w.shape[:-2])
+    batch = 1
+    for d in lead:
+        batch *= d
+    Rp = (R + 31) // 32 * 32
+    want_row, want_col = orient != "col", orient != "row"
+    dev = w.device
+    if out is None:
+        u8 = dict(device=dev, dtype=torch.uint8)
+        rc = torch.empty(lead + (R, Cc // 2), **u8) if want_row else None
+        rs = torch.empty(lead + (R, Cc // 32), **u8) if want_row else None
+        cc = torch.empty(lead + (Cc, Rp // 2), **u8) if want_col else None
+        cs = torch.empty(lead + (Cc, Rp // 32), **u8) if want_col else None
+    else:
+        rc, rs, cc, cs = out
+        for t, n, used in ((rc, R * Cc // 2, want_row), (rs, R * (Cc // 32), want_row), (cc, Cc * Rp // 2, want_col),
+                           (cs, Cc * (Rp // 32), want_col)):
+            _need(not used or (t is not None and _is_u8(t) and t.numel() == batch * n),
+                  "out must be contiguous uint8 tensors of the outputs' sizes")
+    _on(dev, rc, rs, cc, cs)
+    row_stride = Cc if w.is_contiguous() else w.stride(0)
+    a = Quant4Args(C.sizeof(Quant4Args), batch, R, Cc, R * row_stride, row_stride, _ptr(w),
+                   (ORIENT_ROW if want_row else 0) | (ORIENT_COL if want_col else 0), _ptr(rc) if want_row else None,
+                   _ptr(rs) if want_row else None, _ptr(cc) if want_col else None, _ptr(cs) if want_col else None)
+    _call("mxfp4_quantize", a, dev)
+    return rc, rs, cc, cs
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype: str = "bf16",
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Values [..., C] (bf16 or f32) of MXFP4 codes [..., C/2] and scales [..., C/32]."""
+    _need(out_dtype in DTYPE, f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
+    _need(codes.dim() >= 1 and _is_u8(codes) and _is_u8(scales), "codes and scales must be contiguous uint8")
+    Cc = codes.shape[-1] * 2
+    _need(Cc % 32 == 0 and tuple(scales.shape) == tuple(codes.shape[:-1]) + (Cc // 32,),
+          "codes must be [..., C/2] and scales [..., C/32], C a multiple of 32")
+    dev = codes.device
+    dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    shape = tuple(codes.shape[:-1]) + (Cc,)
+    if out is None:
+        out = torch.empty(shape, device=dev, dtype=dt)
+    _on(dev, scales, out)
+    _need(tuple(out.shape) == shape and out.dtype == dt and out.is_contiguous(), "out has another shape or dtype")
+    rows = codes.numel() // max(Cc // 2, 1)
+    a = Dequant4Args(C.sizeof(Dequant4Args), rows, Cc, DTYPE[out_dtype], _ptr(codes), _ptr(scales), _ptr(out))
+    _call("mxfp4_dequantize", a, dev)
+    return out
+
+
+def _expert_ptrs(w, E: int, rows: int, cols: int, dev, what: str):
+    """Host array of the E device pointers of [rows][cols] uint8 matrices: one stacked tensor or a sequence."""
+    if isinstance(w, torch.Tensor):
+        _need(_is_u8(w) and tuple(w.shape) == (E, rows, cols), f"{what} must be contiguous uint8 [{E}, {rows}, {cols}]")
+        _on(dev, w)
+        p, n = w.data_ptr(), rows * cols
+        return (vp * E)(*[p + e * n for e in range(E)])
+    ts = list(w)
+    _need(len(ts) == E and all(_is_u8(t) and tuple(t.shape) == (rows, cols) for t in ts),
+          f"{what} must be {E} contiguous uint8 matrices [{rows}, {cols}]")
+    _on(dev, *ts)
+    return _ptr_array(ts)
+
+
+def mxfp4_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, w, w_scale, split_sizes: Optional[torch.Tensor] = None,
+                       group_offsets: Optional[torch.Tensor] = None, out_dtype: str = "bf16",
+                       total_rows: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[r] = a[r] w_e^T for the rows r of every expert e, on MXFP4 weights.
+    a: MXFP8 codes [rows, K] or MXFP4 codes [rows, K/2], told apart by a_scale [rows, K/32]; w: MXFP4 codes
+    [E, N, K/2] with w_scale [E, N, K/32] (stacked, or a sequence of E matrices).  split_sizes int32 [E] and
+    group_offsets int32 [E] or [E+1]: the groups' row counts and first rows (absent with one expert: all rows).
+    total_rows: rows in all groups at most, where the caller knows fewer than `rows` (T * k).  Rows outside the
+    groups are left as they were.  For the input gradient pass the column form of the weight."""
+    _need(out_dtype in DTYPE, f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
+    _need(a.dim() == 2 and a_scale.dim() == 2 and _is_u8(a) and _is_u8(a_scale) and a.shape[0] == a_scale.shape[0],
+          "a and a_scale must be contiguous uint8 [rows, ...]")
+    rows, K = a.shape[0], a_scale.shape[1] * 32
+    _need(K > 0 and a.shape[1] in (K, K // 2), "a must be [rows, K] (MXFP8) or [rows, K/2] (MXFP4) with a_scale [rows, K/32]")
+    fmt = FORMAT["mxfp8" if a.shape[1] == K else "mxfp4"]
+    E = len(w)
+    _need(E >= 1 and len(w_scale) == E and w[0].dim() == 2, "w must be [E, N, K/2] with w_scale [E, N, K/32]")
+    N = w[0].shape[0] if not isinstance(w, torch.Tensor) else w.shape[1]
+    dev = a.device
+    dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    if out is None:
+        out = torch.empty((rows, N), device=dev, dtype=dt)
+    _need(tuple(out.shape) == (rows, N) and out.dtype == dt and out.is_contiguous(), "out has another shape or dtype")
+    for t, lo in ((split_sizes, E), (group_offsets, E)):
+        _need(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= lo),
+              "split_sizes and group_offsets must be contiguous int32 with an entry for each expert")
+    _on(dev, a_scale, out, split_sizes, group_offsets, workspace)
+    wp = _expert_ptrs(w, E, N, K // 2, dev, "w")
+    wsp = _expert_ptrs(w_scale, E, N, K // 32, dev, "w_scale")
+    g = Gemm4Args(C.sizeof(Gemm4Args), fmt, E, N, K, rows, total_rows or 0, _ptr(split_sizes), _ptr(group_offsets),
+                  _ptr(a), _ptr(a_scale), C.cast(wp, vp), C.cast(wsp, vp), DTYPE[out_dtype], _ptr(out))
+    if workspace is None:
+        workspace = torch.empty(int(lib().mge_gemm4_workspace_bytes(C.byref(g))), device=dev, dtype=torch.uint8)
+    g.workspace, g.workspace_bytes = _ptr(workspace), workspace.numel()
+    _call("mxfp4_grouped_gemm", g, dev)
+    return out
+
+
+def grouped_mlp_fwd_mxfp4(rt: RouteOut, w_gate_up, w_down, w_gate_up_scale, w_down_scale, y_dtype: str = "bf16",
+                          out: Optional[FwdOut] = None) -> FwdOut:
+    """grouped_mlp_fwd for serving on MXFP4 weights: w_gate_up [E, 2F, H/2] and w_down [E, H, F/2] are mxfp4_quantize
+    row codes with their scales; `rt` is an MXFP8 route (activations and h stay in MXFP8)."""
+    _need(rt.prec == "mxfp8", "the route must be prec='mxfp8' (the activations' format)")
+    _need(y_dtype in DTYPE, f"y_dtype must be 'bf16' or 'f32', not {y_dtype!r}")
+    E, H, R = rt.E, rt.H, rt.R
+    F = (w_gate_up.shape[1] if isinstance(w_gate_up, torch.Tensor) else w_gate_up[0].shape[0]) // 2
+    dev = rt.x_perm.device
+    if out is None:
+        out = FwdOut(y_perm=torch.empty((R, H), device=dev, dtype=torch.bfloat16 if y_dtype == "bf16" else torch.float32),
+                     h=torch.empty((R, F), device=dev, dtype=torch.uint8),
+                     h_scale=torch.empty((R, F // 32), device=dev, dtype=torch.uint8))
+    keep = [_expert_ptrs(w_gate_up, E, 2 * F, H // 2, dev, "w_gate_up"),
+            _expert_ptrs(w_down, E, H, F // 2, dev, "w_down"),
+            _expert_ptrs(w_gate_up_scale, E, 2 * F, H // 32, dev, "w_gate_up_scale"),
+            _expert_ptrs(w_down_scale, E, H, F // 32, dev, "w_down_scale")]
+    _on(dev, out.y_perm, out.h, out.h_scale, rt.split_sizes, rt.group_offsets, rt.prob_perm)
+    a = FwdArgs(C.sizeof(FwdArgs), PREC["mxfp8"], E, H, F, rt.T, rt.k, rt.align, _ptr(rt.split_sizes),
+                _ptr(rt.group_offsets), _ptr(rt.prob_perm), _ptr(rt.x_perm), _ptr(rt.x_perm_scale), C.cast(keep[0], vp),
+                C.cast(keep[2], vp), C.cast(keep[1], vp), C.cast(keep[3], vp), DTYPE[y_dtype], _ptr(out.y_perm),
+                _ptr(out.h), _ptr(out.h_scale))
+    if out.workspace is None:
+        out.workspace = torch.empty(max(int(lib().mge_fwd_mxfp4_workspace_bytes(C.byref(a))), 256), device=dev,
+                                    dtype=torch.uint8)
+    a.workspace, a.workspace_bytes = _ptr(out.workspace), out.workspace.numel()
+    _call("grouped_mlp_fwd_mxfp4", a, dev)
     return out

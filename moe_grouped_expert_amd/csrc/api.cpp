@@ -966,6 +966,236 @@ mge_status moe_router_bwd(const mge_router_bwd_args* a, void* stream) {
                            static_cast<hipStream_t>(stream));
 }
 
+// ------------------------------------------------------------------ router choice
+static mge_status check_topk(int T, int E, int k, int score, int dtype, float scale, int64_t ld, const void* logits,
+                             const void* idx) {
+  MGE_REQUIRE(T >= 0, "T must be >= 0 (got %d)", T);
+  MGE_REQUIRE(E >= 1 && E <= 256, "E must be in [1, 256] (got %d)", E);
+  MGE_REQUIRE(k >= 1 && k <= 8 && k <= E, "k must be in [1, min(E, 8)] (got k=%d, E=%d)", k, E);
+  MGE_REQUIRE(score == MGE_SCORE_SOFTMAX || score == MGE_SCORE_SIGMOID, "score must be SOFTMAX or SIGMOID (got %d)", score);
+  MGE_REQUIRE(dtype == MGE_DTYPE_BF16 || dtype == MGE_DTYPE_F32, "logits_dtype must be BF16 or F32 (got %d)", dtype);
+  MGE_REQUIRE(scale - scale == 0.f, "scale must be finite");
+  MGE_REQUIRE(ld >= E, "logits_row_stride must be >= E (got %lld)", static_cast<long long>(ld));
+  MGE_REQUIRE(T == 0 || (logits && idx), "logits / topk_idx NULL");
+  const uintptr_t elem = dtype == MGE_DTYPE_F32 ? 4 : 2;
+  MGE_REQUIRE((reinterpret_cast<uintptr_t>(logits) & (elem - 1)) == 0, "logits misaligned");
+  return MGE_OK;
+}
+// rows of logits may be read 16 bytes at a time
+static bool topk_vec(const void* logits, int dtype, int64_t ld) {
+  return aligned16(logits) && (ld * (dtype == MGE_DTYPE_F32 ? 4 : 2)) % 16 == 0;
+}
+
+mge_status moe_route_topk(const mge_route_topk_args* a, void* stream) {
+  g_err[0] = 0;
+  MGE_REQUIRE(a != nullptr, "args is NULL");
+  MGE_REQUIRE(a->struct_size == sizeof(mge_route_topk_args), "struct_size mismatch");
+  const mge_status st = check_topk(a->T, a->E, a->k, a->score, a->logits_dtype, a->scale, a->logits_row_stride,
+                                   a->logits, a->topk_idx);
+  if (st != MGE_OK) return st;
+  MGE_REQUIRE(a->num_groups >= 1 && a->num_groups <= a->E && a->E % a->num_groups == 0,
+              "num_groups must divide E (got %d, E=%d)", a->num_groups, a->E);
+  MGE_REQUIRE(a->topk_groups >= 1 && a->topk_groups <= a->num_groups, "topk_groups must be in [1, num_groups] (got %d)",
+              a->topk_groups);
+  MGE_REQUIRE(a->k <= a->topk_groups * (a->E / a->num_groups), "k = %d experts do not fit topk_groups = %d groups of %d",
+              a->k, a->topk_groups, a->E / a->num_groups);
+  MGE_REQUIRE(a->group_topn == 1 || a->group_topn == 2, "group_topn must be 1 or 2 (got %d)", a->group_topn);
+  MGE_REQUIRE(a->T == 0 || a->topk_prob, "topk_prob NULL");
+  if (a->T == 0) return MGE_OK;
+  TopkParams p{};
+  p.T = a->T; p.ld = a->logits_row_stride; p.E = a->E; p.k = a->k;
+  p.G = a->num_groups; p.topg = a->topk_groups; p.topn = a->group_topn;
+  p.score = a->score; p.renorm = a->renormalize != 0; p.scale = a->scale;
+  p.logits = a->logits; p.bias = a->bias; p.topk_idx = a->topk_idx; p.topk_prob = a->topk_prob;
+  p.vec = topk_vec(a->logits, a->logits_dtype, a->logits_row_stride);
+  return launch_topk(p, a->logits_dtype, static_cast<hipStream_t>(stream));
+}
+
+mge_status moe_route_topk_bwd(const mge_route_topk_bwd_args* a, void* stream) {
+  g_err[0] = 0;
+  MGE_REQUIRE(a != nullptr, "args is NULL");
+  MGE_REQUIRE(a->struct_size == sizeof(mge_route_topk_bwd_args), "struct_size mismatch");
+  const mge_status st = check_topk(a->T, a->E, a->k, a->score, a->logits_dtype, a->scale, a->logits_row_stride,
+                                   a->logits, a->topk_idx);
+  if (st != MGE_OK) return st;
+  MGE_REQUIRE(a->T == 0 || (a->d_prob && a->d_logits), "d_prob / d_logits NULL");
+  if (a->T == 0) return MGE_OK;
+  TopkBwdParams p{};
+  p.T = a->T; p.ld = a->logits_row_stride; p.E = a->E; p.k = a->k;
+  p.score = a->score; p.renorm = a->renormalize != 0; p.scale = a->scale;
+  p.logits = a->logits; p.topk_idx = a->topk_idx; p.d_prob = a->d_prob; p.d_logits = a->d_logits;
+  p.vec = topk_vec(a->logits, a->logits_dtype, a->logits_row_stride);
+  return launch_topk_bwd(p, a->logits_dtype, static_cast<hipStream_t>(stream));
+}
+
+// ------------------------------------------------------------------ MXFP4
+mge_status mxfp4_quantize(const mge_quant4_args* a, void* stream) {
+  g_err[0] = 0;
+  MGE_REQUIRE(a != nullptr, "args is NULL");
+  MGE_REQUIRE(a->struct_size == sizeof(mge_quant4_args), "struct_size mismatch");
+  MGE_REQUIRE(a->batch >= 0 && a->batch <= 65535 && a->R >= 0 && a->C >= 0, "negative size, or batch above 65535");
+  MGE_REQUIRE(a->C % 32 == 0, "C must be a multiple of 32 (got %d)", a->C);
+  MGE_REQUIRE(a->orient != 0 && (a->orient & ~3u) == 0, "orient must be ROW, COL or ROW|COL");
+  MGE_REQUIRE((a->in || a->R == 0 || a->batch == 0) && aligned16(a->in), "in must be non-NULL (R > 0) and 16-byte aligned");
+  MGE_REQUIRE(a->in_row_stride >= a->C && a->in_row_stride % 8 == 0, "in_row_stride must be >= C and a multiple of 8");
+  MGE_REQUIRE(a->batch <= 1 || (a->in_batch_stride % 8 == 0 && a->in_batch_stride >= int64_t(a->R) * a->in_row_stride),
+              "in_batch_stride too small or not a multiple of 8");
+  MGE_REQUIRE(a->R <= 65535 * 128, "R must be at most %d (got %d)", 65535 * 128, a->R);
+  if (a->batch == 0 || a->R == 0 || a->C == 0) return MGE_OK;   // no element, no output
+  if (a->orient & MGE_ORIENT_ROW)
+    MGE_REQUIRE(a->row_codes && a->row_scales && aligned16(a->row_codes), "row outputs missing or misaligned");
+  if (a->orient & MGE_ORIENT_COL)
+    MGE_REQUIRE(a->col_codes && a->col_scales && aligned16(a->col_codes), "column outputs missing or misaligned");
+  Quant4Params q{};
+  q.in = a->in; q.in_batch_stride = a->in_batch_stride; q.in_row_stride = a->in_row_stride;
+  q.batch = a->batch; q.R = a->R; q.C = a->C; q.Rp = (int64_t(a->R) + 31) / 32 * 32;
+  if (a->orient & MGE_ORIENT_ROW) { q.row_codes = a->row_codes; q.row_scales = a->row_scales; }
+  if (a->orient & MGE_ORIENT_COL) { q.col_codes = a->col_codes; q.col_scales = a->col_scales; }
+  return launch_quant4(q, static_cast<hipStream_t>(stream));
+}
+
+mge_status mxfp4_dequantize(const mge_dequant4_args* a, void* stream) {
+  g_err[0] = 0;
+  MGE_REQUIRE(a != nullptr, "args is NULL");
+  MGE_REQUIRE(a->struct_size == sizeof(mge_dequant4_args), "struct_size mismatch");
+  MGE_REQUIRE(a->rows >= 0 && a->C >= 0 && a->C % 32 == 0, "rows must be >= 0 and C a multiple of 32 (got %lld, %d)",
+              static_cast<long long>(a->rows), a->C);
+  MGE_REQUIRE(a->out_dtype == MGE_DTYPE_BF16 || a->out_dtype == MGE_DTYPE_F32, "out_dtype must be BF16 or F32");
+  if (a->rows == 0 || a->C == 0) return MGE_OK;
+  MGE_REQUIRE(a->codes && aligned16(a->codes) && a->scales && a->out && aligned16(a->out),
+              "codes / scales / out NULL or misaligned");
+  MGE_REQUIRE(a->rows < (int64_t(1) << 38) / (a->C / 32), "too many values");
+  return launch_dequant4(a->rows * (a->C / 32), a->codes, a->scales, a->out_dtype, a->out, static_cast<hipStream_t>(stream));
+}
+
+size_t mge_gemm4_workspace_bytes(const mge_gemm4_args* a) {
+  if (!a || a->struct_size != sizeof(mge_gemm4_args) || a->E < 1 || a->E > 256) return 0;
+  return up256(2 * size_t(a->E) * sizeof(void*));
+}
+
+mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
+  g_err[0] = 0;
+  MGE_REQUIRE(a != nullptr, "args is NULL");
+  MGE_REQUIRE(a->struct_size == sizeof(mge_gemm4_args), "struct_size mismatch");
+  MGE_REQUIRE(a->a_format == MGE_FORMAT_MXFP8 || a->a_format == MGE_FORMAT_MXFP4, "a_format must be MXFP8 or MXFP4 (got %d)",
+              a->a_format);
+  MGE_REQUIRE(a->E >= 1 && a->E <= 256, "E must be in [1, 256] (got %d)", a->E);
+  MGE_REQUIRE(a->N >= 32 && a->N % 32 == 0 && a->K >= 32 && a->K % 32 == 0,
+              "N and K must be positive multiples of 32 (got N=%d, K=%d)", a->N, a->K);
+  MGE_REQUIRE(a->rows >= 0 && a->rows < (int64_t(1) << 31) / a->K, "rows must be in [0, 2^31 / K) (got %lld)",
+              static_cast<long long>(a->rows));
+  MGE_REQUIRE(a->total_rows >= 0, "total_rows must be >= 0");
+  MGE_REQUIRE(int64_t(a->N) * (a->K / 2) < (int64_t(1) << 31), "an expert's weight must be below 2^31 bytes");
+  MGE_REQUIRE((a->split_sizes != nullptr) == (a->group_offsets != nullptr) && (a->split_sizes || a->E == 1),
+              "split_sizes and group_offsets go together, and E > 1 needs both");
+  MGE_REQUIRE(a->out_dtype == MGE_DTYPE_BF16 || a->out_dtype == MGE_DTYPE_F32, "out_dtype must be BF16 or F32");
+  MGE_REQUIRE(a->w && a->w_scale, "weight pointer arrays are NULL");
+  for (int e = 0; e < a->E; ++e)
+    MGE_REQUIRE(a->w[e] && aligned16(a->w[e]) && a->w_scale[e], "weight of expert %d NULL or misaligned, or its scales NULL", e);
+  if (a->rows > 0)
+    MGE_REQUIRE(a->a && aligned16(a->a) && a->a_scale && a->out && aligned16(a->out), "a / a_scale / out NULL or misaligned");
+  const size_t need = mge_gemm4_workspace_bytes(a);
+  if (!a->workspace || a->workspace_bytes < need) {
+    set_error("MXFP4 product workspace needs %zu bytes (got %zu)", need, a->workspace_bytes);
+    return MGE_ERR_WORKSPACE;
+  }
+  if (a->rows == 0) return MGE_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Carve ws(a->workspace);
+  void** tab = static_cast<void**>(ws.take(2 * size_t(a->E) * sizeof(void*)));
+  const void* const* tabs[2] = {reinterpret_cast<const void* const*>(a->w), reinterpret_cast<const void* const*>(a->w_scale)};
+  mge_status st = launch_upload_tables(tabs, 2, a->E, tab, s);
+  if (st != MGE_OK) return st;
+  Gemm4Params p{};
+  p.E = a->E; p.N = a->N; p.K = a->K;
+  p.rows = int(a->rows);
+  p.total = int(a->total_rows > 0 && a->total_rows < a->rows ? a->total_rows : a->rows);
+  p.sizes = a->split_sizes; p.offs = a->group_offsets;
+  p.A = a->a; p.As = a->a_scale;
+  p.W = reinterpret_cast<const uint8_t* const*>(tab);
+  p.Ws = reinterpret_cast<const uint8_t* const*>(tab + a->E);
+  p.C = a->out;
+  return launch_gemm4_store(p, a->a_format == MGE_FORMAT_MXFP4, a->out_dtype == MGE_DTYPE_F32, s);
+}
+
+static size_t fwd4_ws(const mge_fwd_args* a, int R) {
+  size_t n = up256(4 * size_t(a->E) * sizeof(void*));
+  if (!a->h) n += up256(size_t(R) * a->F) + up256(size_t(R) * (a->F / 32));
+  return n;
+}
+
+size_t mge_fwd_mxfp4_workspace_bytes(const mge_fwd_args* a) {
+  if (!a || a->E < 1 || a->E > 256 || a->T < 0 || a->k < 1 || a->align < 1) return 0;
+  return fwd4_ws(a, int(mge_perm_rows(a->T, a->k, a->E, a->align)));
+}
+
+mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
+  g_err[0] = 0;
+  MGE_REQUIRE(a != nullptr, "args is NULL");
+  MGE_REQUIRE(a->struct_size == sizeof(mge_fwd_args), "struct_size mismatch");
+  mge_status st = check_mlp_dims(a->prec, a->E, a->H, a->F, a->T, a->k, a->align);
+  if (st != MGE_OK) return st;
+  if (a->prec != MGE_PREC_MXFP8 || a->saved_gu || a->h_col || a->h_col_scale) {
+    set_error("grouped_mlp_fwd_mxfp4 takes prec MXFP8 (the activations) and has no training mode");
+    return MGE_ERR_UNSUPPORTED;
+  }
+  MGE_REQUIRE(a->split_sizes && a->group_offsets && a->prob_perm, "split_sizes / group_offsets / prob_perm NULL");
+  MGE_REQUIRE(a->x_perm && aligned16(a->x_perm) && a->x_perm_scale, "x_perm / x_perm_scale NULL or misaligned");
+  MGE_REQUIRE(a->w_gate_up && a->w_down && a->w_gate_up_scale && a->w_down_scale, "weight pointer arrays are NULL");
+  for (int e = 0; e < a->E; ++e) {
+    MGE_REQUIRE(a->w_gate_up[e] && aligned16(a->w_gate_up[e]) && a->w_gate_up_scale[e], "w_gate_up[%d] NULL or misaligned", e);
+    MGE_REQUIRE(a->w_down[e] && aligned16(a->w_down[e]) && a->w_down_scale[e], "w_down[%d] NULL or misaligned", e);
+  }
+  MGE_REQUIRE(a->y_dtype == MGE_DTYPE_BF16 || a->y_dtype == MGE_DTYPE_F32, "y_dtype must be BF16 or F32");
+  MGE_REQUIRE(a->y_perm && aligned16(a->y_perm), "y_perm must be non-NULL and 16-byte aligned");
+  if (a->h) MGE_REQUIRE(aligned16(a->h) && a->h_scale, "h misaligned or h_scale NULL");
+  const int64_t R64 = mge_perm_rows(a->T, a->k, a->E, a->align);
+  MGE_REQUIRE(R64 < (int64_t(1) << 31) / (a->H > a->F ? a->H : a->F) && int64_t(a->F) * a->H < (int64_t(1) << 31),
+              "operand too large for 32-bit offsets (rows=%lld H=%d F=%d)", static_cast<long long>(R64), a->H, a->F);
+  const int R = int(R64);
+  const size_t need = fwd4_ws(a, R);
+  if (!a->workspace || a->workspace_bytes < need) {
+    set_error("forward workspace needs %zu bytes (got %zu)", need, a->workspace_bytes);
+    return MGE_ERR_WORKSPACE;
+  }
+  if (a->T == 0) return MGE_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int E = a->E;
+  Carve ws(a->workspace);
+  void** tab = static_cast<void**>(ws.take(4 * size_t(E) * sizeof(void*)));
+  void* h = a->h;
+  uint8_t* hs = a->h_scale;
+  if (!h) {
+    h = ws.take(size_t(R) * a->F);
+    hs = static_cast<uint8_t*>(ws.take(size_t(R) * (a->F / 32)));
+  }
+  const void* const* tabs[4] = {reinterpret_cast<const void* const*>(a->w_gate_up),
+                                reinterpret_cast<const void* const*>(a->w_down),
+                                reinterpret_cast<const void* const*>(a->w_gate_up_scale),
+                                reinterpret_cast<const void* const*>(a->w_down_scale)};
+  st = launch_upload_tables(tabs, 4, E, tab, s);
+  if (st != MGE_OK) return st;
+  const uint8_t* const* dev = reinterpret_cast<const uint8_t* const*>(tab);
+  Gemm4Params g{};
+  g.E = E; g.N = 2 * a->F; g.K = a->H; g.F = a->F;
+  g.rows = R; g.total = a->T * a->k;
+  g.sizes = a->split_sizes; g.offs = a->group_offsets;
+  g.A = static_cast<const uint8_t*>(a->x_perm); g.As = a->x_perm_scale;
+  g.W = dev; g.Ws = dev + 2 * E;
+  g.prob = a->prob_perm;
+  g.h_codes = static_cast<uint8_t*>(h); g.h_scales = hs;
+  st = launch_gemm4_swiglu(g, s);
+  if (st != MGE_OK) return st;
+  Gemm4Params d{};
+  d.E = E; d.N = a->H; d.K = a->F;
+  d.rows = R; d.total = a->T * a->k;
+  d.sizes = a->split_sizes; d.offs = a->group_offsets;
+  d.A = static_cast<const uint8_t*>(h); d.As = hs;
+  d.W = dev + E; d.Ws = dev + 3 * E;
+  d.C = a->y_perm;
+  return launch_gemm4_store(d, false, a->y_dtype == MGE_DTYPE_F32, s);
+}
+
 mge_status mge_check_device_errors(void* route_workspace, void* stream) {
   g_err[0] = 0;
   MGE_REQUIRE(route_workspace != nullptr, "workspace is NULL");

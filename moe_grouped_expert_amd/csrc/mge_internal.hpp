@@ -91,6 +91,60 @@ mge_status route_scratch(void** ptr);
 mge_status launch_router_bwd(int T, int E, int k, const int32_t* idx, const float* prob, const float* dprob,
                              float* dlogits, hipStream_t s);
 
+// moe_route_topk / moe_route_topk_bwd
+struct TopkParams {
+  int64_t T, ld;            // tokens; logits row stride (elements)
+  int E, k, G, topg, topn, score, renorm;
+  float scale;
+  const void* logits;
+  const float* bias;
+  int32_t* topk_idx;
+  float* topk_prob;
+  bool vec;                 // rows of logits may be read 16 bytes at a time
+};
+mge_status launch_topk(const TopkParams& p, int dtype, hipStream_t s);
+struct TopkBwdParams {
+  int64_t T, ld;
+  int E, k, score, renorm;
+  float scale;
+  const void* logits;
+  const int32_t* topk_idx;
+  const float* d_prob;
+  void* d_logits;           // [T][E], the logits' type
+  bool vec;
+};
+mge_status launch_topk_bwd(const TopkBwdParams& p, int dtype, hipStream_t s);
+
+// ------------------------------------------------------------ MXFP4
+struct Quant4Params {
+  const uint16_t* in;
+  int64_t in_batch_stride, in_row_stride;   // elements
+  int batch, C;
+  int64_t R, Rp;                            // rows, and rows padded to 32 (column form)
+  uint8_t* row_codes;  uint8_t* row_scales;
+  uint8_t* col_codes;  uint8_t* col_scales;
+};
+mge_status launch_quant4(const Quant4Params& p, hipStream_t s);
+mge_status launch_dequant4(int64_t blocks, const uint8_t* codes, const uint8_t* scales, int dtype, void* out, hipStream_t s);
+
+// C[r] = A[r] W_e^T with MXFP4 weights; SwiGLU: h from W_e = [gate rows; up rows]
+struct Gemm4Params {
+  int E, N, K, F;
+  int rows;                         // rows of A and C: every group is clamped into them
+  int total;                        // at most this many rows in all groups
+  const int32_t* sizes;             // [E], or NULL: one group of all rows
+  const int32_t* offs;
+  const uint8_t* A;                 // [rows][K] MXFP8 or [rows][K/2] MXFP4 codes
+  const uint8_t* As;                // [rows][K/32]
+  const uint8_t* const* W;          // device table: [N][K/2] codes of each expert
+  const uint8_t* const* Ws;         // device table: [N][K/32]
+  void* C;                          // [rows][N]
+  const float* prob;                // SwiGLU: [rows]
+  uint8_t* h_codes; uint8_t* h_scales;   // SwiGLU: [rows][F], [rows][F/32]
+};
+mge_status launch_gemm4_store(const Gemm4Params& p, bool a4, bool f32, hipStream_t s);
+mge_status launch_gemm4_swiglu(const Gemm4Params& p, hipStream_t s);
+
 // ------------------------------------------------------------ combine / reductions
 // entries of perm_pos outside [0, in_rows) add nothing
 mge_status launch_combine(int T, int k, int H, int in_dtype, int out_dtype, const void* in, int64_t in_rows,

@@ -1,0 +1,70 @@
+"""MXFP4 (E2M1 elements + E8M0 block scales) in fp64 — oracle, test infrastructure only.
+
+OCP Microscaling Formats v1.0: sign, 2 exponent bits (bias 1), 1 mantissa bit — magnitudes 0,
+.5, 1, 1.5, 2, 3, 4, 6; one power-of-two scale per 32 elements, its exponent
+floor(log2(amax)) - 2, clamped to [-127, 127]; elements round to nearest, ties to the even
+code, and saturate at 6.  Packed two to a byte, the even element in the low half.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+from . import mx
+
+VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+BLOCK = 32
+
+
+def encode(v) -> np.ndarray:
+    """fp64 values -> codes 0..15, by the distance to every representable value."""
+    a = np.minimum(np.abs(np.asarray(v, dtype=np.float64)), 6.0)
+    dist = np.abs(a[..., None] - VALUES)
+    best = dist.min(-1, keepdims=True)
+    near = dist == best                                  # two of them on a tie
+    even = near & (np.arange(8) % 2 == 0)
+    code = np.where(near.sum(-1) > 1, even.argmax(-1), near.argmax(-1))
+    return (code | np.where(np.signbit(v), 8, 0)).astype(np.uint8)
+
+
+def quantize_rows(x):
+    """fp64 [R][C] -> packed codes uint8 [R][C/2], scales uint8 [R][C/32]."""
+    x = np.asarray(x, dtype=np.float64)
+    R, C = x.shape
+    b = x.reshape(R, C // BLOCK, BLOCK)
+    amax = np.abs(b).max(-1)
+    _, ex = np.frexp(amax)
+    e = np.clip(np.where(amax > 0, ex - 1 - 2, -127), -127, 127)
+    code = encode(np.ldexp(b, -e[..., None])).reshape(R, C)
+    return code[:, 0::2] | (code[:, 1::2] << 4), (e + 127).astype(np.uint8)
+
+
+def quantize_cols(x):
+    """The row quantization of the transpose, rows padded with zeros to a multiple of 32."""
+    R, C = x.shape
+    xp = np.zeros(((R + 31) // 32 * 32, C))
+    xp[:R] = x
+    return quantize_rows(np.ascontiguousarray(xp.T))
+
+
+def decode(codes, scales) -> np.ndarray:
+    """packed codes [..., C/2], scales [..., C/32] -> fp64 [..., C]; scale byte 255 is NaN."""
+    c = np.asarray(codes)
+    v = np.empty(c.shape[:-1] + (c.shape[-1] * 2,))
+    signed = np.concatenate([VALUES, -VALUES])
+    v[..., 0::2] = signed[c & 15]
+    v[..., 1::2] = signed[c >> 4]
+    s = np.where(np.asarray(scales) == 255, np.nan, np.exp2(np.asarray(scales).astype(np.float64) - 127))
+    return v * np.repeat(s, BLOCK, axis=-1)
+
+
+def decode_rows8(codes, scales) -> np.ndarray:
+    return mx.e4m3_decode(codes) * np.repeat(mx.e8m0_decode(scales), BLOCK, axis=-1)
+
+
+def grouped(a, w, sizes, offsets, out):
+    """out[r] = a[r] w_e^T for the rows of every group, and |a| |w|^T, the scale of its rounding errors."""
+    mag = np.zeros_like(out)
+    for e, (n, o) in enumerate(zip(sizes, offsets)):
+        out[o:o + n] = a[o:o + n] @ w[e].T
+        mag[o:o + n] = np.abs(a[o:o + n]) @ np.abs(w[e]).T
+    return out, mag

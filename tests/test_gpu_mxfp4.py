@@ -1,0 +1,331 @@
+"""GPU parity of the MXFP4 calls against the fp64 oracle.
+
+Quantization and dequantization are compared bit by bit.  Products: small integers whose sums
+are exact in fp32 are compared exactly; for the others, with S = sum_k |a_k w_k| and u = 2^-24,
+  MXFP4 x MXFP4   products have at most 4 significant bits, an instruction of the matrix unit adds
+                  its 128 to fp32 rounding: (K/128 + 8) u S
+  MXFP8 x MXFP4   the unit aligns an instruction's products to the largest one; fp8 operands
+                  showed an error of 5e-5 of the result's norm, 2^-17 of S: 2^-14 S
+plus half a step of bf16 where the result is bf16."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx, mxfp4
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def m():
+    import moe_grouped_expert_amd as mge
+    return mge
+
+
+def bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).cuda().to(torch.bfloat16)
+
+
+def f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def npy(t):
+    return t.cpu().numpy()
+
+
+# ------------------------------------------------------------------------------ formats
+
+def test_every_bf16_value_at_every_scale(m):
+    """Blocks whose first value sets the scale and whose others run through all finite bf16 magnitudes up to it."""
+    from tests.gpu_helpers import say
+    say("[gpu] quantize4 exhaustive")
+    rows = []
+    for top in list(range(0, 255)):                        # exponent field of the block's largest
+        lo = max(0, (top - 4) * 128)
+        v = np.arange(lo, (top + 1) * 128, dtype=np.uint16)
+        pick = np.concatenate([v, v | 0x8000]).astype(np.uint16)
+        pad = (-len(pick)) % 31
+        pick = np.concatenate([pick, np.zeros(pad, np.uint16)]).reshape(-1, 31)
+        first = np.full((len(pick), 1), top * 128 + 64 if top else 3, np.uint16)
+        rows.append(np.concatenate([first, pick], 1))
+    bits = np.concatenate(rows)
+    x = torch.from_numpy(bits.view(np.int16).copy()).cuda().view(torch.bfloat16)
+    ref = (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    rc, rs, _, _ = m.mxfp4_quantize(x)
+    q, s = mxfp4.quantize_rows(ref)
+    np.testing.assert_array_equal(npy(rs), s)
+    np.testing.assert_array_equal(npy(rc), q)
+    for dt in ("bf16", "f32"):
+        np.testing.assert_array_equal(f64(m.mxfp4_dequantize(rc, rs, dt)), mxfp4.decode(q, s))
+
+
+def test_dequantize_every_scale(m):
+    codes = np.tile(np.arange(256, dtype=np.uint8).reshape(16, 16), (256, 1, 1)).reshape(-1, 16)
+    scales = np.repeat(np.arange(256, dtype=np.uint8), 16)[:, None]
+    v = m.mxfp4_dequantize(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), "f32")
+    ref = mxfp4.decode(codes, scales)
+    ref = np.where(np.abs(ref) > 3.4028234e38, np.copysign(np.inf, ref), ref)   # 2^127 times 4, 6
+    np.testing.assert_array_equal(f64(v), ref)
+
+
+@pytest.mark.parametrize("R,C", [(1, 32), (31, 32), (32, 64), (33, 96), (128, 128), (129, 160), (255, 288), (300, 1056), (5, 4096)])
+@pytest.mark.parametrize("orient", ["row", "col", "both"])
+def test_quantize_shapes(m, R, C, orient):
+    from tests.gpu_helpers import say
+    say("[gpu] quantize4", R, C, orient)
+    rng = np.random.default_rng(R * 7 + C)
+    x = rng.standard_normal((R, C)) * np.exp2(rng.integers(-30, 30, (R, 1)))
+    x[rng.random((R, C)) < 0.1] = 0
+    x[:, :32] = 0
+    t = bf16(x)
+    x = f64(t)
+    rc, rs, cc, cs = m.mxfp4_quantize(t, orient)
+    assert (rc is None) == (orient == "col") and (cc is None) == (orient == "row")
+    if rc is not None:
+        q, s = mxfp4.quantize_rows(x)
+        np.testing.assert_array_equal(npy(rc), q)
+        np.testing.assert_array_equal(npy(rs), s)
+    if cc is not None:
+        q, s = mxfp4.quantize_cols(x)
+        np.testing.assert_array_equal(npy(cc), q)
+        np.testing.assert_array_equal(npy(cs), s)
+        np.testing.assert_array_equal(f64(m.mxfp4_dequantize(cc, cs)), mxfp4.decode(q, s))
+
+
+def test_quantize_batch_strides_and_empty(m):
+    rng = np.random.default_rng(3)
+    t = bf16(rng.standard_normal((3, 70, 96)))
+    rc, rs, cc, cs = m.mxfp4_quantize(t, "both")
+    for b in range(3):
+        one = m.mxfp4_quantize(t[b].contiguous(), "both")
+        for x, y in zip((rc, rs, cc, cs), one):
+            assert torch.equal(x[b], y)
+    wide = bf16(rng.standard_normal((70, 256)))
+    v = wide[:, 64:64 + 96]
+    for x, y in zip(m.mxfp4_quantize(v, "both"), m.mxfp4_quantize(v.contiguous(), "both")):
+        assert torch.equal(x, y)
+    e = m.mxfp4_quantize(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), "both")
+    assert e[0].shape == (0, 32) and e[2].shape == (64, 0)
+    assert m.mxfp4_dequantize(e[0], e[1]).shape == (0, 64)
+
+
+# ------------------------------------------------------------------------------ products
+
+def operand(rng, rows, K, fmt, ints):
+    """(codes, scales) on the GPU and the fp64 values they stand for."""
+    x = rng.integers(-3, 4, (rows, K)).astype(np.float64) if ints else rng.standard_normal((rows, K)) * np.exp2(rng.integers(-3, 4, (rows, 1)))
+    if fmt == "mxfp4":
+        q, s = mxfp4.quantize_rows(x)
+        v = mxfp4.decode(q, s) if rows else x
+    else:
+        q, s = mx.quantize_rows(x)
+        v = mxfp4.decode_rows8(q, s) if rows else x
+    return torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), v
+
+
+def groups(sizes, align):
+    off, o = [], 0
+    for n in sizes:
+        off.append(o)
+        o += (n + align - 1) // align * align
+    return np.array(off, np.int64), o
+
+
+def run_gemm(m, sizes, N, K, fmt, out_dtype, ints=False, align=1, extra=0, seed=0, split=True, total=None):
+    from tests.gpu_helpers import say
+    say("[gpu] gemm4", sizes if len(sizes) < 12 else len(sizes), N, K, fmt, out_dtype, "ints" if ints else "")
+    rng = np.random.default_rng(seed + N + K)
+    E = len(sizes)
+    off, R = groups(sizes, align)
+    R += extra
+    a, a_s, av = operand(rng, R, K, fmt, ints)
+    inside = np.zeros(R, bool)
+    for n, o in zip(sizes, off):
+        inside[o:o + n] = True
+    if not inside.all():                                   # rows outside the groups hold NaN bytes
+        bad = torch.from_numpy(~inside).cuda()
+        a[bad], a_s[bad] = 0x7F, 255
+    W, Ws, wv = [], [], []
+    for e in range(E):
+        w, s, v = operand(rng, N, K, "mxfp4", ints)
+        W.append(w); Ws.append(s); wv.append(v)
+    if split:
+        W, Ws = torch.stack(W), torch.stack(Ws)
+    dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    out = torch.full((R, N), 7.0, dtype=dt, device="cuda")
+    sz = torch.tensor(sizes, dtype=torch.int32, device="cuda")
+    of = torch.from_numpy(off.astype(np.int32)).cuda()
+    r = m.mxfp4_grouped_gemm(a, a_s, W, Ws, sz, of, out_dtype, total_rows=total, out=out)
+    assert r is out
+    got = f64(out)
+    ref, mag = mxfp4.grouped(av, wv, sizes, off, np.full((R, N), 7.0))
+    half = 2.0 ** -8 if out_dtype == "bf16" else 0.0
+    if ints:
+        np.testing.assert_array_equal(got, f64(torch.from_numpy(ref).to(dt)))
+        return
+    tol = ((K / 128 + 8) * U if fmt == "mxfp4" else 2.0 ** -14) * mag
+    assert np.all(np.abs(got - ref) <= half * np.abs(ref) + (1 + half) * tol)
+    assert np.all(got[~inside] == 7.0)
+
+
+SHAPES = [([1], 32, 32), ([1], 64, 96), ([2, 0, 3], 96, 160), ([0, 0, 1, 0], 32, 256), ([17], 128, 512), ([16, 33, 1], 160, 640),
+          ([5, 70, 0, 31], 352, 1056), ([300, 1, 129], 288, 384), ([257], 512, 2048), ([1] * 8, 1024, 4096)]
+
+
+@pytest.mark.parametrize("sizes,N,K", SHAPES)
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+def test_gemm(m, sizes, N, K, fmt, out_dtype):
+    run_gemm(m, sizes, N, K, fmt, out_dtype, ints=True)
+    run_gemm(m, sizes, N, K, fmt, out_dtype, align=32, extra=5, seed=1, split=False)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_gemm_many_experts(m, fmt):
+    rng = np.random.default_rng(8)
+    sizes = rng.integers(0, 4, 256)
+    sizes[rng.random(256) < 0.5] = 0
+    run_gemm(m, [int(n) for n in sizes], 64, 128, fmt, "bf16", total=int(sizes.sum()))
+    one = [0] * 255 + [40]
+    run_gemm(m, one, 96, 224, fmt, "bf16", ints=True, total=40)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_gemm_many_rows(m, fmt):
+    run_gemm(m, [700, 0, 1025, 3, 511], 544, 768, fmt, "bf16", ints=True)
+    run_gemm(m, [700, 0, 1025, 3, 511], 544, 800, fmt, "bf16")
+
+
+def test_gemm_dense_and_empty(m):
+    rng = np.random.default_rng(9)
+    a, s, av = operand(rng, 9, 256, "mxfp8", True)
+    w, ws, wv = operand(rng, 64, 256, "mxfp4", True)
+    got = m.mxfp4_grouped_gemm(a, s, w[None], ws[None], out_dtype="f32")
+    np.testing.assert_array_equal(f64(got), av @ wv.T)
+    z = m.mxfp4_grouped_gemm(a[:0], s[:0], w[None], ws[None])
+    assert z.shape == (0, 64)
+
+
+def test_gemm_input_gradient(m):
+    """dX = dY W on the column form of the weight, against the formula and against differences of <dY, X W^T>."""
+    rng = np.random.default_rng(10)
+    N, K, sizes = 96, 64, [3, 0, 5]
+    w = bf16(rng.standard_normal((3, N, K)))
+    _, _, cc, cs = m.mxfp4_quantize(w, "col")
+    dy, dys, dyv = operand(rng, 8, N, "mxfp8", False)
+    sz = torch.tensor(sizes, dtype=torch.int32, device="cuda")
+    of = torch.tensor([0, 3, 3], dtype=torch.int32, device="cuda")
+    dx = f64(m.mxfp4_grouped_gemm(dy, dys, cc, cs, sz, of, "f32"))
+    wt = mxfp4.decode(npy(cc), npy(cs))                    # [E][K][N]
+    ref, mag = mxfp4.grouped(dyv, wt, sizes, [0, 3, 3], np.zeros((8, K)))
+    assert np.all(np.abs(dx - ref) <= 2.0 ** -14 * mag)
+    x = rng.standard_normal((8, K))
+    f = lambda z: sum(np.sum(dyv[o:o + n] * (z[o:o + n] @ wt[e])) for e, (n, o) in enumerate(zip(sizes, [0, 3, 3])))   # noqa: E731
+    for r, c in ((0, 0), (2, 63), (4, 17), (7, 40)):
+        h = np.zeros_like(x)
+        h[r, c] = 0.5
+        # linear in x: the difference is exact but for fp64 rounding
+        assert abs((f(x + h) - f(x - h)) - dx[r, c]) <= 2.0 ** -14 * mag[r, c] + 1e-9
+
+
+# ------------------------------------------------------------------------------ the expert MLP
+
+def layer(m, T, E, k, H, F, seed, align=32, skew=None):
+    rng = np.random.default_rng(seed)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    if skew is not None:
+        l[:, skew] += 20
+    x = bf16(rng.standard_normal((T, H)))
+    wgu, wd = bf16(0.05 * rng.standard_normal((E, 2 * F, H))), bf16(0.05 * rng.standard_normal((E, H, F)))
+    idx, prob = m.moe_route_topk(torch.from_numpy(l).cuda(), k, score="sigmoid", scale=2.0)
+    rt = m.moe_route_permute(None, x, k, E=E, align=align, prec="mxfp8", topk_idx=idx, topk_prob=prob)
+    return rt, m.mxfp4_quantize(wgu), m.mxfp4_quantize(wd)
+
+
+@pytest.mark.parametrize("T,E,k,H,F,align,skew", [(1, 4, 2, 64, 96, 32, None), (5, 8, 2, 160, 32, 1, None), (40, 3, 1, 128, 288, 32, 1),
+                                                  (64, 16, 4, 256, 224, 8, None), (300, 4, 2, 384, 320, 32, None),
+                                                  (1500, 3, 2, 256, 288, 32, 0)])
+def test_mlp(m, T, E, k, H, F, align, skew):
+    from tests.gpu_helpers import say
+    say("[gpu] mlp4", T, E, k, H, F, align)
+    rt, (gc, gs, _, _), (dc, ds, _, _) = layer(m, T, E, k, H, F, T + F, align, skew)
+    f = m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds, y_dtype="f32")
+    sizes, off = npy(rt.split_sizes), npy(rt.group_offsets)
+    valid = npy(rt.perm_src) >= 0
+    X = mxfp4.decode_rows8(npy(rt.x_perm), npy(rt.x_perm_scale))
+    wgu, wd = mxfp4.decode(npy(gc), npy(gs)), mxfp4.decode(npy(dc), npy(ds))
+    gu, mag = mxfp4.grouped(X, wgu, sizes, off, np.zeros((rt.R, 2 * F)))
+    G, V = gu[:, :F], gu[:, F:]
+    p = npy(rt.prob_perm).astype(np.float64)[:, None]
+    sl = G / (1 + np.exp(-G))
+    h = p * sl * V
+    hq = mxfp4.decode_rows8(npy(f.h), npy(f.h_scale))
+    # |silu'| <= 1.1: the products' rounding through h; fp32 arithmetic and exp: 32 u
+    dh = p * (1.1 * np.abs(V) * 2.0 ** -14 * mag[:, :F] + np.abs(sl) * 2.0 ** -14 * mag[:, F:]) + 32 * U * np.abs(h)
+    blk = np.repeat(np.abs(h).reshape(rt.R, -1, 32).max(-1), 32, axis=1) * (1 + 1e-3)
+    # E4M3: half a step is 2^-4 relative, a block's largest may saturate (448 of up to 512: 2^-3), and the
+    # subnormal half step is 2^-10 of a scale of at most amax 2^-8; a scale one binade up doubles that
+    tol = np.where(np.abs(h) > 0.85 * blk, 2.0 ** -3, 2.0 ** -4) * np.abs(h) + 2.0 ** -17 * blk + 1.25 * dh
+    assert np.all(np.abs(hq - h)[valid] <= tol[valid])
+    y, ymag = mxfp4.grouped(hq, wd, sizes, off, np.zeros((rt.R, H)))
+    got = f64(f.y_perm)
+    assert np.all(np.abs(got - y)[valid] <= (2.0 ** -14 * ymag)[valid])
+    b = m.grouped_mlp_fwd_mxfp4(rt, list(gc), list(dc), list(gs), list(ds))
+    assert torch.equal(b.h[torch.from_numpy(valid).cuda()], f.h[torch.from_numpy(valid).cuda()])
+    assert np.all(np.abs(f64(b.y_perm) - got)[valid] <= (2.0 ** -8 * np.abs(got))[valid])
+
+
+def test_mlp_without_h_and_with_kept_outputs(m):
+    import dataclasses
+    rt, (gc, gs, _, _), (dc, ds, _, _) = layer(m, 20, 4, 2, 128, 160, 5)
+    f = m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds)
+    y = m.unpermute_combine(f.y_perm, rt.perm_pos)
+    g = m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds, out=dataclasses.replace(f, y_perm=torch.zeros_like(f.y_perm)))
+    assert g.workspace is f.workspace and torch.equal(m.unpermute_combine(g.y_perm, rt.perm_pos), y)
+
+
+def test_run_together_captured(m):
+    """Choice, permutation, expert MLP on MXFP4 weights, combine and the choice's backward: eager, on another stream,
+    and captured in a graph whose replays alternate with eager work, all bit for bit."""
+    from tests.gpu_helpers import say
+    say("[gpu] mxfp4 layer captured")
+    rng = np.random.default_rng(70)
+    T, E, k, H, F = 37, 8, 3, 256, 160
+    l = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).cuda()
+    bias = torch.from_numpy((0.1 * rng.standard_normal(E)).astype(np.float32)).cuda()
+    x = bf16(rng.standard_normal((T, H)))
+    d = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    wgu, wd = bf16(0.05 * rng.standard_normal((E, 2 * F, H))), bf16(0.05 * rng.standard_normal((E, H, F)))
+
+    def step():
+        gc, gs, _, _ = m.mxfp4_quantize(wgu)
+        dc, ds, _, _ = m.mxfp4_quantize(wd)
+        idx, prob = m.moe_route_topk(l, k, score="sigmoid", bias=bias, num_groups=4, topk_groups=2)
+        rt = m.moe_route_permute(None, x, k, E=E, prec="mxfp8", topk_idx=idx, topk_prob=prob)
+        f = m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds)
+        q, s, _, _ = m.mxfp4_quantize(x)
+        dense = m.mxfp4_grouped_gemm(q, s, gc[:1], gs[:1])
+        return [idx, prob, m.unpermute_combine(f.y_perm, rt.perm_pos), dense, m.mxfp4_dequantize(dc, ds),
+                m.moe_route_topk_bwd(l, idx, d, score="sigmoid")]
+
+    ref = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for rep in range(3):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, out)), rep
+        assert all(torch.equal(a, b) for a, b in zip(ref, step())), ("eager", rep)
+    del graph

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmge.so")
 SOURCES = ["api.cpp", "route.hip", "quant.hip", "gemm_host.cpp", "gemm_mx.hip", "gemm_bf16.hip", "combine.hip", "swiglu.hip",
-           "topk.hip", "quant4.hip", "gemm4.hip"]
+           "topk.hip", "quant4.hip", "gemm4.hip", "gemm_mxfp4.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "-x", "hip", "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

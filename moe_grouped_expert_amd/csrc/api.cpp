@@ -1068,9 +1068,54 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* a, void* stream) {
   return launch_dequant4(a->rows * (a->C / 32), a->codes, a->scales, a->out_dtype, a->out, static_cast<hipStream_t>(stream));
 }
 
+// Rows per expert on average from which the products take the tile kernels (256 rows of C
+// at a time, the weights shared through L2) instead of the weight-streaming ones.
+constexpr int kTile4Rows = 64;
+
+// Whether a product of `total` rows over E experts' [N][K] weights runs on the tile kernels:
+// enough rows, and every operand within their 32-bit offsets.
+static bool tile4(int E, int N, int K, int64_t rows, int64_t total) {
+  const int64_t lim = int64_t(1) << 31;
+  return total >= int64_t(kTile4Rows) * E && int64_t(E) * scale_pack_dwords(N, K / 32) * 4 < lim &&
+         scale_pack_dwords(int(rows), K / 32) * 4 < lim && int64_t(N) * 4 * 256 < lim;
+}
+static size_t tile4_ws(int E, int N, int K, int64_t rows) {
+  return packed_bytes(1, int(rows), K / 32) + packed_bytes(E, N, K / 32);
+}
+// The tile kernels' parameters of C = A W_e^T (the packed scales come from ws)
+static GemmParams tile4_params(const Gemm4Params& p, bool a4, uint32_t* as_p, uint32_t* ws_p) {
+  GemmParams g{};
+  g.mode = RAGGED_M; g.E = p.E; g.sizes = p.sizes; g.offs = p.offs; g.rows = p.rows;
+  g.A = p.A; g.lda = a4 ? p.K / 2 : p.K;
+  g.Asp = as_p; g.asp_ld = p.rows; g.asp_bytes = packed_exact(1, p.rows, p.K / 32);
+  g.Bt = p.W; g.ldb = p.K / 2;
+  g.Bsp = ws_p; g.bsp_ld = p.N; g.bsp_estride = scale_pack_dwords(p.N, p.K / 32);
+  g.bsp_bytes = packed_exact(p.E, p.N, p.K / 32);
+  g.N = p.N; g.K = p.K; g.F = p.F; g.Rp = p.rows;
+  g.prob = p.prob; g.h_codes = p.h_codes; g.h_scales = p.h_scales;
+  g.C = p.C; g.ldc = p.N;
+  return g;
+}
+static ScalePackParams pack_rows(const uint8_t* src, int rows, int kb, uint32_t* dst) {
+  ScalePackParams q{};
+  q.src = src; q.ld = kb; q.batch = 1; q.rows = rows; q.kb = kb; q.dst = dst;
+  return q;
+}
+static ScalePackParams pack_weights(const uint8_t* const* tab, int E, int rows, int kb, uint32_t* dst) {
+  ScalePackParams q{};
+  q.src_tab = tab; q.ld = kb; q.batch = E; q.rows = rows; q.kb = kb; q.dst = dst;
+  return q;
+}
+
+static int64_t gemm4_total(const mge_gemm4_args* a) {
+  return a->total_rows > 0 && a->total_rows < a->rows ? a->total_rows : a->rows;
+}
+
 size_t mge_gemm4_workspace_bytes(const mge_gemm4_args* a) {
-  if (!a || a->struct_size != sizeof(mge_gemm4_args) || a->E < 1 || a->E > 256) return 0;
-  return up256(2 * size_t(a->E) * sizeof(void*));
+  if (!a || a->struct_size != sizeof(mge_gemm4_args) || a->E < 1 || a->E > 256 || a->N < 1 || a->K < 32 || a->rows < 0)
+    return 0;
+  const bool tile = tile4(a->E, a->N, a->K, a->rows, gemm4_total(a));
+  return up256((2 * size_t(a->E) + 2) * sizeof(void*)) + (tile ? tile4_ws(a->E, a->N, a->K, a->rows) : 0);
 }
 
 mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
@@ -1102,24 +1147,50 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
   if (a->rows == 0) return MGE_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
   Carve ws(a->workspace);
-  void** tab = static_cast<void**>(ws.take(2 * size_t(a->E) * sizeof(void*)));
-  const void* const* tabs[2] = {reinterpret_cast<const void* const*>(a->w), reinterpret_cast<const void* const*>(a->w_scale)};
-  mge_status st = launch_upload_tables(tabs, 2, a->E, tab, s);
+  const int E = a->E, KB = a->K / 32;
+  void** tab = static_cast<void**>(ws.take((2 * size_t(E) + 2) * sizeof(void*)));
+  // one group of all rows: its size and offset ride along as the low words of two entries
+  const void* const one_size = reinterpret_cast<const void*>(uintptr_t(a->rows));
+  const void* const one_off = nullptr;
+  const void* const* tabs[4] = {reinterpret_cast<const void* const*>(a->w), reinterpret_cast<const void* const*>(a->w_scale),
+                                a->split_sizes ? nullptr : &one_size, a->split_sizes ? nullptr : &one_off};
+  mge_status st = launch_upload_tables(tabs, 4, E, tab, s);
   if (st != MGE_OK) return st;
   Gemm4Params p{};
-  p.E = a->E; p.N = a->N; p.K = a->K;
+  p.E = E; p.N = a->N; p.K = a->K;
   p.rows = int(a->rows);
-  p.total = int(a->total_rows > 0 && a->total_rows < a->rows ? a->total_rows : a->rows);
+  p.total = int(gemm4_total(a));
   p.sizes = a->split_sizes; p.offs = a->group_offsets;
   p.A = a->a; p.As = a->a_scale;
   p.W = reinterpret_cast<const uint8_t* const*>(tab);
   p.Ws = reinterpret_cast<const uint8_t* const*>(tab + a->E);
   p.C = a->out;
-  return launch_gemm4_store(p, a->a_format == MGE_FORMAT_MXFP4, a->out_dtype == MGE_DTYPE_F32, s);
+  const bool a4 = a->a_format == MGE_FORMAT_MXFP4;
+  if (!tile4(E, a->N, a->K, a->rows, p.total)) return launch_gemm4_store(p, a4, a->out_dtype == MGE_DTYPE_F32, s);
+  if (!p.sizes) {
+    p.sizes = reinterpret_cast<const int32_t*>(tab + 2);
+    p.offs = reinterpret_cast<const int32_t*>(tab + 3);
+  }
+  uint32_t* as_p = static_cast<uint32_t*>(ws.take(packed_bytes(1, p.rows, KB)));
+  uint32_t* ws_p = static_cast<uint32_t*>(ws.take(packed_bytes(E, a->N, KB)));
+  const ScalePackParams pk[2] = {pack_rows(p.As, p.rows, KB, as_p), pack_weights(p.Ws, E, a->N, KB, ws_p)};
+  st = launch_scale_pack_batch(pk, 2, s);
+  if (st != MGE_OK) return st;
+  GemmParams g = tile4_params(p, a4, as_p, ws_p);
+  g.out_dtype = a->out_dtype;
+  g.role = GEMM_DOWN;
+  g.tiles_upper = gemm_tiles_upper(g, p.total);
+  return launch_gemm_mxfp4(g, a4, s);
+}
+
+static bool fwd4_tile(const mge_fwd_args* a, int64_t R) {
+  const int64_t total = int64_t(a->T) * a->k;
+  return tile4(a->E, 2 * a->F, a->H, R, total) && tile4(a->E, a->H, a->F, R, total);
 }
 
 static size_t fwd4_ws(const mge_fwd_args* a, int R) {
   size_t n = up256(4 * size_t(a->E) * sizeof(void*));
+  if (fwd4_tile(a, R)) n += tile4_ws(a->E, 2 * a->F, a->H, R) + tile4_ws(a->E, a->H, a->F, R);
   if (!a->h) n += up256(size_t(R) * a->F) + up256(size_t(R) * (a->F / 32));
   return n;
 }
@@ -1184,7 +1255,26 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
   g.W = dev; g.Ws = dev + 2 * E;
   g.prob = a->prob_perm;
   g.h_codes = static_cast<uint8_t*>(h); g.h_scales = hs;
-  st = launch_gemm4_swiglu(g, s);
+  const bool tile = fwd4_tile(a, R);
+  const int H = a->H, F = a->F;
+  uint32_t *xs_p = nullptr, *wgu_p = nullptr, *hs_p = nullptr, *wd_p = nullptr;
+  if (tile) {
+    xs_p = static_cast<uint32_t*>(ws.take(packed_bytes(1, R, H / 32)));
+    wgu_p = static_cast<uint32_t*>(ws.take(packed_bytes(E, 2 * F, H / 32)));
+    hs_p = static_cast<uint32_t*>(ws.take(packed_bytes(1, R, F / 32)));
+    wd_p = static_cast<uint32_t*>(ws.take(packed_bytes(E, H, F / 32)));
+    const ScalePackParams pk[3] = {pack_rows(g.As, R, H / 32, xs_p), pack_weights(g.Ws, E, 2 * F, H / 32, wgu_p),
+                                   pack_weights(dev + 3 * E, E, H, F / 32, wd_p)};
+    st = launch_scale_pack_batch(pk, 3, s);
+    if (st != MGE_OK) return st;
+    GemmParams t = tile4_params(g, false, xs_p, wgu_p);
+    t.role = GEMM_GATEUP;
+    t.group_m = kMergeShortBand;
+    t.tiles_upper = gemm_tiles_upper(t, g.total);
+    st = launch_gemm_mxfp4(t, false, s);
+  } else {
+    st = launch_gemm4_swiglu(g, s);
+  }
   if (st != MGE_OK) return st;
   Gemm4Params d{};
   d.E = E; d.N = a->H; d.K = a->F;
@@ -1193,7 +1283,14 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
   d.A = static_cast<const uint8_t*>(h); d.As = hs;
   d.W = dev + E; d.Ws = dev + 3 * E;
   d.C = a->y_perm;
-  return launch_gemm4_store(d, false, a->y_dtype == MGE_DTYPE_F32, s);
+  if (!tile) return launch_gemm4_store(d, false, a->y_dtype == MGE_DTYPE_F32, s);
+  st = launch_scale_pack(pack_rows(hs, R, F / 32, hs_p), s);
+  if (st != MGE_OK) return st;
+  GemmParams t = tile4_params(d, false, hs_p, wd_p);
+  t.out_dtype = a->y_dtype;
+  t.role = GEMM_DOWN;
+  t.tiles_upper = gemm_tiles_upper(t, d.total);
+  return launch_gemm_mxfp4(t, false, s);
 }
 
 mge_status mge_check_device_errors(void* route_workspace, void* stream) {

@@ -18,6 +18,10 @@
 //          32h..32h+31) is scaled by the scale register of the lanes with that h, the
 //          byte chosen by op_sel.
 //   BF16:  v_mfma_f32_32x32x16_bf16
+//   MXFP4 weights (B), with MXFP8 or MXFP4 rows (A): the same instruction with 4-bit
+//          operands.  A lane's 16 bytes are the 32 elements of K block h.  MXFP4 x MXFP4
+//          runs at twice the rate, over slices of 256 elements (two scale dwords a row);
+//          beside an MXFP8 A, a slice's B rows are 64 bytes
 // Operands stream HBM -> LDS directly (buffer_load ... lds, no register staging) in
 // 128-byte K slices (128 FP8 or 64 BF16 elements) through 2 LDS stages of 64 KB; a
 // stage is refilled as soon as every wave has read its fragments, so a slice has one
@@ -57,6 +61,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+enum GemmFmt { FMT_BF16 = 0, FMT_MXFP8 = 1, FMT_MXFP8_MXFP4 = 2, FMT_MXFP4 = 3 };   // A (and B) formats
 
 constexpr int G_WAVES_M = 2;
 constexpr int G_WAVES_N = 2;
@@ -129,6 +135,10 @@ __device__ __forceinline__ const T* uniform_ptr(const T* p) {
 // banks (even rows one half, odd rows the other), so the chunk is XOR-ed with
 // (row / 2) mod 8: the 8 rows of each parity land on 8 distinct 16-byte bank groups.
 __device__ __forceinline__ int swz(int row, int chunk) { return row * G_BKB + ((chunk ^ ((row >> 1) & 7)) << 4); }
+
+// The same for 64-byte rows (a 4-bit operand beside an 8-bit one): four rows cover the banks,
+// so the chunk is XOR-ed with (row / 4) mod 4.
+__device__ __forceinline__ int swz64(int row, int chunk) { return row * 64 + ((chunk ^ ((row >> 2) & 3)) << 4); }
 
 // Raw buffer resource over `base` (gfx9 word 3, full 31-bit range) ...
 __device__ __forceinline__ i32x4 make_rsrc(const void* base) {
@@ -225,12 +235,19 @@ constexpr int G_DYN_LDS = G_SCALE_BASE + G_STAGES * G_SCALE_STAGE;
 // this launch runs each of them as four 256 x 64 work items instead (the main launch leaves
 // them out; both take the same decision from the same tile table).  Every output element is
 // still accumulated by one wave over K in the same order: the results are bit-identical.
-template <bool MX, int EPI, int MODE, int OUT, int QT = 0>
+template <int FMT, int EPI, int MODE, int OUT, int QT = 0>
 __device__ __forceinline__ void gemm_body(const GemmParams& p) {
+  constexpr bool MX = FMT != FMT_BF16;
+  constexpr bool A4 = FMT == FMT_MXFP4, B4 = FMT == FMT_MXFP8_MXFP4 || FMT == FMT_MXFP4;
+  static_assert(!B4 || MODE == RAGGED_M, "MXFP4 operands are weights: ragged M only");
+  // bytes of a B row in a slice (an 8-bit A's 128 elements are 64 bytes of a 4-bit B), B rows
+  // of one 1 KB DMA instruction
+  constexpr int BROWB = FMT == FMT_MXFP8_MXFP4 ? G_BKB / 2 : G_BKB;
+  constexpr int BROWS_DMA = 1024 / BROWB;
   static_assert(QT == 0 || (EPI == EPI_STORE && MODE == RAGGED_M), "the quarter-width tail is for plain-store ragged-M GEMMs");
   constexpr int BW = QT ? G_BN / 4 : G_BN;        // output columns (B rows) of a work item
   constexpr int WNB = BW / (32 * G_WAVES_N);       // 32-column MFMA blocks per wave
-  constexpr int NOPS = 8 + BW / 32;                // operand DMA instructions per wave and slice (A: 8)
+  constexpr int NOPS = 8 + BW / (4 * BROWS_DMA);   // operand DMA instructions per wave and slice (A: 8)
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   // LDS byte address of the dynamic shared block (the low half of its generic address)
   const uint32_t lds_base = uniform(int(uint32_t(reinterpret_cast<uintptr_t>(smem))));
@@ -342,7 +359,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     auto rows_left = [](int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); };
     const uint8_t* bmat;
     if constexpr (MODE == RAGGED_M) {
-      t.kbase = 0; t.klo = 0; t.khi = p.K * ELEM;
+      t.kbase = 0; t.klo = 0; t.khi = A4 ? p.K / 2 : p.K * ELEM;
       t.A = p.A + (int64_t(t.off) + t.m0) * p.lda;
       bmat = ld_uniform(p.Bt, t.e);
     } else {
@@ -390,12 +407,14 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   // and odd instructions; instruction i adds i*8 rows.
   const int lchunk0 = (lane & 7) ^ (lane >> 4);
   const int arow0 = wave * 64 + (lane >> 3);
-  const int brow0 = (EPI == EPI_SWIGLU ? (wave & 1) * 64 : wave * (BW / 4)) + (lane >> 3);
+  // (64-byte B rows: lane l -> row +l/4, LDS chunk l%4, global chunk (l%4) ^ (l/16) of swz64)
+  const int brow0 = (EPI == EPI_SWIGLU ? (wave & 1) * 64 : wave * (BW / 4)) + (BROWB == 64 ? lane >> 2 : lane >> 3);
+  const int bchunk64 = (lane & 3) ^ (lane >> 4);
   const uint32_t a_lane[2] = {uint32_t(arow0) * uint32_t(p.lda) + lchunk0 * 16,
                               uint32_t(arow0) * uint32_t(p.lda) + (lchunk0 ^ 4) * 16};
-  const uint32_t b_lane[2] = {uint32_t(brow0) * uint32_t(p.ldb) + lchunk0 * 16,
-                              uint32_t(brow0) * uint32_t(p.ldb) + (lchunk0 ^ 4) * 16};
-  const uint32_t lda8 = uniform(int(8 * p.lda)), ldb8 = uniform(int(8 * p.ldb));
+  const uint32_t b_lane[2] = {uint32_t(brow0) * uint32_t(p.ldb) + (BROWB == 64 ? bchunk64 : lchunk0) * 16,
+                              uint32_t(brow0) * uint32_t(p.ldb) + (BROWB == 64 ? bchunk64 : lchunk0 ^ 4) * 16};
+  const uint32_t lda8 = uniform(int(8 * p.lda)), ldb8 = uniform(int(BROWS_DMA * p.ldb));
 
   // One K slice of tile t into LDS stage `stage` (operands and, MX, its scales); past
   // the last slice every lane is out of range and loads zeros.  prep_slice computes the
@@ -405,6 +424,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   struct SliceDma {
     i32x4 rA, rB, rS;
     uint32_t kadd, out0, out1, la, lb, ls, so;
+    uint32_t outb;              // 64-byte B rows: the lane's chunk is past K
   };
   auto prep_slice = [&](const Tile& t, int kt, int stage) {
     SliceDma c;
@@ -423,17 +443,19 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     c.out0 = ((uint32_t(kb0 - t.klo) | uint32_t(t.khi - 1 - kb0)) >> 31) << 31;
     c.out1 = ((uint32_t(kb1 - t.klo) | uint32_t(t.khi - 1 - kb1)) >> 31) << 31;
     c.kadd = uint32_t(kslice);
+    if constexpr (BROWB == 64) c.outb = (uint32_t(t.khi / 2 - 1 - (kslice / 2 + bchunk64 * 16)) >> 31) << 31;
     // A: 64 rows per wave (8 instructions of 8 rows); B: BW / 4 rows per wave, stored at
     // B row wave * BW / 4 of the stage (SwiGLU: waves 0, 1 the gate rows, 2, 3 the up rows)
     c.la = lds_base + stage * G_STAGE_BYTES + wave * 8 * 1024;
-    c.lb = lds_base + stage * G_STAGE_BYTES + G_BM * G_BKB + wave * (BW / 4) * G_BKB;
+    c.lb = lds_base + stage * G_STAGE_BYTES + G_BM * G_BKB + wave * (BW / 4) * BROWB;
     if constexpr (MX) {
       // wave w brings 128 rows of scale dwords (lanes 0..31, 16 B = 4 rows each):
       // A rows (w&1)*128.. for w < 2, B rows for w >= 2; the dwords of the slice's
       // 128-element group (a slice is exactly one group)
-      const bool slice_ok = kt < t.nkt;
+      // (MXFP4 operands: the slice is two groups, lanes 32..63 bring the second one's dwords)
+      const bool slice_ok = A4 ? 2 * kt + (lane >> 5) < (p.K + 127) / 128 : kt < t.nkt;
       const int half = wave & 1;
-      const int64_t j = t.kbase / G_BKB + kt;
+      const int64_t j = A4 ? 2 * kt : t.kbase / G_BKB + kt;
       int64_t dw;             // first dword of the 128 rows
       const uint32_t* base;
       uint32_t bytes;
@@ -453,7 +475,12 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       // lanes of 4 rows each: 32 (128 rows), fewer for the B rows of a narrow work item
       constexpr int kBLanes0 = BW >= 128 ? 32 : BW / 4, kBLanes1 = BW >= 256 ? 32 : (BW > 128 ? (BW - 128) / 4 : 0);
       const int nlanes = wave < 2 ? 32 : (half == 0 ? kBLanes0 : kBLanes1);
-      c.so = (slice_ok && lane < nlanes) ? uint32_t(dw * 4) + lane * 16 : kInvalid;
+      if constexpr (A4) {
+        const uint32_t ld4 = uint32_t(wave < 2 ? p.asp_ld : p.bsp_ld) * 4;
+        c.so = (slice_ok && (lane & 31) < nlanes) ? uint32_t(dw * 4) + (lane >> 5) * ld4 + (lane & 31) * 16 : kInvalid;
+      } else {
+        c.so = (slice_ok && lane < nlanes) ? uint32_t(dw * 4) + lane * 16 : kInvalid;
+      }
       c.ls = lds_base + G_SCALE_BASE + stage * G_SCALE_STAGE + wave * 1024;
     }
     return c;
@@ -461,6 +488,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   auto dma_operand = [&](const SliceDma& c, int i) {
     const uint32_t out = (i & 1) ? c.out1 : c.out0;
     if (i < 8) dma16(c.rA, c.la + i * 1024, (a_lane[i & 1] + i * lda8 + c.kadd) | out);
+    else if constexpr (BROWB == 64) dma16(c.rB, c.lb + (i - 8) * 1024, (b_lane[0] + (i - 8) * ldb8 + c.kadd / 2) | c.outb);
     else dma16(c.rB, c.lb + (i - 8) * 1024, (b_lane[i & 1] + (i - 8) * ldb8 + c.kadd) | out);
   };
   auto dma_scale = [&](const SliceDma& c) {
@@ -488,13 +516,17 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   //   MX  : 64-element step s (of 2); lane (hi, l32) takes 16-byte chunks 4s + hi and
   //         4s + hi + 2 of its row
   //   BF16: 16-element step s (of 4); lane takes chunk 2s + hi
-  typedef typename std::conditional<MX, i32x8, bf16x8>::type frag_t;
-  constexpr int NSTEP = MX ? 2 : 4;
-  auto read_frags = [&](const uint8_t* sA, const uint8_t* sB, int s, frag_t* af, frag_t* bfr) {
+  //   a 4-bit operand: 64-element step s; lane takes chunk 2s + hi (its K block 2s + hi)
+  typedef typename std::conditional<A4, i32x4, typename std::conditional<MX, i32x8, bf16x8>::type>::type frag_t;
+  typedef typename std::conditional<B4, i32x4, frag_t>::type bfrag_t;
+  constexpr int NSTEP = MX && !A4 ? 2 : 4;
+  auto read_frags = [&](const uint8_t* sA, const uint8_t* sB, int s, frag_t* af, bfrag_t* bfr) {
 #pragma unroll
     for (int mi = 0; mi < G_WMB; ++mi) {
       const int row = (wm * G_WMB + mi) * 32 + l32;
-      if constexpr (MX) {
+      if constexpr (A4) {
+        af[mi] = *reinterpret_cast<const i32x4*>(sA + swz(row, s * 2 + hi));
+      } else if constexpr (MX) {
         const int c = 4 * s + hi;
         const uint4 x0 = *reinterpret_cast<const uint4*>(sA + swz(row, c));
         const uint4 x1 = *reinterpret_cast<const uint4*>(sA + swz(row, c + 2));
@@ -506,7 +538,9 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
 #pragma unroll
     for (int ni = 0; ni < WNB; ++ni) {
       const int row = brow_tile[ni] + l32;
-      if constexpr (MX) {
+      if constexpr (B4) {
+        bfr[ni] = *reinterpret_cast<const i32x4*>(sB + (BROWB == 64 ? swz64(row, s * 2 + hi) : swz(row, s * 2 + hi)));
+      } else if constexpr (MX) {
         const int c = 4 * s + hi;
         const uint4 x0 = *reinterpret_cast<const uint4*>(sB + swz(row, c));
         const uint4 x1 = *reinterpret_cast<const uint4*>(sB + swz(row, c + 2));
@@ -550,7 +584,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     // stall the issuing wave (measured on MI355X).
     constexpr int NMFMA = NSTEP * G_WMB * WNB;
     constexpr int BAR_AT = NMFMA * G_BAR_AT32 / 32;
-    auto mfma_slice = [&](frag_t (*af)[G_WMB], frag_t (*bfr)[WNB], const uint32_t* sa, const uint32_t* sb,
+    auto mfma_slice = [&](frag_t (*af)[G_WMB], bfrag_t (*bfr)[WNB], const uint32_t* sa, const uint32_t* sb,
                           const SliceDma& nx) {
       static_for<0, NMFMA>([&](auto ic) {
         constexpr int i = decltype(ic)::value;
@@ -563,7 +597,18 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
           dma_scale(nx);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (MX) {
+        if constexpr (B4) {
+          // MXFP4 A: group s / 2 of the slice, K block 2 (s % 2) + hi of it
+          constexpr int g = A4 ? s / 2 : 0;
+          const int sh = 8 * (2 * (A4 ? s % 2 : s) + hi);
+          const int xa = int(sa[g * G_WMB + mi] >> sh);
+          const int xb = int(sb[g * WNB + ni] >> sh);
+          i32x8 fa;
+          if constexpr (A4) fa = __builtin_shufflevector(af[s][mi], af[s][mi], 0, 1, 2, 3, -1, -1, -1, -1);
+          else fa = af[s][mi];
+          const i32x8 fb = __builtin_shufflevector(bfr[s][ni], bfr[s][ni], 0, 1, 2, 3, -1, -1, -1, -1);
+          acc[mi][ni] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa, fb, acc[mi][ni], A4 ? 4 : 0, 4, 0, xa, 0, xb);
+        } else if constexpr (MX) {
           const int sh = 8 * (2 * s + hi);
           const int xa = int(sa[mi] >> sh);
           const int xb = int(sb[ni] >> sh);
@@ -606,8 +651,24 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       const int stage = kt & (G_STAGES - 1);
       const uint8_t* sA = smem + stage * G_STAGE_BYTES;
       const uint8_t* sB = sA + G_BM * G_BKB;
-      uint32_t sa[G_WMB], sb[WNB];
-      if constexpr (MX) {
+      constexpr int NG = A4 ? 2 : 1;   // scale groups (128 elements) per slice
+      uint32_t sa[NG * G_WMB], sb[NG * WNB];
+      if constexpr (A4) {
+        const uint8_t* sS = smem + G_SCALE_BASE + stage * G_SCALE_STAGE;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+          for (int mi = 0; mi < G_WMB; ++mi) {
+            const int r = (wm * G_WMB + mi) * 32 + l32;
+            sa[g * G_WMB + mi] = *reinterpret_cast<const uint32_t*>(sS + (r >> 7) * 1024 + g * 512 + (r & 127) * 4);
+          }
+#pragma unroll
+          for (int ni = 0; ni < WNB; ++ni) {
+            const int r = brow_tile[ni] + l32;
+            sb[g * WNB + ni] = *reinterpret_cast<const uint32_t*>(sS + 2048 + (r >> 7) * 1024 + g * 512 + (r & 127) * 4);
+          }
+        }
+      } else if constexpr (MX) {
         const uint8_t* sS = smem + G_SCALE_BASE + stage * G_SCALE_STAGE;
 #pragma unroll
         for (int mi = 0; mi < G_WMB; ++mi) {
@@ -620,7 +681,8 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
           sb[ni] = *reinterpret_cast<const uint32_t*>(sS + 2048 + (r >> 7) * 1024 + (r & 127) * 4);
         }
       }
-      frag_t af[NSTEP][G_WMB], bfr[NSTEP][WNB];
+      frag_t af[NSTEP][G_WMB];
+      bfrag_t bfr[NSTEP][WNB];
 #pragma unroll
       for (int s = 0; s < NSTEP; ++s) read_frags(sA, sB, s, af[s], bfr[s]);
       const SliceDma nx = prep_slice(cur, kt + G_STAGES, stage);

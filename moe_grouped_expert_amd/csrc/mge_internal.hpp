@@ -233,5 +233,8 @@ struct GemmParams {
 // Upper bound of tiles for a RAGGED_M GEMM (host-side, from T*k and E).
 int gemm_tiles_upper(const GemmParams& p, int64_t total_rows_bound);
 mge_status launch_gemm(const GemmParams& p, int prec, hipStream_t s);
+// The same tiles with MXFP4 weights (RAGGED_M; roles GATEUP with MXFP8 rows, or DOWN for a
+// plain store); a4: the rows are MXFP4 too
+mge_status launch_gemm_mxfp4(const GemmParams& p, bool a4, hipStream_t s);
 
 }  // namespace mge

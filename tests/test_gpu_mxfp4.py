@@ -198,10 +198,28 @@ def test_gemm_many_rows(m, fmt):
     run_gemm(m, [700, 0, 1025, 3, 511], 544, 800, fmt, "bf16")
 
 
+@pytest.mark.parametrize("sizes,N,K", [([200], 32, 32), ([129, 64], 96, 96), ([64, 64, 64], 288, 128), ([255, 0, 257], 256, 160),
+                                       ([1, 500], 320, 288), ([256], 512, 256), ([70, 600, 2], 64, 416), ([130], 2080, 1184)])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_gemm_tiles(m, sizes, N, K, fmt):
+    """Enough rows for the tile kernels, with K that ends inside a slice and N inside a tile."""
+    run_gemm(m, sizes, N, K, fmt, "f32", ints=True)
+    run_gemm(m, sizes, N, K, fmt, "bf16", align=32, extra=40, seed=2, split=False)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_gemm_tail_items(m, fmt):
+    """More than a whole round of tiles: the rest runs as quarter-width items, bit for bit as whole tiles would."""
+    run_gemm(m, [2100, 130], 8192, 256, fmt, "bf16", ints=True)
+
+
 def test_gemm_dense_and_empty(m):
     rng = np.random.default_rng(9)
     a, s, av = operand(rng, 9, 256, "mxfp8", True)
     w, ws, wv = operand(rng, 64, 256, "mxfp4", True)
+    got = m.mxfp4_grouped_gemm(a, s, w[None], ws[None], out_dtype="f32")
+    np.testing.assert_array_equal(f64(got), av @ wv.T)
+    a, s, av = operand(rng, 700, 256, "mxfp4", True)
     got = m.mxfp4_grouped_gemm(a, s, w[None], ws[None], out_dtype="f32")
     np.testing.assert_array_equal(f64(got), av @ wv.T)
     z = m.mxfp4_grouped_gemm(a[:0], s[:0], w[None], ws[None])

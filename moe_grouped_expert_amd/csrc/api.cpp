@@ -1008,6 +1008,7 @@ mge_status moe_route_topk(const mge_route_topk_args* a, void* stream) {
   p.score = a->score; p.renorm = a->renormalize != 0; p.scale = a->scale;
   p.logits = a->logits; p.bias = a->bias; p.topk_idx = a->topk_idx; p.topk_prob = a->topk_prob;
   p.vec = topk_vec(a->logits, a->logits_dtype, a->logits_row_stride);
+  p.bvec = aligned16(a->bias);
   return launch_topk(p, a->logits_dtype, static_cast<hipStream_t>(stream));
 }
 

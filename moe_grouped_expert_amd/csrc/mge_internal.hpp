@@ -101,6 +101,8 @@ struct TopkParams {
   int32_t* topk_idx;
   float* topk_prob;
   bool vec;                 // rows of logits may be read 16 bytes at a time
+  bool bvec;                // and bias
+  int lanes;                // lanes of a group (set by the launcher)
 };
 mge_status launch_topk(const TopkParams& p, int dtype, hipStream_t s);
 struct TopkBwdParams {

@@ -144,6 +144,20 @@ def test_near_ties_rank_as_the_formula(m):
     check(m, torch.from_numpy(l).cuda(), 8, "sigmoid", torch.from_numpy(bias).cuda(), 4, 2, 2, bwd=False)
 
 
+@pytest.mark.parametrize("T,E,G,tg", [(300, 16, 4, 2), (300, 15, 3, 2), (3000, 64, 8, 3), (100, 64, 8, 3), (2500, 256, 8, 4), (100, 60, 4, 2)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_close_keys_everywhere(m, T, E, G, tg, score):
+    """Rows of copies of few logits with biases a few fp32 steps apart: pairs, runs and whole groups of keys too close
+    for fp32, in every token, at every width of the kernel."""
+    rng = np.random.default_rng(T + E)
+    l = rng.choice(rng.standard_normal(5).astype(np.float32), (T, E))
+    l[: T // 3] = np.round(l[: T // 3])
+    b = (0.25 + rng.integers(-3, 4, E) * 2.0 ** -24).astype(np.float32)
+    for groups in ((1, 1), (G, tg)):
+        check(m, torch.from_numpy(l).cuda(), 4, score, torch.from_numpy(b).cuda(), *groups, bwd=False)
+        check(m, torch.from_numpy(l).cuda(), 4, score, None, *groups, bwd=False)
+
+
 def test_bias_that_takes_experts_out(m):
     l = logits(50, 16, F32, 20)
     b = bias_of(16, 3)

@@ -685,28 +685,35 @@ def _need(ok: bool, what: str):
 
 def _call(fn: str, a, dev) -> None:
     """One library call on the current stream of `dev`, with `dev` current while it launches."""
-    f = getattr(lib(), fn)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(f(C.byref(a), _stream(dev)), fn)
+    f = getattr(_LIB or lib(), fn)
+    if dev.index == torch._C._cuda_getDevice():
+        code = f(C.byref(a), torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            _check(f(C.byref(a), _stream(dev)), fn)
+            code = f(C.byref(a), _stream(dev))
+    if code:
+        raise MgeError(code, fn)
 
 
 def _on(dev, *ts) -> None:
-    _need(dev.type == "cuda", f"tensors must be on a GPU (got {dev})")
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU (got {dev})")
     for t in ts:
-        _need(t is None or t.device == dev, "tensors on different devices")
+        if t is not None and t.device != dev:
+            raise ValueError("tensors on different devices")
 
 
-def _check_logits(logits, score: str):
-    _need(score in SCORE, f"score must be 'softmax' or 'sigmoid', not {score!r}")
-    _need(logits.dim() == 2 and logits.dtype in _TORCH_DTYPE, "logits must be [T, E], float32 or bfloat16")
-    _need(logits.shape[1] <= 1 or logits.stride(1) == 1, "the experts of a row of logits must be contiguous")
-
-
-def _row_stride(t) -> int:
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+def _check_logits(logits, score: str) -> int:
+    """Checks the router's logits; returns their row stride."""
+    if score not in SCORE:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', not {score!r}")
+    if logits.dim() != 2 or logits.dtype not in _TORCH_DTYPE:
+        raise ValueError("logits must be [T, E], float32 or bfloat16")
+    T, E = logits.shape
+    ld, one = logits.stride()
+    if one != 1 and E > 1:
+        raise ValueError("the experts of a row of logits must be contiguous")
+    return ld if T > 1 else E
 
 
 def moe_route_topk(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
@@ -717,19 +724,23 @@ def moe_route_topk(logits: torch.Tensor, k: int, score: str = "softmax", bias: O
     score "softmax" or "sigmoid"; bias: fp32 [E], added to the scores for the choice only; num_groups / topk_groups:
     choose among the topk_groups best of num_groups equal groups, ranked by the sum of their group_topn (1 or 2)
     best; renormalize: weights divided by their sum; all weights times scale.  out: the pair to write into."""
-    _check_logits(logits, score)
+    ld = _check_logits(logits, score)
     T, E = logits.shape
     dev = logits.device
-    idx, prob = out if out is not None else (torch.empty((T, k), device=dev, dtype=torch.int32),
-                                             torch.empty((T, k), device=dev, dtype=torch.float32))
-    _on(dev, bias, idx, prob)
-    _need(bias is None or (bias.dtype == torch.float32 and bias.is_contiguous() and bias.numel() == E),
-          "bias must be contiguous float32 [E]")
-    _need(idx.dtype == torch.int32 and prob.dtype == torch.float32 and idx.shape == (T, k) and prob.shape == (T, k)
-          and idx.is_contiguous() and prob.is_contiguous(), "out must be contiguous (int32 [T, k], float32 [T, k])")
+    _on(dev, bias)
+    if bias is not None and (bias.dtype != torch.float32 or not bias.is_contiguous() or bias.numel() != E):
+        raise ValueError("bias must be contiguous float32 [E]")
+    if out is None:
+        _need(k >= 1, "k must be >= 1")
+        idx, prob = logits.new_empty((T, k), dtype=torch.int32), logits.new_empty((T, k), dtype=torch.float32)
+    else:
+        idx, prob = out
+        _on(dev, idx, prob)
+        _need(idx.dtype == torch.int32 and prob.dtype == torch.float32 and idx.shape == (T, k) and prob.shape == (T, k)
+              and idx.is_contiguous() and prob.is_contiguous(), "out must be contiguous (int32 [T, k], float32 [T, k])")
     a = RouteTopkArgs(C.sizeof(RouteTopkArgs), T, E, k, SCORE[score], num_groups, topk_groups, group_topn,
-                      1 if renormalize else 0, scale, _TORCH_DTYPE[logits.dtype], _row_stride(logits), _ptr(logits),
-                      _ptr(bias), _ptr(idx), _ptr(prob))
+                      1 if renormalize else 0, scale, _TORCH_DTYPE[logits.dtype], ld, logits.data_ptr(),
+                      None if bias is None else bias.data_ptr(), idx.data_ptr(), prob.data_ptr())
     _call("moe_route_topk", a, dev)
     return idx, prob
 
@@ -738,12 +749,12 @@ def moe_route_topk_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, d_prob: tor
                        renormalize: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """d_logits [T, E] (the logits' dtype, contiguous) from the forward's logits and choice and d_prob fp32 [T, k];
     score, renormalize and scale as the forward had them (the choice and its bias have no gradient)."""
-    _check_logits(logits, score)
+    ld = _check_logits(logits, score)
     T, E = logits.shape
     dev = logits.device
-    if out is None:
-        out = torch.empty((T, E), device=dev, dtype=logits.dtype)
     _on(dev, topk_idx, d_prob, out)
+    if out is None:
+        out = logits.new_empty((T, E))
     _need(topk_idx.dim() == 2 and topk_idx.shape[0] == T and topk_idx.dtype == torch.int32 and topk_idx.is_contiguous(),
           "topk_idx must be contiguous int32 [T, k]")
     _need(d_prob.shape == topk_idx.shape and d_prob.dtype == torch.float32 and d_prob.is_contiguous(),
@@ -751,8 +762,8 @@ def moe_route_topk_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, d_prob: tor
     _need(out.shape == (T, E) and out.dtype == logits.dtype and out.is_contiguous(),
           "out must be contiguous [T, E] of the logits' dtype")
     a = RouteTopkBwdArgs(C.sizeof(RouteTopkBwdArgs), T, E, topk_idx.shape[1], SCORE[score], 1 if renormalize else 0,
-                         scale, _TORCH_DTYPE[logits.dtype], _row_stride(logits), _ptr(logits), _ptr(topk_idx),
-                         _ptr(d_prob), _ptr(out))
+                         scale, _TORCH_DTYPE[logits.dtype], ld, logits.data_ptr(), topk_idx.data_ptr(),
+                         d_prob.data_ptr(), out.data_ptr())
     _call("moe_route_topk_bwd", a, dev)
     return out
 
@@ -780,19 +791,20 @@ def mxfp4_quantize(w: torch.Tensor, orient: str = "row", out=None):
     Rp = (R + 31) // 32 * 32
     want_row, want_col = orient != "col", orient != "row"
     dev = w.device
+    _on(dev)
     if out is None:
-        u8 = dict(device=dev, dtype=torch.uint8)
-        rc = torch.empty(lead + (R, Cc // 2), **u8) if want_row else None
-        rs = torch.empty(lead + (R, Cc // 32), **u8) if want_row else None
-        cc = torch.empty(lead + (Cc, Rp // 2), **u8) if want_col else None
-        cs = torch.empty(lead + (Cc, Rp // 32), **u8) if want_col else None
+        u8 = torch.uint8
+        rc = w.new_empty(lead + (R, Cc // 2), dtype=u8) if want_row else None
+        rs = w.new_empty(lead + (R, Cc // 32), dtype=u8) if want_row else None
+        cc = w.new_empty(lead + (Cc, Rp // 2), dtype=u8) if want_col else None
+        cs = w.new_empty(lead + (Cc, Rp // 32), dtype=u8) if want_col else None
     else:
         rc, rs, cc, cs = out
+        _on(dev, rc, rs, cc, cs)
         for t, n, used in ((rc, R * Cc // 2, want_row), (rs, R * (Cc // 32), want_row), (cc, Cc * Rp // 2, want_col),
                            (cs, Cc * (Rp // 32), want_col)):
             _need(not used or (t is not None and _is_u8(t) and t.numel() == batch * n),
                   "out must be contiguous uint8 tensors of the outputs' sizes")
-    _on(dev, rc, rs, cc, cs)
     row_stride = Cc if w.is_contiguous() else w.stride(0)
     a = Quant4Args(C.sizeof(Quant4Args), batch, R, Cc, R * row_stride, row_stride, _ptr(w),
                    (ORIENT_ROW if want_row else 0) | (ORIENT_COL if want_col else 0), _ptr(rc) if want_row else None,
@@ -812,10 +824,11 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype: str =
     dev = codes.device
     dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
     shape = tuple(codes.shape[:-1]) + (Cc,)
-    if out is None:
-        out = torch.empty(shape, device=dev, dtype=dt)
     _on(dev, scales, out)
-    _need(tuple(out.shape) == shape and out.dtype == dt and out.is_contiguous(), "out has another shape or dtype")
+    if out is None:
+        out = codes.new_empty(shape, dtype=dt)
+    else:
+        _need(tuple(out.shape) == shape and out.dtype == dt and out.is_contiguous(), "out has another shape or dtype")
     rows = codes.numel() // max(Cc // 2, 1)
     a = Dequant4Args(C.sizeof(Dequant4Args), rows, Cc, DTYPE[out_dtype], _ptr(codes), _ptr(scales), _ptr(out))
     _call("mxfp4_dequantize", a, dev)
@@ -853,23 +866,26 @@ def mxfp4_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, w, w_scale, split
     _need(K > 0 and a.shape[1] in (K, K // 2), "a must be [rows, K] (MXFP8) or [rows, K/2] (MXFP4) with a_scale [rows, K/32]")
     fmt = FORMAT["mxfp8" if a.shape[1] == K else "mxfp4"]
     E = len(w)
-    _need(E >= 1 and len(w_scale) == E and w[0].dim() == 2, "w must be [E, N, K/2] with w_scale [E, N, K/32]")
-    N = w[0].shape[0] if not isinstance(w, torch.Tensor) else w.shape[1]
+    stacked = isinstance(w, torch.Tensor)
+    _need(E >= 1 and len(w_scale) == E and (w.dim() == 3 if stacked else w[0].dim() == 2),
+          "w must be [E, N, K/2] with w_scale [E, N, K/32]")
+    N = w.shape[1] if stacked else w[0].shape[0]
     dev = a.device
     dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
-    if out is None:
-        out = torch.empty((rows, N), device=dev, dtype=dt)
-    _need(tuple(out.shape) == (rows, N) and out.dtype == dt and out.is_contiguous(), "out has another shape or dtype")
-    for t, lo in ((split_sizes, E), (group_offsets, E)):
-        _need(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= lo),
-              "split_sizes and group_offsets must be contiguous int32 with an entry for each expert")
     _on(dev, a_scale, out, split_sizes, group_offsets, workspace)
+    if out is None:
+        out = a.new_empty((rows, N), dtype=dt)
+    else:
+        _need(tuple(out.shape) == (rows, N) and out.dtype == dt and out.is_contiguous(), "out has another shape or dtype")
+    for t in (split_sizes, group_offsets):
+        _need(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= E),
+              "split_sizes and group_offsets must be contiguous int32 with an entry for each expert")
     wp = _expert_ptrs(w, E, N, K // 2, dev, "w")
     wsp = _expert_ptrs(w_scale, E, N, K // 32, dev, "w_scale")
     g = Gemm4Args(C.sizeof(Gemm4Args), fmt, E, N, K, rows, total_rows or 0, _ptr(split_sizes), _ptr(group_offsets),
-                  _ptr(a), _ptr(a_scale), C.cast(wp, vp), C.cast(wsp, vp), DTYPE[out_dtype], _ptr(out))
+                  _ptr(a), _ptr(a_scale), C.addressof(wp), C.addressof(wsp), DTYPE[out_dtype], _ptr(out))
     if workspace is None:
-        workspace = torch.empty(int(lib().mge_gemm4_workspace_bytes(C.byref(g))), device=dev, dtype=torch.uint8)
+        workspace = a.new_empty(lib().mge_gemm4_workspace_bytes(C.byref(g)))
     g.workspace, g.workspace_bytes = _ptr(workspace), workspace.numel()
     _call("mxfp4_grouped_gemm", g, dev)
     return out
@@ -883,23 +899,29 @@ def grouped_mlp_fwd_mxfp4(rt: RouteOut, w_gate_up, w_down, w_gate_up_scale, w_do
     _need(y_dtype in DTYPE, f"y_dtype must be 'bf16' or 'f32', not {y_dtype!r}")
     E, H, R = rt.E, rt.H, rt.R
     F = (w_gate_up.shape[1] if isinstance(w_gate_up, torch.Tensor) else w_gate_up[0].shape[0]) // 2
-    dev = rt.x_perm.device
+    x = rt.x_perm
+    dev = x.device
+    dt = torch.bfloat16 if y_dtype == "bf16" else torch.float32
+    _on(dev, rt.x_perm_scale, rt.split_sizes, rt.group_offsets, rt.prob_perm)
     if out is None:
-        out = FwdOut(y_perm=torch.empty((R, H), device=dev, dtype=torch.bfloat16 if y_dtype == "bf16" else torch.float32),
-                     h=torch.empty((R, F), device=dev, dtype=torch.uint8),
-                     h_scale=torch.empty((R, F // 32), device=dev, dtype=torch.uint8))
+        out = FwdOut(y_perm=x.new_empty((R, H), dtype=dt), h=x.new_empty((R, F)), h_scale=x.new_empty((R, F // 32)))
+    else:
+        _on(dev, out.y_perm, out.h, out.h_scale, out.workspace)
+        _need(tuple(out.y_perm.shape) == (R, H) and out.y_perm.dtype == dt and out.y_perm.is_contiguous(),
+              "out.y_perm has another shape or dtype")
+        _need(out.h is None or (tuple(out.h.shape) == (R, F) and _is_u8(out.h) and out.h_scale is not None
+                                and tuple(out.h_scale.shape) == (R, F // 32) and _is_u8(out.h_scale)),
+              "out.h / out.h_scale have another shape or dtype")
     keep = [_expert_ptrs(w_gate_up, E, 2 * F, H // 2, dev, "w_gate_up"),
             _expert_ptrs(w_down, E, H, F // 2, dev, "w_down"),
             _expert_ptrs(w_gate_up_scale, E, 2 * F, H // 32, dev, "w_gate_up_scale"),
             _expert_ptrs(w_down_scale, E, H, F // 32, dev, "w_down_scale")]
-    _on(dev, out.y_perm, out.h, out.h_scale, rt.split_sizes, rt.group_offsets, rt.prob_perm)
     a = FwdArgs(C.sizeof(FwdArgs), PREC["mxfp8"], E, H, F, rt.T, rt.k, rt.align, _ptr(rt.split_sizes),
-                _ptr(rt.group_offsets), _ptr(rt.prob_perm), _ptr(rt.x_perm), _ptr(rt.x_perm_scale), C.cast(keep[0], vp),
-                C.cast(keep[2], vp), C.cast(keep[1], vp), C.cast(keep[3], vp), DTYPE[y_dtype], _ptr(out.y_perm),
+                _ptr(rt.group_offsets), _ptr(rt.prob_perm), _ptr(x), _ptr(rt.x_perm_scale), C.addressof(keep[0]),
+                C.addressof(keep[2]), C.addressof(keep[1]), C.addressof(keep[3]), DTYPE[y_dtype], _ptr(out.y_perm),
                 _ptr(out.h), _ptr(out.h_scale))
     if out.workspace is None:
-        out.workspace = torch.empty(max(int(lib().mge_fwd_mxfp4_workspace_bytes(C.byref(a))), 256), device=dev,
-                                    dtype=torch.uint8)
+        out.workspace = x.new_empty(max(lib().mge_fwd_mxfp4_workspace_bytes(C.byref(a)), 256))
     a.workspace, a.workspace_bytes = _ptr(out.workspace), out.workspace.numel()
     _call("grouped_mlp_fwd_mxfp4", a, dev)
     return out

@@ -1069,15 +1069,28 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* a, void* stream) {
   return launch_dequant4(a->rows * (a->C / 32), a->codes, a->scales, a->out_dtype, a->out, static_cast<hipStream_t>(stream));
 }
 
-// Rows per expert on average from which the products take the tile kernels (256 rows of C
-// at a time, the weights shared through L2) instead of the weight-streaming ones.
-constexpr int kTile4Rows = 64;
+// Rows per expert on average past which the products take the tile kernels instead of the
+// weight-streaming ones (which read the weights again for every 16 or 32 rows).  Down product,
+// 8 experts of [4096][14336]: 8 rows each 57 us streamed, 68 tiled; 64 rows each 174, 76.  One
+// [8192][8192]: 16 rows 20 us streamed, 26 tiled; 32 rows 33, 26.
+constexpr int kTile4Rows = 18;
+// Tiles of 64 rows or of 256: a 256 x 256 tile takes its CU as long as one and a half rounds of
+// 64 x 128 tiles take the chip, whatever part of it is padding.  Measured (64-row, 256-row):
+// [8192][8192], 512 rows 55, 86 us; 1024 rows 113, 91; 8 x [4096][14336] in 4 bits, 1024 rows
+// 76, 98 us, 2048 rows 123, 117; gate-up of 512 tokens 199, 206 us, of 256 tokens 149, 196.
+constexpr int64_t kSmallTiles = 640;   // 64 x 128 tiles worth a round of 256 x 256 ones on 256 CUs
+static bool small_tiles4(int E, int N, int64_t total) {
+  // (group sizes are on the device: half a tile of padding a group, and a tile at least)
+  const int64_t ms = (total + 63) / 64 + E / 2;
+  const int64_t ml = std::max(int64_t(E), (total + 255) / 256 + E / 2);
+  return ms * ((N + 127) / 128) <= kSmallTiles * ((ml * ((N + 255) / 256) + 255) / 256);
+}
 
 // Whether a product of `total` rows over E experts' [N][K] weights runs on the tile kernels:
 // enough rows, and every operand within their 32-bit offsets.
 static bool tile4(int E, int N, int K, int64_t rows, int64_t total) {
   const int64_t lim = int64_t(1) << 31;
-  return total >= int64_t(kTile4Rows) * E && int64_t(E) * scale_pack_dwords(N, K / 32) * 4 < lim &&
+  return total > int64_t(kTile4Rows) * E && int64_t(E) * scale_pack_dwords(N, K / 32) * 4 < lim &&
          scale_pack_dwords(int(rows), K / 32) * 4 < lim && int64_t(N) * 4 * 256 < lim;
 }
 static size_t tile4_ws(int E, int N, int K, int64_t rows) {
@@ -1097,6 +1110,21 @@ static GemmParams tile4_params(const Gemm4Params& p, bool a4, uint32_t* as_p, ui
   g.C = p.C; g.ldc = p.N;
   return g;
 }
+// Whether the rows of a product's scale matrices may be read 16 bytes at a time
+static bool scales_vec(const uint8_t* as, const uint8_t* const* ws, int E, int K) {
+  bool v = (K / 32) % 16 == 0 && aligned16(as);
+  for (int e = 0; e < E && v; ++e) v = aligned16(ws[e]);
+  return v;
+}
+// Few experts' pointers travel in the streaming kernels' arguments (no table to upload first)
+static void inline_weights(Gemm4Params& p, const uint8_t* const* w, const uint8_t* const* ws) {
+  if (p.E > kGemm4Inline) return;
+  p.W = nullptr;
+  for (int e = 0; e < p.E; ++e) {
+    p.Wv[e] = w[e];
+    p.Wsv[e] = ws[e];
+  }
+}
 static ScalePackParams pack_rows(const uint8_t* src, int rows, int kb, uint32_t* dst) {
   ScalePackParams q{};
   q.src = src; q.ld = kb; q.batch = 1; q.rows = rows; q.kb = kb; q.dst = dst;
@@ -1106,6 +1134,12 @@ static ScalePackParams pack_weights(const uint8_t* const* tab, int E, int rows, 
   ScalePackParams q{};
   q.src_tab = tab; q.ld = kb; q.batch = E; q.rows = rows; q.kb = kb; q.dst = dst;
   return q;
+}
+
+static mge_status launch_tile4(GemmParams& g, bool a4, int64_t total, hipStream_t s) {
+  if (small_tiles4(g.E, g.N, total)) return launch_gemm_mxfp4_small(g, a4, total, s);
+  g.tiles_upper = gemm_tiles_upper(g, total);
+  return launch_gemm_mxfp4(g, a4, s);
 }
 
 static int64_t gemm4_total(const mge_gemm4_args* a) {
@@ -1155,7 +1189,9 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
   const void* const one_off = nullptr;
   const void* const* tabs[4] = {reinterpret_cast<const void* const*>(a->w), reinterpret_cast<const void* const*>(a->w_scale),
                                 a->split_sizes ? nullptr : &one_size, a->split_sizes ? nullptr : &one_off};
-  mge_status st = launch_upload_tables(tabs, 4, E, tab, s);
+  const bool tile = tile4(E, a->N, a->K, a->rows, gemm4_total(a));
+  mge_status st = MGE_OK;
+  if (tile || E > kGemm4Inline) st = launch_upload_tables(tabs, 4, E, tab, s);
   if (st != MGE_OK) return st;
   Gemm4Params p{};
   p.E = E; p.N = a->N; p.K = a->K;
@@ -1166,8 +1202,12 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
   p.W = reinterpret_cast<const uint8_t* const*>(tab);
   p.Ws = reinterpret_cast<const uint8_t* const*>(tab + a->E);
   p.C = a->out;
+  p.vec = scales_vec(p.As, a->w_scale, E, p.K);
   const bool a4 = a->a_format == MGE_FORMAT_MXFP4;
-  if (!tile4(E, a->N, a->K, a->rows, p.total)) return launch_gemm4_store(p, a4, a->out_dtype == MGE_DTYPE_F32, s);
+  if (!tile) {
+    inline_weights(p, a->w, a->w_scale);
+    return launch_gemm4_store(p, a4, a->out_dtype == MGE_DTYPE_F32, s);
+  }
   if (!p.sizes) {
     p.sizes = reinterpret_cast<const int32_t*>(tab + 2);
     p.offs = reinterpret_cast<const int32_t*>(tab + 3);
@@ -1180,8 +1220,7 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
   GemmParams g = tile4_params(p, a4, as_p, ws_p);
   g.out_dtype = a->out_dtype;
   g.role = GEMM_DOWN;
-  g.tiles_upper = gemm_tiles_upper(g, p.total);
-  return launch_gemm_mxfp4(g, a4, s);
+  return launch_tile4(g, a4, p.total, s);
 }
 
 static bool fwd4_tile(const mge_fwd_args* a, int64_t R) {
@@ -1245,7 +1284,8 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
                                 reinterpret_cast<const void* const*>(a->w_down),
                                 reinterpret_cast<const void* const*>(a->w_gate_up_scale),
                                 reinterpret_cast<const void* const*>(a->w_down_scale)};
-  st = launch_upload_tables(tabs, 4, E, tab, s);
+  const bool tile = fwd4_tile(a, R);
+  if (tile || E > kGemm4Inline) st = launch_upload_tables(tabs, 4, E, tab, s);
   if (st != MGE_OK) return st;
   const uint8_t* const* dev = reinterpret_cast<const uint8_t* const*>(tab);
   Gemm4Params g{};
@@ -1256,7 +1296,7 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
   g.W = dev; g.Ws = dev + 2 * E;
   g.prob = a->prob_perm;
   g.h_codes = static_cast<uint8_t*>(h); g.h_scales = hs;
-  const bool tile = fwd4_tile(a, R);
+  g.vec = scales_vec(g.As, a->w_gate_up_scale, E, g.K);
   const int H = a->H, F = a->F;
   uint32_t *xs_p = nullptr, *wgu_p = nullptr, *hs_p = nullptr, *wd_p = nullptr;
   if (tile) {
@@ -1271,9 +1311,9 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
     GemmParams t = tile4_params(g, false, xs_p, wgu_p);
     t.role = GEMM_GATEUP;
     t.group_m = kMergeShortBand;
-    t.tiles_upper = gemm_tiles_upper(t, g.total);
-    st = launch_gemm_mxfp4(t, false, s);
+    st = launch_tile4(t, false, g.total, s);
   } else {
+    inline_weights(g, reinterpret_cast<const uint8_t* const*>(a->w_gate_up), a->w_gate_up_scale);
     st = launch_gemm4_swiglu(g, s);
   }
   if (st != MGE_OK) return st;
@@ -1284,14 +1324,17 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
   d.A = static_cast<const uint8_t*>(h); d.As = hs;
   d.W = dev + E; d.Ws = dev + 3 * E;
   d.C = a->y_perm;
-  if (!tile) return launch_gemm4_store(d, false, a->y_dtype == MGE_DTYPE_F32, s);
+  d.vec = scales_vec(d.As, a->w_down_scale, E, d.K);
+  if (!tile) {
+    inline_weights(d, reinterpret_cast<const uint8_t* const*>(a->w_down), a->w_down_scale);
+    return launch_gemm4_store(d, false, a->y_dtype == MGE_DTYPE_F32, s);
+  }
   st = launch_scale_pack(pack_rows(hs, R, F / 32, hs_p), s);
   if (st != MGE_OK) return st;
   GemmParams t = tile4_params(d, false, hs_p, wd_p);
   t.out_dtype = a->y_dtype;
   t.role = GEMM_DOWN;
-  t.tiles_upper = gemm_tiles_upper(t, d.total);
-  return launch_gemm_mxfp4(t, false, s);
+  return launch_tile4(t, false, d.total, s);
 }
 
 mge_status mge_check_device_errors(void* route_workspace, void* stream) {

@@ -30,10 +30,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int S4_WAVES = 4;
-constexpr int S4_THREADS = 64 * S4_WAVES;
-constexpr int S4_STEP = 128;     // elements of K per matrix instruction
-constexpr int S4_U = 4;          // steps whose loads are in flight together
+constexpr int S4_CHUNK = 16;     // K blocks (of 32) a wave takes at a time: 4 matrix instructions a row block
 constexpr int kS4Rsrc = 0x00020000;
 constexpr uint32_t kS4Out = 0x80000000u;   // an offset past every bound
 
@@ -50,10 +47,10 @@ __device__ __forceinline__ i32x8 s4_frag(u32x4 a, u32x4 b) {
   return i32x8{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
 }
 
-template <bool A4, int NB, int MB, bool SWIGLU, bool F32>
-__global__ __launch_bounds__(S4_THREADS) void gemm4_stream_kernel(Gemm4Params p) {
-  __shared__ __attribute__((aligned(16))) f32x4 red[S4_WAVES][NB * MB][64];
-  __shared__ int32_t s_pick;
+template <int W, bool A4, int NB, int MB, bool SWIGLU, bool F32, bool VEC>
+__global__ __launch_bounds__(64 * W) void gemm4_stream_kernel(Gemm4Params p) {
+  __shared__ __attribute__((aligned(16))) f32x4 red[W][NB * MB][64];
+  __shared__ int32_t s_pick, s_cnt[4];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = tid >> 6;
@@ -64,15 +61,14 @@ __global__ __launch_bounds__(S4_THREADS) void gemm4_stream_kernel(Gemm4Params p)
   // min(E, rows) of them, which is the grid)
   int e = 0;
   if (p.sizes) {
+    static_assert(W >= 4, "a thread for each of up to 256 experts");
     if (tid == 0) s_pick = -1;
-    __syncthreads();
     const bool some = tid < p.E && p.sizes[tid] > 0;
     const uint64_t mask = __ballot(some);
-    __shared__ int32_t s_cnt[S4_WAVES];
-    if (lane == 0) s_cnt[wave] = __popcll(mask);
+    if (lane == 0 && wave < 4) s_cnt[wave] = __popcll(mask);
     __syncthreads();
     int before = __popcll(mask & ((uint64_t(1) << lane) - 1));
-    for (int w = 0; w < wave; ++w) before += s_cnt[w];
+    for (int w = 0; w < wave && w < 4; ++w) before += s_cnt[w];
     if (some && before == int(blockIdx.y)) s_pick = tid;
     __syncthreads();
     e = __builtin_amdgcn_readfirstlane(s_pick);
@@ -87,25 +83,30 @@ __global__ __launch_bounds__(S4_THREADS) void gemm4_stream_kernel(Gemm4Params p)
   size = __builtin_amdgcn_readfirstlane(size);
 
   const int K = p.K, KB = K / 32;
-  const int steps = (K + S4_STEP - 1) / S4_STEP;
+  const int chunks = (KB + S4_CHUNK - 1) / S4_CHUNK;
   const uint32_t wrow = uint32_t(K) / 2;
   const int nrows = SWIGLU ? 2 * p.F : p.N;
-  const __amdgpu_buffer_rsrc_t rW = s4_rsrc(p.W[e], uint32_t(nrows) * wrow);
-  const __amdgpu_buffer_rsrc_t rS = s4_rsrc(p.Ws[e], uint32_t(nrows) * uint32_t(KB));
+  const __amdgpu_buffer_rsrc_t rW = s4_rsrc(p.W ? p.W[e] : p.Wv[e], uint32_t(nrows) * wrow);
+  const __amdgpu_buffer_rsrc_t rS = s4_rsrc(p.W ? p.Ws[e] : p.Wsv[e], uint32_t(nrows) * uint32_t(KB));
   // first weight row of block b
   auto brow = [&](int b) {
-    if constexpr (SWIGLU) return int(blockIdx.x) * 32 + (b & 1) * 16 + (b >= 2 ? p.F : 0);
+    if constexpr (SWIGLU) return int(blockIdx.x) * (NB * 8) + (b % (NB / 2)) * 16 + (b >= NB / 2 ? p.F : 0);
     else return int(blockIdx.x) * (NB * 16) + b * 16;
   };
   uint32_t w_off[NB], s_off[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int n = brow(b) + i16;
-    const bool in = n < nrows;
-    w_off[b] = in ? uint32_t(n) * wrow + 16u * q : kS4Out;
-    s_off[b] = in ? uint32_t(n) * uint32_t(KB) + q : kS4Out;
+    // (SwiGLU: ffn columns past F are neither gate nor up rows of this workgroup)
+    const bool in = SWIGLU ? n - (b >= NB / 2 ? p.F : 0) < p.F : n < nrows;
+    w_off[b] = in ? uint32_t(n) * wrow : kS4Out;
+    s_off[b] = in ? uint32_t(n) * uint32_t(KB) : kS4Out;
   }
-
+  // K blocks of a chunk: step 2t + j takes block 8t + 2q + j in the lanes q (so that two steps
+  // read whole lines of 128 bytes); an 8-bit operand's lane q has halves q % 2 of the blocks
+  // that its lanes q / 2 and 2 + q / 2 scale
+  const uint32_t sh0 = 16 * (q & 1);
+  const bool odd2 = (q >> 1) != 0;
   const uint32_t arow = A4 ? wrow : uint32_t(K);
   for (int m0 = 0; m0 < size; m0 += 16 * MB) {
     const int mv = size - m0 < 16 * MB ? size - m0 : 16 * MB;
@@ -116,33 +117,51 @@ __global__ __launch_bounds__(S4_THREADS) void gemm4_stream_kernel(Gemm4Params p)
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int m = 0; m < MB; ++m) acc[b][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s0 = wave * S4_U; s0 < steps; s0 += S4_WAVES * S4_U) {
-      u32x4 w[S4_U][NB], a[S4_U][MB], a2[S4_U][MB];
-      uint32_t ws[S4_U][NB], as[S4_U][MB];
+    for (int c = wave; c < chunks; c += W) {
+      const uint32_t k0 = uint32_t(c) * S4_CHUNK;
+      u32x4 w[4][NB], a[4][MB], a2[4][MB];
+      u32x4 ws[NB], as[MB];
 #pragma unroll
-      for (int u = 0; u < S4_U; ++u) {
-        const int s = s0 + u;
-        const bool kin = s * 4 + q < KB;                 // the lane's K block exists
+      for (int b = 0; b < NB; ++b) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          w[u][b] = s4_load16(rW, kin ? w_off[b] + uint32_t(s) * 64u : kS4Out);
-          ws[u][b] = s4_load1(rS, kin ? s_off[b] + uint32_t(s) * 4u : kS4Out);
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t blk = k0 + 8 * (u >> 1) + 2 * q + (u & 1);
+          w[u][b] = s4_load16(rW, VEC || blk < uint32_t(KB) ? w_off[b] + blk * 16 : kS4Out);
         }
+        if constexpr (VEC) {
+          ws[b] = s4_load16(rS, s_off[b] + k0);
+        } else {
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-          const uint32_t row = uint32_t(m * 16 + i16);
-          as[u][m] = s4_load1(rAs, kin ? row * uint32_t(KB) + uint32_t(s) * 4u + q : kS4Out);
-          if constexpr (A4) {
-            a[u][m] = s4_load16(rA, kin ? row * arow + uint32_t(s) * 64u + 16u * q : kS4Out);
-          } else {
-            const uint32_t k0 = uint32_t(s) * 128u + 16u * q;
-            a[u][m] = s4_load16(rA, k0 < uint32_t(K) ? row * arow + k0 : kS4Out);
-            a2[u][m] = s4_load16(rA, k0 + 64u < uint32_t(K) ? row * arow + k0 + 64u : kS4Out);
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t blk = k0 + 8 * (u >> 1) + 2 * q + (u & 1);
+            ws[b][u] = s4_load1(rS, blk < uint32_t(KB) ? s_off[b] + blk : kS4Out);
           }
         }
       }
 #pragma unroll
-      for (int u = 0; u < S4_U; ++u)
+      for (int m = 0; m < MB; ++m) {
+        const uint32_t row = uint32_t(m * 16 + i16);
+        if constexpr (VEC) as[m] = s4_load16(rAs, row * uint32_t(KB) + k0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t blk = k0 + 8 * (u >> 1) + 2 * q + (u & 1);
+          if constexpr (!VEC) as[m][u] = s4_load1(rAs, blk < uint32_t(KB) ? row * uint32_t(KB) + blk : kS4Out);
+          if constexpr (A4) {
+            a[u][m] = s4_load16(rA, VEC || blk < uint32_t(KB) ? row * arow + blk * 16 : kS4Out);
+          } else {
+            const uint32_t b1 = k0 + 8 * (u >> 1) + 2 * (q >> 1) + (u & 1);
+            a[u][m] = s4_load16(rA, VEC || b1 < uint32_t(KB) ? row * arow + b1 * 32 + 16 * (q & 1) : kS4Out);
+            a2[u][m] = s4_load16(rA, VEC || b1 + 4 < uint32_t(KB) ? row * arow + (b1 + 4) * 32 + 16 * (q & 1) : kS4Out);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        // the scale byte of block 8 (u / 2) + 2 q + u % 2
+        auto sc = [&](const u32x4& v) {
+          if constexpr (VEC) return int((odd2 ? v[2 * (u >> 1) + 1] : v[2 * (u >> 1)]) >> (sh0 + 8 * (u & 1)));
+          else return int(v[u]);
+        };
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -150,9 +169,10 @@ __global__ __launch_bounds__(S4_THREADS) void gemm4_stream_kernel(Gemm4Params p)
             const u32x4 z = {0, 0, 0, 0};
             const i32x8 fw = s4_frag(w[u][b], z);
             const i32x8 fa = A4 ? s4_frag(a[u][m], z) : s4_frag(a[u][m], a2[u][m]);
-            acc[b][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa, acc[b][m], 4, A4 ? 4 : 0, 0,
-                                                                         int(ws[u][b]), 0, int(as[u][m]));
+            acc[b][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa, acc[b][m], 4, A4 ? 4 : 0, 0, sc(ws[b]), 0,
+                                                                         sc(as[m]));
           }
+      }
     }
     // join the waves' sums in wave order
     __syncthreads();
@@ -162,10 +182,10 @@ __global__ __launch_bounds__(S4_THREADS) void gemm4_stream_kernel(Gemm4Params p)
       for (int m = 0; m < MB; ++m) red[wave][b * MB + m][lane] = acc[b][m];
     __syncthreads();
     if constexpr (!SWIGLU) {
-      for (int j = wave; j < NB * MB; j += S4_WAVES) {
+      for (int j = wave; j < NB * MB; j += W) {
         f32x4 c = red[0][j][lane];
 #pragma unroll
-        for (int w = 1; w < S4_WAVES; ++w) {
+        for (int w = 1; w < W; ++w) {
           const f32x4 x = red[w][j][lane];
           c.x += x.x; c.y += x.y; c.z += x.z; c.w += x.w;
         }
@@ -178,16 +198,21 @@ __global__ __launch_bounds__(S4_THREADS) void gemm4_stream_kernel(Gemm4Params p)
         }
       }
     } else {
-      // token block m: wave m % 4.  Blocks 0, 1 hold gate columns 0..15, 16..31, blocks 2, 3
-      // the up columns; the lane has columns 4q .. 4q + 3 of each, token i16
-      for (int m = wave; m < MB; m += S4_WAVES) {
+      // item j: 32 ffn columns (set j / MB) of token block j % MB.  Their gate columns 0..15
+      // and 16..31 are blocks 2 set, 2 set + 1, their up columns NB / 2 blocks further; the
+      // lane has columns 4q .. 4q + 3 of each, token i16
+      for (int j = wave; j < (NB / 4) * MB; j += W) {
+        const int m = j % MB, set = j / MB;
+        const int f0 = int(blockIdx.x) * (NB * 8) + set * 32;
+        if (f0 >= p.F) continue;   // uniform
         f32x4 c[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          c[b] = red[0][b * MB + m][lane];
+          const int at = (2 * set + (b & 1) + (b >= 2 ? NB / 2 : 0)) * MB + m;
+          c[b] = red[0][at][lane];
 #pragma unroll
-          for (int w = 1; w < S4_WAVES; ++w) {
-            const f32x4 x = red[w][b * MB + m][lane];
+          for (int w = 1; w < W; ++w) {
+            const f32x4 x = red[w][at][lane];
             c[b].x += x.x; c[b].y += x.y; c[b].z += x.z; c[b].w += x.w;
           }
         }
@@ -198,20 +223,20 @@ __global__ __launch_bounds__(S4_THREADS) void gemm4_stream_kernel(Gemm4Params p)
         float h[8];
         float amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float G = c[j >> 2][j & 3], U = c[2 + (j >> 2)][j & 3];
-          h[j] = pr * silu_f(G) * U;
-          amax = fmaxf(amax, fabsf(h[j]));
+        for (int i = 0; i < 8; ++i) {
+          const float G = c[i >> 2][i & 3], U = c[2 + (i >> 2)][i & 3];
+          h[i] = pr * silu_f(G) * U;
+          amax = fmaxf(amax, fabsf(h[i]));
         }
         amax = fmaxf(amax, __shfl_xor(amax, 16));
         amax = fmaxf(amax, __shfl_xor(amax, 32));
         const uint32_t sc = mx_scale_byte(amax);
         const float inv = mx_inv_scale(sc);
         if (live) {
-          uint8_t* hc = p.h_codes + r * p.F + int64_t(blockIdx.x) * 32;
+          uint8_t* hc = p.h_codes + r * p.F + f0;
           *reinterpret_cast<uint32_t*>(hc + 4 * q) = e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
           *reinterpret_cast<uint32_t*>(hc + 16 + 4 * q) = e4m3x4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv);
-          if (q == 0) p.h_scales[r * (p.F / 32) + blockIdx.x] = uint8_t(sc);
+          if (q == 0) p.h_scales[r * (p.F / 32) + f0 / 32] = uint8_t(sc);
         }
       }
     }
@@ -222,27 +247,48 @@ __global__ __launch_bounds__(S4_THREADS) void gemm4_stream_kernel(Gemm4Params p)
 // Groups that can have rows: the kernel's grid in y
 static int groups_upper(const Gemm4Params& p) { return !p.sizes ? 1 : int(p.E < p.total ? p.E : p.total); }
 
-template <bool A4, int NB, int MB, bool SWIGLU, bool F32>
-static mge_status launch_stream(const Gemm4Params& p, int nblocks, const char* name, hipStream_t s) {
+template <int W, bool A4, int NB, int MB, bool SWIGLU, bool F32>
+static mge_status launch_stream(const Gemm4Params& p, const char* name, hipStream_t s) {
+  const int cols = SWIGLU ? p.F : p.N, per = SWIGLU ? NB * 8 : NB * 16;
+  const dim3 grid(unsigned((cols + per - 1) / per), unsigned(groups_upper(p)));
   ProfScope prof(s, name);
-  hipLaunchKernelGGL((gemm4_stream_kernel<A4, NB, MB, SWIGLU, F32>), dim3(unsigned(nblocks), unsigned(groups_upper(p))),
-                     dim3(S4_THREADS), 0, s, p);
+  if (p.vec) hipLaunchKernelGGL((gemm4_stream_kernel<W, A4, NB, MB, SWIGLU, F32, true>), grid, dim3(64 * W), 0, s, p);
+  else hipLaunchKernelGGL((gemm4_stream_kernel<W, A4, NB, MB, SWIGLU, F32, false>), grid, dim3(64 * W), 0, s, p);
   return hip_check(name);
+}
+
+// Workgroups from which a wider workgroup (fewer reads of the tokens) beats a narrower one
+// (more CUs at work), and 8 waves for each below a CU's fill of 4-wave ones.  Down product of 2
+// experts x [4096][14336], 1 row each (512 blocks of 16 rows): 16 rows a workgroup 14.5 us, 32
+// 16.5, 64 23; of 7 experts, 8 waves x 64 rows 44 us, 4 waves x 64 rows 47, 8 waves x 32 rows 60.
+// Two token blocks a pass (MB = 2) past 12 rows an expert on average: gate-up and down of 64
+// tokens, top-2 of 8 experts, 249 -> 219 us; of 32 tokens it costs 201 for 165.
+constexpr int64_t kStreamWgs = 512;
+constexpr int kStreamRows2 = 12;
+
+template <bool A4, bool F32>
+static mge_status launch_store(const Gemm4Params& p, const char* name, hipStream_t s) {
+  const int64_t blocks = int64_t((p.N + 15) / 16) * groups_upper(p);
+  if (p.total > int64_t(kStreamRows2) * p.E) {
+    if (blocks < 4 * kStreamWgs) return launch_stream<8, A4, 2, 2, false, F32>(p, name, s);
+    return launch_stream<4, A4, 4, 2, false, F32>(p, name, s);
+  }
+  if (blocks < 2 * kStreamWgs) return launch_stream<8, A4, 1, 1, false, F32>(p, name, s);
+  if (blocks < 4 * kStreamWgs) return launch_stream<8, A4, 2, 1, false, F32>(p, name, s);
+  if (blocks < 8 * kStreamWgs) return launch_stream<8, A4, 4, 1, false, F32>(p, name, s);
+  return launch_stream<4, A4, 4, 1, false, F32>(p, name, s);
 }
 
 mge_status launch_gemm4_store(const Gemm4Params& p, bool a4, bool f32, hipStream_t s) {
   if (p.total <= 0 || p.rows <= 0 || p.N <= 0) return MGE_OK;
-  const int nb = (p.N + 31) / 32;
-  if (a4)
-    return f32 ? launch_stream<true, 2, 1, false, true>(p, nb, "gemm4_stream_mxfp4", s)
-               : launch_stream<true, 2, 1, false, false>(p, nb, "gemm4_stream_mxfp4", s);
-  return f32 ? launch_stream<false, 2, 1, false, true>(p, nb, "gemm4_stream_mxfp8", s)
-             : launch_stream<false, 2, 1, false, false>(p, nb, "gemm4_stream_mxfp8", s);
+  if (a4) return f32 ? launch_store<true, true>(p, "gemm4_stream_mxfp4", s) : launch_store<true, false>(p, "gemm4_stream_mxfp4", s);
+  return f32 ? launch_store<false, true>(p, "gemm4_stream_mxfp8", s) : launch_store<false, false>(p, "gemm4_stream_mxfp8", s);
 }
 
 mge_status launch_gemm4_swiglu(const Gemm4Params& p, hipStream_t s) {
   if (p.total <= 0 || p.rows <= 0) return MGE_OK;
-  return launch_stream<false, 4, 1, true, false>(p, p.F / 32, "gemm4_swiglu", s);
+  if (p.total > int64_t(kStreamRows2) * p.E) return launch_stream<4, false, 4, 2, true, false>(p, "gemm4_swiglu", s);
+  return launch_stream<4, false, 4, 1, true, false>(p, "gemm4_swiglu", s);
 }
 
 }  // namespace mge

@@ -235,7 +235,7 @@ constexpr int G_DYN_LDS = G_SCALE_BASE + G_STAGES * G_SCALE_STAGE;
 // this launch runs each of them as four 256 x 64 work items instead (the main launch leaves
 // them out; both take the same decision from the same tile table).  Every output element is
 // still accumulated by one wave over K in the same order: the results are bit-identical.
-template <int FMT, int EPI, int MODE, int OUT, int QT = 0>
+template <int FMT, int EPI, int MODE, int OUT, int QT = 0, int SM = 0>
 __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   constexpr bool MX = FMT != FMT_BF16;
   constexpr bool A4 = FMT == FMT_MXFP4, B4 = FMT == FMT_MXFP8_MXFP4 || FMT == FMT_MXFP4;
@@ -245,15 +245,22 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   constexpr int BROWB = FMT == FMT_MXFP8_MXFP4 ? G_BKB / 2 : G_BKB;
   constexpr int BROWS_DMA = 1024 / BROWB;
   static_assert(QT == 0 || (EPI == EPI_STORE && MODE == RAGGED_M), "the quarter-width tail is for plain-store ragged-M GEMMs");
-  constexpr int BW = QT ? G_BN / 4 : G_BN;        // output columns (B rows) of a work item
+  static_assert(SM == 0 || (QT == 0 && MODE == RAGGED_M && EPI != EPI_SWIGLU_BWD), "64-row tiles: ragged-M forward GEMMs");
+  constexpr int WMB = SM ? 1 : G_WMB;              // 32-row MFMA blocks per wave
+  constexpr int BM = G_WAVES_M * WMB * 32;         // rows of a tile
+  constexpr int TN = SM ? SM : G_BN;               // columns of a tile
+  constexpr int BW = QT ? G_BN / 4 : TN;           // output columns (B rows) of a work item
+  constexpr int STAGE = SM ? BM * G_BKB + BW * BROWB : G_STAGE_BYTES;   // operand bytes of an LDS stage
+  constexpr int SCALES = G_STAGES * STAGE;         // the scales behind the stages
+  constexpr int NA = BM / 32;                      // A's DMA instructions per wave and slice
   constexpr int WNB = BW / (32 * G_WAVES_N);       // 32-column MFMA blocks per wave
-  constexpr int NOPS = 8 + BW / (4 * BROWS_DMA);   // operand DMA instructions per wave and slice (A: 8)
+  constexpr int NOPS = NA + BW / (4 * BROWS_DMA);  // operand DMA instructions per wave and slice
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   // LDS byte address of the dynamic shared block (the low half of its generic address)
   const uint32_t lds_base = uniform(int(uint32_t(reinterpret_cast<uintptr_t>(smem))));
   __shared__ int32_t s_prefix[G_MAXE + 1];
   __shared__ int32_t s_mtiles[G_MAXE];
-  __shared__ __attribute__((aligned(16))) float s_prob[G_BM];   // SwiGLU: routing probability of each tile row
+  __shared__ __attribute__((aligned(16))) float s_prob[BM];   // SwiGLU: routing probability of each tile row
   __shared__ __attribute__((aligned(16))) float s_inv[G_WAVES_M * G_WAVES_N * 32];   // SwiGLU: row-scale broadcast
 
   const int tid = threadIdx.x;
@@ -276,7 +283,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   constexpr int ELEM = MX ? 1 : 2;           // bytes per element
 
   // ---- tile table: tiles of expert e = mtiles(e) * ntiles
-  const int ncols_per_tile = (EPI == EPI_SWIGLU) ? G_BN / 2 : G_BN;
+  const int ncols_per_tile = (EPI == EPI_SWIGLU) ? TN / 2 : TN;
   const int ncols = (EPI == EPI_SWIGLU) ? p.F : p.N;
   const int ntiles = (ncols + ncols_per_tile - 1) / ncols_per_tile;
   // A group's span, clamped into the R permuted rows, so that maps other than the routing
@@ -287,8 +294,8 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   if (tid == 0) {
     int acc = 0;
     for (int e = 0; e < p.E; ++e) {
-      int mt = MODE == RAGGED_M ? (group_size(p.sizes[e], group_off(p.offs[e])) + G_BM - 1) / G_BM
-                                : (p.M + G_BM - 1) / G_BM;
+      int mt = MODE == RAGGED_M ? (group_size(p.sizes[e], group_off(p.offs[e])) + BM - 1) / BM
+                                : (p.M + BM - 1) / BM;
       s_prefix[e] = acc;
       s_mtiles[e] = mt;
       acc += mt * ntiles;
@@ -352,7 +359,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     t.nt = within / gm;
     t.off = uniform(group_off(ld_uniform(p.offs, t.e)));
     t.m_valid = MODE == RAGGED_M ? uniform(group_size(ld_uniform(p.sizes, t.e), t.off)) : p.M;
-    t.m0 = mt * G_BM;
+    t.m0 = mt * BM;
     // K range in bytes.  RAGGED_M: [0, K).  RAGGED_K: the expert's token span
     // [off, off + roundup32(size)) of the column forms; the loop starts at the slice
     // boundary below it and the chunks outside the span load as zeros.
@@ -370,13 +377,13 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       t.A = p.A + int64_t(t.m0) * p.lda;
       bmat = p.B;
     }
-    t.arec = uint32_t(rows_left(t.m_valid - t.m0, G_BM)) * uint32_t(p.lda);
+    t.arec = uint32_t(rows_left(t.m_valid - t.m0, BM)) * uint32_t(p.lda);
     if constexpr (EPI == EPI_SWIGLU) {
-      t.nb = t.nt * (G_BN / 2);
+      t.nb = t.nt * (TN / 2);
       t.B = bmat + int64_t(t.nb) * p.ldb;
-      t.brec = uint32_t(rows_left(p.F - t.nb, G_BN / 2)) * uint32_t(p.ldb);
+      t.brec = uint32_t(rows_left(p.F - t.nb, TN / 2)) * uint32_t(p.ldb);
     } else {
-      t.nb = t.nt * G_BN + quarter * BW;
+      t.nb = t.nt * TN + quarter * BW;
       t.B = bmat + int64_t(t.nb) * p.ldb;
       t.brec = uint32_t(rows_left(p.N - t.nb, BW)) * uint32_t(p.ldb);
     }
@@ -406,7 +413,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   // path.  Lane offsets (row start + chunk) relative to the tile's first row, for even
   // and odd instructions; instruction i adds i*8 rows.
   const int lchunk0 = (lane & 7) ^ (lane >> 4);
-  const int arow0 = wave * 64 + (lane >> 3);
+  const int arow0 = wave * (BM / 4) + (lane >> 3);
   // (64-byte B rows: lane l -> row +l/4, LDS chunk l%4, global chunk (l%4) ^ (l/16) of swz64)
   const int brow0 = (EPI == EPI_SWIGLU ? (wave & 1) * 64 : wave * (BW / 4)) + (BROWB == 64 ? lane >> 2 : lane >> 3);
   const int bchunk64 = (lane & 3) ^ (lane >> 4);
@@ -446,8 +453,8 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     if constexpr (BROWB == 64) c.outb = (uint32_t(t.khi / 2 - 1 - (kslice / 2 + bchunk64 * 16)) >> 31) << 31;
     // A: 64 rows per wave (8 instructions of 8 rows); B: BW / 4 rows per wave, stored at
     // B row wave * BW / 4 of the stage (SwiGLU: waves 0, 1 the gate rows, 2, 3 the up rows)
-    c.la = lds_base + stage * G_STAGE_BYTES + wave * 8 * 1024;
-    c.lb = lds_base + stage * G_STAGE_BYTES + G_BM * G_BKB + wave * (BW / 4) * BROWB;
+    c.la = lds_base + stage * STAGE + wave * NA * 1024;
+    c.lb = lds_base + stage * STAGE + BM * G_BKB + wave * (BW / 4) * BROWB;
     if constexpr (MX) {
       // wave w brings 128 rows of scale dwords (lanes 0..31, 16 B = 4 rows each):
       // A rows (w&1)*128.. for w < 2, B rows for w >= 2; the dwords of the slice's
@@ -474,22 +481,23 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       c.rS = make_rsrc_n(base, bytes);
       // lanes of 4 rows each: 32 (128 rows), fewer for the B rows of a narrow work item
       constexpr int kBLanes0 = BW >= 128 ? 32 : BW / 4, kBLanes1 = BW >= 256 ? 32 : (BW > 128 ? (BW - 128) / 4 : 0);
-      const int nlanes = wave < 2 ? 32 : (half == 0 ? kBLanes0 : kBLanes1);
+      constexpr int kALanes0 = BM >= 128 ? 32 : BM / 4, kALanes1 = BM >= 256 ? 32 : 0;
+      const int nlanes = wave < 2 ? (half == 0 ? kALanes0 : kALanes1) : (half == 0 ? kBLanes0 : kBLanes1);
       if constexpr (A4) {
         const uint32_t ld4 = uint32_t(wave < 2 ? p.asp_ld : p.bsp_ld) * 4;
         c.so = (slice_ok && (lane & 31) < nlanes) ? uint32_t(dw * 4) + (lane >> 5) * ld4 + (lane & 31) * 16 : kInvalid;
       } else {
         c.so = (slice_ok && lane < nlanes) ? uint32_t(dw * 4) + lane * 16 : kInvalid;
       }
-      c.ls = lds_base + G_SCALE_BASE + stage * G_SCALE_STAGE + wave * 1024;
+      c.ls = lds_base + SCALES + stage * G_SCALE_STAGE + wave * 1024;
     }
     return c;
   };
   auto dma_operand = [&](const SliceDma& c, int i) {
     const uint32_t out = (i & 1) ? c.out1 : c.out0;
-    if (i < 8) dma16(c.rA, c.la + i * 1024, (a_lane[i & 1] + i * lda8 + c.kadd) | out);
-    else if constexpr (BROWB == 64) dma16(c.rB, c.lb + (i - 8) * 1024, (b_lane[0] + (i - 8) * ldb8 + c.kadd / 2) | c.outb);
-    else dma16(c.rB, c.lb + (i - 8) * 1024, (b_lane[i & 1] + (i - 8) * ldb8 + c.kadd) | out);
+    if (i < NA) dma16(c.rA, c.la + i * 1024, (a_lane[i & 1] + i * lda8 + c.kadd) | out);
+    else if constexpr (BROWB == 64) dma16(c.rB, c.lb + (i - NA) * 1024, (b_lane[0] + (i - NA) * ldb8 + c.kadd / 2) | c.outb);
+    else dma16(c.rB, c.lb + (i - NA) * 1024, (b_lane[i & 1] + (i - NA) * ldb8 + c.kadd) | out);
   };
   auto dma_scale = [&](const SliceDma& c) {
     if constexpr (MX) dma16(c.rS, c.ls, c.so);
@@ -522,8 +530,8 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   constexpr int NSTEP = MX && !A4 ? 2 : 4;
   auto read_frags = [&](const uint8_t* sA, const uint8_t* sB, int s, frag_t* af, bfrag_t* bfr) {
 #pragma unroll
-    for (int mi = 0; mi < G_WMB; ++mi) {
-      const int row = (wm * G_WMB + mi) * 32 + l32;
+    for (int mi = 0; mi < WMB; ++mi) {
+      const int row = (wm * WMB + mi) * 32 + l32;
       if constexpr (A4) {
         af[mi] = *reinterpret_cast<const i32x4*>(sA + swz(row, s * 2 + hi));
       } else if constexpr (MX) {
@@ -566,9 +574,9 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       if (m0 + tid < m_valid) my_prob = p.prob[off + m0 + tid];
     }
 
-    f32x16 acc[G_WMB][WNB];
+    f32x16 acc[WMB][WNB];
 #pragma unroll
-    for (int mi = 0; mi < G_WMB; ++mi)
+    for (int mi = 0; mi < WMB; ++mi)
 #pragma unroll
       for (int ni = 0; ni < WNB; ++ni)
 #pragma unroll
@@ -582,14 +590,14 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     // CU's texture-address path moves about 54 bytes per clock, so a slice's DMAs need
     // well over half of the slice's MFMA time; packed closer they fill its queue and
     // stall the issuing wave (measured on MI355X).
-    constexpr int NMFMA = NSTEP * G_WMB * WNB;
+    constexpr int NMFMA = NSTEP * WMB * WNB;
     constexpr int BAR_AT = NMFMA * G_BAR_AT32 / 32;
-    auto mfma_slice = [&](frag_t (*af)[G_WMB], bfrag_t (*bfr)[WNB], const uint32_t* sa, const uint32_t* sb,
+    auto mfma_slice = [&](frag_t (*af)[WMB], bfrag_t (*bfr)[WNB], const uint32_t* sa, const uint32_t* sb,
                           const SliceDma& nx) {
       static_for<0, NMFMA>([&](auto ic) {
         constexpr int i = decltype(ic)::value;
-        constexpr int s = i / (G_WMB * WNB);
-        constexpr int mi = (i % (G_WMB * WNB)) / WNB;
+        constexpr int s = i / (WMB * WNB);
+        constexpr int mi = (i % (WMB * WNB)) / WNB;
         constexpr int ni = i % WNB;
         if constexpr (i == BAR_AT) {
           __builtin_amdgcn_sched_barrier(0);
@@ -601,7 +609,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
           // MXFP4 A: group s / 2 of the slice, K block 2 (s % 2) + hi of it
           constexpr int g = A4 ? s / 2 : 0;
           const int sh = 8 * (2 * (A4 ? s % 2 : s) + hi);
-          const int xa = int(sa[g * G_WMB + mi] >> sh);
+          const int xa = int(sa[g * WMB + mi] >> sh);
           const int xb = int(sb[g * WNB + ni] >> sh);
           i32x8 fa;
           if constexpr (A4) fa = __builtin_shufflevector(af[s][mi], af[s][mi], 0, 1, 2, 3, -1, -1, -1, -1);
@@ -649,18 +657,18 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     }
     for (int kt = 0; kt < nkt; ++kt) {
       const int stage = kt & (G_STAGES - 1);
-      const uint8_t* sA = smem + stage * G_STAGE_BYTES;
-      const uint8_t* sB = sA + G_BM * G_BKB;
+      const uint8_t* sA = smem + stage * STAGE;
+      const uint8_t* sB = sA + BM * G_BKB;
       constexpr int NG = A4 ? 2 : 1;   // scale groups (128 elements) per slice
-      uint32_t sa[NG * G_WMB], sb[NG * WNB];
+      uint32_t sa[NG * WMB], sb[NG * WNB];
       if constexpr (A4) {
-        const uint8_t* sS = smem + G_SCALE_BASE + stage * G_SCALE_STAGE;
+        const uint8_t* sS = smem + SCALES + stage * G_SCALE_STAGE;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
 #pragma unroll
-          for (int mi = 0; mi < G_WMB; ++mi) {
-            const int r = (wm * G_WMB + mi) * 32 + l32;
-            sa[g * G_WMB + mi] = *reinterpret_cast<const uint32_t*>(sS + (r >> 7) * 1024 + g * 512 + (r & 127) * 4);
+          for (int mi = 0; mi < WMB; ++mi) {
+            const int r = (wm * WMB + mi) * 32 + l32;
+            sa[g * WMB + mi] = *reinterpret_cast<const uint32_t*>(sS + (r >> 7) * 1024 + g * 512 + (r & 127) * 4);
           }
 #pragma unroll
           for (int ni = 0; ni < WNB; ++ni) {
@@ -669,10 +677,10 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
           }
         }
       } else if constexpr (MX) {
-        const uint8_t* sS = smem + G_SCALE_BASE + stage * G_SCALE_STAGE;
+        const uint8_t* sS = smem + SCALES + stage * G_SCALE_STAGE;
 #pragma unroll
-        for (int mi = 0; mi < G_WMB; ++mi) {
-          const int r = (wm * G_WMB + mi) * 32 + l32;
+        for (int mi = 0; mi < WMB; ++mi) {
+          const int r = (wm * WMB + mi) * 32 + l32;
           sa[mi] = *reinterpret_cast<const uint32_t*>(sS + (r >> 7) * 1024 + (r & 127) * 4);
         }
 #pragma unroll
@@ -681,7 +689,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
           sb[ni] = *reinterpret_cast<const uint32_t*>(sS + 2048 + (r >> 7) * 1024 + (r & 127) * 4);
         }
       }
-      frag_t af[NSTEP][G_WMB];
+      frag_t af[NSTEP][WMB];
       bfrag_t bfr[NSTEP][WNB];
 #pragma unroll
       for (int s = 0; s < NSTEP; ++s) read_frags(sA, sB, s, af[s], bfr[s]);
@@ -709,14 +717,14 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     // ---------------------------------------------------------------- epilogues
     // Accumulator element r of block (mi, ni) is row 8*(r/4) + 4*hi + (r%4) and column
     // l32 of that 32 x 32 block.
-    const int wrow0 = m0 + wm * G_WMB * 32;   // wave's first row (group-local)
+    const int wrow0 = m0 + wm * WMB * 32;   // wave's first row (group-local)
     if constexpr (EPI == EPI_STORE) {
       // Lane (hi, l32) stores column l32 of each 32 x 32 block, rows 8*(r/4) + 4*hi +
       // r%4; the record bound of the resource ends at the last valid row of the wave's
       // 128-row span and lanes whose column is past N get an offset beyond every bound.
       constexpr int ESZ = OUT == OUT_BF16 ? 2 : 4;
       int vr = m_valid - wrow0;
-      vr = uniform(vr < 0 ? 0 : (vr > G_WMB * 32 ? G_WMB * 32 : vr));
+      vr = uniform(vr < 0 ? 0 : (vr > WMB * 32 ? WMB * 32 : vr));
       uint8_t* cbase;
       if constexpr (MODE == RAGGED_M) {
         cbase = static_cast<uint8_t*>(p.C) + (int64_t(off) + wrow0) * p.ldc * ESZ;
@@ -726,7 +734,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       }
       const uint32_t rowb = uint32_t(p.ldc) * ESZ;
       const __amdgpu_buffer_rsrc_t rC = __builtin_amdgcn_make_buffer_rsrc(cbase, 0, int(uint32_t(vr) * rowb), kRsrcFlags);
-      static_for<0, G_WMB>([&](auto mic) {
+      static_for<0, WMB>([&](auto mic) {
         constexpr int mi = decltype(mic)::value;
         if (wrow0 + mi * 32 >= m_valid) return;
         static_for<0, WNB>([&](auto nic) {
@@ -765,14 +773,14 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       // stores go through buffer resources whose record bound ends at the group's last
       // row, so rows past it are dropped by the hardware range check; 32-row blocks past
       // the group and 32-column blocks past F are skipped whole (wave-uniform).
-      s_prob[tid] = my_prob;
+      if (BM >= G_THREADS || tid < BM) s_prob[tid] = my_prob;
       lds_barrier();   // (the next tile's first slice stays in flight)
       constexpr int hb = G_WNB / 2;
       const int F = p.F;
       const int F2 = 2 * F;
       const bool train = p.saved_gu != nullptr;
       int vr = m_valid - wrow0;                         // valid rows of the wave's span
-      vr = uniform(vr < 0 ? 0 : (vr > G_WMB * 32 ? G_WMB * 32 : vr));
+      vr = uniform(vr < 0 ? 0 : (vr > WMB * 32 ? WMB * 32 : vr));
       const int64_t grow0 = int64_t(off) + wrow0;       // permuted row of span row 0
       auto rsrc = [](const void* base, uint32_t bytes) {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, int(bytes), kRsrcFlags);
@@ -786,7 +794,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
         rHs = rH;
       }
       rGU = rsrc(train ? p.saved_gu + grow0 * F2 : p.saved_gu, train ? uint32_t(vr) * F2 * 2 : 0u);
-      static_for<0, G_WMB>([&](auto mic) {
+      static_for<0, WMB>([&](auto mic) {
         constexpr int mi = decltype(mic)::value;
         const int rb = mi * 32;                          // block row within the span
         if (wrow0 + rb >= m_valid) return;               // past the group and its padding
@@ -794,7 +802,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
         float pr[16];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float4 q = *reinterpret_cast<const float4*>(&s_prob[wm * G_WMB * 32 + rb + 8 * g + 4 * hi]);
+          const float4 q = *reinterpret_cast<const float4*>(&s_prob[wm * WMB * 32 + rb + 8 * g + 4 * hi]);
           pr[4 * g] = q.x; pr[4 * g + 1] = q.y; pr[4 * g + 2] = q.z; pr[4 * g + 3] = q.w;
         }
         static_for<0, hb>([&](auto jc) {
@@ -910,11 +918,11 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       // sums of dh silu(G) U (d_prob), with dG (columns f) and dU (columns F + f) written in
       // row form (32-column blocks: the half-wave reduce-scatter of the forward) and column
       // form (32-row blocks: 16 rows in a lane, 16 in the lane 32 apart), MXFP8 or bf16.
-      s_prob[tid] = my_prob;
+      if (BM >= G_THREADS || tid < BM) s_prob[tid] = my_prob;
       lds_barrier();
       const int F = p.F, F2 = 2 * F;
       int vr = m_valid - wrow0;                         // valid rows of the wave's span
-      vr = uniform(vr < 0 ? 0 : (vr > G_WMB * 32 ? G_WMB * 32 : vr));
+      vr = uniform(vr < 0 ? 0 : (vr > WMB * 32 ? WMB * 32 : vr));
       const int64_t grow0 = int64_t(off) + wrow0;       // permuted row of span row 0
       const int fw0 = nt * G_BN + wn * (G_WNB * 32);    // the wave's first ffn column
       // staging: per buffer G then U, each 8 DMA blocks of 4 rows x 256 bytes, 1088 bytes
@@ -977,7 +985,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
         const int buf = mi & 1;
         // block mi's G, U have landed (block mi + 1's, the newest 16 operations, may still
         // be on their way); asm with a memory clobber, so that no LDS read moves above it
-        if (mi + 1 < G_WMB) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+        if (mi + 1 < WMB) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
         else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         const int rb = mi * 32;                          // block row within the span
         if (wrow0 + rb < m_valid) {                      // wave-uniform
@@ -985,7 +993,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
           float pr[16];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const float4 q = *reinterpret_cast<const float4*>(&s_prob[wm * G_WMB * 32 + rb + 8 * g + 4 * hi]);
+            const float4 q = *reinterpret_cast<const float4*>(&s_prob[wm * WMB * 32 + rb + 8 * g + 4 * hi]);
             pr[4 * g] = q.x; pr[4 * g + 1] = q.y; pr[4 * g + 2] = q.z; pr[4 * g + 3] = q.w;
           }
           float dps[16];
@@ -1000,7 +1008,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
               if ((r & 3) == 0) {                          // four accumulators at a time (register peak)
-                static_for<0, G_WMB>([&](auto mc) {
+                static_for<0, WMB>([&](auto mc) {
                   constexpr int m = decltype(mc)::value;
                   if (mi == m) {                           // wave-uniform
 #pragma unroll
@@ -1087,16 +1095,16 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
             p.dprob_part[(grow0 + lrow(l32 >> 1)) * p.dprob_nparts + nt * 2 + wn] = ps;
         }
         // the buffer takes block mi + 2 once this wave's reads of it have completed
-        if (mi + 2 < G_WMB) {
+        if (mi + 2 < WMB) {
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           issue_gu(mi + 2, buf);
         }
       };
       if constexpr (MXO) {
 #pragma clang loop unroll(disable)
-        for (int mi = 0; mi < G_WMB; ++mi) row_block(mi);
+        for (int mi = 0; mi < WMB; ++mi) row_block(mi);
       } else {
-        static_for<0, G_WMB>([&](auto mic) { row_block(decltype(mic)::value); });
+        static_for<0, WMB>([&](auto mic) { row_block(decltype(mic)::value); });
       }
       }
     }
@@ -1117,6 +1125,22 @@ static inline int device_cus() {
     cus[dev] = v > 0 ? v : 256;
   }
   return cus[dev];
+}
+
+// Operand and scale bytes in LDS of the 64-row tiles (SM columns, 4-bit B rows of browb bytes)
+constexpr int gemm_small_lds(int sm, int browb) {
+  return G_STAGES * (64 * G_BKB + sm * browb) + G_STAGES * G_SCALE_STAGE;
+}
+// Persistent launch of a 64-row-tile kernel that runs `per_cu` workgroups on a CU
+template <typename Kern>
+static mge_status launch_gemm_small(Kern kern, const char* name, const GemmParams& p, int per_cu, int lds, hipStream_t s) {
+  hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  int grid = device_cus() * per_cu;
+  if (p.tiles_upper < grid) grid = p.tiles_upper;
+  if (grid <= 0) return MGE_OK;
+  ProfScope prof(s, name);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(G_THREADS), lds, s, p);
+  return hip_check(name);
 }
 
 // Persistent launch: one workgroup per CU (the kernel holds one workgroup per CU by its

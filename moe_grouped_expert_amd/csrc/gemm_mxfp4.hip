@@ -20,6 +20,21 @@ MGE_GEMM_TAIL_KERNEL(gemm_store_f32_tail_mxfp8_mxfp4, FMT_MXFP8_MXFP4, OUT_F32)
 MGE_GEMM_TAIL_KERNEL(gemm_store_tail_mxfp4, FMT_MXFP4, OUT_BF16)
 MGE_GEMM_TAIL_KERNEL(gemm_store_f32_tail_mxfp4, FMT_MXFP4, OUT_F32)
 
+// 64-row tiles of SM columns; PER_CU workgroups share a CU
+#define MGE_GEMM_SMALL_KERNEL(name, FMT, EPI, OUT, SM, PER_CU) \
+  __global__ __launch_bounds__(G_THREADS, PER_CU) void name(GemmParams p) { gemm_body<FMT, EPI, RAGGED_M, OUT, 0, SM>(p); }
+
+MGE_GEMM_SMALL_KERNEL(gemm_gateup_swiglu64_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_SWIGLU, OUT_NONE, 256, 2)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x128_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_BF16, 128, 3)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x128_f32_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_F32, 128, 3)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x64_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_BF16, 64, 4)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x64_f32_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_F32, 64, 4)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x128_mxfp4, FMT_MXFP4, EPI_STORE, OUT_BF16, 128, 2)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x128_f32_mxfp4, FMT_MXFP4, EPI_STORE, OUT_F32, 128, 2)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x64_mxfp4, FMT_MXFP4, EPI_STORE, OUT_BF16, 64, 3)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x64_f32_mxfp4, FMT_MXFP4, EPI_STORE, OUT_F32, 64, 3)
+
+#undef MGE_GEMM_SMALL_KERNEL
 #undef MGE_GEMM_TAIL_KERNEL
 #undef MGE_GEMM_KERNEL
 
@@ -31,6 +46,32 @@ mge_status launch_gemm_mxfp4(const GemmParams& p, bool a4, hipStream_t s) {
                : launch_gemm_split(gemm_store_mxfp4, gemm_store_tail_mxfp4, "gemm_mxfp4", p, s);
   return f32 ? launch_gemm_split(gemm_store_f32_mxfp8_mxfp4, gemm_store_f32_tail_mxfp8_mxfp4, "gemm_mxfp8_mxfp4", p, s)
              : launch_gemm_split(gemm_store_mxfp8_mxfp4, gemm_store_tail_mxfp8_mxfp4, "gemm_mxfp8_mxfp4", p, s);
+}
+
+// 64-row tiles, of 64 columns where 128 would leave CUs without one: 8 groups x [4096][14336],
+// 64 rows each, 64 x 64 tiles 92 us, 64 x 128 tiles (256 of them) 124.
+constexpr int64_t kWideTiles = 512;
+mge_status launch_gemm_mxfp4_small(const GemmParams& p0, bool a4, int64_t rows_bound, hipStream_t s) {
+  GemmParams p = p0;
+  const int64_t mt = (rows_bound + 63) / 64 + p.E;
+  constexpr int B8 = G_BKB / 2, B4 = G_BKB;
+  if (p.role == GEMM_GATEUP) {
+    p.tiles_upper = int(mt * ((p.F + 127) / 128));
+    return launch_gemm_small(gemm_gateup_swiglu64_mxfp8_mxfp4, "gemm_gateup_swiglu64_mxfp4", p, 2, gemm_small_lds(256, B8), s);
+  }
+  const bool f32 = p.out_dtype == MGE_DTYPE_F32;
+  const bool wide = (mt - p.E / 2) * ((p.N + 127) / 128) >= kWideTiles;
+  p.tiles_upper = int(mt * (wide ? (p.N + 127) / 128 : (p.N + 63) / 64));
+  if (wide) {
+    if (a4)
+      return launch_gemm_small(f32 ? gemm_store64x128_f32_mxfp4 : gemm_store64x128_mxfp4, "gemm64_mxfp4", p, 2, gemm_small_lds(128, B4), s);
+    return launch_gemm_small(f32 ? gemm_store64x128_f32_mxfp8_mxfp4 : gemm_store64x128_mxfp8_mxfp4, "gemm64_mxfp8_mxfp4", p, 3,
+                             gemm_small_lds(128, B8), s);
+  }
+  if (a4)
+    return launch_gemm_small(f32 ? gemm_store64x64_f32_mxfp4 : gemm_store64x64_mxfp4, "gemm64_mxfp4", p, 3, gemm_small_lds(64, B4), s);
+  return launch_gemm_small(f32 ? gemm_store64x64_f32_mxfp8_mxfp4 : gemm_store64x64_mxfp8_mxfp4, "gemm64_mxfp8_mxfp4", p, 4,
+                           gemm_small_lds(64, B8), s);
 }
 
 }  // namespace mge

@@ -130,6 +130,7 @@ mge_status launch_quant4(const Quant4Params& p, hipStream_t s);
 mge_status launch_dequant4(int64_t blocks, const uint8_t* codes, const uint8_t* scales, int dtype, void* out, hipStream_t s);
 
 // C[r] = A[r] W_e^T with MXFP4 weights; SwiGLU: h from W_e = [gate rows; up rows]
+constexpr int kGemm4Inline = 64;    // experts whose weight pointers may travel in the arguments
 struct Gemm4Params {
   int E, N, K, F;
   int rows;                         // rows of A and C: every group is clamped into them
@@ -138,11 +139,14 @@ struct Gemm4Params {
   const int32_t* offs;
   const uint8_t* A;                 // [rows][K] MXFP8 or [rows][K/2] MXFP4 codes
   const uint8_t* As;                // [rows][K/32]
-  const uint8_t* const* W;          // device table: [N][K/2] codes of each expert
+  const uint8_t* const* W;          // device table: [N][K/2] codes of each expert (NULL: Wv)
   const uint8_t* const* Ws;         // device table: [N][K/32]
+  const uint8_t* Wv[kGemm4Inline];
+  const uint8_t* Wsv[kGemm4Inline];
   void* C;                          // [rows][N]
   const float* prob;                // SwiGLU: [rows]
   uint8_t* h_codes; uint8_t* h_scales;   // SwiGLU: [rows][F], [rows][F/32]
+  bool vec;                         // every row of the scale matrices may be read 16 bytes at a time
 };
 mge_status launch_gemm4_store(const Gemm4Params& p, bool a4, bool f32, hipStream_t s);
 mge_status launch_gemm4_swiglu(const Gemm4Params& p, hipStream_t s);
@@ -238,5 +242,7 @@ mge_status launch_gemm(const GemmParams& p, int prec, hipStream_t s);
 // The same tiles with MXFP4 weights (RAGGED_M; roles GATEUP with MXFP8 rows, or DOWN for a
 // plain store); a4: the rows are MXFP4 too
 mge_status launch_gemm_mxfp4(const GemmParams& p, bool a4, hipStream_t s);
+// ... in tiles of 64 rows (tiles_upper is set here, from the bound on all groups' rows)
+mge_status launch_gemm_mxfp4_small(const GemmParams& p, bool a4, int64_t rows_bound, hipStream_t s);
 
 }  // namespace mge

@@ -645,7 +645,7 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* args, void* stream);
  * The matrix unit adds the 128 products of one instruction with less than fp32's precision
  * when the operands are MXFP8 (about 1e-5 relative to the sum's magnitude); MXFP4 products
  * add exactly to fp32 rounding.
- * Workspace: mge_gemm4_workspace_bytes(args).
+ * Workspace: mge_gemm4_workspace_bytes(args) bytes, which is 0 (NULL allowed) for few rows.
  * Errors: MGE_ERR_INVALID_ARG for E outside [1, 256], N or K not a positive multiple of 32,
  * rows < 0 or >= 2^31 / K, an expert's weight of 2^31 bytes or more, unknown formats, NULL or
  * misaligned (16-byte) a / out / weights, NULL scales, one of split_sizes / group_offsets

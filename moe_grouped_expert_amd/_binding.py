@@ -885,8 +885,10 @@ def mxfp4_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, w, w_scale, split
     g = Gemm4Args(C.sizeof(Gemm4Args), fmt, E, N, K, rows, total_rows or 0, _ptr(split_sizes), _ptr(group_offsets),
                   _ptr(a), _ptr(a_scale), C.addressof(wp), C.addressof(wsp), DTYPE[out_dtype], _ptr(out))
     if workspace is None:
-        workspace = a.new_empty(lib().mge_gemm4_workspace_bytes(C.byref(g)))
-    g.workspace, g.workspace_bytes = _ptr(workspace), workspace.numel()
+        need = lib().mge_gemm4_workspace_bytes(C.byref(g))
+        workspace = a.new_empty(need) if need else None
+    if workspace is not None:
+        g.workspace, g.workspace_bytes = workspace.data_ptr(), workspace.numel()
     _call("mxfp4_grouped_gemm", g, dev)
     return out
 

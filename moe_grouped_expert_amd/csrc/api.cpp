@@ -1026,6 +1026,7 @@ mge_status moe_route_topk_bwd(const mge_route_topk_bwd_args* a, void* stream) {
   p.score = a->score; p.renorm = a->renormalize != 0; p.scale = a->scale;
   p.logits = a->logits; p.topk_idx = a->topk_idx; p.d_prob = a->d_prob; p.d_logits = a->d_logits;
   p.vec = topk_vec(a->logits, a->logits_dtype, a->logits_row_stride);
+  p.ovec = topk_vec(a->d_logits, a->logits_dtype, a->E);
   return launch_topk_bwd(p, a->logits_dtype, static_cast<hipStream_t>(stream));
 }
 
@@ -1078,7 +1079,7 @@ constexpr int kTile4Rows = 18;
 // 64 x 128 tiles take the chip, whatever part of it is padding.  Measured (64-row, 256-row):
 // [8192][8192], 512 rows 55, 86 us; 1024 rows 113, 91; 8 x [4096][14336] in 4 bits, 1024 rows
 // 76, 98 us, 2048 rows 123, 117; gate-up of 512 tokens 199, 206 us, of 256 tokens 149, 196.
-constexpr int64_t kSmallTiles = 640;   // 64 x 128 tiles worth a round of 256 x 256 ones on 256 CUs
+constexpr int64_t kSmallTiles = 700;   // 64 x 128 tiles worth a round of 256 x 256 ones on 256 CUs
 static bool small_tiles4(int E, int N, int64_t total) {
   // (group sizes are on the device: half a tile of padding a group, and a tile at least)
   const int64_t ms = (total + 63) / 64 + E / 2;
@@ -1150,6 +1151,7 @@ size_t mge_gemm4_workspace_bytes(const mge_gemm4_args* a) {
   if (!a || a->struct_size != sizeof(mge_gemm4_args) || a->E < 1 || a->E > 256 || a->N < 1 || a->K < 32 || a->rows < 0)
     return 0;
   const bool tile = tile4(a->E, a->N, a->K, a->rows, gemm4_total(a));
+  if (!tile && a->E <= kGemm4Inline) return 0;   // the pointers travel in the arguments
   return up256((2 * size_t(a->E) + 2) * sizeof(void*)) + (tile ? tile4_ws(a->E, a->N, a->K, a->rows) : 0);
 }
 
@@ -1175,7 +1177,7 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
   if (a->rows > 0)
     MGE_REQUIRE(a->a && aligned16(a->a) && a->a_scale && a->out && aligned16(a->out), "a / a_scale / out NULL or misaligned");
   const size_t need = mge_gemm4_workspace_bytes(a);
-  if (!a->workspace || a->workspace_bytes < need) {
+  if (need > 0 && (!a->workspace || a->workspace_bytes < need)) {
     set_error("MXFP4 product workspace needs %zu bytes (got %zu)", need, a->workspace_bytes);
     return MGE_ERR_WORKSPACE;
   }

@@ -48,9 +48,10 @@ mge_status launch_gemm_mxfp4(const GemmParams& p, bool a4, hipStream_t s) {
              : launch_gemm_split(gemm_store_mxfp8_mxfp4, gemm_store_tail_mxfp8_mxfp4, "gemm_mxfp8_mxfp4", p, s);
 }
 
-// 64-row tiles, of 64 columns where 128 would leave CUs without one: 8 groups x [4096][14336],
-// 64 rows each, 64 x 64 tiles 92 us, 64 x 128 tiles (256 of them) 124.
-constexpr int64_t kWideTiles = 512;
+// 64-row tiles, of 64 columns where 128 would leave CUs without one.  8 groups x [4096][14336]:
+// 64 x 64 and 64 x 128 tiles take 91 and 93 us for 256 rows (about 256 of the wide tiles), 132
+// and 100 us for 512 rows (384); one [2048][2048] of 32 rows 3.5 and 4.6 us.
+constexpr int64_t kWideTiles = 320;
 mge_status launch_gemm_mxfp4_small(const GemmParams& p0, bool a4, int64_t rows_bound, hipStream_t s) {
   GemmParams p = p0;
   const int64_t mt = (rows_bound + 63) / 64 + p.E;

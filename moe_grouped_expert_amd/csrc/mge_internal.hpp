@@ -113,7 +113,7 @@ struct TopkBwdParams {
   const int32_t* topk_idx;
   const float* d_prob;
   void* d_logits;           // [T][E], the logits' type
-  bool vec;
+  bool vec, ovec;           // rows of logits, of d_logits may be accessed 16 bytes at a time
 };
 mge_status launch_topk_bwd(const TopkBwdParams& p, int dtype, hipStream_t s);
 

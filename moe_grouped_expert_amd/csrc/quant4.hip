@@ -11,19 +11,22 @@
 // nearest even and saturates (equal to the definition over all finite bf16 values at every
 // scale, on MI355X).
 //
-// One workgroup (512 threads) owns a 128 x 128 tile, staged in LDS; a thread quantizes one
-// block of 32 values of a row, then one of a column.  HBM-bound: 2 B read and 17/32 B
-// written per element and orientation.
+// One workgroup (512 threads) owns a tile of 128 rows x 256 columns, staged in LDS; a thread
+// quantizes two blocks of 32 values of a row, then two of a column.  A tile row's codes are
+// then a whole line of 128 bytes (128 columns: 10% slower); a tile of 256 x 256, whose column
+// pieces are whole lines too, leaves one workgroup a CU and is 13% slower, and scale bytes
+// gathered into dwords change nothing.  HBM-bound: 2 B read and 17/32 B written per element and
+// orientation.  [28672][4096]: rows 60 us (4.9 TB/s), columns 65, both 86 (4.2 TB/s).
 #include "mge_common.hpp"
 #include "mge_internal.hpp"
 
 namespace mge {
 
 constexpr int Q4_ROWS = 128;
-constexpr int Q4_COLS = 128;
+constexpr int Q4_COLS = 256;
 constexpr int Q4_THREADS = 512;
 constexpr int Q4_STRIDE = Q4_COLS + 8;   // bf16 elements per LDS row
-constexpr int Q4_GRP = 16;               // extra bf16 per 32 rows: the 4 row groups of a column fall on other banks
+constexpr int Q4_GRP = 16;               // extra bf16 per 32 rows: the row groups of a column fall on other banks
 __device__ __forceinline__ int q4_at(int row, int col) { return row * Q4_STRIDE + (row >> 5) * Q4_GRP + col; }
 
 typedef __bf16 bf16v2 __attribute__((ext_vector_type(2)));
@@ -62,50 +65,60 @@ __global__ __launch_bounds__(Q4_THREADS) void quant4_kernel(Quant4Params p) {
   const int64_t r0 = int64_t(blockIdx.y) * Q4_ROWS;
   const int b = blockIdx.z;
   const uint16_t* in = p.in + int64_t(b) * p.in_batch_stride;
-  // whole lines into LDS: 16 lanes per tile row, 4 rounds of 32 rows; outside: zeros
-  const int lr = tid >> 4, ch = (tid & 15) * 8;
-  uint4 val[4];
-  bool ok[4];
+  // whole lines into LDS: Q4_COLS / 8 lanes per tile row, all of a thread's loads in flight
+  // together; outside: zeros
+  constexpr int LANES = Q4_COLS / 8, ROUND = Q4_THREADS / LANES, NL = Q4_ROWS / ROUND;
+  const int lr = tid / LANES, ch = (tid % LANES) * 8;
+  uint4 val[NL];
+  bool ok[NL];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t rg = r0 + 32 * i + lr;
+  for (int i = 0; i < NL; ++i) {
+    const int64_t rg = r0 + ROUND * i + lr;
     ok[i] = rg < p.R && c0 + ch < p.C;
     val[i] = *reinterpret_cast<const uint4*>(in + (ok[i] ? rg * p.in_row_stride + c0 + ch : 0));
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint4*>(tile + q4_at(32 * i + lr, ch)) = ok[i] ? val[i] : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < NL; ++i)
+    *reinterpret_cast<uint4*>(tile + q4_at(ROUND * i + lr, ch)) = ok[i] ? val[i] : make_uint4(0, 0, 0, 0);
   lds_barrier();
   if (p.row_codes) {   // uniform
-    const int rl = tid >> 2, cl = (tid & 3) * 32;
-    const int64_t r = r0 + rl;
-    if (r < p.R && c0 + cl < p.C) {
-      uint32_t w[16], out[4];
-      const uint4* t4 = reinterpret_cast<const uint4*>(tile + q4_at(rl, cl));
+    constexpr int PER = Q4_COLS / 32;   // blocks of a tile row
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 q = t4[i];
-        w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+    for (int i = tid; i < Q4_ROWS * PER; i += Q4_THREADS) {
+      const int rl = i / PER, cl = (i % PER) * 32;
+      const int64_t r = r0 + rl;
+      if (r < p.R && c0 + cl < p.C) {
+        uint32_t w[16], out[4];
+        const uint4* t4 = reinterpret_cast<const uint4*>(tile + q4_at(rl, cl));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 q = t4[j];
+          w[4 * j] = q.x; w[4 * j + 1] = q.y; w[4 * j + 2] = q.z; w[4 * j + 3] = q.w;
+        }
+        const uint32_t s = quant32_fp4(w, out);
+        const int64_t blk = ((int64_t(b) * p.R + r) * p.C + c0 + cl) / 32;
+        reinterpret_cast<uint4*>(p.row_codes)[blk] = make_uint4(out[0], out[1], out[2], out[3]);
+        p.row_scales[blk] = uint8_t(s);
       }
-      const uint32_t s = quant32_fp4(w, out);
-      const int64_t blk = ((int64_t(b) * p.R + r) * p.C + c0 + cl) / 32;
-      reinterpret_cast<uint4*>(p.row_codes)[blk] = make_uint4(out[0], out[1], out[2], out[3]);
-      p.row_scales[blk] = uint8_t(s);
     }
   }
   if (p.col_codes) {
-    const int cc = tid >> 2, rb = (tid & 3) * 32;
-    const int col = c0 + cc;
-    const int64_t row = r0 + rb;
-    if (col < p.C && row < p.Rp) {
-      uint32_t w[16], out[4];
+    constexpr int PER = Q4_ROWS / 32;   // blocks of a tile column
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        w[i] = uint32_t(tile[q4_at(rb + 2 * i, cc)]) | (uint32_t(tile[q4_at(rb + 2 * i + 1, cc)]) << 16);
-      const uint32_t s = quant32_fp4(w, out);
-      const int64_t blk = ((int64_t(b) * p.C + col) * p.Rp + row) / 32;
-      reinterpret_cast<uint4*>(p.col_codes)[blk] = make_uint4(out[0], out[1], out[2], out[3]);
-      p.col_scales[blk] = uint8_t(s);
+    for (int i = tid; i < Q4_COLS * PER; i += Q4_THREADS) {
+      const int cc = i / PER, rb = (i % PER) * 32;
+      const int col = c0 + cc;
+      const int64_t row = r0 + rb;
+      if (col < p.C && row < p.Rp) {
+        uint32_t w[16], out[4];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          w[j] = uint32_t(tile[q4_at(rb + 2 * j, cc)]) | (uint32_t(tile[q4_at(rb + 2 * j + 1, cc)]) << 16);
+        const uint32_t s = quant32_fp4(w, out);
+        const int64_t blk = ((int64_t(b) * p.C + col) * p.Rp + row) / 32;
+        reinterpret_cast<uint4*>(p.col_codes)[blk] = make_uint4(out[0], out[1], out[2], out[3]);
+        p.col_scales[blk] = uint8_t(s);
+      }
     }
   }
 }
@@ -118,19 +131,31 @@ mge_status launch_quant4(const Quant4Params& p, hipStream_t s) {
   return hip_check("quant4_kernel");
 }
 
-// Dequantize: one thread per block of 32, 16 code bytes in, 32 values out.  A scale byte of
-// 255 is the format's NaN and gives NaN.
+// Dequantize: a lane takes 4 code bytes (8 values), so that a wave's stores are whole lines
+// (a lane with a whole block of 32 is 1.8 times slower).  HBM-bound: 17/32 B read, 2 or 4
+// written per value; [28672][4096] to bf16 55 us (5.4 TB/s, the codes partly from cache).
+// A scale byte of 255 is the format's NaN and gives NaN.
+constexpr int DQ_THREADS = 256;
+constexpr int DQ_PER = 4;   // dwords of codes a thread takes, DQ_THREADS apart
+
 template <bool F32>
-__global__ __launch_bounds__(256) void dequant4_kernel(int64_t blocks, const uint4* __restrict__ codes,
-                                                       const uint8_t* __restrict__ scales, void* __restrict__ out) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= blocks) return;
-  const uint4 q = codes[i];
-  const uint32_t c[4] = {q.x, q.y, q.z, q.w};
-  const uint32_t s = scales[i];
-  const float scale = s == 255 ? __uint_as_float(0x7fc00000u) : e8m0_value(s);
+__global__ __launch_bounds__(DQ_THREADS) void dequant4_kernel(int64_t dwords, const uint32_t* __restrict__ codes,
+                                                              const uint8_t* __restrict__ scales, void* __restrict__ out) {
+  const int64_t base = int64_t(blockIdx.x) * (DQ_THREADS * DQ_PER) + threadIdx.x;
+  uint32_t c[DQ_PER], s[DQ_PER];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < DQ_PER; ++j) {
+    const int64_t i = base + j * DQ_THREADS;
+    if (i < dwords) {
+      c[j] = codes[i];
+      s[j] = scales[i >> 2];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < DQ_PER; ++j) {
+    const int64_t i = base + j * DQ_THREADS;
+    if (i >= dwords) return;
+    const float scale = s[j] == 255 ? __uint_as_float(0x7fc00000u) : e8m0_value(s[j]);
     float v[8];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
@@ -141,23 +166,23 @@ __global__ __launch_bounds__(256) void dequant4_kernel(int64_t blocks, const uin
       v[n] = ((x & 8u) ? -mag : mag) * scale;
     }
     if constexpr (F32) {
-      float4* o = static_cast<float4*>(out) + i * 8 + j * 2;
+      float4* o = static_cast<float4*>(out) + i * 2;
       o[0] = make_float4(v[0], v[1], v[2], v[3]);
       o[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-      static_cast<uint4*>(out)[i * 4 + j] = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+      static_cast<uint4*>(out)[i] = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
     }
   }
 }
 
 mge_status launch_dequant4(int64_t blocks, const uint8_t* codes, const uint8_t* scales, int dtype, void* out, hipStream_t s) {
   if (blocks <= 0) return MGE_OK;
-  const dim3 grid(unsigned((blocks + 255) / 256));
+  const int64_t dwords = blocks * 4;
+  const dim3 grid(unsigned((dwords + DQ_THREADS * DQ_PER - 1) / (DQ_THREADS * DQ_PER)));
+  const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
   ProfScope prof(s, "dequant_fp4");
-  if (dtype == MGE_DTYPE_F32)
-    hipLaunchKernelGGL(dequant4_kernel<true>, grid, dim3(256), 0, s, blocks, reinterpret_cast<const uint4*>(codes), scales, out);
-  else
-    hipLaunchKernelGGL(dequant4_kernel<false>, grid, dim3(256), 0, s, blocks, reinterpret_cast<const uint4*>(codes), scales, out);
+  if (dtype == MGE_DTYPE_F32) hipLaunchKernelGGL(dequant4_kernel<true>, grid, dim3(DQ_THREADS), 0, s, dwords, c, scales, out);
+  else hipLaunchKernelGGL(dequant4_kernel<false>, grid, dim3(DQ_THREADS), 0, s, dwords, c, scales, out);
   return hip_check("dequant4_kernel");
 }
 

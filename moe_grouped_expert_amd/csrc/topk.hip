@@ -522,7 +522,7 @@ __global__ __launch_bounds__(TK_THREADS) void route_topk2_kernel(TopkParams p) {
 template <int V, typename LT>
 __global__ __launch_bounds__(TK_THREADS) void route_topk_bwd_kernel(TopkBwdParams p) {
   constexpr int LD = TK_ROW * V;
-  __shared__ float so[TK_TOKENS * LD];
+  __shared__ __attribute__((aligned(16))) float so[TK_TOKENS * LD];
   const int tid = threadIdx.x;
   const int rl = tid & (TK_ROW - 1);
   const int tok = tid / TK_ROW;
@@ -601,15 +601,32 @@ __global__ __launch_bounds__(TK_THREADS) void route_topk_bwd_kernel(TopkBwdParam
   lds_barrier();
   if (first) so[tok * LD + idx] += total;
   lds_barrier();
-  // the rows of the workgroup are contiguous in the output
+  // the rows of the workgroup are contiguous in the output: 16 bytes a thread where rows are
+  // whole numbers of them
   const int64_t t0 = int64_t(blockIdx.x) * TK_TOKENS;
   const int rows = int(p.T - t0 < TK_TOKENS ? p.T - t0 : TK_TOKENS);
   LT* out = static_cast<LT*>(p.d_logits) + t0 * E;
-  for (int i = tid; i < rows * E; i += TK_THREADS) {
-    const int r = i / E;
-    const float x = so[r * LD + (i - r * E)];
-    if constexpr (sizeof(LT) == 4) out[i] = x;
-    else out[i] = f32_to_bf16(x);
+  constexpr int PER = 16 / sizeof(LT);
+  if (p.ovec) {   // uniform
+    const int n = E / PER;
+    for (int i = tid; i < rows * n; i += TK_THREADS) {
+      const int r = i / n;
+      const float* f = so + r * LD + (i - r * n) * PER;
+      uint4 q;
+      if constexpr (sizeof(LT) == 4) {
+        q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+      } else {
+        q = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
+      }
+      reinterpret_cast<uint4*>(out)[i] = q;
+    }
+  } else {
+    for (int i = tid; i < rows * E; i += TK_THREADS) {
+      const int r = i / E;
+      const float x = so[r * LD + (i - r * E)];
+      if constexpr (sizeof(LT) == 4) out[i] = x;
+      else out[i] = f32_to_bf16(x);
+    }
   }
 }
 

@@ -98,8 +98,9 @@ def test_grouped_gemm4(kw, word):
 
 
 def test_workspaces():
-    assert gemm(workspace=None)[0] == b.MGE_ERR_WORKSPACE
-    r, err = gemm(workspace_bytes=8)
+    assert gemm(workspace=None, rows=800)[0] == b.MGE_ERR_WORKSPACE
+    assert gemm(workspace=None, rows=0)[0] == b.MGE_OK
+    r, err = gemm(workspace_bytes=8, rows=800)
     assert r == b.MGE_ERR_WORKSPACE and "workspace needs" in err
     assert b.lib().mge_gemm4_workspace_bytes(None) == 0
     assert b.lib().mge_fwd_mxfp4_workspace_bytes(None) == 0

@@ -1070,11 +1070,15 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* a, void* stream) {
   return launch_dequant4(a->rows * (a->C / 32), a->codes, a->scales, a->out_dtype, a->out, static_cast<hipStream_t>(stream));
 }
 
-// Rows per expert on average past which the products take the tile kernels instead of the
-// weight-streaming ones (which read the weights again for every 16 or 32 rows).  Down product,
-// 8 experts of [4096][14336]: 8 rows each 57 us streamed, 68 tiled; 64 rows each 174, 76.  One
-// [8192][8192]: 16 rows 20 us streamed, 26 tiled; 32 rows 33, 26.
-constexpr int kTile4Rows = 18;
+// The weight-streaming kernels read an expert's weights again for every 32 rows, from L2, where
+// the tile kernels read them once but need their scales packed and a pointer table (two more
+// launches, about 8 us).  Streaming is kept while the rows past 16 an expert, times an expert's
+// bytes, stay below kStreamBytes, at no more than kStreamRows an expert (a pass takes a workgroup
+// about 2 us however small the weights are).  Times of a whole call, streamed and tiled:
+// [2048][2048], 64 rows 11 and 19 us, 128 rows 17 and 19, 256 rows 31 and 17; [8192][4096], 32 rows 12
+// and 19 us, 64 rows 18 and 19; 8 experts of [4096][14336], 8 rows each 57 and 68 us, 64 rows each 174 and 76.
+constexpr int64_t kStreamBytes = int64_t(768) << 20;
+constexpr int kStreamRows = 144;
 // Tiles of 64 rows or of 256: a 256 x 256 tile takes its CU as long as one and a half rounds of
 // 64 x 128 tiles take the chip, whatever part of it is padding.  Measured (64-row, 256-row):
 // [8192][8192], 512 rows 55, 86 us; 1024 rows 113, 91; 8 x [4096][14336] in 4 bits, 1024 rows
@@ -1091,7 +1095,7 @@ static bool small_tiles4(int E, int N, int64_t total) {
 // enough rows, and every operand within their 32-bit offsets.
 static bool tile4(int E, int N, int K, int64_t rows, int64_t total) {
   const int64_t lim = int64_t(1) << 31;
-  return total > int64_t(kTile4Rows) * E && int64_t(E) * scale_pack_dwords(N, K / 32) * 4 < lim &&
+  return ((total - 16 * int64_t(E)) * (int64_t(N) * K / 2) > kStreamBytes || total > int64_t(kStreamRows) * E) && int64_t(E) * scale_pack_dwords(N, K / 32) * 4 < lim &&
          scale_pack_dwords(int(rows), K / 32) * 4 < lim && int64_t(N) * 4 * 256 < lim;
 }
 static size_t tile4_ws(int E, int N, int K, int64_t rows) {

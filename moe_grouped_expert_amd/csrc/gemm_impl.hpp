@@ -235,10 +235,17 @@ constexpr int G_DYN_LDS = G_SCALE_BASE + G_STAGES * G_SCALE_STAGE;
 // this launch runs each of them as four 256 x 64 work items instead (the main launch leaves
 // them out; both take the same decision from the same tile table).  Every output element is
 // still accumulated by one wave over K in the same order: the results are bit-identical.
-template <int FMT, int EPI, int MODE, int OUT, int QT = 0, int SM = 0>
+// SM = 64, 128 or 256: tiles of 64 rows x SM columns (a wave 32 x SM/2), for groups of some
+// tens of rows, whose products read the weights faster than 256-row tiles would compute on
+// padding; with their smaller stages two workgroups share a CU.
+// NST: LDS stages.  A stage that is computed on for less than the latency of its refill bounds
+// the loop by that latency, so the 64-row tiles take more stages where few of them share a CU
+// (the quarter-width tail is bound by its operand bytes from L2: a third stage changed nothing).
+template <int FMT, int EPI, int MODE, int OUT, int QT = 0, int SM = 0, int NST = G_STAGES>
 __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   constexpr bool MX = FMT != FMT_BF16;
   constexpr bool A4 = FMT == FMT_MXFP4, B4 = FMT == FMT_MXFP8_MXFP4 || FMT == FMT_MXFP4;
+  static_assert(NST >= 2 && NST <= 4, "the prologue issues 2 to 4 slices");
   static_assert(!B4 || MODE == RAGGED_M, "MXFP4 operands are weights: ragged M only");
   // bytes of a B row in a slice (an 8-bit A's 128 elements are 64 bytes of a 4-bit B), B rows
   // of one 1 KB DMA instruction
@@ -250,8 +257,9 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   constexpr int BM = G_WAVES_M * WMB * 32;         // rows of a tile
   constexpr int TN = SM ? SM : G_BN;               // columns of a tile
   constexpr int BW = QT ? G_BN / 4 : TN;           // output columns (B rows) of a work item
-  constexpr int STAGE = SM ? BM * G_BKB + BW * BROWB : G_STAGE_BYTES;   // operand bytes of an LDS stage
-  constexpr int SCALES = G_STAGES * STAGE;         // the scales behind the stages
+  // operand bytes of one of the NST LDS stages; the scales are behind the stages
+  constexpr int STAGE = SM || NST != G_STAGES ? BM * G_BKB + BW * BROWB : G_STAGE_BYTES;
+  constexpr int SCALES = NST * STAGE;
   constexpr int NA = BM / 32;                      // A's DMA instructions per wave and slice
   constexpr int WNB = BW / (32 * G_WAVES_N);       // 32-column MFMA blocks per wave
   constexpr int NOPS = NA + BW / (4 * BROWS_DMA);  // operand DMA instructions per wave and slice
@@ -648,15 +656,19 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       lds_barrier();   // no wave still reads a stage
       issue_slice(cur, 0, 0);
       issue_slice(cur, 1, 1);
-      vm_barrier<DMA_PER_SLICE>();   // slice 0 resident, slice 1 may be on its way
+      if constexpr (NST > 2) issue_slice(cur, 2, 2);
+      if constexpr (NST > 3) issue_slice(cur, 3, 3);
+      vm_barrier<(NST - 1) * DMA_PER_SLICE>();   // slice 0 resident, the others may be on their way
     } else if (cur_issued == 1) {
       issue_slice(cur, 1, 1);
-      vm_barrier<DMA_PER_SLICE>();   // slice 0 and the epilogue's stores done
+      if constexpr (NST > 2) issue_slice(cur, 2, 2);
+      if constexpr (NST > 3) issue_slice(cur, 3, 3);
+      vm_barrier<(NST - 1) * DMA_PER_SLICE>();   // slice 0 and the epilogue's stores done
     } else {
       vm_barrier<0>();               // prefetched slices 0, 1 and the epilogue's stores
     }
     for (int kt = 0; kt < nkt; ++kt) {
-      const int stage = kt & (G_STAGES - 1);
+      const int stage = NST == 2 || NST == 4 ? kt & (NST - 1) : kt % NST;
       const uint8_t* sA = smem + stage * STAGE;
       const uint8_t* sB = sA + BM * G_BKB;
       constexpr int NG = A4 ? 2 : 1;   // scale groups (128 elements) per slice
@@ -693,10 +705,10 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       bfrag_t bfr[NSTEP][WNB];
 #pragma unroll
       for (int s = 0; s < NSTEP; ++s) read_frags(sA, sB, s, af[s], bfr[s]);
-      const SliceDma nx = prep_slice(cur, kt + G_STAGES, stage);
+      const SliceDma nx = prep_slice(cur, kt + NST, stage);
       mfma_slice(af, bfr, sa, sb, nx);
       __builtin_amdgcn_sched_barrier(0);
-      vm_barrier<DMA_PER_SLICE>();   // slice kt+1 resident (kt+2 still on its way)
+      vm_barrier<(NST - 1) * DMA_PER_SLICE>();   // slice kt+1 resident (the later ones still on their way)
     }
     __builtin_amdgcn_s_waitcnt(0);   // the past-the-end (all-zero) slices have landed
     acc_settle();                    // the last MFMA results are readable
@@ -1127,9 +1139,9 @@ static inline int device_cus() {
   return cus[dev];
 }
 
-// Operand and scale bytes in LDS of the 64-row tiles (SM columns, 4-bit B rows of browb bytes)
-constexpr int gemm_small_lds(int sm, int browb) {
-  return G_STAGES * (64 * G_BKB + sm * browb) + G_STAGES * G_SCALE_STAGE;
+// Bytes in LDS of nst stages of `rows` A rows and `cols` 4-bit B rows of browb bytes, and scales
+constexpr int gemm_stage_lds(int rows, int cols, int browb, int nst) {
+  return nst * (rows * G_BKB + cols * browb + G_SCALE_STAGE);
 }
 // Persistent launch of a 64-row-tile kernel that runs `per_cu` workgroups on a CU
 template <typename Kern>

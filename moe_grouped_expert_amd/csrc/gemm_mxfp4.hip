@@ -20,19 +20,23 @@ MGE_GEMM_TAIL_KERNEL(gemm_store_f32_tail_mxfp8_mxfp4, FMT_MXFP8_MXFP4, OUT_F32)
 MGE_GEMM_TAIL_KERNEL(gemm_store_tail_mxfp4, FMT_MXFP4, OUT_BF16)
 MGE_GEMM_TAIL_KERNEL(gemm_store_f32_tail_mxfp4, FMT_MXFP4, OUT_F32)
 
-// 64-row tiles of SM columns; PER_CU workgroups share a CU
-#define MGE_GEMM_SMALL_KERNEL(name, FMT, EPI, OUT, SM, PER_CU) \
-  __global__ __launch_bounds__(G_THREADS, PER_CU) void name(GemmParams p) { gemm_body<FMT, EPI, RAGGED_M, OUT, 0, SM>(p); }
+// 64-row tiles of SM columns with NST LDS stages; PER_CU workgroups share a CU.  Stages against
+// workgroups at the same LDS: down product of 128 tokens, top-2 of 8 experts [4096][14336], 64
+// columns: 4 stages x 2 workgroups 67 us, 2 x 4 86; one [8192][8192] of 512 rows, 128 columns: 3 x 2
+// 39 us, 2 x 3 51; in 4 bits, 300 rows over 8 experts, 64 columns: 3 x 2 59 us, 2 x 3 69; 512 rows,
+// 128 columns: 2 x 2 70 us, 3 x 1 74.
+#define MGE_GEMM_SMALL_KERNEL(name, FMT, EPI, OUT, SM, PER_CU, NST) \
+  __global__ __launch_bounds__(G_THREADS, PER_CU) void name(GemmParams p) { gemm_body<FMT, EPI, RAGGED_M, OUT, 0, SM, NST>(p); }
 
-MGE_GEMM_SMALL_KERNEL(gemm_gateup_swiglu64_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_SWIGLU, OUT_NONE, 256, 2)
-MGE_GEMM_SMALL_KERNEL(gemm_store64x128_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_BF16, 128, 3)
-MGE_GEMM_SMALL_KERNEL(gemm_store64x128_f32_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_F32, 128, 3)
-MGE_GEMM_SMALL_KERNEL(gemm_store64x64_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_BF16, 64, 4)
-MGE_GEMM_SMALL_KERNEL(gemm_store64x64_f32_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_F32, 64, 4)
-MGE_GEMM_SMALL_KERNEL(gemm_store64x128_mxfp4, FMT_MXFP4, EPI_STORE, OUT_BF16, 128, 2)
-MGE_GEMM_SMALL_KERNEL(gemm_store64x128_f32_mxfp4, FMT_MXFP4, EPI_STORE, OUT_F32, 128, 2)
-MGE_GEMM_SMALL_KERNEL(gemm_store64x64_mxfp4, FMT_MXFP4, EPI_STORE, OUT_BF16, 64, 3)
-MGE_GEMM_SMALL_KERNEL(gemm_store64x64_f32_mxfp4, FMT_MXFP4, EPI_STORE, OUT_F32, 64, 3)
+MGE_GEMM_SMALL_KERNEL(gemm_gateup_swiglu64_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_SWIGLU, OUT_NONE, 256, 2, 2)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x128_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_BF16, 128, 2, 3)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x128_f32_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_F32, 128, 2, 3)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x64_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_BF16, 64, 2, 4)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x64_f32_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_F32, 64, 2, 4)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x128_mxfp4, FMT_MXFP4, EPI_STORE, OUT_BF16, 128, 2, 2)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x128_f32_mxfp4, FMT_MXFP4, EPI_STORE, OUT_F32, 128, 2, 2)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x64_mxfp4, FMT_MXFP4, EPI_STORE, OUT_BF16, 64, 2, 3)
+MGE_GEMM_SMALL_KERNEL(gemm_store64x64_f32_mxfp4, FMT_MXFP4, EPI_STORE, OUT_F32, 64, 2, 3)
 
 #undef MGE_GEMM_SMALL_KERNEL
 #undef MGE_GEMM_TAIL_KERNEL
@@ -58,21 +62,21 @@ mge_status launch_gemm_mxfp4_small(const GemmParams& p0, bool a4, int64_t rows_b
   constexpr int B8 = G_BKB / 2, B4 = G_BKB;
   if (p.role == GEMM_GATEUP) {
     p.tiles_upper = int(mt * ((p.F + 127) / 128));
-    return launch_gemm_small(gemm_gateup_swiglu64_mxfp8_mxfp4, "gemm_gateup_swiglu64_mxfp4", p, 2, gemm_small_lds(256, B8), s);
+    return launch_gemm_small(gemm_gateup_swiglu64_mxfp8_mxfp4, "gemm_gateup_swiglu64_mxfp4", p, 2, gemm_stage_lds(64, 256, B8, 2), s);
   }
   const bool f32 = p.out_dtype == MGE_DTYPE_F32;
   const bool wide = (mt - p.E / 2) * ((p.N + 127) / 128) >= kWideTiles;
   p.tiles_upper = int(mt * (wide ? (p.N + 127) / 128 : (p.N + 63) / 64));
   if (wide) {
     if (a4)
-      return launch_gemm_small(f32 ? gemm_store64x128_f32_mxfp4 : gemm_store64x128_mxfp4, "gemm64_mxfp4", p, 2, gemm_small_lds(128, B4), s);
-    return launch_gemm_small(f32 ? gemm_store64x128_f32_mxfp8_mxfp4 : gemm_store64x128_mxfp8_mxfp4, "gemm64_mxfp8_mxfp4", p, 3,
-                             gemm_small_lds(128, B8), s);
+      return launch_gemm_small(f32 ? gemm_store64x128_f32_mxfp4 : gemm_store64x128_mxfp4, "gemm64_mxfp4", p, 2, gemm_stage_lds(64, 128, B4, 2), s);
+    return launch_gemm_small(f32 ? gemm_store64x128_f32_mxfp8_mxfp4 : gemm_store64x128_mxfp8_mxfp4, "gemm64_mxfp8_mxfp4", p, 2,
+                             gemm_stage_lds(64, 128, B8, 3), s);
   }
   if (a4)
-    return launch_gemm_small(f32 ? gemm_store64x64_f32_mxfp4 : gemm_store64x64_mxfp4, "gemm64_mxfp4", p, 3, gemm_small_lds(64, B4), s);
-  return launch_gemm_small(f32 ? gemm_store64x64_f32_mxfp8_mxfp4 : gemm_store64x64_mxfp8_mxfp4, "gemm64_mxfp8_mxfp4", p, 4,
-                           gemm_small_lds(64, B8), s);
+    return launch_gemm_small(f32 ? gemm_store64x64_f32_mxfp4 : gemm_store64x64_mxfp4, "gemm64_mxfp4", p, 2, gemm_stage_lds(64, 64, B4, 3), s);
+  return launch_gemm_small(f32 ? gemm_store64x64_f32_mxfp8_mxfp4 : gemm_store64x64_mxfp8_mxfp4, "gemm64_mxfp8_mxfp4", p, 2,
+                           gemm_stage_lds(64, 64, B8, 4), s);
 }
 
 }  // namespace mge

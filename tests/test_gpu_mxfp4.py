@@ -199,12 +199,30 @@ def test_gemm_many_rows(m, fmt):
 
 
 @pytest.mark.parametrize("sizes,N,K", [([200], 32, 32), ([129, 64], 96, 96), ([64, 64, 64], 288, 128), ([255, 0, 257], 256, 160),
-                                       ([1, 500], 320, 288), ([256], 512, 256), ([70, 600, 2], 64, 416), ([130], 2080, 1184)])
+                                       ([1, 500], 320, 288), ([256], 512, 256), ([70, 600, 2], 64, 416), ([130], 2080, 1184),
+                                       ([300, 150], 96, 96), ([500, 0, 257], 256, 160), ([400, 90, 200], 288, 128), ([641], 64, 32),
+                                       ([3, 600], 1056, 224)])
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
 def test_gemm_tiles(m, sizes, N, K, fmt):
     """Enough rows for the tile kernels, with K that ends inside a slice and N inside a tile."""
     run_gemm(m, sizes, N, K, fmt, "f32", ints=True)
     run_gemm(m, sizes, N, K, fmt, "bf16", align=32, extra=40, seed=2, split=False)
+
+
+@pytest.mark.parametrize("K", [32, 128, 160, 288, 416])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_gemm_large_tiles(m, fmt, K):
+    """Enough rows and columns for 256-row tiles."""
+    run_gemm(m, [2500, 0, 700], 2080, K, fmt, "bf16", ints=True)
+    run_gemm(m, [2500, 1, 700], 2080, K, fmt, "f32", align=32, extra=7, seed=3)
+
+
+@pytest.mark.parametrize("rows", [17, 33, 48, 100])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_gemm_stream_passes(m, fmt, rows):
+    """Several passes over the weights, one and two token blocks a pass, rows of scales aligned to 16 bytes and not."""
+    run_gemm(m, [rows, 5, 0, 2 * rows], 1024, 512, fmt, "bf16", ints=True)
+    run_gemm(m, [1, rows], 8224, 544, fmt, "f32", seed=4)
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
@@ -264,7 +282,7 @@ def layer(m, T, E, k, H, F, seed, align=32, skew=None):
 
 @pytest.mark.parametrize("T,E,k,H,F,align,skew", [(1, 4, 2, 64, 96, 32, None), (5, 8, 2, 160, 32, 1, None), (40, 3, 1, 128, 288, 32, 1),
                                                   (64, 16, 4, 256, 224, 8, None), (300, 4, 2, 384, 320, 32, None),
-                                                  (1500, 3, 2, 256, 288, 32, 0)])
+                                                  (1500, 3, 2, 256, 288, 32, 0), (2000, 3, 2, 160, 1056, 32, None)])
 def test_mlp(m, T, E, k, H, F, align, skew):
     from tests.gpu_helpers import say
     say("[gpu] mlp4", T, E, k, H, F, align)

@@ -779,12 +779,18 @@ def mxfp4_quantize(w: torch.Tensor, orient: str = "row", out=None):
     [..., R, C/2] (two elements a byte, the even one in the low half) and scales uint8 [..., R, C/32]; the column
     form is that of the transpose, R padded to 32: [..., C, Rp/2] and [..., C, Rp/32].  orient "row", "col" or
     "both".  w: contiguous, or a 2-D matrix with a row stride that is a multiple of 8."""
-    _need(w.dtype == torch.bfloat16 and w.dim() >= 2, "w must be bfloat16 [..., R, C]")
-    _need(orient in ("row", "col", "both"), f"orient must be 'row', 'col' or 'both', not {orient!r}")
-    strided = w.dim() == 2 and (w.shape[1] <= 1 or w.stride(1) == 1) and w.stride(0) >= w.shape[1]
-    _need(w.is_contiguous() or strided, "w must be contiguous, or a matrix of contiguous rows")
-    R, Cc = w.shape[-2], w.shape[-1]
-    lead = tuple(w.shape[:-2])
+    shape = w.shape
+    if w.dtype != torch.bfloat16 or len(shape) < 2:
+        raise ValueError("w must be bfloat16 [..., R, C]")
+    if orient not in ("row", "col", "both"):
+        raise ValueError(f"orient must be 'row', 'col' or 'both', not {orient!r}")
+    R, Cc = shape[-2], shape[-1]
+    row_stride = Cc
+    if not w.is_contiguous():
+        row_stride = w.stride(0)
+        if len(shape) != 2 or (Cc > 1 and w.stride(1) != 1) or row_stride < Cc:
+            raise ValueError("w must be contiguous, or a matrix of contiguous rows")
+    lead = tuple(shape[:-2])
     batch = 1
     for d in lead:
         batch *= d
@@ -792,12 +798,13 @@ def mxfp4_quantize(w: torch.Tensor, orient: str = "row", out=None):
     want_row, want_col = orient != "col", orient != "row"
     dev = w.device
     _on(dev)
+    rc = rs = cc = cs = None
     if out is None:
         u8 = torch.uint8
-        rc = w.new_empty(lead + (R, Cc // 2), dtype=u8) if want_row else None
-        rs = w.new_empty(lead + (R, Cc // 32), dtype=u8) if want_row else None
-        cc = w.new_empty(lead + (Cc, Rp // 2), dtype=u8) if want_col else None
-        cs = w.new_empty(lead + (Cc, Rp // 32), dtype=u8) if want_col else None
+        if want_row:
+            rc, rs = w.new_empty(lead + (R, Cc // 2), dtype=u8), w.new_empty(lead + (R, Cc // 32), dtype=u8)
+        if want_col:
+            cc, cs = w.new_empty(lead + (Cc, Rp // 2), dtype=u8), w.new_empty(lead + (Cc, Rp // 32), dtype=u8)
     else:
         rc, rs, cc, cs = out
         _on(dev, rc, rs, cc, cs)
@@ -805,8 +812,7 @@ def mxfp4_quantize(w: torch.Tensor, orient: str = "row", out=None):
                            (cs, Cc * (Rp // 32), want_col)):
             _need(not used or (t is not None and _is_u8(t) and t.numel() == batch * n),
                   "out must be contiguous uint8 tensors of the outputs' sizes")
-    row_stride = Cc if w.is_contiguous() else w.stride(0)
-    a = Quant4Args(C.sizeof(Quant4Args), batch, R, Cc, R * row_stride, row_stride, _ptr(w),
+    a = Quant4Args(C.sizeof(Quant4Args), batch, R, Cc, R * row_stride, row_stride, w.data_ptr(),
                    (ORIENT_ROW if want_row else 0) | (ORIENT_COL if want_col else 0), _ptr(rc) if want_row else None,
                    _ptr(rs) if want_row else None, _ptr(cc) if want_col else None, _ptr(cs) if want_col else None)
     _call("mxfp4_quantize", a, dev)
@@ -816,21 +822,22 @@ def mxfp4_quantize(w: torch.Tensor, orient: str = "row", out=None):
 def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype: str = "bf16",
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Values [..., C] (bf16 or f32) of MXFP4 codes [..., C/2] and scales [..., C/32]."""
-    _need(out_dtype in DTYPE, f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
-    _need(codes.dim() >= 1 and _is_u8(codes) and _is_u8(scales), "codes and scales must be contiguous uint8")
-    Cc = codes.shape[-1] * 2
-    _need(Cc % 32 == 0 and tuple(scales.shape) == tuple(codes.shape[:-1]) + (Cc // 32,),
-          "codes must be [..., C/2] and scales [..., C/32], C a multiple of 32")
+    if out_dtype not in DTYPE:
+        raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
+    if codes.dim() < 1 or not _is_u8(codes) or not _is_u8(scales):
+        raise ValueError("codes and scales must be contiguous uint8")
+    lead, Cc = tuple(codes.shape[:-1]), codes.shape[-1] * 2
+    if Cc % 32 or scales.shape != lead + (Cc // 32,):
+        raise ValueError("codes must be [..., C/2] and scales [..., C/32], C a multiple of 32")
     dev = codes.device
     dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
-    shape = tuple(codes.shape[:-1]) + (Cc,)
     _on(dev, scales, out)
     if out is None:
-        out = codes.new_empty(shape, dtype=dt)
-    else:
-        _need(tuple(out.shape) == shape and out.dtype == dt and out.is_contiguous(), "out has another shape or dtype")
+        out = codes.new_empty(lead + (Cc,), dtype=dt)
+    elif out.shape != lead + (Cc,) or out.dtype != dt or not out.is_contiguous():
+        raise ValueError("out has another shape or dtype")
     rows = codes.numel() // max(Cc // 2, 1)
-    a = Dequant4Args(C.sizeof(Dequant4Args), rows, Cc, DTYPE[out_dtype], _ptr(codes), _ptr(scales), _ptr(out))
+    a = Dequant4Args(C.sizeof(Dequant4Args), rows, Cc, DTYPE[out_dtype], codes.data_ptr(), scales.data_ptr(), out.data_ptr())
     _call("mxfp4_dequantize", a, dev)
     return out
 
@@ -838,14 +845,13 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype: str =
 def _expert_ptrs(w, E: int, rows: int, cols: int, dev, what: str):
     """Host array of the E device pointers of [rows][cols] uint8 matrices: one stacked tensor or a sequence."""
     if isinstance(w, torch.Tensor):
-        _need(_is_u8(w) and tuple(w.shape) == (E, rows, cols), f"{what} must be contiguous uint8 [{E}, {rows}, {cols}]")
-        _on(dev, w)
+        if w.shape != (E, rows, cols) or not _is_u8(w) or w.device != dev:
+            raise ValueError(f"{what} must be contiguous uint8 [{E}, {rows}, {cols}] on {dev}")
         p, n = w.data_ptr(), rows * cols
-        return (vp * E)(*[p + e * n for e in range(E)])
+        return (vp * E)(*range(p, p + E * n, n)) if E > 1 and n else (vp * E)(*[p] * E)
     ts = list(w)
-    _need(len(ts) == E and all(_is_u8(t) and tuple(t.shape) == (rows, cols) for t in ts),
-          f"{what} must be {E} contiguous uint8 matrices [{rows}, {cols}]")
-    _on(dev, *ts)
+    if len(ts) != E or not all(t.shape == (rows, cols) and _is_u8(t) and t.device == dev for t in ts):
+        raise ValueError(f"{what} must be {E} contiguous uint8 matrices [{rows}, {cols}] on {dev}")
     return _ptr_array(ts)
 
 
@@ -859,34 +865,38 @@ def mxfp4_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, w, w_scale, split
     group_offsets int32 [E] or [E+1]: the groups' row counts and first rows (absent with one expert: all rows).
     total_rows: rows in all groups at most, where the caller knows fewer than `rows` (T * k).  Rows outside the
     groups are left as they were.  For the input gradient pass the column form of the weight."""
-    _need(out_dtype in DTYPE, f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
-    _need(a.dim() == 2 and a_scale.dim() == 2 and _is_u8(a) and _is_u8(a_scale) and a.shape[0] == a_scale.shape[0],
-          "a and a_scale must be contiguous uint8 [rows, ...]")
-    rows, K = a.shape[0], a_scale.shape[1] * 32
-    _need(K > 0 and a.shape[1] in (K, K // 2), "a must be [rows, K] (MXFP8) or [rows, K/2] (MXFP4) with a_scale [rows, K/32]")
-    fmt = FORMAT["mxfp8" if a.shape[1] == K else "mxfp4"]
+    if out_dtype not in DTYPE:
+        raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
+    if a.dim() != 2 or a_scale.dim() != 2 or not _is_u8(a) or not _is_u8(a_scale):
+        raise ValueError("a and a_scale must be contiguous uint8 [rows, ...]")
+    rows, ka = a.shape
+    K = a_scale.shape[1] * 32
+    if a_scale.shape[0] != rows or K == 0 or (ka != K and ka != K // 2):
+        raise ValueError("a must be [rows, K] (MXFP8) or [rows, K/2] (MXFP4) with a_scale [rows, K/32]")
     E = len(w)
     stacked = isinstance(w, torch.Tensor)
-    _need(E >= 1 and len(w_scale) == E and (w.dim() == 3 if stacked else w[0].dim() == 2),
-          "w must be [E, N, K/2] with w_scale [E, N, K/32]")
+    if E < 1 or len(w_scale) != E or (w.dim() != 3 if stacked else w[0].dim() != 2):
+        raise ValueError("w must be [E, N, K/2] with w_scale [E, N, K/32]")
     N = w.shape[1] if stacked else w[0].shape[0]
     dev = a.device
     dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
     _on(dev, a_scale, out, split_sizes, group_offsets, workspace)
     if out is None:
         out = a.new_empty((rows, N), dtype=dt)
-    else:
-        _need(tuple(out.shape) == (rows, N) and out.dtype == dt and out.is_contiguous(), "out has another shape or dtype")
+    elif out.shape != (rows, N) or out.dtype != dt or not out.is_contiguous():
+        raise ValueError("out has another shape or dtype")
     for t in (split_sizes, group_offsets):
-        _need(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= E),
-              "split_sizes and group_offsets must be contiguous int32 with an entry for each expert")
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < E):
+            raise ValueError("split_sizes and group_offsets must be contiguous int32 with an entry for each expert")
     wp = _expert_ptrs(w, E, N, K // 2, dev, "w")
     wsp = _expert_ptrs(w_scale, E, N, K // 32, dev, "w_scale")
-    g = Gemm4Args(C.sizeof(Gemm4Args), fmt, E, N, K, rows, total_rows or 0, _ptr(split_sizes), _ptr(group_offsets),
-                  _ptr(a), _ptr(a_scale), C.addressof(wp), C.addressof(wsp), DTYPE[out_dtype], _ptr(out))
+    g = Gemm4Args(C.sizeof(Gemm4Args), FORMAT["mxfp8"] if ka == K else FORMAT["mxfp4"], E, N, K, rows, total_rows or 0,
+                  _ptr(split_sizes), _ptr(group_offsets), a.data_ptr(), a_scale.data_ptr(), C.addressof(wp),
+                  C.addressof(wsp), DTYPE[out_dtype], out.data_ptr())
     if workspace is None:
         need = lib().mge_gemm4_workspace_bytes(C.byref(g))
-        workspace = a.new_empty(need) if need else None
+        if need:
+            workspace = a.new_empty(need)
     if workspace is not None:
         g.workspace, g.workspace_bytes = workspace.data_ptr(), workspace.numel()
     _call("mxfp4_grouped_gemm", g, dev)

@@ -103,6 +103,7 @@ struct TopkParams {
   bool vec;                 // rows of logits may be read 16 bytes at a time
   bool bvec;                // and bias
   int lanes;                // lanes of a group (set by the launcher)
+  bool full;                // every lane has as many experts as it can hold (set by the launcher)
 };
 mge_status launch_topk(const TopkParams& p, int dtype, hipStream_t s);
 struct TopkBwdParams {

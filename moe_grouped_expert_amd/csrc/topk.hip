@@ -145,7 +145,7 @@ __device__ __forceinline__ void load_logits(const LT* row, int e0, int end, bool
     }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) l[v] = l[v] == l[v] ? l[v] : -INFINITY;
+  for (int v = 0; v < V; ++v) l[v] = fmaxf(l[v], -INFINITY);   // (the maximum of a NaN and a number is the number)
 }
 
 // Differences to the largest logit that stay defined when both are infinite
@@ -169,10 +169,14 @@ __device__ __forceinline__ int take_best(uint64_t* key, int e0) {
   return int(at);
 }
 
+// min and max of numbers as one instruction (fminf and fmaxf first canonicalize what they
+// cannot see to be the result of arithmetic)
+__device__ __forceinline__ float max_num(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+__device__ __forceinline__ float min_num(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -INFINITY); }
 // the two largest so far, a >= b
 __device__ __forceinline__ void two_best(float x, float& a, float& b) {
   b = __builtin_amdgcn_fmed3f(a, b, x);
-  a = fmaxf(a, x);
+  a = max_num(a, x);
 }
 __device__ __forceinline__ void two_best(double x, double& a, double& b) {
   b = x > a ? a : (x > b ? x : b);
@@ -372,24 +376,29 @@ __global__ __launch_bounds__(TK_THREADS) void route_topk2_kernel(TopkParams p) {
   }
 
   // 24-bit steps below the largest key.  Masked experts: kMasked, in index order; keys under
-  // -2^100 (masks by the type's lowest value) are left out of the span and share kLow.
-  constexpr uint32_t kSteps = 0xfffff0u, kLow = 0xfffff8u, kMasked = 0xfffffcu, kGone = 0xffffffffu;
+  // -2^100 (masks by the type's lowest value) are left out of the span and share its last step.
+  constexpr uint32_t kSteps = 0xfffff0u, kMasked = 0xfffffcu, kGone = 0xffffffffu;
   float hi = x[0], lo = INFINITY;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    hi = fmaxf(hi, x[v]);
-    lo = fminf(lo, x[v] > -0x1p100f ? x[v] : INFINITY);
+    hi = max_num(hi, x[v]);
+    lo = min_num(lo, x[v] > -0x1p100f ? x[v] : INFINITY);
   }
   hi = row_reduce<ROW>(hi, MaxOp());
   lo = row_reduce<ROW>(lo, MinOp());
-  const float scale = hi > lo ? float(kSteps) / (hi - lo) : 0.f;
+  const float scale = hi > lo ? float(kSteps) / (hi - lo) : 1.f;
   uint32_t key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     // (where hi or the scale is not finite, many steps are equal, and checked below; NaN: 0)
     uint32_t q = uint32_t(fminf(fmaxf((hi - x[v]) * scale, 0.f), float(kSteps)));
-    q = x[v] > -0x1p100f ? q : (x[v] == -INFINITY ? kMasked : kLow);
-    key[v] = e0 + v < end ? (q << 8) | uint32_t(e0 + v) : kGone;
+    q = x[v] == -INFINITY ? kMasked : q;
+    key[v] = (q << 8) | uint32_t(e0 + v);
+  }
+  if (!p.full) {   // uniform: some lanes have fewer than V experts
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (e0 + v >= end) key[v] = kGone;
   }
   // Bound on how far the difference of two fp32 keys is from the formula's.  u = 2^-24.
   // Sigmoid: the argument's rounding moves s by |l| s (1 - s) 1.5 u < 0.4 u, exp, add and
@@ -403,16 +412,20 @@ __global__ __launch_bounds__(TK_THREADS) void route_topk2_kernel(TopkParams p) {
     const float ahead = keep_groups<ROW, V, GROUPS>(by, key, kGone, p, e0, rl, p.lanes, walk);
     if constexpr (BY_SCORE) again = !(ahead > 2.f * (p.bias ? eps : base));
   }
-  // k + 2 rounds; lane r of the row keeps round r's
+  // k + 1 rounds; lane r of the row keeps round r's
   uint32_t from = 0, slot = kGone;
-#pragma unroll 1
-  for (int r = 0; r < p.k + 2; ++r) {
+  auto round = [&]() {
     uint32_t d = key[0] - from;
 #pragma unroll
     for (int v = 1; v < V; ++v) d = min(d, key[v] - from);
     const uint32_t got = row_reduce<ROW>(d, MinOp()) + from;
-    if (rl == r) slot = got;
     from = got == kGone ? got : got + 1;
+    return got;
+  };
+#pragma unroll 1
+  for (int r = 0; r <= p.k; ++r) {
+    const uint32_t got = round();
+    if (rl == r) slot = got;
   }
   int mine = int(slot & 255u);
   {
@@ -427,7 +440,7 @@ __global__ __launch_bounds__(TK_THREADS) void route_topk2_kernel(TopkParams p) {
         if constexpr (sizeof(LT) == 4) return float(row[e]);
         else return bf16_to_f32(row[e]);
       };
-      const uint32_t last = __shfl(step, p.k - 1, ROW), out = __shfl(step, p.k + 1, ROW);
+      const uint32_t last = __shfl(step, p.k - 1, ROW), out = round() >> 8;   // slots k - 1, k + 1
       const bool masked = step >= kMasked;
       const float lm = masked ? -INFINITY : logit(mine);
       // gap: slot k + 1 is clearly behind slot k - 1, the choice is among slots 0 .. k.  alike:
@@ -653,7 +666,8 @@ static void launch_topk_form(const TopkParams& p, bool by_score, hipStream_t s) 
 }
 
 template <int ROW, int V>
-static void launch_topk_row(const TopkParams& p, int dtype, bool by_score, bool groups, hipStream_t s) {
+static void launch_topk_row(TopkParams p, int dtype, bool by_score, bool groups, hipStream_t s) {
+  p.full = p.E == ROW * V;   // (groups: then every group is whole lanes too)
   auto form = [&](auto lt) {
     using LT = decltype(lt);
     if (!groups) launch_topk_form<ROW, V, LT, TK_NO_GROUPS>(p, by_score, s);

@@ -192,7 +192,7 @@ struct LaneExperts {
 template <int V, int GROUPS>
 __device__ __forceinline__ LaneExperts lane_experts(int E, int G, int rl, int lanes) {
   if constexpr (GROUPS == TK_LANES) {
-    const int g = rl / lanes, gs = E / G;
+    const int g = rl >> (31 - __builtin_clz(lanes)), gs = E / G;   // (lanes is a power of two)
     const int e0 = g * gs + (rl - g * lanes) * V;
     return LaneExperts{e0, g < G ? (g + 1) * gs : 0};
   } else {
@@ -228,7 +228,7 @@ __device__ __forceinline__ KF keep_groups(const KF* by, UK* key, UK gone, const 
       if (lanes >= 32) merge(__shfl_xor(a, 16), __shfl_xor(b, 16));
     }
     const KF mine = p.topn == 2 && b > none ? a + b : a;
-    const int g = rl / lanes;
+    const int g = rl >> (31 - __builtin_clz(lanes));
     int before = 0;
 #pragma unroll 4
     for (int j = 0; j < G; ++j) {
@@ -362,13 +362,29 @@ __global__ __launch_bounds__(TK_THREADS) void route_topk2_kernel(TopkParams p) {
     inv = sum > 0.f ? 1.f / sum : 0.f;
   }
   if constexpr (BY_SCORE) {
-    float b[V];
-    if (p.bias) load_logits<V>(p.bias, e0, end, p.bvec, b);
+    // (the branches are uniform and outside the loops, so that the loops are straight code)
+    if (sigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float sc = sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-l[v])) : by[v] * inv;
-      x[v] = p.bias ? (l[v] == -INFINITY ? -INFINITY : sc + b[v]) : l[v];
-      by[v] = p.bias || l[v] == -INFINITY ? x[v] : sc;
+      for (int v = 0; v < V; ++v) by[v] = __builtin_amdgcn_rcpf(1.f + __expf(-l[v]));
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) by[v] *= inv;
+    }
+    if (p.bias) {
+      float b[V];
+      load_logits<V>(p.bias, e0, end, p.bvec, b);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float k = by[v] + b[v];
+        x[v] = l[v] == -INFINITY ? -INFINITY : k;
+        by[v] = x[v];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[v] = l[v];
+        by[v] = l[v] == -INFINITY ? -INFINITY : by[v];
+      }
     }
   } else {
 #pragma unroll

@@ -301,7 +301,7 @@ mge_status grouped_mlp_fwd(const mge_fwd_args* args, void* stream);
  * with prec = MGE_PREC_MXFP8 (x_perm, h: MXFP8 as there) and w_gate_up / w_down the MXFP4
  * codes ([2F][H/2], [H][F/2]; mxfp4_quantize ROW) with their scales ([2F][H/32],
  * [H][F/32]).  h is quantized to MXFP8 in the gate-up product's epilogue.
- * Workspace: mge_fwd_mxfp4_workspace_bytes(args).
+ * Workspace: mge_fwd_mxfp4_workspace_bytes(args) bytes, 16-byte aligned.
  * Errors: as grouped_mlp_fwd; MGE_ERR_UNSUPPORTED for training (saved_gu, h_col or
  * h_col_scale given) or prec BF16.
  * ---------------------------------------------------------------------------- */
@@ -534,7 +534,8 @@ mge_status moe_router_bwd(const mge_router_bwd_args* args, void* stream);
  * Errors: MGE_ERR_INVALID_ARG for T < 0, E outside [1, 256], k outside [1, min(E, 8)], an
  * unknown score or dtype, num_groups < 1 or not dividing E, topk_groups outside
  * [1, num_groups], k > topk_groups * E / num_groups, group_topn other than 1 or 2, a scale
- * that is not finite, a row stride below E, NULL logits / topk_idx / topk_prob (T > 0).
+ * that is not finite, a row stride below E, NULL logits / topk_idx / topk_prob (T > 0), or
+ * a pointer not aligned to its elements.
  * T = 0 is a no-op.  No workspace.
  * ---------------------------------------------------------------------------- */
 enum { MGE_SCORE_SOFTMAX = 0, MGE_SCORE_SIGMOID = 1 };
@@ -567,7 +568,7 @@ mge_status moe_route_topk(const mge_route_topk_args* args, void* stream);
  * and 0 elsewhere.  Slots with an index outside [0, E) take no part; slots that share an
  * expert add up in slot order.  d_logits has the logits' type, [T][E] contiguous, every
  * element written (sums in fp32, one rounding for bf16).
- * Errors: as moe_route_topk, and MGE_ERR_INVALID_ARG for a NULL d_prob / d_logits (T > 0).
+ * Errors: as moe_route_topk, and MGE_ERR_INVALID_ARG for a NULL or misaligned d_prob / d_logits.
  * ---------------------------------------------------------------------------- */
 typedef struct mge_route_topk_bwd_args {
   uint32_t struct_size;
@@ -645,10 +646,10 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* args, void* stream);
  * The matrix unit adds the 128 products of one instruction with less than fp32's precision
  * when the operands are MXFP8 (about 1e-5 relative to the sum's magnitude); MXFP4 products
  * add exactly to fp32 rounding.
- * Workspace: mge_gemm4_workspace_bytes(args) bytes, which is 0 (NULL allowed) for few rows.
+ * Workspace: mge_gemm4_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for few rows.
  * Errors: MGE_ERR_INVALID_ARG for E outside [1, 256], N or K not a positive multiple of 32,
  * rows < 0 or >= 2^31 / K, an expert's weight of 2^31 bytes or more, unknown formats, NULL or
- * misaligned (16-byte) a / out / weights, NULL scales, one of split_sizes / group_offsets
+ * misaligned (16-byte) a / out / weights / workspace, NULL scales, one of split_sizes / group_offsets
  * without the other or E > 1 without both; MGE_ERR_WORKSPACE.
  * ---------------------------------------------------------------------------- */
 enum { MGE_FORMAT_MXFP8 = 0, MGE_FORMAT_MXFP4 = 1 };

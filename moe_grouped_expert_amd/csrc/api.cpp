@@ -981,6 +981,7 @@ static mge_status check_topk(int T, int E, int k, int score, int dtype, float sc
   MGE_REQUIRE((reinterpret_cast<uintptr_t>(logits) & (elem - 1)) == 0, "logits misaligned");
   return MGE_OK;
 }
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 // rows of logits may be read 16 bytes at a time
 static bool topk_vec(const void* logits, int dtype, int64_t ld) {
   return aligned16(logits) && (ld * (dtype == MGE_DTYPE_F32 ? 4 : 2)) % 16 == 0;
@@ -1002,6 +1003,7 @@ mge_status moe_route_topk(const mge_route_topk_args* a, void* stream) {
   MGE_REQUIRE(a->group_topn == 1 || a->group_topn == 2, "group_topn must be 1 or 2 (got %d)", a->group_topn);
   MGE_REQUIRE(a->T == 0 || a->topk_prob, "topk_prob NULL");
   if (a->T == 0) return MGE_OK;
+  MGE_REQUIRE(aligned4(a->topk_idx) && aligned4(a->topk_prob) && aligned4(a->bias), "topk_idx / topk_prob / bias misaligned");
   TopkParams p{};
   p.T = a->T; p.ld = a->logits_row_stride; p.E = a->E; p.k = a->k;
   p.G = a->num_groups; p.topg = a->topk_groups; p.topn = a->group_topn;
@@ -1021,6 +1023,9 @@ mge_status moe_route_topk_bwd(const mge_route_topk_bwd_args* a, void* stream) {
   if (st != MGE_OK) return st;
   MGE_REQUIRE(a->T == 0 || (a->d_prob && a->d_logits), "d_prob / d_logits NULL");
   if (a->T == 0) return MGE_OK;
+  MGE_REQUIRE(aligned4(a->topk_idx) && aligned4(a->d_prob) &&
+                  (reinterpret_cast<uintptr_t>(a->d_logits) & (a->logits_dtype == MGE_DTYPE_F32 ? 3 : 1)) == 0,
+              "topk_idx / d_prob / d_logits misaligned");
   TopkBwdParams p{};
   p.T = a->T; p.ld = a->logits_row_stride; p.E = a->E; p.k = a->k;
   p.score = a->score; p.renorm = a->renormalize != 0; p.scale = a->scale;
@@ -1095,8 +1100,9 @@ static bool small_tiles4(int E, int N, int64_t total) {
 // enough rows, and every operand within their 32-bit offsets.
 static bool tile4(int E, int N, int K, int64_t rows, int64_t total) {
   const int64_t lim = int64_t(1) << 31;
-  return ((total - 16 * int64_t(E)) * (int64_t(N) * K / 2) > kStreamBytes || total > int64_t(kStreamRows) * E) && int64_t(E) * scale_pack_dwords(N, K / 32) * 4 < lim &&
-         scale_pack_dwords(int(rows), K / 32) * 4 < lim && int64_t(N) * 4 * 256 < lim;
+  const bool many = (total - 16 * int64_t(E)) * (int64_t(N) * K / 2) > kStreamBytes || total > int64_t(kStreamRows) * E;
+  return many && int64_t(E) * scale_pack_dwords(N, K / 32) * 4 < lim && scale_pack_dwords(int(rows), K / 32) * 4 < lim &&
+         int64_t(N) * 4 * 256 < lim;
 }
 static size_t tile4_ws(int E, int N, int K, int64_t rows) {
   return packed_bytes(1, int(rows), K / 32) + packed_bytes(E, N, K / 32);
@@ -1185,6 +1191,7 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
     set_error("MXFP4 product workspace needs %zu bytes (got %zu)", need, a->workspace_bytes);
     return MGE_ERR_WORKSPACE;
   }
+  MGE_REQUIRE(need == 0 || aligned16(a->workspace), "workspace must be 16-byte aligned");
   if (a->rows == 0) return MGE_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
   Carve ws(a->workspace);
@@ -1275,6 +1282,7 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
     set_error("forward workspace needs %zu bytes (got %zu)", need, a->workspace_bytes);
     return MGE_ERR_WORKSPACE;
   }
+  MGE_REQUIRE(aligned16(a->workspace), "workspace must be 16-byte aligned");
   if (a->T == 0) return MGE_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int E = a->E;

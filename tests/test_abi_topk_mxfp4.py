@@ -32,7 +32,8 @@ BWD = dict(T=4, E=16, k=2, score=0, scale=1.0, logits_dtype=0, logits_row_stride
     (dict(scale=float("nan")), "scale"), (dict(logits_row_stride=15), "stride"), (dict(logits=None), "NULL"),
     (dict(logits=P + 2), "misaligned"), (dict(topk_idx=None), "NULL"), (dict(topk_prob=None), "NULL"),
     (dict(num_groups=3), "num_groups"), (dict(num_groups=0), "num_groups"), (dict(topk_groups=0), "topk_groups"),
-    (dict(topk_groups=5), "topk_groups"), (dict(k=5, topk_groups=1), "fit"), (dict(group_topn=3), "group_topn")])
+    (dict(topk_groups=5), "topk_groups"), (dict(k=5, topk_groups=1), "fit"), (dict(group_topn=3), "group_topn"),
+    (dict(bias=P + 2), "misaligned"), (dict(topk_idx=P + 1), "misaligned"), (dict(topk_prob=P + 2), "misaligned")])
 def test_route_topk(kw, word):
     r, err = call("moe_route_topk", b.RouteTopkArgs, **{**TOPK, **kw})
     assert r == b.MGE_ERR_INVALID_ARG and word in err, err
@@ -41,7 +42,8 @@ def test_route_topk(kw, word):
 @pytest.mark.parametrize("kw,word", [
     (dict(T=-1), "T"), (dict(E=300), "E"), (dict(k=9), "k"), (dict(score=-1), "score"), (dict(logits_dtype=7), "dtype"),
     (dict(logits_row_stride=1), "stride"), (dict(d_prob=None), "NULL"), (dict(d_logits=None), "NULL"),
-    (dict(topk_idx=None), "NULL"), (dict(scale=float("nan")), "scale")])
+    (dict(topk_idx=None), "NULL"), (dict(scale=float("nan")), "scale"), (dict(topk_idx=P + 2), "misaligned"),
+    (dict(d_prob=P + 2), "misaligned"), (dict(d_logits=P + 1), "misaligned"), (dict(d_logits=P + 2, logits_dtype=1), "misaligned")])
 def test_route_topk_bwd(kw, word):
     r, err = call("moe_route_topk_bwd", b.RouteTopkBwdArgs, **{**BWD, **kw})
     assert r == b.MGE_ERR_INVALID_ARG and word in err, err
@@ -102,6 +104,10 @@ def test_workspaces():
     assert gemm(workspace=None, rows=0)[0] == b.MGE_OK
     r, err = gemm(workspace_bytes=8, rows=800)
     assert r == b.MGE_ERR_WORKSPACE and "workspace needs" in err
+    r, err = gemm(workspace=P + 8, workspace_bytes=1 << 24, rows=800)
+    assert r == b.MGE_ERR_INVALID_ARG and "aligned" in err
+    r, err = mlp(workspace=P + 8)
+    assert r == b.MGE_ERR_INVALID_ARG and "aligned" in err
     assert b.lib().mge_gemm4_workspace_bytes(None) == 0
     assert b.lib().mge_fwd_mxfp4_workspace_bytes(None) == 0
 

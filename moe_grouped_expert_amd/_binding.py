@@ -907,7 +907,8 @@ def grouped_mlp_fwd_mxfp4(rt: RouteOut, w_gate_up, w_down, w_gate_up_scale, w_do
                           out: Optional[FwdOut] = None) -> FwdOut:
     """grouped_mlp_fwd for serving on MXFP4 weights: w_gate_up [E, 2F, H/2] and w_down [E, H, F/2] are mxfp4_quantize
     row codes with their scales; `rt` is an MXFP8 route (activations and h stay in MXFP8)."""
-    _need(rt.prec == "mxfp8", "the route must be prec='mxfp8' (the activations' format)")
+    _need(rt.prec == "mxfp8" and rt.x_perm is not None and rt.x_perm_scale is not None,
+          "the route must be prec='mxfp8' and carry the permuted activations and their scales")
     _need(y_dtype in DTYPE, f"y_dtype must be 'bf16' or 'f32', not {y_dtype!r}")
     E, H, R = rt.E, rt.H, rt.R
     F = (w_gate_up.shape[1] if isinstance(w_gate_up, torch.Tensor) else w_gate_up[0].shape[0]) // 2

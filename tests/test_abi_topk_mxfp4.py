@@ -153,3 +153,16 @@ def test_python_checks():
                lambda: m.mxfp4_grouped_gemm(f(4, 64), f(4, 2, **u8), f(1, 32, 32, **u8), f(1, 32, 2, **u8))):
         with pytest.raises(ValueError):
             fn()
+
+
+def test_python_route_without_activations():
+    """An MXFP8 route made without x has nothing to multiply."""
+    import moe_grouped_expert_amd as m
+    z = torch.zeros(2, dtype=torch.int32)
+    u8 = dict(dtype=torch.uint8)
+    w, ws = torch.zeros(2, 64, 32, **u8), torch.zeros(2, 64, 2, **u8)
+    for prec, x, xs in (("mxfp8", None, None), ("mxfp8", torch.zeros(32, 64, **u8), None), ("bf16", torch.zeros(32, 64), None)):
+        rt = b.RouteOut(T=4, E=2, k=1, H=64, align=32, prec=prec, R=32, topk_idx=z, topk_prob=z, split_sizes=z, group_offsets=z,
+                        perm_src=z, perm_pos=z, prob_perm=z, x_perm=x, x_perm_scale=xs)
+        with pytest.raises(ValueError, match="route"):
+            m.grouped_mlp_fwd_mxfp4(rt, w, w, ws, ws)

@@ -591,7 +591,8 @@ mge_status moe_route_topk_bwd(const mge_route_topk_bwd_args* args, void* stream)
  * mxfp8_quantize: magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign.  Per block of 32 values
  * e = floor(log2(amax)) - 2 clamped to [-127, 127] (all-zero block: -127), scale byte
  * e + 127, element = v / 2^e to the nearest E2M1 value (ties to even), saturating at 6
- * (OCP MX v1.0).  Two elements share a byte, the even one in the low half.
+ * (OCP MX v1.0).  Two elements share a byte, the even one in the low half.  A block with
+ * an infinity or NaN gets the scale byte 255 (NaN; its codes have no meaning).
  * in, batch, R, C, strides, orient: as mxfp8_quantize.
  * ROW: row_codes [b][R][C/2], row_scales [b][R][C/32].
  * COL: col_codes [b][C][Rp/2], col_scales [b][C][Rp/32], Rp = R rounded up to 32 (zero
@@ -645,7 +646,8 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* args, void* stream);
  * outside the groups are untouched.
  * The matrix unit adds the 128 products of one instruction with less than fp32's precision
  * when the operands are MXFP8 (about 1e-5 relative to the sum's magnitude); MXFP4 products
- * add exactly to fp32 rounding.
+ * add exactly to fp32 rounding.  A NaN (scale byte 255, E4M3 code 0x7f) reaches the elements
+ * of out whose row or column it belongs to, and no others.
  * Workspace: mge_gemm4_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for few rows.
  * Errors: MGE_ERR_INVALID_ARG for E outside [1, 256], N or K not a positive multiple of 32,
  * rows < 0 or >= 2^31 / K, an expert's weight of 2^31 bytes or more, unknown formats, NULL or

@@ -6,6 +6,9 @@
 // the E8M0 range; an element is v / 2^e rounded to the nearest E2M1 value (ties to even),
 // saturating at 6.  Two codes share a byte, the even element in the low half.
 //
+// E2M1 has no code for infinity or NaN: a block that holds one gets the scale byte 255, the
+// format's NaN, so that it shows in what is computed from it.
+//
 // The amax of bf16 values is taken on their bits (magnitudes order as integers), so the
 // scale needs no arithmetic, and v_cvt_scalef32_pk_fp4_bf16 divides by the scale, rounds to
 // nearest even and saturates (equal to the definition over all finite bf16 values at every
@@ -43,7 +46,7 @@ __device__ __forceinline__ uint32_t quant32_fp4(const uint32_t* w, uint32_t* out
     hi = umax(hi, w[i] & 0x7fff0000u);
     lo = umax(lo, w[i] & 0x00007fffu);
   }
-  const int field = int(umax(hi >> 16, lo) >> 7);   // exponent field of the amax
+  const int field = int(umax(hi >> 16, lo) >> 7);   // exponent field of the amax (255: an infinity or NaN in the block)
   const uint32_t s = uint32_t(field < 2 ? 0 : field - 2);
   const float scale = e8m0_value(s);
 #pragma unroll
@@ -55,7 +58,7 @@ __device__ __forceinline__ uint32_t quant32_fp4(const uint32_t* w, uint32_t* out
     v = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(v, __builtin_bit_cast(bf16v2, w[4 * i + 3]), scale, 3);
     out[i] = v;
   }
-  return s;
+  return field == 255 ? 255u : s;
 }
 
 __global__ __launch_bounds__(Q4_THREADS) void quant4_kernel(Quant4Params p) {

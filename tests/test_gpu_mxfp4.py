@@ -111,6 +111,25 @@ def test_quantize_batch_strides_and_empty(m):
     assert m.mxfp4_dequantize(e[0], e[1]).shape == (0, 64)
 
 
+def test_quantize_infinity_and_nan(m):
+    """A block with an infinity or NaN becomes a NaN block in both forms; the others stay as they are."""
+    rng = np.random.default_rng(12)
+    x = rng.standard_normal((64, 96)).astype(np.float32)
+    for (r, c), v in {(3, 5): np.inf, (3, 40): -np.inf, (40, 95): np.nan, (63, 0): 3.3e38}.items():
+        x[r, c] = v
+    t = bf16(x)
+    rc, rs, cc, cs = m.mxfp4_quantize(t, "both")
+    x = f64(t)
+    bad = ~np.isfinite(x)
+    ok = np.where(bad, 0, x)
+    for codes, scales, b, ref in ((rc, rs, bad, mxfp4.quantize_rows(ok)), (cc, cs, bad.T, mxfp4.quantize_cols(ok))):
+        b = b.reshape(b.shape[0], -1, 32).any(-1)
+        np.testing.assert_array_equal(npy(scales), np.where(b, 255, ref[1]))
+        keep = np.repeat(~b, 16, axis=1)
+        np.testing.assert_array_equal(npy(codes)[keep], ref[0][keep])
+        assert np.isnan(f64(m.mxfp4_dequantize(codes, scales))).sum() == 32 * b.sum()
+
+
 # ------------------------------------------------------------------------------ products
 
 def operand(rng, rows, K, fmt, ints):
@@ -229,6 +248,25 @@ def test_gemm_stream_passes(m, fmt, rows):
 def test_gemm_tail_items(m, fmt):
     """More than a whole round of tiles: the rest runs as quarter-width items, bit for bit as whole tiles would."""
     run_gemm(m, [2100, 130], 8192, 256, fmt, "bf16", ints=True)
+
+
+@pytest.mark.parametrize("rows", [5, 40, 300, 2500])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_gemm_nan_stays_in_its_row_and_column(m, fmt, rows):
+    rng = np.random.default_rng(13)
+    N, K = (2080, 288) if rows > 2000 else (96, 288)
+    a, a_s, av = operand(rng, rows, K, fmt, True)
+    w, w_s, wv = operand(rng, N, K, "mxfp4", True)
+    ref = av @ wv.T
+    a_s[rows // 2, 7] = 255
+    w_s[N - 2, 3] = 255
+    ref[rows // 2] = np.nan
+    ref[:, N - 2] = np.nan
+    if fmt == "mxfp8":
+        a[1, 200] = 0x7F
+        ref[1] = np.nan
+    got = m.mxfp4_grouped_gemm(a, a_s, w[None], w_s[None], out_dtype="f32")
+    np.testing.assert_array_equal(f64(got), ref)
 
 
 def test_gemm_dense_and_empty(m):

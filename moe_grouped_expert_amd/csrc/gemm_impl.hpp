@@ -235,6 +235,9 @@ constexpr int G_DYN_LDS = G_SCALE_BASE + G_STAGES * G_SCALE_STAGE;
 // this launch runs each of them as four 256 x 64 work items instead (the main launch leaves
 // them out; both take the same decision from the same tile table).  Every output element is
 // still accumulated by one wave over K in the same order: the results are bit-identical.
+// QT = 2: the same with quadrants of 128 x 128, which need two thirds (8-bit A) or four fifths
+// (4-bit) of a quarter-width item's operand bytes and leave out a tile's rows past its group;
+// two workgroups share a CU.
 // SM = 64, 128 or 256: tiles of 64 rows x SM columns (a wave 32 x SM/2), for groups of some
 // tens of rows, whose products read the weights faster than 256-row tiles would compute on
 // padding; with their smaller stages two workgroups share a CU.
@@ -253,12 +256,13 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   constexpr int BROWS_DMA = 1024 / BROWB;
   static_assert(QT == 0 || (EPI == EPI_STORE && MODE == RAGGED_M), "the quarter-width tail is for plain-store ragged-M GEMMs");
   static_assert(SM == 0 || (QT == 0 && MODE == RAGGED_M && EPI != EPI_SWIGLU_BWD), "64-row tiles: ragged-M forward GEMMs");
-  constexpr int WMB = SM ? 1 : G_WMB;              // 32-row MFMA blocks per wave
-  constexpr int BM = G_WAVES_M * WMB * 32;         // rows of a tile
+  constexpr int WMB = SM ? 1 : (QT == 2 ? 2 : G_WMB);   // 32-row MFMA blocks per wave
+  constexpr int BM = G_WAVES_M * WMB * 32;         // rows of a work item
+  constexpr int TM = QT == 2 ? 2 * BM : BM;        // rows of a tile
   constexpr int TN = SM ? SM : G_BN;               // columns of a tile
-  constexpr int BW = QT ? G_BN / 4 : TN;           // output columns (B rows) of a work item
+  constexpr int BW = QT == 2 ? G_BN / 2 : (QT ? G_BN / 4 : TN);   // output columns (B rows) of a work item
   // operand bytes of one of the NST LDS stages; the scales are behind the stages
-  constexpr int STAGE = SM || NST != G_STAGES ? BM * G_BKB + BW * BROWB : G_STAGE_BYTES;
+  constexpr int STAGE = SM || QT == 2 || NST != G_STAGES ? BM * G_BKB + BW * BROWB : G_STAGE_BYTES;
   constexpr int SCALES = NST * STAGE;
   constexpr int NA = BM / 32;                      // A's DMA instructions per wave and slice
   constexpr int WNB = BW / (32 * G_WAVES_N);       // 32-column MFMA blocks per wave
@@ -302,8 +306,8 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   if (tid == 0) {
     int acc = 0;
     for (int e = 0; e < p.E; ++e) {
-      int mt = MODE == RAGGED_M ? (group_size(p.sizes[e], group_off(p.offs[e])) + BM - 1) / BM
-                                : (p.M + BM - 1) / BM;
+      int mt = MODE == RAGGED_M ? (group_size(p.sizes[e], group_off(p.offs[e])) + TM - 1) / TM
+                                : (p.M + TM - 1) / TM;
       s_prefix[e] = acc;
       s_mtiles[e] = mt;
       acc += mt * ntiles;
@@ -332,6 +336,11 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     }
     items = uniform(items);
     t_full = uniform(t_full);
+    if constexpr (QT == 2) {
+      // at most an item a workgroup: an equal run of them for each XCD
+      const int per = (items + 7) >> 3;
+      if ((nwg & 7) == 0) vid = int(blockIdx.x >> 3) < per ? int(blockIdx.x & 7) * per + int(blockIdx.x >> 3) : items;
+    }
   }
 
   // every tile quantity is wave-uniform: kept in scalar registers
@@ -367,7 +376,8 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     t.nt = within / gm;
     t.off = uniform(group_off(ld_uniform(p.offs, t.e)));
     t.m_valid = MODE == RAGGED_M ? uniform(group_size(ld_uniform(p.sizes, t.e), t.off)) : p.M;
-    t.m0 = mt * BM;
+    t.m0 = mt * TM;
+    if constexpr (QT == 2) t.m0 += (quarter >> 1) * BM;
     // K range in bytes.  RAGGED_M: [0, K).  RAGGED_K: the expert's token span
     // [off, off + roundup32(size)) of the column forms; the loop starts at the slice
     // boundary below it and the chunks outside the span load as zeros.
@@ -391,11 +401,14 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
       t.B = bmat + int64_t(t.nb) * p.ldb;
       t.brec = uint32_t(rows_left(p.F - t.nb, TN / 2)) * uint32_t(p.ldb);
     } else {
-      t.nb = t.nt * TN + quarter * BW;
+      t.nb = t.nt * TN + (QT == 2 ? quarter & 1 : quarter) * BW;
       t.B = bmat + int64_t(t.nb) * p.ldb;
       t.brec = uint32_t(rows_left(p.N - t.nb, BW)) * uint32_t(p.ldb);
     }
     t.nkt = (t.khi - t.kbase + G_BKB - 1) / G_BKB;
+    if constexpr (QT == 2) {
+      if (t.m0 >= t.m_valid) t.nkt = 0;   // nothing but padding
+    }
     if constexpr (MX) {
       // packed scales: dword (j, row) at row + j * ld holds the 4 blocks of K elements
       // [128j, 128j + 128); slice kt is group kbase/128 + kt
@@ -1171,11 +1184,12 @@ static mge_status launch_gemm_kernel(Kern kern, const char* name, const GemmPara
 // A plain-store ragged-M GEMM as two launches: the main kernel over the whole rounds of
 // its grid, then the tail kernel over the rest as quarter-width work items (each kernel
 // finds its share on the device: the tile count depends on the group sizes there).
+// per_cu, lds: the tail kernel's workgroups on a CU and their LDS.
 template <typename KernMain, typename KernTail>
 static mge_status launch_gemm_split(KernMain kmain, KernTail ktail, const char* name, const GemmParams& p0,
-                                    hipStream_t s) {
+                                    hipStream_t s, int per_cu = 1, int lds = G_DYN_LDS) {
   hipFuncSetAttribute(reinterpret_cast<const void*>(kmain), hipFuncAttributeMaxDynamicSharedMemorySize, G_DYN_LDS);
-  hipFuncSetAttribute(reinterpret_cast<const void*>(ktail), hipFuncAttributeMaxDynamicSharedMemorySize, G_DYN_LDS);
+  hipFuncSetAttribute(reinterpret_cast<const void*>(ktail), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   const int cus = device_cus();
   int grid = cus;
   if (p0.tiles_upper < grid) grid = p0.tiles_upper;
@@ -1190,10 +1204,10 @@ static mge_status launch_gemm_split(KernMain kmain, KernTail ktail, const char* 
   mge_status st = hip_check(name);
   if (st != MGE_OK) return st;
   // at most two rounds of quarter-width items (the kernel exits at once when there is no tail)
-  const int tail_grid = (p0.tiles_upper < grid ? p0.tiles_upper : grid);
+  const int tail_grid = (p0.tiles_upper < grid ? p0.tiles_upper : grid) * per_cu;
   {
     ProfScope prof(s, name);
-    hipLaunchKernelGGL(ktail, dim3(tail_grid), dim3(G_THREADS), G_DYN_LDS, s, p);
+    hipLaunchKernelGGL(ktail, dim3(tail_grid), dim3(G_THREADS), lds, s, p);
   }
   return hip_check(name);
 }

@@ -8,7 +8,7 @@ namespace mge {
 #define MGE_GEMM_KERNEL(name, FMT, EPI, OUT) \
   __global__ __launch_bounds__(G_THREADS, 1) void name(GemmParams p) { gemm_body<FMT, EPI, RAGGED_M, OUT>(p); }
 #define MGE_GEMM_TAIL_KERNEL(name, FMT, OUT) \
-  __global__ __launch_bounds__(G_THREADS, 1) void name(GemmParams p) { gemm_body<FMT, EPI_STORE, RAGGED_M, OUT, 1>(p); }
+  __global__ __launch_bounds__(G_THREADS, 2) void name(GemmParams p) { gemm_body<FMT, EPI_STORE, RAGGED_M, OUT, 2>(p); }
 
 MGE_GEMM_KERNEL(gemm_gateup_swiglu_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_SWIGLU, OUT_NONE)
 MGE_GEMM_KERNEL(gemm_store_mxfp8_mxfp4, FMT_MXFP8_MXFP4, EPI_STORE, OUT_BF16)
@@ -45,11 +45,12 @@ MGE_GEMM_SMALL_KERNEL(gemm_store64x64_f32_mxfp4, FMT_MXFP4, EPI_STORE, OUT_F32, 
 mge_status launch_gemm_mxfp4(const GemmParams& p, bool a4, hipStream_t s) {
   if (p.role == GEMM_GATEUP) return launch_gemm_kernel(gemm_gateup_swiglu_mxfp8_mxfp4, "gemm_gateup_swiglu_mxfp4", p, s);
   const bool f32 = p.out_dtype == MGE_DTYPE_F32;
+  constexpr int lds8 = gemm_stage_lds(128, 128, G_BKB / 2, 2), lds4 = gemm_stage_lds(128, 128, G_BKB, 2);
   if (a4)
-    return f32 ? launch_gemm_split(gemm_store_f32_mxfp4, gemm_store_f32_tail_mxfp4, "gemm_mxfp4", p, s)
-               : launch_gemm_split(gemm_store_mxfp4, gemm_store_tail_mxfp4, "gemm_mxfp4", p, s);
-  return f32 ? launch_gemm_split(gemm_store_f32_mxfp8_mxfp4, gemm_store_f32_tail_mxfp8_mxfp4, "gemm_mxfp8_mxfp4", p, s)
-             : launch_gemm_split(gemm_store_mxfp8_mxfp4, gemm_store_tail_mxfp8_mxfp4, "gemm_mxfp8_mxfp4", p, s);
+    return f32 ? launch_gemm_split(gemm_store_f32_mxfp4, gemm_store_f32_tail_mxfp4, "gemm_mxfp4", p, s, 2, lds4)
+               : launch_gemm_split(gemm_store_mxfp4, gemm_store_tail_mxfp4, "gemm_mxfp4", p, s, 2, lds4);
+  return f32 ? launch_gemm_split(gemm_store_f32_mxfp8_mxfp4, gemm_store_f32_tail_mxfp8_mxfp4, "gemm_mxfp8_mxfp4", p, s, 2, lds8)
+             : launch_gemm_split(gemm_store_mxfp8_mxfp4, gemm_store_tail_mxfp8_mxfp4, "gemm_mxfp8_mxfp4", p, s, 2, lds8);
 }
 
 // 64-row tiles, of 64 columns where 128 would leave CUs without one.  8 groups x [4096][14336]:

@@ -1076,14 +1076,15 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* a, void* stream) {
 }
 
 // The weight-streaming kernels read an expert's weights again for every 32 rows, from L2, where
-// the tile kernels read them once but need their scales packed and a pointer table (two more
-// launches, about 8 us).  Streaming is kept while the rows past 16 an expert, times an expert's
+// the tile kernels read them once but need their scales packed (another launch, and a read and a
+// write of the scales).  Streaming is kept while the rows past 16 an expert, times an expert's
 // bytes, stay below kStreamBytes, at no more than kStreamRows an expert (a pass takes a workgroup
 // about 2 us however small the weights are).  Times of a whole call, streamed and tiled:
-// [2048][2048], 64 rows 11 and 19 us, 128 rows 17 and 19, 256 rows 31 and 17; [8192][4096], 32 rows 12
-// and 19 us, 64 rows 18 and 19; 8 experts of [4096][14336], 8 rows each 57 and 68 us, 64 rows each 174 and 76.
-constexpr int64_t kStreamBytes = int64_t(768) << 20;
-constexpr int kStreamRows = 144;
+// [2048][2048], 80 rows 12.6 and 14.8 us, 104 rows 16.0 and 14.6; [8192][4096], 32 rows 11 and 17.5
+// us, 64 rows 17.7 both; 8 experts of [2048][4096], 256 rows 17 and 21 us, 288 uneven 26 and 21; 8
+// experts of [4096][14336], 64 rows 56 and 76 us, 224 uneven 105 and 80.
+constexpr int64_t kStreamBytes = int64_t(576) << 20;
+constexpr int kStreamRows = 96;
 // Tiles of 64 rows or of 256: a 256 x 256 tile takes its CU as long as one and a half rounds of
 // 64 x 128 tiles take the chip, whatever part of it is padding.  Measured (64-row, 256-row):
 // [8192][8192], 512 rows 55, 86 us; 1024 rows 113, 91; 8 x [4096][14336] in 4 bits, 1024 rows
@@ -1147,6 +1148,20 @@ static ScalePackParams pack_weights(const uint8_t* const* tab, int E, int rows, 
   return q;
 }
 
+// The tile path's pointer tables: in the pack launch's arguments for few experts, else uploaded
+static mge_status pack_and_upload(const ScalePackParams* pk, int n, const void* const* const* tabs, int ntab, int E, void** dst,
+                                  hipStream_t s) {
+  if (E > kInlineExperts) {
+    const mge_status st = launch_upload_tables(tabs, ntab, E, dst, s);
+    return st != MGE_OK ? st : launch_scale_pack_batch(pk, n, s);
+  }
+  PtrTables u{};
+  u.dst = const_cast<const void**>(dst);
+  for (int t = 0; t < ntab && tabs[t]; ++t)
+    for (int e = 0; e < E; ++e) u.p[u.n++] = tabs[t][e];
+  return launch_scale_pack_batch(pk, n, s, &u);
+}
+
 static mge_status launch_tile4(GemmParams& g, bool a4, int64_t total, hipStream_t s) {
   if (small_tiles4(g.E, g.N, total)) return launch_gemm_mxfp4_small(g, a4, total, s);
   g.tiles_upper = gemm_tiles_upper(g, total);
@@ -1204,7 +1219,7 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
                                 a->split_sizes ? nullptr : &one_size, a->split_sizes ? nullptr : &one_off};
   const bool tile = tile4(E, a->N, a->K, a->rows, gemm4_total(a));
   mge_status st = MGE_OK;
-  if (tile || E > kGemm4Inline) st = launch_upload_tables(tabs, 4, E, tab, s);
+  if (!tile && E > kGemm4Inline) st = launch_upload_tables(tabs, 4, E, tab, s);
   if (st != MGE_OK) return st;
   Gemm4Params p{};
   p.E = E; p.N = a->N; p.K = a->K;
@@ -1228,7 +1243,7 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
   uint32_t* as_p = static_cast<uint32_t*>(ws.take(packed_bytes(1, p.rows, KB)));
   uint32_t* ws_p = static_cast<uint32_t*>(ws.take(packed_bytes(E, a->N, KB)));
   const ScalePackParams pk[2] = {pack_rows(p.As, p.rows, KB, as_p), pack_weights(p.Ws, E, a->N, KB, ws_p)};
-  st = launch_scale_pack_batch(pk, 2, s);
+  st = pack_and_upload(pk, 2, tabs, 4, E, tab, s);
   if (st != MGE_OK) return st;
   GemmParams g = tile4_params(p, a4, as_p, ws_p);
   g.out_dtype = a->out_dtype;
@@ -1299,7 +1314,7 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
                                 reinterpret_cast<const void* const*>(a->w_gate_up_scale),
                                 reinterpret_cast<const void* const*>(a->w_down_scale)};
   const bool tile = fwd4_tile(a, R);
-  if (tile || E > kGemm4Inline) st = launch_upload_tables(tabs, 4, E, tab, s);
+  if (!tile && E > kGemm4Inline) st = launch_upload_tables(tabs, 4, E, tab, s);
   if (st != MGE_OK) return st;
   const uint8_t* const* dev = reinterpret_cast<const uint8_t* const*>(tab);
   Gemm4Params g{};
@@ -1320,7 +1335,7 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
     wd_p = static_cast<uint32_t*>(ws.take(packed_bytes(E, H, F / 32)));
     const ScalePackParams pk[3] = {pack_rows(g.As, R, H / 32, xs_p), pack_weights(g.Ws, E, 2 * F, H / 32, wgu_p),
                                    pack_weights(dev + 3 * E, E, H, F / 32, wd_p)};
-    st = launch_scale_pack_batch(pk, 3, s);
+    st = pack_and_upload(pk, 3, tabs, 4, E, tab, s);
     if (st != MGE_OK) return st;
     GemmParams t = tile4_params(g, false, xs_p, wgu_p);
     t.role = GEMM_GATEUP;

@@ -64,7 +64,15 @@ struct ScalePackParams {
 };
 mge_status launch_scale_pack(const ScalePackParams& p, hipStream_t s);
 constexpr int SP_MAXD = 8;   // scale packs per batched launch
-mge_status launch_scale_pack_batch(const ScalePackParams* list, int n, hipStream_t s);
+// Device pointers that a launch writes to dst[0 .. n), from its arguments (src_tab of its
+// matrices points into dst)
+constexpr int kInlineExperts = 64;
+struct PtrTables {
+  const void** dst;
+  int n;
+  const void* p[4 * kInlineExperts];
+};
+mge_status launch_scale_pack_batch(const ScalePackParams* list, int n, hipStream_t s, const PtrTables* tables = nullptr);
 inline int64_t scale_pack_dwords(int rows, int kb) { return int64_t(rows) * ((kb + 3) / 4); }
 
 // ------------------------------------------------------------ routing / permutation
@@ -131,7 +139,7 @@ mge_status launch_quant4(const Quant4Params& p, hipStream_t s);
 mge_status launch_dequant4(int64_t blocks, const uint8_t* codes, const uint8_t* scales, int dtype, void* out, hipStream_t s);
 
 // C[r] = A[r] W_e^T with MXFP4 weights; SwiGLU: h from W_e = [gate rows; up rows]
-constexpr int kGemm4Inline = 64;    // experts whose weight pointers may travel in the arguments
+constexpr int kGemm4Inline = kInlineExperts;    // experts whose weight pointers may travel in the arguments
 struct Gemm4Params {
   int E, N, K, F;
   int rows;                         // rows of A and C: every group is clamped into them

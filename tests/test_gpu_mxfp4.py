@@ -236,6 +236,37 @@ def test_gemm_large_tiles(m, fmt, K):
     run_gemm(m, [2500, 1, 700], 2080, K, fmt, "f32", align=32, extra=7, seed=3)
 
 
+@pytest.mark.parametrize("E", [64, 65, 130])
+def test_gemm_tiles_many_experts(m, E):
+    """The tile kernels with as many pointers as a launch carries, and more."""
+    run_gemm(m, [97 + e % 5 for e in range(E)], 64, 96, "mxfp8", "bf16", ints=True, align=8)
+
+
+def test_tiles_captured(m):
+    """A product and a layer on the tile kernels in a graph, replayed between eager calls."""
+    rng = np.random.default_rng(71)
+    rt, (gc, gs, _, _), (dc, ds, _, _) = layer(m, 700, 3, 2, 128, 96, 9)
+    a, a_s, _ = operand(rng, 600, 160, "mxfp4", False)
+    w, w_s, _ = operand(rng, 320, 160, "mxfp4", False)
+
+    def step():
+        y = m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds).y_perm
+        return m.mxfp4_grouped_gemm(a, a_s, w[None], w_s[None]), m.unpermute_combine(y, rt.perm_pos)
+
+    ref = [t.clone() for t in step()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for rep in range(3):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(ref, out)), rep
+        assert all(torch.equal(x, y) for x, y in zip(ref, step())), ("eager", rep)
+    del graph
+
+
 @pytest.mark.parametrize("rows", [17, 33, 48, 100])
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
 def test_gemm_stream_passes(m, fmt, rows):

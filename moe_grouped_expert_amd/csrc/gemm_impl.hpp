@@ -237,7 +237,8 @@ constexpr int G_DYN_LDS = G_SCALE_BASE + G_STAGES * G_SCALE_STAGE;
 // still accumulated by one wave over K in the same order: the results are bit-identical.
 // QT = 2: the same with quadrants of 128 x 128, which need two thirds (8-bit A) or four fifths
 // (4-bit) of a quarter-width item's operand bytes and leave out a tile's rows past its group;
-// two workgroups share a CU.
+// two workgroups share a CU.  64 to 90 tiles of [4096][14336], 4-bit rows: 51-88 us as
+// quarter widths, 45-60 as quadrants; 3 or 4 stages and one workgroup a CU 45-87.
 // SM = 64, 128 or 256: tiles of 64 rows x SM columns (a wave 32 x SM/2), for groups of some
 // tens of rows, whose products read the weights faster than 256-row tiles would compute on
 // padding; with their smaller stages two workgroups share a CU.

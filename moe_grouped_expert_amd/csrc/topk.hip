@@ -26,6 +26,11 @@
 // is the formula's choice if neighbouring slots are further apart than the bound, or are equal
 // because their inputs are.  Otherwise slots 0 .. k alone are put in order by 64-bit keys, one
 // a lane, or, where more experts could belong to the choice, a wave makes it in 64 bits.
+// (All in 64 bits, 16384 tokens of 256 experts with a sigmoid, a bias and groups took 78 us.)
+//
+// Measured, kernel alone, where an empty launch takes 4 us: 4 tokens x 256 experts (sigmoid,
+// bias, 8 groups) 3.9 us; 16384 of them 15 us, bound by vector issue (1060 instructions a wave,
+// four waves a SIMD, 70% of the slots; the 17 MB alone are 3.6 us); 32768 x 8, softmax, bf16 5.6 us.
 #include <math.h>
 
 #include <type_traits>
@@ -547,7 +552,8 @@ __global__ __launch_bounds__(TK_THREADS) void route_topk2_kernel(TopkParams p) {
 //   softmax, renormalised dl_i = w_i (d_i - sum_j w_j d_j)   (all other terms cancel)
 //   softmax               dl_e = s_e ([e chosen] d_e - sum_j s_j d_j) for every expert
 // and 0 elsewhere.  The row is built in LDS (the chosen experts are scattered) and leaves
-// as whole lines.  A repeated index adds its slots in slot order.
+// as whole lines.  A repeated index adds its slots in slot order.  Bound by its writes:
+// 16384 x 256 fp32 8.1 us, of which an empty launch is 4 (16.8 MB written).
 template <int V, typename LT>
 __global__ __launch_bounds__(TK_THREADS) void route_topk_bwd_kernel(TopkBwdParams p) {
   constexpr int LD = TK_ROW * V;

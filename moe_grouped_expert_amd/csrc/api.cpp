@@ -1173,7 +1173,8 @@ static int64_t gemm4_total(const mge_gemm4_args* a) {
 }
 
 size_t mge_gemm4_workspace_bytes(const mge_gemm4_args* a) {
-  if (!a || a->struct_size != sizeof(mge_gemm4_args) || a->E < 1 || a->E > 256 || a->N < 1 || a->K < 32 || a->rows < 0)
+  if (!a || a->struct_size != sizeof(mge_gemm4_args) || a->E < 1 || a->E > 256 || a->N < 1 || a->K < 32 || a->rows < 0 ||
+      a->rows >= (int64_t(1) << 31) / a->K || int64_t(a->N) * (a->K / 2) >= (int64_t(1) << 31))
     return 0;
   const bool tile = tile4(a->E, a->N, a->K, a->rows, gemm4_total(a));
   if (!tile && a->E <= kGemm4Inline) return 0;   // the pointers travel in the arguments
@@ -1264,8 +1265,10 @@ static size_t fwd4_ws(const mge_fwd_args* a, int R) {
 }
 
 size_t mge_fwd_mxfp4_workspace_bytes(const mge_fwd_args* a) {
-  if (!a || a->E < 1 || a->E > 256 || a->T < 0 || a->k < 1 || a->align < 1) return 0;
-  return fwd4_ws(a, int(mge_perm_rows(a->T, a->k, a->E, a->align)));
+  if (!a || a->E < 1 || a->E > 256 || a->T < 0 || a->k < 1 || a->align < 1 || a->H < 1 || a->F < 1) return 0;
+  const int64_t R = mge_perm_rows(a->T, a->k, a->E, a->align);
+  if (R >= (int64_t(1) << 31) / std::max(a->H, a->F) || int64_t(a->F) * a->H >= (int64_t(1) << 31) || a->F >= 1 << 30) return 0;
+  return fwd4_ws(a, int(R));
 }
 
 mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {

@@ -1,0 +1,38 @@
+"""The host code of the router-choice and MXFP4 calls under AddressSanitizer and
+UndefinedBehaviorSanitizer (CPU only), as tests/test_host_sanitizers.py does for the others."""
+import concurrent.futures as cf
+import os
+import subprocess
+
+import pytest
+
+from tests.test_host_sanitizers import CLANGXX, CSRC, HIPCC, ROOT
+
+pytestmark = pytest.mark.skipif(not (os.path.exists(HIPCC) and os.path.exists(CLANGXX)), reason="ROCm toolchain missing")
+
+
+def test_topk_mxfp4_host_code_under_asan_ubsan(tmp_path):
+    from moe_grouped_expert_amd import build as b
+    san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
+           "-Xarch_host", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer"]
+
+    def compile_one(src):
+        obj = str(tmp_path / (os.path.basename(src) + ".o"))
+        path = src if os.path.isabs(src) else os.path.join(CSRC, src)
+        r = subprocess.run([HIPCC, *b.FLAGS, "-O1", "-g", *san, "-c", path, "-o", obj], capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-3000:]
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        objs = list(ex.map(compile_one, b.SOURCES + [os.path.join(ROOT, "tests", "host_san", "abi_driver_topk_mxfp4.cpp")]))
+    exe = str(tmp_path / "abi_driver_topk_mxfp4")
+    r = subprocess.run([CLANGXX, "-fsanitize=address,undefined", "-o", exe, *objs, "-L/opt/rocm/lib", "-lamdhip64",
+                        "-Wl,-rpath,/opt/rocm/lib"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:halt_on_error=1:abort_on_error=0",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1", HIP_VISIBLE_DEVICES="")
+    env.pop("LD_PRELOAD", None)
+    r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=120)
+    out = r.stdout + r.stderr
+    assert "ERROR: AddressSanitizer" not in out and "runtime error" not in out, out[-4000:]
+    assert r.returncode == 0 and "abi_driver_topk_mxfp4 ok" in r.stdout, out[-4000:]

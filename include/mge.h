@@ -301,7 +301,8 @@ mge_status grouped_mlp_fwd(const mge_fwd_args* args, void* stream);
  * with prec = MGE_PREC_MXFP8 (x_perm, h: MXFP8 as there) and w_gate_up / w_down the MXFP4
  * codes ([2F][H/2], [H][F/2]; mxfp4_quantize ROW) with their scales ([2F][H/32],
  * [H][F/32]).  h is quantized to MXFP8 in the gate-up product's epilogue.
- * Workspace: mge_fwd_mxfp4_workspace_bytes(args) bytes, 16-byte aligned.
+ * Workspace: mge_fwd_mxfp4_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for
+ * few rows with h given.
  * Errors: as grouped_mlp_fwd; MGE_ERR_UNSUPPORTED for training (saved_gu, h_col or
  * h_col_scale given) or prec BF16.
  * ---------------------------------------------------------------------------- */

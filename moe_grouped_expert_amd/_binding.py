@@ -645,14 +645,10 @@ def unpermute_combine(inp: torch.Tensor, perm_pos: torch.Tensor, weights: Option
     dev = inp.device
     if out is None:
         out = torch.empty((T, H), device=dev, dtype=torch.bfloat16 if out_dtype == "bf16" else torch.float32)
-    a = CombineArgs()
-    a.struct_size = C.sizeof(CombineArgs)
-    a.T, a.k, a.H = T, k, H
-    a.in_dtype = DTYPE["bf16"] if inp.dtype == torch.bfloat16 else DTYPE["f32"]
-    a.out_dtype = DTYPE["bf16"] if out.dtype == torch.bfloat16 else DTYPE["f32"]
-    a.in_, a.perm_pos, a.weights, a.out = _ptr(inp), _ptr(perm_pos), _ptr(weights), _ptr(out)
-    a.in_rows = inp.shape[0]
-    _check(lib().unpermute_combine(C.byref(a), _stream(dev)), "unpermute_combine")
+    a = CombineArgs(C.sizeof(CombineArgs), T, k, H, DTYPE["bf16"] if inp.dtype == torch.bfloat16 else DTYPE["f32"],
+                    DTYPE["bf16"] if out.dtype == torch.bfloat16 else DTYPE["f32"], inp.data_ptr(), perm_pos.data_ptr(),
+                    _ptr(weights), out.data_ptr(), inp.shape[0])
+    _call("unpermute_combine", a, dev)
     return out
 
 
@@ -934,7 +930,10 @@ def grouped_mlp_fwd_mxfp4(rt: RouteOut, w_gate_up, w_down, w_gate_up_scale, w_do
                 C.addressof(keep[2]), C.addressof(keep[1]), C.addressof(keep[3]), DTYPE[y_dtype], _ptr(out.y_perm),
                 _ptr(out.h), _ptr(out.h_scale))
     if out.workspace is None:
-        out.workspace = x.new_empty(max(lib().mge_fwd_mxfp4_workspace_bytes(C.byref(a)), 256))
-    a.workspace, a.workspace_bytes = _ptr(out.workspace), out.workspace.numel()
+        need = lib().mge_fwd_mxfp4_workspace_bytes(C.byref(a))
+        if need:
+            out.workspace = x.new_empty(need)
+    if out.workspace is not None:
+        a.workspace, a.workspace_bytes = out.workspace.data_ptr(), out.workspace.numel()
     _call("grouped_mlp_fwd_mxfp4", a, dev)
     return out

@@ -1229,7 +1229,7 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* a, void* stream) {
   p.sizes = a->split_sizes; p.offs = a->group_offsets;
   p.A = a->a; p.As = a->a_scale;
   p.W = reinterpret_cast<const uint8_t* const*>(tab);
-  p.Ws = reinterpret_cast<const uint8_t* const*>(tab + a->E);
+  p.Ws = tab ? reinterpret_cast<const uint8_t* const*>(tab + a->E) : nullptr;
   p.C = a->out;
   p.vec = scales_vec(p.As, a->w_scale, E, p.K);
   const bool a4 = a->a_format == MGE_FORMAT_MXFP4;
@@ -1258,8 +1258,9 @@ static bool fwd4_tile(const mge_fwd_args* a, int64_t R) {
 }
 
 static size_t fwd4_ws(const mge_fwd_args* a, int R) {
-  size_t n = up256(4 * size_t(a->E) * sizeof(void*));
-  if (fwd4_tile(a, R)) n += tile4_ws(a->E, 2 * a->F, a->H, R) + tile4_ws(a->E, a->H, a->F, R);
+  const bool tile = fwd4_tile(a, R);
+  size_t n = tile || a->E > kGemm4Inline ? up256(4 * size_t(a->E) * sizeof(void*)) : 0;   // else the pointers travel in the arguments
+  if (tile) n += tile4_ws(a->E, 2 * a->F, a->H, R) + tile4_ws(a->E, a->H, a->F, R);
   if (!a->h) n += up256(size_t(R) * a->F) + up256(size_t(R) * (a->F / 32));
   return n;
 }
@@ -1296,16 +1297,17 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
               "operand too large for 32-bit offsets (rows=%lld H=%d F=%d)", static_cast<long long>(R64), a->H, a->F);
   const int R = int(R64);
   const size_t need = fwd4_ws(a, R);
-  if (!a->workspace || a->workspace_bytes < need) {
+  if (need > 0 && (!a->workspace || a->workspace_bytes < need)) {
     set_error("forward workspace needs %zu bytes (got %zu)", need, a->workspace_bytes);
     return MGE_ERR_WORKSPACE;
   }
-  MGE_REQUIRE(aligned16(a->workspace), "workspace must be 16-byte aligned");
+  MGE_REQUIRE(need == 0 || aligned16(a->workspace), "workspace must be 16-byte aligned");
   if (a->T == 0) return MGE_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int E = a->E;
   Carve ws(a->workspace);
-  void** tab = static_cast<void**>(ws.take(4 * size_t(E) * sizeof(void*)));
+  const bool tile = fwd4_tile(a, R);
+  void** tab = tile || E > kGemm4Inline ? static_cast<void**>(ws.take(4 * size_t(E) * sizeof(void*))) : nullptr;
   void* h = a->h;
   uint8_t* hs = a->h_scale;
   if (!h) {
@@ -1316,7 +1318,6 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
                                 reinterpret_cast<const void* const*>(a->w_down),
                                 reinterpret_cast<const void* const*>(a->w_gate_up_scale),
                                 reinterpret_cast<const void* const*>(a->w_down_scale)};
-  const bool tile = fwd4_tile(a, R);
   if (!tile && E > kGemm4Inline) st = launch_upload_tables(tabs, 4, E, tab, s);
   if (st != MGE_OK) return st;
   const uint8_t* const* dev = reinterpret_cast<const uint8_t* const*>(tab);
@@ -1325,7 +1326,7 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
   g.rows = R; g.total = a->T * a->k;
   g.sizes = a->split_sizes; g.offs = a->group_offsets;
   g.A = static_cast<const uint8_t*>(a->x_perm); g.As = a->x_perm_scale;
-  g.W = dev; g.Ws = dev + 2 * E;
+  g.W = dev; g.Ws = dev ? dev + 2 * E : nullptr;
   g.prob = a->prob_perm;
   g.h_codes = static_cast<uint8_t*>(h); g.h_scales = hs;
   g.vec = scales_vec(g.As, a->w_gate_up_scale, E, g.K);
@@ -1354,7 +1355,7 @@ mge_status grouped_mlp_fwd_mxfp4(const mge_fwd_args* a, void* stream) {
   d.rows = R; d.total = a->T * a->k;
   d.sizes = a->split_sizes; d.offs = a->group_offsets;
   d.A = static_cast<const uint8_t*>(h); d.As = hs;
-  d.W = dev + E; d.Ws = dev + 3 * E;
+  d.W = dev ? dev + E : nullptr; d.Ws = dev ? dev + 3 * E : nullptr;
   d.C = a->y_perm;
   d.vec = scales_vec(d.As, a->w_down_scale, E, d.K);
   if (!tile) {

@@ -646,7 +646,7 @@ __global__ __launch_bounds__(TK_THREADS) void route_topk_bwd_kernel(TopkBwdParam
   if (p.ovec) {   // uniform
     const int n = E / PER;
     for (int i = tid; i < rows * n; i += TK_THREADS) {
-      const int r = i / n;
+      const int r = E == LD ? 0 : i / n;   // (uniform; whole rows follow one another)
       const float* f = so + r * LD + (i - r * n) * PER;
       uint4 q;
       if constexpr (sizeof(LT) == 4) {

@@ -300,7 +300,10 @@ mge_status grouped_mlp_fwd(const mge_fwd_args* args, void* stream);
  * grouped_mlp_fwd_mxfp4 — grouped_mlp_fwd for serving on MXFP4 weights: the same arguments
  * with prec = MGE_PREC_MXFP8 (x_perm, h: MXFP8 as there) and w_gate_up / w_down the MXFP4
  * codes ([2F][H/2], [H][F/2]; mxfp4_quantize ROW) with their scales ([2F][H/32],
- * [H][F/32]).  h is quantized to MXFP8 in the gate-up product's epilogue.
+ * [H][F/32]).  h is quantized to MXFP8 in the gate-up product's epilogue; a block of h with
+ * an infinity or NaN gets the scale byte 255 (NaN; its codes have no meaning).  A NaN in x_perm
+ * (scale byte 255, E4M3 code 0x7f) thus makes its row of y_perm NaN, one in w_gate_up every row of
+ * its expert, one in w_down its column of the expert's rows.
  * Workspace: mge_fwd_mxfp4_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for
  * few rows with h given.
  * Errors: as grouped_mlp_fwd; MGE_ERR_UNSUPPORTED for training (saved_gu, h_col or

@@ -226,16 +226,16 @@ __global__ __launch_bounds__(64 * W) void gemm4_stream_kernel(Gemm4Params p) {
         const int64_t r = int64_t(off) + m0 + row;
         const float pr = live ? p.prob[r] : 0.f;
         float h[8];
-        float amax = 0.f;
+        uint32_t amax = 0;   // as bits: a NaN or infinity stays on top and makes the block a NaN block
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float G = c[i >> 2][i & 3], U = c[2 + (i >> 2)][i & 3];
           h[i] = pr * silu_f(G) * U;
-          amax = fmaxf(amax, fabsf(h[i]));
+          amax = umax(amax, __float_as_uint(h[i]) & 0x7fffffffu);
         }
-        amax = fmaxf(amax, __shfl_xor(amax, 16));
-        amax = fmaxf(amax, __shfl_xor(amax, 32));
-        const uint32_t sc = mx_scale_byte(amax);
+        amax = umax(amax, uint32_t(__shfl_xor(int(amax), 16)));
+        amax = umax(amax, uint32_t(__shfl_xor(int(amax), 32)));
+        const uint32_t sc = mx_scale_byte_nan(amax);
         const float inv = mx_inv_scale(sc);
         if (live) {
           uint8_t* hc = p.h_codes + r * p.F + f0;

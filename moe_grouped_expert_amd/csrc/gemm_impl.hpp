@@ -871,7 +871,8 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
           if constexpr (MX) {
             // row form: one scale per (row, 32-column block), shared by the half-wave
             float inv[16];
-            const uint32_t sc = row_block_inv16(h, l32, inv, s_inv + wave * 32 + hi * 16);   // sc: row l32 / 2
+            // (MXFP4 weights have no code for a NaN and mark it in the scale: h keeps it the same way)
+            const uint32_t sc = row_block_inv16<B4>(h, l32, inv, s_inv + wave * 32 + hi * 16);   // sc: row l32 / 2
             // codes of 4 consecutive rows: a lane holds its column's 4 codes (bytes =
             // rows); a 4 x 4 byte transpose inside each quad of lanes (16-bit halves with
             // the lane 2 apart, then bytes with the lane 1 apart) leaves row (l32 % 4) of

@@ -39,6 +39,13 @@ __device__ __forceinline__ uint32_t mx_scale_byte(float amax) {
   return uint32_t(s < 0 ? 0 : s);
 }
 
+// The same where the block may hold an infinity or NaN, from the largest of the values' bit
+// patterns without signs (as integers a NaN is above an infinity and that above all finite
+// values): 255, the format's NaN, so that it shows in what is computed from the block.
+__device__ __forceinline__ uint32_t mx_scale_byte_nan(uint32_t bits) {
+  return bits >= 0x7f800000u ? 255u : mx_scale_byte(__uint_as_float(bits));
+}
+
 // 2^-e for the scale byte s (e = s - 127): fp32 with exponent field 254 - s.
 __device__ __forceinline__ float mx_inv_scale(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 
@@ -124,6 +131,13 @@ __device__ __forceinline__ uint32_t max_abs_bits(uint32_t a, uint32_t b) {
   return r;
 }
 
+// The same where a NaN on either side gives NaN (above every other result, as bits)
+__device__ __forceinline__ uint32_t max_abs_bits_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("v_maximum3_f32 %0, |%1|, |%2|, |%2|" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
   return uint32_t(__builtin_amdgcn_mov_dpp(int(v), CTRL, 0xf, 0xf, true));
@@ -143,6 +157,8 @@ __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b 
 // 16 floats of LDS per half-wave (lanes 2r, 2r + 1 write row r's, every lane reads all
 // 16 back): one wave's LDS accesses are performed in issue order, and a wave barrier keeps
 // the compiler from moving the reads above the write.  Needs all 64 lanes.
+// NANS: a block with an infinity or NaN gets the scale byte 255 (its codes have no meaning).
+template <bool NANS = false>
 __device__ __forceinline__ uint32_t row_block_inv16(const float* v, int l32, float* inv, float* slot) {
   const bool b3 = (l32 & 8) != 0, b2 = (l32 & 4) != 0, b1 = (l32 & 2) != 0;
   // m1[i]: row i + 8*b4, amax over lanes c, c ^ 16
@@ -150,7 +166,7 @@ __device__ __forceinline__ uint32_t row_block_inv16(const float* v, int l32, flo
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const U32Pair x = permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 8]));
-    m1[i] = max_abs_bits(x.a, x.b);
+    m1[i] = NANS ? max_abs_bits_nan(x.a, x.b) : max_abs_bits(x.a, x.b);
   }
   // m2[i]: row i + 4*b3 + 8*b4 (partner: lane ^ 8)
   uint32_t m2[4];
@@ -163,7 +179,7 @@ __device__ __forceinline__ uint32_t row_block_inv16(const float* v, int l32, flo
   // m4: row b1 + 2*b2 + 4*b3 + 8*b4 = l32 / 2 (partner: lane ^ 2); then lane ^ 1 holds the same row
   uint32_t m4 = umax(b1 ? m3[1] : m3[0], dpp_u<0x4E>(b1 ? m3[0] : m3[1]));
   m4 = umax(m4, dpp_u<0xB1>(m4));
-  const uint32_t sc = mx_scale_byte(__uint_as_float(m4));
+  const uint32_t sc = NANS ? mx_scale_byte_nan(m4) : mx_scale_byte(__uint_as_float(m4));
   slot[l32 >> 1] = mx_inv_scale(sc);
   __builtin_amdgcn_wave_barrier();   // the other lanes' writes before the reads (no instruction)
 #pragma unroll

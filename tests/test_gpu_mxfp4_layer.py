@@ -1,0 +1,68 @@
+"""GPU tests of grouped_mlp_fwd_mxfp4 beside those of test_gpu_mxfp4.py: what a NaN does on its way through the
+layer."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_mxfp4 import layer, npy
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import moe_grouped_expert_amd as mge
+    return mge
+
+
+# tokens, experts, k, H, F: the streaming kernels, 64-row tiles, 256-row tiles of the gate-up product
+PATHS = [(6, 4, 2, 128, 96), (40, 3, 2, 512, 160), (300, 4, 2, 384, 320), (2000, 3, 2, 256, 1056)]
+
+
+@pytest.mark.parametrize("T,E,k,H,F", PATHS)
+def test_nan_reaches_the_rows_it_belongs_to(m, T, E, k, H, F):
+    """A NaN block of a weight (scale byte 255) makes every row of its expert NaN, one of a row of x that row, an E4M3
+    NaN the same, and a row whose products overflow fp32 too; no other row changes a bit."""
+    from tests.gpu_helpers import say
+    say("[gpu] mlp4 nan", T, E, k, H, F)
+    rt, (gc, gs, _, _), (dc, ds, _, _) = layer(m, T, E, k, H, F, T + E)
+    valid = npy(rt.perm_src) >= 0
+    ref = m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds, y_dtype="f32")
+    ref_y, ref_h, ref_s = ref.y_perm.clone(), ref.h.clone(), ref.h_scale.clone()
+    sizes, off = npy(rt.split_sizes), npy(rt.group_offsets)
+    e = int(sizes.argmax())
+    o, n = int(off[e]), int(sizes[e])
+    rows = np.arange(o, o + n)
+
+    def run(hit, blocks):
+        """hit: the rows that turn into NaN; blocks: whether only one block of 32 of their h does."""
+        f = m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds, y_dtype="f32")
+        bad = np.zeros(rt.R, bool)
+        bad[hit] = True
+        keep = torch.from_numpy(valid & ~bad).cuda()
+        assert np.isnan(npy(f.y_perm)[bad]).all()
+        assert torch.equal(f.y_perm[keep], ref_y[keep]) and torch.equal(f.h[keep], ref_h[keep])
+        assert torch.equal(f.h_scale[keep], ref_s[keep])
+        s = npy(f.h_scale)[bad]
+        if blocks is None:
+            assert (s == 255).all()
+        else:
+            assert (s[:, blocks] == 255).all() and (np.delete(s, blocks, 1) != 255).all()
+
+    for row, blk in ((F - 3, (F - 3) // 32), (F + 5, 0)):      # a gate row, an up row
+        old = gs[e, row, 1].clone()
+        gs[e, row, 1] = 255
+        run(rows, blk)
+        gs[e, row, 1] = old
+    r = o + n // 2
+    old = rt.x_perm_scale[r].clone()
+    rt.x_perm_scale[r, H // 32 - 1] = 255
+    run([r], None)
+    rt.x_perm_scale[r] = 254                                   # |x| of 2^127 and more
+    run([r], None)
+    rt.x_perm_scale[r] = old
+    old = rt.x_perm[r, 3].clone()
+    rt.x_perm[r, 3] = 0x7F                                     # the E4M3 NaN
+    run([r], None)
+    rt.x_perm[r, 3] = old
+    run([], None)

@@ -1,9 +1,12 @@
-"""GPU tests of grouped_mlp_fwd_mxfp4 beside those of test_gpu_mxfp4.py: what a NaN does on its way through the
-layer."""
+"""GPU tests of the MXFP4 layer and products beside those of test_gpu_mxfp4.py: what a NaN does on its way through the
+layer, more experts than a launch carries pointers for, and h in the workspace."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
 
+from tests import test_gpu_mxfp4 as base
 from tests.test_gpu_mxfp4 import layer, npy
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +69,31 @@ def test_nan_reaches_the_rows_it_belongs_to(m, T, E, k, H, F):
     run([r], None)
     rt.x_perm[r, 3] = old
     run([], None)
+
+
+# streaming with the pointers in the arguments and in tables; 64-row tiles with both
+MANY = [(9, 64, 2, 64, 32), (9, 65, 2, 64, 96), (30, 256, 8, 96, 64), (3300, 64, 2, 64, 64), (3300, 65, 2, 96, 64), (13000, 256, 2, 64, 32)]
+
+
+@pytest.mark.parametrize("T,E,k,H,F", MANY)
+def test_mlp_many_experts(m, T, E, k, H, F):
+    """Against the 64-bit products, by the tolerances of test_mlp."""
+    base.test_mlp(m, T, E, k, H, F, 8, None)
+
+
+@pytest.mark.parametrize("T,E,k,H,F", [PATHS[0], PATHS[2], MANY[1], MANY[4]])
+def test_mlp_with_h_in_the_workspace(m, T, E, k, H, F):
+    """h = None: the same y, bit for bit, and a second call in the workspace of the first."""
+    from tests.gpu_helpers import say
+    say("[gpu] mlp4 without h", T, E, k, H, F)
+    rt, (gc, gs, _, _), (dc, ds, _, _) = layer(m, T, E, k, H, F, T + 1)
+    rows = torch.from_numpy(npy(rt.perm_src) >= 0).cuda()
+    f = m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds)
+    g = dataclasses.replace(f, y_perm=torch.full_like(f.y_perm, 7.0), h=None, h_scale=None, workspace=None)
+    assert m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds, out=g) is g
+    assert g.h is None and g.workspace.numel() >= rt.R * F
+    assert torch.equal(g.y_perm[rows], f.y_perm[rows]) and bool((g.y_perm[~rows] == 7.0).all())
+    ws = g.workspace
+    g.y_perm.fill_(7.0)
+    m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds, out=g)
+    assert g.workspace is ws and torch.equal(g.y_perm[rows], f.y_perm[rows])

@@ -1,5 +1,6 @@
 """GPU tests of the MXFP4 layer and products beside those of test_gpu_mxfp4.py: what a NaN does on its way through the
-layer, more experts than a launch carries pointers for, and h in the workspace."""
+layer, more experts than a launch carries pointers for,
+h in the workspace, and the tail items of a product bit by bit."""
 import dataclasses
 
 import numpy as np
@@ -7,7 +8,7 @@ import pytest
 import torch
 
 from tests import test_gpu_mxfp4 as base
-from tests.test_gpu_mxfp4 import layer, npy
+from tests.test_gpu_mxfp4 import layer, npy, operand
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +98,25 @@ def test_mlp_with_h_in_the_workspace(m, T, E, k, H, F):
     g.y_perm.fill_(7.0)
     m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds, out=g)
     assert g.workspace is ws and torch.equal(g.y_perm[rows], f.y_perm[rows])
+
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+def test_tail_items_equal_whole_tiles(m, fmt, out_dtype):
+    """320 tiles of 256 x 256 are a whole round of 256 and 64 that run as quadrants; half of the columns are 160 tiles
+    without a tail.  An element is summed in the same order in both: the same bits, of rounded data too."""
+    from tests.gpu_helpers import say
+    say("[gpu] gemm4 tail bits", fmt, out_dtype)
+    rng = np.random.default_rng(31)
+    sizes, N, K = [2100, 130], 8192, 288
+    a, a_s, _ = operand(rng, sum(sizes), K, fmt, False)
+    w, w_s, _ = operand(rng, 2 * N, K, "mxfp4", False)
+    w, w_s = w.reshape(2, N, -1), w_s.reshape(2, N, -1)
+    sz = torch.tensor(sizes, dtype=torch.int32, device="cuda")
+    of = torch.tensor([0, sizes[0]], dtype=torch.int32, device="cuda")
+    whole = m.mxfp4_grouped_gemm(a, a_s, w, w_s, sz, of, out_dtype)
+    for lo in (0, N // 2):
+        half = m.mxfp4_grouped_gemm(a, a_s, w[:, lo:lo + N // 2].contiguous(), w_s[:, lo:lo + N // 2].contiguous(), sz, of,
+                                    out_dtype)
+        assert torch.equal(whole[:, lo:lo + N // 2], half)

@@ -540,7 +540,7 @@ mge_status moe_router_bwd(const mge_router_bwd_args* args, void* stream);
  * [1, num_groups], k > topk_groups * E / num_groups, group_topn other than 1 or 2, a scale
  * that is not finite, a row stride below E, NULL logits / topk_idx / topk_prob (T > 0), or
  * a pointer not aligned to its elements.
- * T = 0 is a no-op.  No workspace.
+ * T = 0 is a no-op.  No workspace.  Calls of more than 2^25 tokens are several launches.
  * ---------------------------------------------------------------------------- */
 enum { MGE_SCORE_SOFTMAX = 0, MGE_SCORE_SIGMOID = 1 };
 

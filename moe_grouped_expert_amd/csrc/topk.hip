@@ -678,6 +678,9 @@ static void with_width(int E, F&& f) {
 // Tokens up to which a token takes a whole wave: the chip's SIMDs have few waves each then,
 // and the call is as long as one wave's chain of dependent steps.
 constexpr int64_t TK_WAVE_TOKENS = 2048;
+// Tokens of one launch, which has to stay below 2^32 threads (64 a token at most); more of them
+// follow in further launches.
+constexpr int64_t TK_LAUNCH_TOKENS = int64_t(1) << 25;
 
 template <int ROW, int V, typename LT, int GROUPS>
 static void launch_topk_form(const TopkParams& p, bool by_score, hipStream_t s) {
@@ -725,33 +728,55 @@ mge_status launch_topk(const TopkParams& p0, int dtype, hipStream_t s) {
   if (groups && (gs * (dtype == MGE_DTYPE_F32 ? 4 : 2)) % 16 != 0) p.vec = false;
   if (groups && (gs * 4) % 16 != 0) p.bvec = false;
   ProfScope prof(s, "route_topk2");
-  if (v16 == 0 || (p.T <= TK_WAVE_TOKENS && v16 > 1)) {
-    // (v64 = 0: groups that fit no power of two of lanes walk LDS, a token a wave)
-    p.lanes = v64 ? l64 : 0;
-    if (v64 == 1) launch_topk_row<64, 1>(p, dtype, by_score, groups, s);
-    else if (v64 == 2) launch_topk_row<64, 2>(p, dtype, by_score, groups, s);
-    else launch_topk_row<64, 4>(p, dtype, by_score, groups, s);
-  } else {
-    p.lanes = l16;
-    if (v16 == 1) launch_topk_row<16, 1>(p, dtype, by_score, groups, s);
-    else if (v16 == 2) launch_topk_row<16, 2>(p, dtype, by_score, groups, s);
-    else if (v16 == 4) launch_topk_row<16, 4>(p, dtype, by_score, groups, s);
-    else if (v16 == 8) launch_topk_row<16, 8>(p, dtype, by_score, groups, s);
-    else launch_topk_row<16, 16>(p, dtype, by_score, groups, s);
+  const bool wave = v16 == 0 || (p0.T <= TK_WAVE_TOKENS && v16 > 1);
+  // (v64 = 0: groups that fit no power of two of lanes walk LDS, a token a wave)
+  p.lanes = wave ? (v64 ? l64 : 0) : l16;
+  const int64_t esz = dtype == MGE_DTYPE_F32 ? 4 : 2;
+  for (int64_t t0 = 0; t0 < p0.T; t0 += TK_LAUNCH_TOKENS) {
+    p.T = p0.T - t0 < TK_LAUNCH_TOKENS ? p0.T - t0 : TK_LAUNCH_TOKENS;
+    p.logits = static_cast<const uint8_t*>(p0.logits) + t0 * p.ld * esz;
+    p.topk_idx = p0.topk_idx + t0 * p.k;
+    p.topk_prob = p0.topk_prob + t0 * p.k;
+    if (!wave) {
+      if (v16 == 1) launch_topk_row<16, 1>(p, dtype, by_score, groups, s);
+      else if (v16 == 2) launch_topk_row<16, 2>(p, dtype, by_score, groups, s);
+      else if (v16 == 4) launch_topk_row<16, 4>(p, dtype, by_score, groups, s);
+      else if (v16 == 8) launch_topk_row<16, 8>(p, dtype, by_score, groups, s);
+      else launch_topk_row<16, 16>(p, dtype, by_score, groups, s);
+    } else if (v64 == 1) {
+      launch_topk_row<64, 1>(p, dtype, by_score, groups, s);
+    } else if (v64 == 2) {
+      launch_topk_row<64, 2>(p, dtype, by_score, groups, s);
+    } else {
+      launch_topk_row<64, 4>(p, dtype, by_score, groups, s);
+    }
+    const mge_status st = hip_check("route_topk2_kernel");
+    if (st != MGE_OK) return st;
   }
-  return hip_check("route_topk2_kernel");
+  return MGE_OK;
 }
 
-mge_status launch_topk_bwd(const TopkBwdParams& p, int dtype, hipStream_t s) {
-  if (p.T <= 0) return MGE_OK;
-  const dim3 grid(unsigned((p.T + TK_TOKENS - 1) / TK_TOKENS)), block(TK_THREADS);
+mge_status launch_topk_bwd(const TopkBwdParams& p0, int dtype, hipStream_t s) {
+  if (p0.T <= 0) return MGE_OK;
+  TopkBwdParams p = p0;
+  const int64_t esz = dtype == MGE_DTYPE_F32 ? 4 : 2;
   ProfScope prof(s, "route_topk_bwd");
-  with_width(p.E, [&](auto w) {
-    constexpr int V = decltype(w)::value;
-    if (dtype == MGE_DTYPE_F32) hipLaunchKernelGGL((route_topk_bwd_kernel<V, float>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((route_topk_bwd_kernel<V, uint16_t>), grid, block, 0, s, p);
-  });
-  return hip_check("route_topk_bwd_kernel");
+  for (int64_t t0 = 0; t0 < p0.T; t0 += TK_LAUNCH_TOKENS) {
+    p.T = p0.T - t0 < TK_LAUNCH_TOKENS ? p0.T - t0 : TK_LAUNCH_TOKENS;
+    p.logits = static_cast<const uint8_t*>(p0.logits) + t0 * p.ld * esz;
+    p.topk_idx = p0.topk_idx + t0 * p.k;
+    p.d_prob = p0.d_prob + t0 * p.k;
+    p.d_logits = static_cast<uint8_t*>(p0.d_logits) + t0 * p.E * esz;
+    const dim3 grid(unsigned((p.T + TK_TOKENS - 1) / TK_TOKENS)), block(TK_THREADS);
+    with_width(p.E, [&](auto w) {
+      constexpr int V = decltype(w)::value;
+      if (dtype == MGE_DTYPE_F32) hipLaunchKernelGGL((route_topk_bwd_kernel<V, float>), grid, block, 0, s, p);
+      else hipLaunchKernelGGL((route_topk_bwd_kernel<V, uint16_t>), grid, block, 0, s, p);
+    });
+    const mge_status st = hip_check("route_topk_bwd_kernel");
+    if (st != MGE_OK) return st;
+  }
+  return MGE_OK;
 }
 
 }  // namespace mge

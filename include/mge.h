@@ -305,7 +305,8 @@ mge_status grouped_mlp_fwd(const mge_fwd_args* args, void* stream);
  * (scale byte 255, E4M3 code 0x7f) thus makes its row of y_perm NaN, one in w_gate_up every row of
  * its expert, one in w_down its column of the expert's rows.
  * Workspace: mge_fwd_mxfp4_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for
- * few rows with h given.
+ * few rows over at most 64 experts with h given (more experts' pointers go through it, and it
+ * is asked for whatever T, 0 included).
  * Errors: as grouped_mlp_fwd; MGE_ERR_UNSUPPORTED for training (saved_gu, h_col or
  * h_col_scale given) or prec BF16.
  * ---------------------------------------------------------------------------- */
@@ -650,9 +651,12 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* args, void* stream);
  * outside the groups are untouched.
  * With MXFP8 rows the matrix unit adds products in eights of consecutive k and cuts off what
  * lies 2^-13 below the largest product of an eight (as in the MXFP8 calls; about 1e-5 of
- * sum |a w| for a long K, up to 1e-4 for a short one); MXFP4 products add to fp32 rounding.  A NaN (scale byte 255, E4M3 code 0x7f) reaches the elements
- * of out whose row or column it belongs to, and no others.
- * Workspace: mge_gemm4_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for few rows.
+ * sum |a w| for a long K, up to 1e-4 for a short one); MXFP4 products add to fp32 rounding.
+ * A NaN (scale byte 255, E4M3 code 0x7f) reaches the elements of out whose row or column it
+ * belongs to, and no others.
+ * Workspace: mge_gemm4_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for few rows
+ * over at most 64 experts (more experts' pointers go through it, and it is asked for whatever
+ * rows, 0 included).
  * Errors: MGE_ERR_INVALID_ARG for E outside [1, 256], N or K not a positive multiple of 32,
  * rows < 0 or >= 2^31 / K, an expert's weight of 2^31 bytes or more, unknown formats, NULL or
  * misaligned (16-byte) a / out / weights / workspace, NULL scales, one of split_sizes / group_offsets

@@ -1,0 +1,37 @@
+"""Limits of the MXFP4 calls (CPU): when a workspace is needed, and sizes past a launch."""
+import ctypes as C
+import os
+
+import pytest
+
+from moe_grouped_expert_amd import _binding as b
+from tests import test_abi_topk_mxfp4 as base
+
+pytestmark = pytest.mark.skipif(not os.path.exists(b.LIB_PATH), reason="libmge.so not built")
+
+
+def many(fn, st, E, names, **kw):
+    w = (b.vp * E)(*[base.P] * E)
+    return base.call(fn, st, E=E, **{n: C.cast(w, b.vp) for n in names}, **kw)
+
+
+@pytest.mark.parametrize("E,need", [(1, False), (64, False), (65, True), (256, True)])
+@pytest.mark.parametrize("rows", [0, 1, 8])
+def test_few_rows_need_a_workspace_past_64_experts(E, need, rows):
+    """The weights' pointers travel with the launch for up to 64 experts, else in the workspace, empty calls included."""
+    kw = dict(a_format=0, N=64, K=64, rows=rows, split_sizes=base.P, group_offsets=base.P, a=base.P, a_scale=base.P, out=base.P)
+    g = b.Gemm4Args(struct_size=C.sizeof(b.Gemm4Args), E=E, **kw)
+    assert (b.lib().mge_gemm4_workspace_bytes(C.byref(g)) > 0) == need
+    if need:
+        assert many("mxfp4_grouped_gemm", b.Gemm4Args, E, ("w", "w_scale"), **kw)[0] == b.MGE_ERR_WORKSPACE
+    elif rows == 0:
+        assert many("mxfp4_grouped_gemm", b.Gemm4Args, E, ("w", "w_scale"), **kw)[0] == b.MGE_OK
+    kw = dict(prec=1, H=64, F=64, T=rows, k=1, align=32, split_sizes=base.P, group_offsets=base.P, prob_perm=base.P,
+              x_perm=base.P, x_perm_scale=base.P, y_perm=base.P, h=base.P, h_scale=base.P)
+    f = b.FwdArgs(struct_size=C.sizeof(b.FwdArgs), E=E, **kw)
+    assert (b.lib().mge_fwd_mxfp4_workspace_bytes(C.byref(f)) > 0) == need
+    names = ("w_gate_up", "w_gate_up_scale", "w_down", "w_down_scale")
+    if need:
+        assert many("grouped_mlp_fwd_mxfp4", b.FwdArgs, E, names, **kw)[0] == b.MGE_ERR_WORKSPACE
+    elif rows == 0:
+        assert many("grouped_mlp_fwd_mxfp4", b.FwdArgs, E, names, **kw)[0] == b.MGE_OK

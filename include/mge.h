@@ -603,7 +603,8 @@ mge_status moe_route_topk_bwd(const mge_route_topk_bwd_args* args, void* stream)
  * COL: col_codes [b][C][Rp/2], col_scales [b][C][Rp/32], Rp = R rounded up to 32 (zero
  * padded) — the ROW quantization of the transpose (the operand of an input gradient:
  * dX = dY W is mxfp4_grouped_gemm with W's column form).
- * Errors: as mxfp8_quantize (without segments and tensor scale); batch <= 65535.
+ * Errors: as mxfp8_quantize (without segments and tensor scale); batch <= 65535,
+ * R <= 65535 * 128, C <= 2^31 - 256.
  * ---------------------------------------------------------------------------- */
 typedef struct mge_quant4_args {
   uint32_t struct_size;

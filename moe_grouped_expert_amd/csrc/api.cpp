@@ -1049,6 +1049,8 @@ mge_status mxfp4_quantize(const mge_quant4_args* a, void* stream) {
               "in_batch_stride too small or not a multiple of 8");
   MGE_REQUIRE(a->R <= 65535 * 128, "R must be at most %d (got %d)", 65535 * 128, a->R);
   if (a->batch == 0 || a->R == 0 || a->C == 0) return MGE_OK;   // no element, no output
+  // (a launch's x extent is 512 threads for 256 columns, and below 2^32)
+  MGE_REQUIRE(a->C <= 0x7fffff00, "C must be at most %d (got %d)", 0x7fffff00, a->C);
   if (a->orient & MGE_ORIENT_ROW)
     MGE_REQUIRE(a->row_codes && a->row_scales && aligned16(a->row_codes), "row outputs missing or misaligned");
   if (a->orient & MGE_ORIENT_COL)

@@ -35,3 +35,12 @@ def test_few_rows_need_a_workspace_past_64_experts(E, need, rows):
         assert many("grouped_mlp_fwd_mxfp4", b.FwdArgs, E, names, **kw)[0] == b.MGE_ERR_WORKSPACE
     elif rows == 0:
         assert many("grouped_mlp_fwd_mxfp4", b.FwdArgs, E, names, **kw)[0] == b.MGE_OK
+
+
+@pytest.mark.parametrize("C_,ok", [(0x7fffff00, True), (0x7fffff20, False), (0x7fffffe0, False)])
+def test_quantize_columns_past_a_launch(C_, ok):
+    """A launch has 512 threads for 256 columns and fewer than 2^32 threads a row of workgroups; within the limit the
+    call goes on to what its other arguments lack."""
+    kw = {**base.QUANT, "R": 1, "C": C_, "in_row_stride": 1 << 31, "row_codes": None, "col_codes": None}
+    r, err = base.call("mxfp4_quantize", b.Quant4Args, **kw)
+    assert r == b.MGE_ERR_INVALID_ARG and ("row outputs missing" if ok else "C must be at most") in err, err

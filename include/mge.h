@@ -625,7 +625,8 @@ mge_status mxfp4_quantize(const mge_quant4_args* args, void* stream);
  * [rows][C/2], scales [rows][C/32] -> out [rows][C] bf16 or fp32 (exact in both, apart
  * from bf16's and fp32's largest values; a scale byte of 255, the format's NaN, gives NaN).
  * Errors: MGE_ERR_INVALID_ARG for rows < 0, C not a multiple of 32 or negative, an unknown
- * dtype, NULL or misaligned (16-byte) codes / out, NULL scales.
+ * dtype, NULL or misaligned (16-byte) codes / out, NULL scales, or more than 2^32 - 1024
+ * blocks of 32.
  * ---------------------------------------------------------------------------- */
 typedef struct mge_dequant4_args {
   uint32_t struct_size;

@@ -1071,9 +1071,10 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* a, void* stream) {
               static_cast<long long>(a->rows), a->C);
   MGE_REQUIRE(a->out_dtype == MGE_DTYPE_BF16 || a->out_dtype == MGE_DTYPE_F32, "out_dtype must be BF16 or F32");
   if (a->rows == 0 || a->C == 0) return MGE_OK;
+  // (a launch has a thread for each block, in workgroups of 256, and fewer than 2^32)
+  MGE_REQUIRE(a->rows <= ((int64_t(1) << 32) - 1024) / (a->C / 32), "too many values (at most 2^32 - 1024 blocks of 32)");
   MGE_REQUIRE(a->codes && aligned16(a->codes) && a->scales && a->out && aligned16(a->out),
               "codes / scales / out NULL or misaligned");
-  MGE_REQUIRE(a->rows < (int64_t(1) << 38) / (a->C / 32), "too many values");
   return launch_dequant4(a->rows * (a->C / 32), a->codes, a->scales, a->out_dtype, a->out, static_cast<hipStream_t>(stream));
 }
 

@@ -44,3 +44,11 @@ def test_quantize_columns_past_a_launch(C_, ok):
     kw = {**base.QUANT, "R": 1, "C": C_, "in_row_stride": 1 << 31, "row_codes": None, "col_codes": None}
     r, err = base.call("mxfp4_quantize", b.Quant4Args, **kw)
     assert r == b.MGE_ERR_INVALID_ARG and ("row outputs missing" if ok else "C must be at most") in err, err
+
+
+@pytest.mark.parametrize("rows,C_,ok", [((1 << 32) - 1024, 32, True), ((1 << 32) - 1023, 32, False), ((1 << 31) - 512, 64, True),
+                                        ((1 << 31) - 511, 64, False)])
+def test_dequantize_blocks_past_a_launch(rows, C_, ok):
+    """A thread a block of 32 values; within the limit the call goes on to what its other arguments lack."""
+    r, err = base.call("mxfp4_dequantize", b.Dequant4Args, rows=rows, C=C_, out_dtype=0, codes=base.P, scales=base.P, out=None)
+    assert r == b.MGE_ERR_INVALID_ARG and ("NULL" if ok else "too many") in err, err

@@ -679,11 +679,17 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+# The current device and a device's current stream: torch's shortcuts, which make no objects,
+# or its public calls where it has none.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
+
+
 def _call(fn: str, a, dev) -> None:
     """One library call on the current stream of `dev`, with `dev` current while it launches."""
     f = getattr(_LIB or lib(), fn)
-    if dev.index == torch._C._cuda_getDevice():
-        code = f(C.byref(a), torch._C._cuda_getCurrentRawStream(dev.index))
+    if dev.index == _current_device():
+        code = f(C.byref(a), _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
             code = f(C.byref(a), _stream(dev))

@@ -880,6 +880,7 @@ def mxfp4_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, w, w_scale, split
     if E < 1 or len(w_scale) != E or (w.dim() != 3 if stacked else w[0].dim() != 2):
         raise ValueError("w must be [E, N, K/2] with w_scale [E, N, K/32]")
     N = w.shape[1] if stacked else w[0].shape[0]
+    _need(workspace is None or workspace.is_contiguous(), "workspace must be contiguous")
     dev = a.device
     dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
     _on(dev, a_scale, out, split_sizes, group_offsets, workspace)
@@ -917,6 +918,7 @@ def grouped_mlp_fwd_mxfp4(rt: RouteOut, w_gate_up, w_down, w_gate_up_scale, w_do
     x = rt.x_perm
     dev = x.device
     dt = torch.bfloat16 if y_dtype == "bf16" else torch.float32
+    _need(out is None or out.workspace is None or out.workspace.is_contiguous(), "out.workspace must be contiguous")
     _on(dev, rt.x_perm_scale, rt.split_sizes, rt.group_offsets, rt.prob_perm)
     if out is None:
         out = FwdOut(y_perm=x.new_empty((R, H), dtype=dt), h=x.new_empty((R, F)), h_scale=x.new_empty((R, F // 32)))

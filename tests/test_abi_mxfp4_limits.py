@@ -52,3 +52,20 @@ def test_dequantize_blocks_past_a_launch(rows, C_, ok):
     """A thread a block of 32 values; within the limit the call goes on to what its other arguments lack."""
     r, err = base.call("mxfp4_dequantize", b.Dequant4Args, rows=rows, C=C_, out_dtype=0, codes=base.P, scales=base.P, out=None)
     assert r == b.MGE_ERR_INVALID_ARG and ("NULL" if ok else "too many") in err, err
+
+
+def test_python_workspaces_are_contiguous():
+    """A strided workspace would be written between its elements too."""
+    import torch
+
+    import moe_grouped_expert_amd as m
+    u8 = dict(dtype=torch.uint8)
+    z, i = torch.zeros, torch.zeros(2, dtype=torch.int32)
+    ws = z(1 << 16, 2, **u8)[:, 0]
+    with pytest.raises(ValueError, match="workspace"):
+        m.mxfp4_grouped_gemm(z(4, 64, **u8), z(4, 2, **u8), z(1, 32, 32, **u8), z(1, 32, 2, **u8), workspace=ws)
+    rt = b.RouteOut(T=4, E=2, k=1, H=64, align=32, prec="mxfp8", R=66, topk_idx=i, topk_prob=i, split_sizes=i, group_offsets=i,
+                    perm_src=i, perm_pos=i, prob_perm=i, x_perm=z(66, 64, **u8), x_perm_scale=z(66, 2, **u8))
+    out = b.FwdOut(y_perm=z(66, 64, dtype=torch.bfloat16), h=None, workspace=ws)
+    with pytest.raises(ValueError, match="workspace"):
+        m.grouped_mlp_fwd_mxfp4(rt, z(2, 64, 32, **u8), z(2, 64, 16, **u8), z(2, 64, 2, **u8), z(2, 64, 1, **u8), out=out)

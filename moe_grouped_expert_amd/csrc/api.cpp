@@ -1078,20 +1078,24 @@ mge_status mxfp4_dequantize(const mge_dequant4_args* a, void* stream) {
   return launch_dequant4(a->rows * (a->C / 32), a->codes, a->scales, a->out_dtype, a->out, static_cast<hipStream_t>(stream));
 }
 
-// The weight-streaming kernels read an expert's weights again for every 32 rows, from L2, where
+// The weight-streaming kernels read an expert's weights again for every 32 rows, where
 // the tile kernels read them once but need their scales packed (another launch, and a read and a
 // write of the scales).  Streaming is kept while the rows past 16 an expert, times an expert's
 // bytes, stay below kStreamBytes, at no more than kStreamRows an expert (a pass takes a workgroup
-// about 2 us however small the weights are).  Times of a whole call, streamed and tiled:
-// [2048][2048], 80 rows 12.6 and 14.8 us, 104 rows 16.0 and 14.6; [8192][4096], 32 rows 11 and 17.5
-// us, 64 rows 17.7 both; 8 experts of [2048][4096], 256 rows 17 and 21 us, 288 uneven 26 and 21; 8
-// experts of [4096][14336], 64 rows 56 and 76 us, 224 uneven 105 and 80.
+// about 2 us however small the weights are).  Times of a whole call with MXFP8 rows, streamed and
+// tiled: [2048][2048], 80 rows 13.0 and 14.5 us, 104 rows 16.5 and 14.3; [8192][4096], 32 rows 11.5
+// and 18.3 us, 64 rows 18.5 both; 8 experts of [2048][4096], 256 rows 18.6 and 24.4 us, 288 uneven
+// 29.2 and 24.8; 8 experts of [4096][14336], 64 rows 56 and 76 us, 128 rows 61 and 77, 256 even 72
+// and 79, 224 uneven (3 to 70 an expert) 115 and 124.  The rule has the averages only: 64 rows that
+// all go to one of the 8 experts stream in 87 us, where tiles would take 57.
 constexpr int64_t kStreamBytes = int64_t(576) << 20;
 constexpr int kStreamRows = 96;
 // Tiles of 64 rows or of 256: a 256 x 256 tile takes its CU as long as one and a half rounds of
-// 64 x 128 tiles take the chip, whatever part of it is padding.  Measured (64-row, 256-row):
-// [8192][8192], 512 rows 55, 86 us; 1024 rows 113, 91; 8 x [4096][14336] in 4 bits, 1024 rows
-// 76, 98 us, 2048 rows 123, 117; gate-up of 512 tokens 199, 206 us, of 256 tokens 149, 196.
+// 64 x 128 tiles take the chip, whatever part of it is padding.  Measured, whole calls (the better
+// 64-row kernel, 256-row; taken: *): [8192][8192], 512 rows 51*, 90 us; 768 rows 86, 91*; 1024 rows
+// 88, 91*; 1536 rows 125, 96*; in 4 bits, 768 rows 63, 62*; 8 x [4096][14336], 1024 rows 103*, 153;
+// 1536 rows 161, 155*; 2048 rows 170, 176*; 3000 rows 236, 176*; in 4 bits, 1024 rows 85*, 104 us,
+// 1536 rows 126, 112*; 2048 rows 129, 128*.
 constexpr int64_t kSmallTiles = 700;   // 64 x 128 tiles worth a round of 256 x 256 ones on 256 CUs
 static bool small_tiles4(int E, int N, int64_t total) {
   // (group sizes are on the device: half a tile of padding a group, and a tile at least)

@@ -8,12 +8,14 @@
 // those rows once, straight into registers, and add their partial sums through LDS at the
 // end, in wave order.  The weights are the matrix unit's row operand and 16 or 32 tokens (MB
 // = 1, 2) its columns (v_mfma_scale_f32_16x16x128_f8f6f4); more rows than that in a group take
-// further passes over the same weights, which then come from L2.  A chunk's 16 blocks are
+// further passes over the same weights.  Those come from L2 only where the rows that the
+// workgroups of an XCD go over fit it: a further pass over 8 experts x [4096][14336] takes as long
+// as the first (32 rows an expert 72 us, 64 129, 96 184).  A chunk's 16 blocks are
 // dealt to the 4 matrix instructions so that the loads of two of them read whole lines and
 // the row's 16 scale bytes are one load (VEC: rows of scales aligned to it).
 //   HBM-bound: 8 experts x [28672][4096], 32 rows 97 us (5.3 TB/s of codes and scales); the
-// gate-up and down products of 8 tokens, top-2 of 8 experts (4096 x 14336) 84 and 50 us.  One row
-// x [2048][4096] takes 5.3 us, where an empty launch takes 4.
+// gate-up and down products of 8 tokens, top-2 of 8 experts (4096 x 14336) 84 and 50 us, of 64 (MB
+// = 2) 127 and 64.  One row x [2048][4096] takes 5.3 us, where an empty launch takes 4.
 //   Operand layout (measured on gfx950): lane 16q + i feeds row / column i.  A 4-bit
 //   operand is the 32 elements of K block q (16 bytes); an 8-bit one is elements
 //   16q .. 16q + 15 and 64 + 16q .. 64 + 16q + 15 of the 128; both are scaled by the E8M0

@@ -72,7 +72,7 @@ constexpr int G_BM = G_WAVES_M * G_WMB * 32;
 constexpr int G_BN = G_WAVES_N * G_WNB * 32;
 constexpr int G_BKB = 128;                    // K bytes per slice: one whole 128-byte line per operand row
 #ifndef G_TAIL_SPLIT
-#define G_TAIL_SPLIT 1   // plain-store ragged-M GEMMs: the grid's last round as quarter-width items
+#define G_TAIL_SPLIT 1   // plain-store ragged-M GEMMs: the grid's last round as four items a tile (QT)
 #endif
 #ifndef G_EPI_GROUP
 #define G_EPI_GROUP 1   // SwiGLU epilogues: 32 x 32 blocks the scheduler may interleave
@@ -321,8 +321,8 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   int vid = blockIdx.x;
   if ((nwg & 7) == 0) vid = (blockIdx.x & 7) * (nwg >> 3) + (blockIdx.x >> 3);
   // Work items of this launch.  With tail_split the tiles past the main launch's last whole
-  // round go to the tail launch as quarter-width items, when there are at most two rounds of
-  // those (each item streams the whole A slice, so it takes well over a quarter of a tile's
+  // round go to the tail launch as four items each, when there are at most two rounds of
+  // those (a quarter-width item streams the whole A slice, so it takes well over a quarter of a tile's
   // time).  Both launches decide from the same numbers: the tile count and the main grid.
   int items = total, t_full = total;
   {
@@ -1184,7 +1184,7 @@ static mge_status launch_gemm_kernel(Kern kern, const char* name, const GemmPara
 }
 
 // A plain-store ragged-M GEMM as two launches: the main kernel over the whole rounds of
-// its grid, then the tail kernel over the rest as quarter-width work items (each kernel
+// its grid, then the tail kernel over the rest as quarter-width or quadrant work items (each kernel
 // finds its share on the device: the tile count depends on the group sizes there).
 // per_cu, lds: the tail kernel's workgroups on a CU and their LDS.
 template <typename KernMain, typename KernTail>
@@ -1205,7 +1205,7 @@ static mge_status launch_gemm_split(KernMain kmain, KernTail ktail, const char* 
   }
   mge_status st = hip_check(name);
   if (st != MGE_OK) return st;
-  // at most two rounds of quarter-width items (the kernel exits at once when there is no tail)
+  // at most two rounds of those items (the kernel exits at once when there is no tail)
   const int tail_grid = (p0.tiles_upper < grid ? p0.tiles_upper : grid) * per_cu;
   {
     ProfScope prof(s, name);

@@ -58,9 +58,12 @@ mge_status launch_gemm_mxfp4(const GemmParams& p, bool a4, hipStream_t s) {
              : launch_gemm_split(gemm_store_mxfp8_mxfp4, gemm_store_tail_mxfp8_mxfp4, "gemm_mxfp8_mxfp4", p, s, 2, lds8);
 }
 
-// 64-row tiles, of 64 columns where 128 would leave CUs without one.  8 groups x [4096][14336]:
-// 64 x 64 and 64 x 128 tiles take 91 and 93 us for 256 rows (about 256 of the wide tiles), 132
-// and 100 us for 512 rows (384); one [2048][2048] of 32 rows 3.5 and 4.6 us.
+// 64-row tiles, of 64 columns where 128 would leave CUs without one.  Whole calls with 64 x 64 and
+// 64 x 128 tiles (number of the wide ones by the rule's count), MXFP8 rows: 8 groups x [4096][14336],
+// 256 rows 79 and 99 us (256), 512 rows 83 and 105 (384), 768 rows 122 and 96 (512); [8192][8192],
+// 256 rows 40 and 49 (320), 512 rows 69 and 51 (576); 8 x [2048][4096], 512 rows 26.7 and 23.4 (192);
+// [2048][2048], 128 rows 14.6 and 15.6 (48).  Between 320 and about 450 tiles the narrow ones, with
+// their deeper stages, are the faster by a fifth: the bound was read before they had them.
 constexpr int64_t kWideTiles = 320;
 mge_status launch_gemm_mxfp4_small(const GemmParams& p0, bool a4, int64_t rows_bound, hipStream_t s) {
   GemmParams p = p0;

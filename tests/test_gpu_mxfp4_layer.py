@@ -1,6 +1,5 @@
 """GPU tests of the MXFP4 layer and products beside those of test_gpu_mxfp4.py: what a NaN does on its way through the
-layer, more experts than a launch carries pointers for,
-h in the workspace, and the tail items of a product bit by bit."""
+layer, more experts than a launch carries pointers for, h in the workspace, and the tail items of a product bit by bit."""
 import dataclasses
 
 import numpy as np
@@ -98,7 +97,6 @@ def test_mlp_with_h_in_the_workspace(m, T, E, k, H, F):
     g.y_perm.fill_(7.0)
     m.grouped_mlp_fwd_mxfp4(rt, gc, dc, gs, ds, out=g)
     assert g.workspace is ws and torch.equal(g.y_perm[rows], f.y_perm[rows])
-
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])

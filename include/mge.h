@@ -17,7 +17,9 @@
  *   unpermute_combine   out[t] = sum over the k slots of in[perm_pos[t][i]]
  * the router's other scores (moe_route_topk, moe_route_topk_bwd: softmax or sigmoid, balance
  * bias, groups), MXFP4 weights (mxfp4_quantize, mxfp4_dequantize, mxfp4_grouped_gemm,
- * grouped_mlp_fwd_mxfp4)
+ * grouped_mlp_fwd_mxfp4), the norm before the layer (rmsnorm_fwd, rmsnorm_bwd), FP8 with one
+ * fp32 scale per block of 128 (fp8_block_quantize, fp8_block_dequantize,
+ * fp8_block_grouped_gemm, fp8_block_grouped_wgrad, grouped_mlp_fwd_fp8_block)
  * and the router backward (moe_router_bwd: d_logits from d_prob), the forward without
  * the fusion (grouped_mlp_fwd_unfused, the baseline the fusion is measured against) and
  * the one scale of FP8 with one scale per tensor (mge_tensor_scale; the quantizers then
@@ -686,6 +688,258 @@ typedef struct mge_gemm4_args {
 
 size_t mge_gemm4_workspace_bytes(const mge_gemm4_args* args);
 mge_status mxfp4_grouped_gemm(const mge_gemm4_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * rmsnorm_fwd — the norm before an expert layer: the residual's addition, the
+ * root-mean-square norm and its output in 16 or 32 bits and in FP8 with one fp32 scale per
+ * block of 128 (the format of fp8_block_quantize), in one pass.  Per row of H values:
+ *   r    = x + residual, rounded to x's type and written to residual_out (without a
+ *          residual: r = x, nothing written)
+ *   rstd = 1 / sqrt(mean(r^2) + eps)            (fp32; of the rounded r)
+ *   y    = r * rstd * weight                     (fp32, rounded once to y's type)
+ *   codes, scales: the 1 x 128 row form of the fp32 y (ceil(H/128) scales a row)
+ * y and codes are optional, one is needed; rstd is optional (the backward takes it).
+ * residual_out may be residual or, with x_row_stride = H, x itself; y, codes and scales may
+ * not overlap an input.  x: row stride x_row_stride elements; everything else contiguous.
+ * A row whose sum of squares is past fp32's range gives rstd 0.  NaN and infinities stay in
+ * their row.
+ * Errors: MGE_ERR_INVALID_ARG for T < 0, H not a multiple of 32 in [32, 16384], unknown
+ * dtypes, an x_row_stride below H or not a multiple of 8, eps negative or not finite, one of
+ * residual / residual_out or of codes / scales without the other, no output, NULL or
+ * misaligned pointers (16 bytes; scales and rstd 4).  T = 0 is a no-op.  No workspace.
+ * ---------------------------------------------------------------------------- */
+typedef struct mge_rmsnorm_args {
+  uint32_t struct_size;
+  int32_t T, H;
+  int32_t x_dtype;                       /* MGE_DTYPE_*: x, residual, residual_out */
+  int32_t weight_dtype, y_dtype;         /* MGE_DTYPE_* */
+  float eps;
+  int64_t x_row_stride;                  /* elements */
+  const void* x;                         /* [T][H] */
+  const void* residual;                  /* [T][H] or NULL */
+  const void* weight;                    /* [H] */
+  void* residual_out;                    /* [T][H], with residual */
+  void* y;                               /* [T][H] or NULL */
+  uint8_t* codes;                        /* [T][H] or NULL */
+  float* scales;                         /* [T][ceil(H/128)], with codes */
+  float* rstd;                           /* [T] or NULL */
+} mge_rmsnorm_args;
+
+mge_status rmsnorm_fwd(const mge_rmsnorm_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * rmsnorm_bwd — gradients of rmsnorm_fwd's y with respect to r and the weight.  With x the
+ * forward's r (residual_out, or x without a residual), g = dy * weight, xhat = x * rstd:
+ *   dx       = rstd * (g - xhat * mean(g * xhat)) + d_residual
+ *   d_weight = sum over the rows of dy * xhat       (fp32, overwritten, a fixed order)
+ * d_residual: the gradient that reaches residual_out from what reads it, or NULL; the
+ * gradient of x and of residual is dx alike.  dx may be dy, x or d_residual where the types
+ * and strides are the same.  d_weight may be NULL (no workspace then).
+ * Workspace: mge_rmsnorm_bwd_workspace_bytes(T, H) bytes, 16-byte aligned.
+ * Errors: as rmsnorm_fwd; MGE_ERR_WORKSPACE.  T = 0 writes a zero d_weight.
+ * ---------------------------------------------------------------------------- */
+typedef struct mge_rmsnorm_bwd_args {
+  uint32_t struct_size;
+  int32_t T, H;
+  int32_t x_dtype;                       /* MGE_DTYPE_*: x, d_residual, dx */
+  int32_t weight_dtype, dy_dtype;        /* MGE_DTYPE_* */
+  int64_t x_row_stride, dy_row_stride;   /* elements */
+  const void* dy;                        /* [T][H] */
+  const void* x;                         /* [T][H] */
+  const void* weight;                    /* [H] */
+  const float* rstd;                     /* [T] */
+  const void* d_residual;                /* [T][H] or NULL */
+  void* dx;                              /* [T][H] */
+  float* d_weight;                       /* [H] or NULL */
+  void* workspace;
+  size_t workspace_bytes;
+} mge_rmsnorm_bwd_args;
+
+size_t mge_rmsnorm_bwd_workspace_bytes(int32_t T, int32_t H);
+mge_status rmsnorm_bwd(const mge_rmsnorm_bwd_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * fp8_block_quantize — BF16 -> E4M3 with one fp32 scale per block of 128: 1 x 128 values
+ * along the rows (activations) or 128 x 128 (weights); the last block of an axis may be
+ * shorter.  Per block, with m = max(amax, 2^-100): scale = m / 448 and element = E4M3
+ * round-to-nearest-even of v * (448 / m) (both quotients correctly rounded fp32), value =
+ * element * scale.  A block with an infinity or NaN gets the scale NaN (its codes have no
+ * meaning).
+ * in, batch, R, C, strides, orient: as mxfp8_quantize.
+ * 1X128   ROW: row_codes [b][R][C], row_scales [b][R][ceil(C/128)].
+ *         COL: col_codes [b][C][Rp], col_scales [b][C][ceil(R/128)], Rp = R rounded up to 32
+ *         (zero padded) — the ROW quantization of the transpose, blocks along the rows.
+ * 128X128 ROW: row_codes [b][R][C], row_scales [b][ceil(R/128)][ceil(C/128)].
+ *         COL: the same codes and scales transposed, [b][C][Rp] and [b][ceil(C/128)]
+ *         [ceil(R/128)] (the weight operand of an input gradient).
+ * rows: optional map of output rows (batch 1, 1X128): row r is row rows[r] of in, zeros where
+ * rows[r] is outside [0, src_rows) (perm_src of moe_route_permute: the tokens are permuted
+ * as they are quantized).
+ * Errors: MGE_ERR_INVALID_ARG for an unknown block or orientation, negative sizes, C not a
+ * multiple of 32, C or R above 2^31 - 256, a map with batch > 1 or 128X128, strides too small
+ * or not multiples of 8, NULL or misaligned pointers (16 bytes; scales and rows 4).
+ * batch, R or C = 0 is a no-op.
+ * ---------------------------------------------------------------------------- */
+enum { MGE_BLOCK_1X128 = 0, MGE_BLOCK_128X128 = 1 };
+
+typedef struct mge_quant_fb_args {
+  uint32_t struct_size;
+  int32_t block;             /* MGE_BLOCK_* */
+  int32_t batch, R, C;
+  int64_t in_batch_stride, in_row_stride;
+  const uint16_t* in;
+  const int32_t* rows;       /* [R] or NULL */
+  int64_t src_rows;          /* rows of in, with rows */
+  uint32_t orient;           /* MGE_ORIENT_ROW | MGE_ORIENT_COL */
+  uint8_t* row_codes;
+  float* row_scales;
+  uint8_t* col_codes;
+  float* col_scales;
+} mge_quant_fb_args;
+
+mge_status fp8_block_quantize(const mge_quant_fb_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * fp8_block_dequantize — the values element * scale of `batch` matrices of contiguous codes
+ * [R][C] with scales [R][ceil(C/128)] (1X128) or [ceil(R/128)][ceil(C/128)] (128X128) -> out
+ * [batch][R][C] bf16 or fp32 (one rounding).  E4M3's NaN codes (0x7f, 0xff) and NaN scales
+ * give NaN.
+ * Errors: MGE_ERR_INVALID_ARG for negative sizes, C not a multiple of 32, C or R above
+ * 2^31 - 256, an unknown block or dtype, NULL or misaligned (16-byte; scales 4) pointers.
+ * ---------------------------------------------------------------------------- */
+typedef struct mge_dequant_fb_args {
+  uint32_t struct_size;
+  int32_t block;             /* MGE_BLOCK_* */
+  int32_t batch, R, C;
+  int32_t out_dtype;         /* MGE_DTYPE_* */
+  const uint8_t* codes;
+  const float* scales;
+  void* out;
+} mge_dequant_fb_args;
+
+mge_status fp8_block_dequantize(const mge_dequant_fb_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * fp8_block_grouped_gemm — the grouped product of FP8 operands with one fp32 scale per block
+ * of 128: for every expert e and row r of its group, with b over the blocks of 128 of K,
+ *   out[r][n] = sum_b a_scale[s][b] w_scale_e[n / 128][b] (sum_{k in b} a[s][k] w_e[n][k])
+ * s = a_rows[r] (zeros where outside [0, src_rows)), or s = r without a map; so the tokens
+ * need no permuted copy (a_rows = perm_src).  a: codes [src_rows][K], scales
+ * [src_rows][ceil(K/128)]; w, w_scale: [host] arrays of E device pointers, codes [N][K] and
+ * scales [ceil(N/128)][ceil(K/128)] (fp8_block_quantize 1X128 ROW and 128X128 ROW; for the
+ * input gradient 128X128 COL, the weight as [K][N]).  out bf16 or fp32, one rounding.
+ * Groups, total_rows: as mxfp4_grouped_gemm.  Rows outside the groups are untouched.
+ * A block's 128 products are added on the matrix unit, in eights of which what lies 2^-13
+ * below the largest product is cut off; the blocks are added in fp32.
+ * A NaN (scale, E4M3 code 0x7f) reaches its row of out (a), or its column or the 128 columns
+ * of its scale, in its expert's rows (w), and no other element.
+ * Workspace: mge_gemm_fb_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for
+ * few rows over at most 64 experts.
+ * Errors: MGE_ERR_INVALID_ARG for E outside [1, 256], N or K not a positive multiple of 32,
+ * N above 2^22, rows or src_rows < 0 or >= 2^31 / K, src_rows other than rows without a map,
+ * an expert's weight of 2^31 bytes or more, an unknown dtype, NULL or misaligned pointers
+ * (codes, out, workspace 16 bytes, scales and a_rows 4), one of split_sizes / group_offsets
+ * without the other or E > 1 without both; MGE_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------------- */
+typedef struct mge_gemm_fb_args {
+  uint32_t struct_size;
+  int32_t E, N, K;
+  int64_t rows;                          /* rows of out (and of the groups) */
+  int64_t total_rows;
+  const int32_t* split_sizes;            /* [E] or NULL */
+  const int32_t* group_offsets;          /* [E] (or [E+1]) or NULL */
+  const int32_t* a_rows;                 /* [rows] or NULL */
+  int64_t src_rows;                      /* rows of a */
+  const uint8_t* a;
+  const float* a_scale;
+  const uint8_t* const* w;               /* [host] E pointers */
+  const float* const* w_scale;           /* [host] E pointers */
+  int32_t out_dtype;                     /* MGE_DTYPE_* */
+  void* out;                             /* [rows][N] */
+  void* workspace;
+  size_t workspace_bytes;
+} mge_gemm_fb_args;
+
+size_t mge_gemm_fb_workspace_bytes(const mge_gemm_fb_args* args);
+mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * fp8_block_grouped_wgrad — the gradient of every expert's weight in that product, both
+ * operands with blocks of 128 along the tokens: with b over the blocks of the group's rows,
+ *   dw_e[n][k] = sum_b dy_scale[n][b] x_scale[k][b] (sum_{t in b} dy[n][t] x[k][t])
+ * dy: codes [N][rows], scales [N][ceil(rows/128)]; x: codes [K][rows], scales
+ * [K][ceil(rows/128)] (fp8_block_quantize 1X128 COL of the permuted dY and X).  Groups:
+ * split_sizes / group_offsets, the offsets multiples of 128 (align = 128), so that no block
+ * belongs to two experts, and the codes between a group's last row and the next multiple of 32
+ * zero (as the permuted layout's padding is); both NULL (E = 1): all rows.  Other offsets give
+ * wrong results, but no access outside the buffers.
+ * dw: [host] array of E device pointers, [N][K] fp32 or bf16, overwritten (an expert without
+ * rows: zeros), or fp32 with accumulate != 0: added to.
+ * Sums, NaN: as fp8_block_grouped_gemm.
+ * Workspace: mge_wgrad_fb_workspace_bytes(args) bytes, 16-byte aligned.
+ * Errors: as fp8_block_grouped_gemm, N and K at most 2^22, rows a multiple of 32 in
+ * [0, 2^31 / max(N, K)), accumulate with bf16; MGE_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------------- */
+typedef struct mge_wgrad_fb_args {
+  uint32_t struct_size;
+  int32_t E, N, K;
+  int64_t rows;                          /* columns of dy and x (tokens, padding included) */
+  const int32_t* split_sizes;            /* [E] or NULL */
+  const int32_t* group_offsets;          /* [E] (or [E+1]) or NULL */
+  const uint8_t* dy;
+  const float* dy_scale;
+  const uint8_t* x;
+  const float* x_scale;
+  int32_t out_dtype;                     /* MGE_DTYPE_* */
+  int32_t accumulate;
+  void* const* dw;                       /* [host] E pointers */
+  void* workspace;
+  size_t workspace_bytes;
+} mge_wgrad_fb_args;
+
+size_t mge_wgrad_fb_workspace_bytes(const mge_wgrad_fb_args* args);
+mge_status fp8_block_grouped_wgrad(const mge_wgrad_fb_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * grouped_mlp_fwd_fp8_block — the gated expert MLP for serving on weights in FP8 with one
+ * fp32 scale per block of 128: per row r of expert e's group, with s = perm_src[r] (s = r
+ * without it; zeros where outside [0, x_rows)) and p = prob_perm[r] (1 without it),
+ *   [G U] = x[s] W_gate_up[e]^T,  h = p * silu(G) * U,  y_perm[r] = h W_down[e]^T
+ * as two fp8_block_grouped_gemm products; h is quantized (1 x 128) in the first one's
+ * epilogue and stays in the workspace.  x: codes [x_rows][H], scales [x_rows][ceil(H/128)],
+ * one row a token (rmsnorm_fwd, fp8_block_quantize).  Weights: [2F][H] (gate rows first) with
+ * scales [ceil(2F/128)][ceil(H/128)], [H][F] with [ceil(H/128)][ceil(F/128)].  split_sizes,
+ * group_offsets, perm_src, prob_perm: as moe_route_permute writes them (rows =
+ * mge_perm_rows); with none of them and E = 1 it is a dense gated MLP (a shared expert).
+ * total_rows: an upper bound of the groups' row count the caller knows (T*k), or 0.  Rows
+ * outside the groups are untouched.
+ * Workspace: mge_fwd_fb_workspace_bytes(args) bytes, 16-byte aligned.
+ * Errors: as fp8_block_grouped_gemm for both products; MGE_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------------- */
+typedef struct mge_fwd_fb_args {
+  uint32_t struct_size;
+  int32_t E, H, F;
+  int64_t rows;                          /* rows of y_perm (and of the groups) */
+  int64_t total_rows;
+  const int32_t* split_sizes;            /* [E] or NULL */
+  const int32_t* group_offsets;          /* [E] (or [E+1]) or NULL */
+  const int32_t* perm_src;               /* [rows] or NULL */
+  const float* prob_perm;                /* [rows] or NULL */
+  int64_t x_rows;                        /* rows of x */
+  const uint8_t* x;
+  const float* x_scale;
+  const uint8_t* const* w_gate_up;       /* [host] E pointers */
+  const float* const* w_gate_up_scale;   /* [host] E pointers */
+  const uint8_t* const* w_down;          /* [host] E pointers */
+  const float* const* w_down_scale;      /* [host] E pointers */
+  int32_t y_dtype;                       /* MGE_DTYPE_* */
+  void* y_perm;                          /* [rows][H] */
+  void* workspace;
+  size_t workspace_bytes;
+} mge_fwd_fb_args;
+
+size_t mge_fwd_fb_workspace_bytes(const mge_fwd_fb_args* args);
+mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* args, void* stream);
 
 /* ------------------------------------------------------------------------------ helpers */
 const char* mge_status_string(mge_status s);

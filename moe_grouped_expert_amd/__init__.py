@@ -7,9 +7,11 @@ outputs with torch.  The library must be built (``python -m
 moe_grouped_expert_amd.build``); without it every call raises.
 """
 from ._binding import (  # noqa: F401
-    BwdOut, FwdOut, MgeError, RouteOut, check_device_errors, fwd_saved_bytes, grouped_mlp_bwd, grouped_mlp_fwd,
+    BwdOut, FwdOut, MgeError, RmsnormOut, RouteOut, check_device_errors, fwd_saved_bytes, grouped_mlp_bwd, grouped_mlp_fwd,
     grouped_mlp_fwd_mxfp4, grouped_mlp_fwd_unfused,
     lib,
+    fp8_block_dequantize, fp8_block_grouped_gemm, fp8_block_grouped_wgrad, fp8_block_quantize, grouped_mlp_fwd_fp8_block,
+    rmsnorm_bwd, rmsnorm_fwd,
     moe_route_topk, moe_route_topk_bwd, mxfp4_dequantize, mxfp4_grouped_gemm, mxfp4_quantize,
     moe_route_permute, moe_router_bwd, mxfp8_quantize, perm_rows, profile_start, profile_stop, tensor_scale,
     unpermute_combine,

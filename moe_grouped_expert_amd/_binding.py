@@ -22,6 +22,7 @@ DTYPE = {"bf16": 0, "f32": 1}
 SCORE = {"softmax": 0, "sigmoid": 1}
 FORMAT = {"mxfp8": 0, "mxfp4": 1}
 ORIENT_ROW, ORIENT_COL = 1, 2
+BLOCK = {"1x128": 0, "128x128": 1}
 ROUTE_WANT_COL, ROUTE_PROB_GIVEN = 1, 2
 
 vp = C.c_void_p
@@ -124,8 +125,54 @@ class Gemm4Args(C.Structure):
                 ("w_scale", vp), ("out_dtype", i32), ("out", vp), ("workspace", vp), ("workspace_bytes", C.c_size_t)]
 
 
+class RmsnormArgs(C.Structure):
+    _fields_ = [("struct_size", u32), ("T", i32), ("H", i32), ("x_dtype", i32), ("weight_dtype", i32), ("y_dtype", i32),
+                ("eps", C.c_float), ("x_row_stride", i64), ("x", vp), ("residual", vp), ("weight", vp),
+                ("residual_out", vp), ("y", vp), ("codes", vp), ("scales", vp), ("rstd", vp)]
+
+
+class RmsnormBwdArgs(C.Structure):
+    _fields_ = [("struct_size", u32), ("T", i32), ("H", i32), ("x_dtype", i32), ("weight_dtype", i32), ("dy_dtype", i32),
+                ("x_row_stride", i64), ("dy_row_stride", i64), ("dy", vp), ("x", vp), ("weight", vp), ("rstd", vp),
+                ("d_residual", vp), ("dx", vp), ("d_weight", vp), ("workspace", vp), ("workspace_bytes", C.c_size_t)]
+
+
+class QuantFbArgs(C.Structure):
+    _fields_ = [("struct_size", u32), ("block", i32), ("batch", i32), ("R", i32), ("C", i32), ("in_batch_stride", i64),
+                ("in_row_stride", i64), ("in_", vp), ("rows", vp), ("src_rows", i64), ("orient", u32), ("row_codes", vp),
+                ("row_scales", vp), ("col_codes", vp), ("col_scales", vp)]
+
+
+class DequantFbArgs(C.Structure):
+    _fields_ = [("struct_size", u32), ("block", i32), ("batch", i32), ("R", i32), ("C", i32), ("out_dtype", i32),
+                ("codes", vp), ("scales", vp), ("out", vp)]
+
+
+class GemmFbArgs(C.Structure):
+    _fields_ = [("struct_size", u32), ("E", i32), ("N", i32), ("K", i32), ("rows", i64), ("total_rows", i64),
+                ("split_sizes", vp), ("group_offsets", vp), ("a_rows", vp), ("src_rows", i64), ("a", vp), ("a_scale", vp),
+                ("w", vp), ("w_scale", vp), ("out_dtype", i32), ("out", vp), ("workspace", vp),
+                ("workspace_bytes", C.c_size_t)]
+
+
+class WgradFbArgs(C.Structure):
+    _fields_ = [("struct_size", u32), ("E", i32), ("N", i32), ("K", i32), ("rows", i64), ("split_sizes", vp),
+                ("group_offsets", vp), ("dy", vp), ("dy_scale", vp), ("x", vp), ("x_scale", vp), ("out_dtype", i32),
+                ("accumulate", i32), ("dw", vp), ("workspace", vp), ("workspace_bytes", C.c_size_t)]
+
+
+class FwdFbArgs(C.Structure):
+    _fields_ = [("struct_size", u32), ("E", i32), ("H", i32), ("F", i32), ("rows", i64), ("total_rows", i64),
+                ("split_sizes", vp), ("group_offsets", vp), ("perm_src", vp), ("prob_perm", vp), ("x_rows", i64), ("x", vp),
+                ("x_scale", vp), ("w_gate_up", vp), ("w_gate_up_scale", vp), ("w_down", vp), ("w_down_scale", vp),
+                ("y_dtype", i32), ("y_perm", vp), ("workspace", vp), ("workspace_bytes", C.c_size_t)]
+
+
 _LIB = None
-EXPORTS = ["moe_route_topk", "moe_route_topk_bwd", "mxfp4_quantize", "mxfp4_dequantize", "mge_gemm4_workspace_bytes",
+EXPORTS = ["rmsnorm_fwd", "mge_rmsnorm_bwd_workspace_bytes", "rmsnorm_bwd", "fp8_block_quantize", "fp8_block_dequantize",
+           "mge_gemm_fb_workspace_bytes", "fp8_block_grouped_gemm", "mge_wgrad_fb_workspace_bytes",
+           "fp8_block_grouped_wgrad", "mge_fwd_fb_workspace_bytes", "grouped_mlp_fwd_fp8_block",
+           "moe_route_topk", "moe_route_topk_bwd", "mxfp4_quantize", "mxfp4_dequantize", "mge_gemm4_workspace_bytes",
            "mxfp4_grouped_gemm", "mge_fwd_mxfp4_workspace_bytes", "grouped_mlp_fwd_mxfp4",
            "mge_perm_rows", "mge_route_workspace_bytes", "moe_route_permute", "moe_route_permute_noalloc",
            "mxfp8_quantize",
@@ -167,7 +214,17 @@ def lib():
         L.mge_gemm4_workspace_bytes.argtypes = [C.POINTER(Gemm4Args)]
         L.mge_fwd_mxfp4_workspace_bytes.restype = C.c_size_t
         L.mge_fwd_mxfp4_workspace_bytes.argtypes = [C.POINTER(FwdArgs)]
-        for name, st in (("moe_route_topk", RouteTopkArgs), ("moe_route_topk_bwd", RouteTopkBwdArgs),
+        L.mge_rmsnorm_bwd_workspace_bytes.restype = C.c_size_t
+        L.mge_rmsnorm_bwd_workspace_bytes.argtypes = [i32, i32]
+        for name, st in (("mge_gemm_fb_workspace_bytes", GemmFbArgs), ("mge_wgrad_fb_workspace_bytes", WgradFbArgs),
+                         ("mge_fwd_fb_workspace_bytes", FwdFbArgs)):
+            getattr(L, name).restype = C.c_size_t
+            getattr(L, name).argtypes = [C.POINTER(st)]
+        for name, st in (("rmsnorm_fwd", RmsnormArgs), ("rmsnorm_bwd", RmsnormBwdArgs),
+                         ("fp8_block_quantize", QuantFbArgs), ("fp8_block_dequantize", DequantFbArgs),
+                         ("fp8_block_grouped_gemm", GemmFbArgs), ("fp8_block_grouped_wgrad", WgradFbArgs),
+                         ("grouped_mlp_fwd_fp8_block", FwdFbArgs),
+                         ("moe_route_topk", RouteTopkArgs), ("moe_route_topk_bwd", RouteTopkBwdArgs),
                          ("mxfp4_quantize", Quant4Args), ("mxfp4_dequantize", Dequant4Args),
                          ("mxfp4_grouped_gemm", Gemm4Args), ("grouped_mlp_fwd_mxfp4", FwdArgs),
                          ("moe_route_permute", RouteArgs), ("moe_route_permute_noalloc", RouteArgs),
@@ -944,4 +1001,342 @@ def grouped_mlp_fwd_mxfp4(rt: RouteOut, w_gate_up, w_down, w_gate_up_scale, w_do
     if out.workspace is not None:
         a.workspace, a.workspace_bytes = out.workspace.data_ptr(), out.workspace.numel()
     _call("grouped_mlp_fwd_mxfp4", a, dev)
+    return out
+
+
+# ------------------------------------------------------------------------------ norm
+
+@dataclass
+class RmsnormOut:
+    y: Optional[torch.Tensor] = None
+    codes: Optional[torch.Tensor] = None
+    scales: Optional[torch.Tensor] = None
+    residual: Optional[torch.Tensor] = None
+    rstd: Optional[torch.Tensor] = None
+
+
+def _rows_of(t: torch.Tensor, what: str):
+    """[..., H] as rows: (T, H, row stride) of a contiguous tensor, or of a matrix of contiguous rows."""
+    if t.dim() < 1 or t.dtype not in _TORCH_DTYPE:
+        raise ValueError(f"{what} must be [..., H], float32 or bfloat16")
+    H = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // H if H else 0), H, H
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{what} must be contiguous, or a matrix of contiguous rows")
+    return t.shape[0], H, t.stride(0) if t.shape[0] > 1 else H
+
+
+def _like(t, shape, dtype, what: str):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {dtype} {list(shape)}")
+
+
+def _fblocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+                form: Optional[str] = None, want_y: bool = True, y_dtype: str = "bf16",
+                out: Optional[RmsnormOut] = None) -> RmsnormOut:
+    """y = r * rstd * weight with r = x + residual and rstd = 1 / sqrt(mean(r^2) + eps) over the last axis.
+    x: [..., H] bf16 or fp32, contiguous or a matrix of strided rows; residual: the same type, contiguous; weight: [H]
+    bf16 or fp32.  -> RmsnormOut: y (bf16 or f32 by y_dtype; None without want_y), residual (r, rounded to x's type;
+    None without a residual), rstd fp32 [...] and with form="fp8_block" codes uint8 [..., H] and scales fp32
+    [..., ceil(H / 128)], the 1x128 row form of the unrounded y.  out: the tensors to write into (out.residual may be
+    `residual` itself); those absent there are not written."""
+    T, H, ld = _rows_of(x, "x")
+    if form not in (None, "fp8_block"):
+        raise ValueError(f"form must be None or 'fp8_block', not {form!r}")
+    if y_dtype not in DTYPE:
+        raise ValueError(f"y_dtype must be 'bf16' or 'f32', not {y_dtype!r}")
+    dev, lead = x.device, tuple(x.shape[:-1])
+    ydt = torch.bfloat16 if y_dtype == "bf16" else torch.float32
+    _on(dev, weight, residual)
+    if weight.dim() != 1 or weight.shape[0] != H or weight.dtype not in _TORCH_DTYPE or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous [H], float32 or bfloat16")
+    if residual is not None:
+        _like(residual, x.shape, x.dtype, "residual")
+    if out is None:
+        _need(want_y or form is not None, "no output asked for (want_y or form)")
+        f32 = torch.float32
+        out = RmsnormOut(y=x.new_empty(x.shape, dtype=ydt) if want_y else None,
+                         residual=None if residual is None else x.new_empty(x.shape), rstd=x.new_empty(lead, dtype=f32))
+        if form is not None:
+            out.codes, out.scales = x.new_empty(x.shape, dtype=torch.uint8), x.new_empty(lead + (_fblocks(H),), dtype=f32)
+    else:
+        _on(dev, out.y, out.codes, out.scales, out.residual, out.rstd)
+        _need((residual is None) == (out.residual is None), "out.residual goes with residual")
+        for t, shape, dt, what in ((out.y, x.shape, ydt, "out.y"), (out.codes, x.shape, torch.uint8, "out.codes"),
+                                   (out.scales, lead + (_fblocks(H),), torch.float32, "out.scales"),
+                                   (out.residual, x.shape, x.dtype, "out.residual"), (out.rstd, lead, torch.float32, "out.rstd")):
+            if t is not None:
+                _like(t, shape, dt, what)
+    a = RmsnormArgs(C.sizeof(RmsnormArgs), T, H, _TORCH_DTYPE[x.dtype], _TORCH_DTYPE[weight.dtype], DTYPE[y_dtype], eps, ld,
+                    x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(out.residual), _ptr(out.y), _ptr(out.codes),
+                    _ptr(out.scales), _ptr(out.rstd))
+    _call("rmsnorm_fwd", a, dev)
+    return out
+
+
+def rmsnorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                d_residual: Optional[torch.Tensor] = None, want_dw: bool = True, out=None):
+    """(dx, d_weight) of rmsnorm_fwd: x is what the norm was taken of (the forward's residual, or x without one), rstd
+    the forward's.  dx has x's type, d_residual (x's type) added: the gradient of x and of the residual alike.
+    d_weight: fp32 [H], None without want_dw.  out: the pair to write into."""
+    T, H, ld = _rows_of(x, "x")
+    Ty, Hy, dld = _rows_of(dy, "dy")
+    _need(tuple(dy.shape) == tuple(x.shape), "dy must have x's shape")
+    dev, lead = x.device, tuple(x.shape[:-1])
+    _on(dev, dy, weight, rstd, d_residual)
+    if weight.dim() != 1 or weight.shape[0] != H or weight.dtype not in _TORCH_DTYPE or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous [H], float32 or bfloat16")
+    _like(rstd, lead, torch.float32, "rstd")
+    if d_residual is not None:
+        _like(d_residual, x.shape, x.dtype, "d_residual")
+    if out is None:
+        dx, dw = x.new_empty(x.shape), x.new_empty(H, dtype=torch.float32) if want_dw else None
+    else:
+        dx, dw = out
+        _on(dev, dx, dw)
+        _like(dx, x.shape, x.dtype, "dx")
+        if dw is not None:
+            _like(dw, (H,), torch.float32, "d_weight")
+    need = lib().mge_rmsnorm_bwd_workspace_bytes(T, H) if dw is not None else 0
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
+    a = RmsnormBwdArgs(C.sizeof(RmsnormBwdArgs), T, H, _TORCH_DTYPE[x.dtype], _TORCH_DTYPE[weight.dtype],
+                       _TORCH_DTYPE[dy.dtype], ld, dld, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+                       _ptr(d_residual), dx.data_ptr(), _ptr(dw), _ptr(ws), need)
+    _call("rmsnorm_bwd", a, dev)
+    return dx, dw
+
+
+# ------------------------------------------------------------------------------ FP8, blocks of 128
+
+def _is_f32(t) -> bool:
+    return t.dtype == torch.float32 and t.is_contiguous()
+
+
+def fp8_block_quantize(x: torch.Tensor, orient: str = "row", block: str = "1x128", rows: Optional[torch.Tensor] = None,
+                       out=None):
+    """BF16 [..., R, C] -> (row_codes, row_scales, col_codes, col_scales) in E4M3 with one fp32 scale per block of 128
+    (absent ones None).  block "1x128": scales [..., R, ceil(C/128)], and of the transposed form codes [..., C, Rp] (R
+    padded to 32) with scales [..., C, ceil(R/128)]; block "128x128": scales [..., ceil(R/128), ceil(C/128)], the
+    transposed form's the transpose.  orient "row", "col" or "both".  rows: int32 map of the output's rows (a 1x128
+    matrix): row r is x[rows[r]], zeros where that is outside x.  x: contiguous, or a matrix of strided rows."""
+    shape = x.shape
+    if x.dtype != torch.bfloat16 or len(shape) < 2:
+        raise ValueError("x must be bfloat16 [..., R, C]")
+    if orient not in ("row", "col", "both"):
+        raise ValueError(f"orient must be 'row', 'col' or 'both', not {orient!r}")
+    if block not in BLOCK:
+        raise ValueError(f"block must be '1x128' or '128x128', not {block!r}")
+    src, Cc = shape[-2], shape[-1]
+    ld = Cc
+    if not x.is_contiguous():
+        if len(shape) != 2 or (Cc > 1 and x.stride(1) != 1) or (src > 1 and x.stride(0) < Cc):
+            raise ValueError("x must be contiguous, or a matrix of contiguous rows")
+        ld = x.stride(0) if src > 1 else Cc
+    lead = tuple(shape[:-2])
+    batch = 1
+    for d in lead:
+        batch *= d
+    dev = x.device
+    _on(dev, rows)
+    R = src
+    if rows is not None:
+        _need(rows.dim() == 1 and rows.dtype == torch.int32 and rows.is_contiguous(), "rows must be contiguous int32 [R]")
+        _need(len(shape) == 2 and block == "1x128", "rows needs a matrix and block='1x128'")
+        R = rows.shape[0]
+    Rp, nr, nc = (R + 31) // 32 * 32, _fblocks(R), _fblocks(Cc)
+    want_row, want_col = orient != "col", orient != "row"
+    tile = block == "128x128"
+    shapes = ((R, Cc), (nr, nc) if tile else (R, nc), (Cc, Rp), (nc, nr) if tile else (Cc, nr))
+    used = (want_row, want_row, want_col, want_col)
+    if out is None:
+        dts = (torch.uint8, torch.float32, torch.uint8, torch.float32)
+        out = [x.new_empty(lead + s, dtype=dt) if u else None for s, dt, u in zip(shapes, dts, used)]
+    else:
+        _on(dev, *out)
+        for i, (t, s, u) in enumerate(zip(out, shapes, used)):
+            _need(not u or (t is not None and tuple(t.shape) == lead + s and (_is_f32(t) if i & 1 else _is_u8(t))),
+                  "out must be contiguous uint8 codes and float32 scales of the outputs' sizes")
+    rc, rs, cc, cs = (t if u else None for t, u in zip(out, used))
+    a = QuantFbArgs(C.sizeof(QuantFbArgs), BLOCK[block], batch, R, Cc, src * ld, ld, x.data_ptr(), _ptr(rows), src,
+                    (ORIENT_ROW if want_row else 0) | (ORIENT_COL if want_col else 0), _ptr(rc), _ptr(rs), _ptr(cc), _ptr(cs))
+    _call("fp8_block_quantize", a, dev)
+    return rc, rs, cc, cs
+
+
+def fp8_block_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype: str = "bf16",
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Values [..., R, C] (bf16 or f32) of E4M3 codes uint8 [..., R, C] and their fp32 scales, [..., R, ceil(C/128)] or
+    [..., ceil(R/128), ceil(C/128)] (told apart by their shape)."""
+    if out_dtype not in DTYPE:
+        raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
+    if codes.dim() < 2 or not _is_u8(codes) or not _is_f32(scales):
+        raise ValueError("codes must be contiguous uint8 [..., R, C], scales contiguous float32")
+    lead, R, Cc = tuple(codes.shape[:-2]), codes.shape[-2], codes.shape[-1]
+    rowwise = tuple(scales.shape) == lead + (R, _fblocks(Cc))
+    if not rowwise and tuple(scales.shape) != lead + (_fblocks(R), _fblocks(Cc)):
+        raise ValueError("scales must be [..., R, ceil(C/128)] or [..., ceil(R/128), ceil(C/128)]")
+    dev = codes.device
+    dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    _on(dev, scales, out)
+    if out is None:
+        out = codes.new_empty(codes.shape, dtype=dt)
+    else:
+        _like(out, codes.shape, dt, "out")
+    batch = 1
+    for d in lead:
+        batch *= d
+    a = DequantFbArgs(C.sizeof(DequantFbArgs), BLOCK["1x128" if rowwise else "128x128"], batch, R, Cc, DTYPE[out_dtype],
+                      codes.data_ptr(), scales.data_ptr(), out.data_ptr())
+    _call("fp8_block_dequantize", a, dev)
+    return out
+
+
+def _expert_ptrs_of(w, E: int, rows: int, cols: int, dev, dtype, what: str):
+    """_expert_ptrs for matrices of any type."""
+    if isinstance(w, torch.Tensor):
+        if w.shape != (E, rows, cols) or w.dtype != dtype or not w.is_contiguous() or w.device != dev:
+            raise ValueError(f"{what} must be contiguous {dtype} [{E}, {rows}, {cols}] on {dev}")
+        p, n = w.data_ptr(), rows * cols * w.element_size()
+        return (vp * E)(*range(p, p + E * n, n)) if E > 1 and n else (vp * E)(*[p] * E)
+    ts = list(w)
+    if len(ts) != E or not all(t.shape == (rows, cols) and t.dtype == dtype and t.is_contiguous() and t.device == dev for t in ts):
+        raise ValueError(f"{what} must be {E} contiguous {dtype} matrices [{rows}, {cols}] on {dev}")
+    return _ptr_array(ts)
+
+
+def _check_groups(split_sizes, group_offsets, E: int):
+    for t in (split_sizes, group_offsets):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < E):
+            raise ValueError("split_sizes and group_offsets must be contiguous int32 with an entry for each expert")
+
+
+def _codes_rows(a, a_scale, what: str):
+    if a.dim() != 2 or not _is_u8(a) or not _is_f32(a_scale) or tuple(a_scale.shape) != (a.shape[0], _fblocks(a.shape[1])):
+        raise ValueError(f"{what} must be contiguous uint8 [rows, K] with float32 scales [rows, ceil(K/128)]")
+    return a.shape
+
+
+def _work(need: int, ws, like):
+    """The workspace of a call: the caller's, or a new one of the bytes it needs."""
+    if ws is not None:
+        _need(ws.is_contiguous(), "workspace must be contiguous")
+        return ws
+    return like.new_empty(need, dtype=torch.uint8) if need else None
+
+
+def fp8_block_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, w, w_scale, split_sizes: Optional[torch.Tensor] = None,
+                           group_offsets: Optional[torch.Tensor] = None, a_rows: Optional[torch.Tensor] = None,
+                           out_dtype: str = "bf16", total_rows: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[r] = a[r] w_e^T for the rows r of every expert e, in FP8 with one fp32 scale per block of 128.
+    a: E4M3 codes [rows, K] with a_scale [rows, ceil(K/128)]; w: codes [E, N, K] with w_scale [E, ceil(N/128),
+    ceil(K/128)] (stacked, or sequences of E matrices).  a_rows: int32 [rows of out], row r then reads a[a_rows[r]]
+    (zeros where that is outside a): a route's perm_src.  split_sizes, group_offsets, total_rows: as
+    mxfp4_grouped_gemm.  Rows outside the groups are left as they were.  For the input gradient pass the transposed
+    form of the weight."""
+    if out_dtype not in DTYPE:
+        raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
+    src, K = _codes_rows(a, a_scale, "a")
+    dev = a.device
+    _on(dev, a_scale, out, split_sizes, group_offsets, a_rows, workspace)
+    E = len(w)
+    stacked = isinstance(w, torch.Tensor)
+    if E < 1 or len(w_scale) != E or (w.dim() != 3 if stacked else w[0].dim() != 2):
+        raise ValueError("w must be [E, N, K] with w_scale [E, ceil(N/128), ceil(K/128)]")
+    N = w.shape[1] if stacked else w[0].shape[0]
+    rows = src
+    if a_rows is not None:
+        _need(a_rows.dim() == 1 and a_rows.dtype == torch.int32 and a_rows.is_contiguous(), "a_rows must be contiguous int32 [rows]")
+        rows = a_rows.shape[0]
+    _check_groups(split_sizes, group_offsets, E)
+    dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    if out is None:
+        out = a.new_empty((rows, N), dtype=dt)
+    else:
+        _like(out, (rows, N), dt, "out")
+    wp = _expert_ptrs_of(w, E, N, K, dev, torch.uint8, "w")
+    wsp = _expert_ptrs_of(w_scale, E, _fblocks(N), _fblocks(K), dev, torch.float32, "w_scale")
+    g = GemmFbArgs(C.sizeof(GemmFbArgs), E, N, K, rows, total_rows or 0, _ptr(split_sizes), _ptr(group_offsets), _ptr(a_rows),
+                   src, a.data_ptr(), a_scale.data_ptr(), C.addressof(wp), C.addressof(wsp), DTYPE[out_dtype], out.data_ptr())
+    ws = _work(lib().mge_gemm_fb_workspace_bytes(C.byref(g)), workspace, a)
+    if ws is not None:
+        g.workspace, g.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call("fp8_block_grouped_gemm", g, dev)
+    return out
+
+
+def fp8_block_grouped_wgrad(dy: torch.Tensor, dy_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
+                            split_sizes: Optional[torch.Tensor] = None, group_offsets: Optional[torch.Tensor] = None,
+                            out_dtype: str = "f32", accumulate: bool = False, out=None,
+                            workspace: Optional[torch.Tensor] = None):
+    """dw [E, N, K] (f32 or bf16): the gradient of every expert's weight [N, K] from the transposed forms of the
+    permuted dY, codes [N, rows] with dy_scale [N, ceil(rows/128)], and X, [K, rows] with [K, ceil(rows/128)]
+    (fp8_block_quantize "col").  split_sizes, group_offsets: the groups, at multiples of 128 rows (align=128), with
+    zero rows after each up to the next multiple of 32; absent: one expert, all rows.  out: [E, N, K], or a sequence of
+    E matrices; accumulate adds to it (f32)."""
+    if out_dtype not in DTYPE:
+        raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
+    N, rows = _codes_rows(dy, dy_scale, "dy")
+    K, xrows = _codes_rows(x, x_scale, "x")
+    _need(xrows == rows, "dy and x must have the same rows")
+    dev = dy.device
+    _on(dev, dy_scale, x, x_scale, split_sizes, group_offsets, workspace)
+    E = 1 if split_sizes is None else split_sizes.numel()
+    _check_groups(split_sizes, group_offsets, E)
+    dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    if out is None:
+        _need(not accumulate, "accumulate needs out")
+        out = dy.new_empty((E, N, K), dtype=dt)
+    ptrs = _expert_ptrs_of(out, E, N, K, dev, dt, "out")
+    g = WgradFbArgs(C.sizeof(WgradFbArgs), E, N, K, rows, _ptr(split_sizes), _ptr(group_offsets), dy.data_ptr(),
+                    dy_scale.data_ptr(), x.data_ptr(), x_scale.data_ptr(), DTYPE[out_dtype], 1 if accumulate else 0,
+                    C.addressof(ptrs))
+    ws = _work(lib().mge_wgrad_fb_workspace_bytes(C.byref(g)), workspace, dy)
+    if ws is not None:
+        g.workspace, g.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call("fp8_block_grouped_wgrad", g, dev)
+    return out
+
+
+def grouped_mlp_fwd_fp8_block(rt: Optional[RouteOut], x: torch.Tensor, x_scale: torch.Tensor, w_gate_up, w_down, w_gate_up_scale,
+                              w_down_scale, y_dtype: str = "bf16", out: Optional[FwdOut] = None) -> FwdOut:
+    """The expert MLP for serving on weights in FP8 with one fp32 scale per block of 128: w_gate_up [E, 2F, H] and w_down
+    [E, H, F] E4M3 codes with their scales ([E, ceil(2F/128), ceil(H/128)], [E, ceil(H/128), ceil(F/128)]).
+    x: codes [T, H] with x_scale [T, ceil(H/128)], one row a token (rmsnorm_fwd, fp8_block_quantize); the route's maps
+    (moe_route_permute with x=None will do) gather them.  rt None: one expert that all rows of x go through, with weight
+    1 (a dense gated MLP).  -> FwdOut with y_perm [R, H] ([T, H] without a route)."""
+    _need(y_dtype in DTYPE, f"y_dtype must be 'bf16' or 'f32', not {y_dtype!r}")
+    T, H = _codes_rows(x, x_scale, "x")
+    dev = x.device
+    E = len(w_gate_up) if rt is None else rt.E
+    _need(rt is not None or E == 1, "without a route there is one expert")
+    _need(rt is None or rt.T == T, "x must have a row for each of the route's tokens")
+    R = T if rt is None else rt.R
+    F = (w_gate_up.shape[1] if isinstance(w_gate_up, torch.Tensor) else w_gate_up[0].shape[0]) // 2
+    dt = torch.bfloat16 if y_dtype == "bf16" else torch.float32
+    _on(dev, x_scale)
+    if rt is not None:
+        _on(dev, rt.split_sizes, rt.group_offsets, rt.perm_src, rt.prob_perm)
+    if out is None:
+        out = FwdOut(y_perm=x.new_empty((R, H), dtype=dt), h=None)
+    else:
+        _on(dev, out.y_perm, out.workspace)
+        _like(out.y_perm, (R, H), dt, "out.y_perm")
+    u8, f32 = torch.uint8, torch.float32
+    keep = [_expert_ptrs_of(w_gate_up, E, 2 * F, H, dev, u8, "w_gate_up"),
+            _expert_ptrs_of(w_gate_up_scale, E, _fblocks(2 * F), _fblocks(H), dev, f32, "w_gate_up_scale"),
+            _expert_ptrs_of(w_down, E, H, F, dev, u8, "w_down"),
+            _expert_ptrs_of(w_down_scale, E, _fblocks(H), _fblocks(F), dev, f32, "w_down_scale")]
+    maps = (None,) * 4 if rt is None else (_ptr(rt.split_sizes), _ptr(rt.group_offsets), _ptr(rt.perm_src), _ptr(rt.prob_perm))
+    a = FwdFbArgs(C.sizeof(FwdFbArgs), E, H, F, R, T if rt is None else rt.T * rt.k, *maps, T, x.data_ptr(), x_scale.data_ptr(),
+                  *(C.addressof(k) for k in keep), DTYPE[y_dtype], out.y_perm.data_ptr())
+    out.workspace = _work(lib().mge_fwd_fb_workspace_bytes(C.byref(a)), out.workspace, x)
+    if out.workspace is not None:
+        a.workspace, a.workspace_bytes = out.workspace.data_ptr(), out.workspace.numel() * out.workspace.element_size()
+    _call("grouped_mlp_fwd_fp8_block", a, dev)
     return out

@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmge.so")
 SOURCES = ["api.cpp", "route.hip", "quant.hip", "gemm_host.cpp", "gemm_mx.hip", "gemm_bf16.hip", "combine.hip", "swiglu.hip",
-           "topk.hip", "quant4.hip", "gemm4.hip", "gemm_mxfp4.hip"]
+           "topk.hip", "quant4.hip", "gemm4.hip", "gemm_mxfp4.hip",
+           "api_fb.cpp", "norm.hip", "quant_fb.hip", "stream_fb.hip", "gemm_fb.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "-x", "hip", "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -71,9 +71,7 @@ ProfScope::~ProfScope() {
   if (slot < int(g_prof_rec.size())) hipEventRecord(g_prof_rec[slot].stop, stream);
 }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
-static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Gate-up (SwiGLU) GEMM: an expert's M-tile remainder under 4 joins its last raster band.
 // Two same-job A/B pairs on the Mixtral-shaped training step: gate-up 1.97 -> 1.93 and
@@ -88,18 +86,6 @@ constexpr int kMergeShortBand = 1;
 // grows from 3.0 to 4.6 GB per launch, so it keeps 8.
 constexpr int kBandDwDown = 4;
 constexpr int kBandDwGateUp = 8;
-
-// Bump allocator over the caller's workspace.
-struct Carve {
-  uint8_t* base;
-  size_t used = 0;
-  explicit Carve(void* b) : base(static_cast<uint8_t*>(b)) {}
-  void* take(size_t bytes) {
-    void* p = base ? base + used : nullptr;
-    used += up256(bytes);
-    return p;
-  }
-};
 
 static mge_status check_common(int T, int E, int k, int H, int align) {
   MGE_REQUIRE(T >= 0, "T must be >= 0 (got %d)", T);
@@ -981,7 +967,6 @@ static mge_status check_topk(int T, int E, int k, int score, int dtype, float sc
   MGE_REQUIRE((reinterpret_cast<uintptr_t>(logits) & (elem - 1)) == 0, "logits misaligned");
   return MGE_OK;
 }
-static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 // rows of logits may be read 16 bytes at a time
 static bool topk_vec(const void* logits, int dtype, int64_t ld) {
   return aligned16(logits) && (ld * (dtype == MGE_DTYPE_F32 ? 4 : 2)) % 16 == 0;

@@ -1,0 +1,492 @@
+// Grouped products of FP8 operands with one fp32 scale per block of 128, for groups of many rows:
+//   C[r][n]   = sum over blocks b of sa[r][b] sw_e[n / 128][b] (sum over k in b of A[r][k] W_e[n][k])
+//   dW_e[n][k] = sum over blocks b of sy[n][b] sx[k][b] (sum over the tokens t in b of dY[t][n] X[t][k])
+// The matrix unit has no fp32 scales, so a block's 128 products are summed on it from zero
+// (v_mfma_f32_16x16x128_f8f6f4, one instruction a block) and the vector unit adds the partial sum,
+// scaled, to the fp32 accumulators: acc += d * s, 4 FMAs for each 32-cycle matrix instruction.
+//
+// The weights (for dW: X) are the matrix unit's row operand and the tokens (dY) its columns, so a
+// lane's results are 4 consecutive columns of one row of C: its token scale is one register, the
+// weight scale is the same in all lanes (dW has a scale a column of C too, a second multiply), and
+// the results leave as 4 consecutive values.
+//
+// Tiles of 256 x 256, 8 waves, each 128 x 64 (8 x 4 blocks of 16 x 16, 128 accumulators: they have to
+// be vector registers, which only half of the file is for one wave a SIMD, so two waves share one).
+// Operands come HBM -> LDS directly in slices of 128 bytes, two stages of 64 KB.  The tokens' fragments
+// of a slice (32 registers) are read first and the weights' streamed behind the matrix instructions, so
+// the tokens' half of a stage and the first half of the weights' are free at mid-slice and refilled from
+// there on (one and a half slices to arrive), the rest at the slice's end.
+#include "gemm_impl.hpp"
+
+#include "fp8b.hpp"
+
+namespace mge {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int FT = 256;                       // rows of a tile on both sides
+constexpr int FT_THREADS = 512;
+constexpr int FT_OP = FT * 128;               // bytes of an operand in a stage
+constexpr int FT_STAGE = 2 * FT_OP;           // tokens, then weights
+constexpr int FT_SCALES = 2 * FT_STAGE;       // then, per stage, the tokens' scales and (dW) the row operand's
+constexpr int FT_LDS = FT_SCALES + 2 * 2 * FT * 4;
+
+// 4 x 4 transpose over the lanes 16 apart: lane 16q + i gives v[j] for j = 0..3 and gets v[q] of the
+// lanes 16p + i in v[p]
+__device__ __forceinline__ void transpose4(uint32_t* v) {
+  const U32Pair a = permlane32_swap(v[0], v[2]), b = permlane32_swap(v[1], v[3]);
+  const U32Pair c = permlane16_swap(a.a, b.a), d = permlane16_swap(a.b, b.b);
+  v[0] = c.a; v[1] = c.b; v[2] = d.a; v[3] = d.b;
+}
+
+// 4 bytes per lane from buffer offset `voff` straight into LDS at lds_addr + 4 * lane
+__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds_addr), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+
+struct FtTile {
+  int valid, e, off, m_valid, m0, n0, nkt, kbase, khi;
+};
+
+// KR: dW (FbWgrad), else C (FbGemm).  SW: the SwiGLU epilogue.
+template <bool KR, bool SW, int OUT, typename P>
+__device__ __forceinline__ void fb_tile_body(const P& p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int32_t s_prefix[G_MAXE + 1];
+  __shared__ int32_t s_mtiles[G_MAXE];
+  __shared__ uint32_t s_amax[SW ? 2 * FT : 1];
+  const uint32_t lds_base = uniform(int(uint32_t(reinterpret_cast<uintptr_t>(smem))));
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = uniform(tid >> 6);
+  const int wn = wave & 1, wt = wave >> 1;    // the wave's half of each 128 weight rows, its 64 tokens
+  // derived again from an opaque copy of the lane at the top of every tile and after its K loop, so
+  // that one phase's addresses are not kept in registers through the other
+  int i16 = lane & 15, q = lane >> 4;
+  auto rederive_lane = [&]() {
+    int v = lane;
+    asm volatile("" : "+v"(v));
+    i16 = v & 15;
+    q = v >> 4;
+  };
+
+  int ncols = KR ? p.K : p.N;                              // columns of C
+  if constexpr (SW) ncols = p.F;
+  const int per = SW ? FT / 2 : FT;
+  const int ntiles = (ncols + per - 1) / per;
+  auto group_off = [&](int off) { return off < 0 ? 0 : (off > p.rows ? p.rows : off); };
+  auto group_size = [&](int size, int off) { return size < 0 ? 0 : (size > p.rows - off ? p.rows - off : size); };
+  if constexpr (!KR) {
+    for (int e = tid; e < p.E; e += FT_THREADS)
+      s_mtiles[e] = ((p.sizes ? group_size(p.sizes[e], group_off(p.offs[e])) : p.rows) + FT - 1) / FT;
+    __syncthreads();
+    if (tid == 0) {
+      int acc = 0;
+      for (int e = 0; e < p.E; ++e) {
+        s_prefix[e] = acc;
+        acc += s_mtiles[e] * ntiles;
+      }
+      s_prefix[p.E] = acc;
+    }
+    __syncthreads();
+  }
+  const int ymt = KR ? (p.N + FT - 1) / FT : 0;
+  const int total = KR ? p.E * ymt * ntiles : uniform(s_prefix[p.E]);
+  const int nwg = gridDim.x;
+  int vid = blockIdx.x;
+  if ((nwg & 7) == 0) vid = (blockIdx.x & 7) * (nwg >> 3) + (blockIdx.x >> 3);
+
+  auto decode = [&](int tile) {
+    FtTile t{};
+    t.valid = tile < total;
+    if (!t.valid) return t;
+    int local, mtn;
+    if constexpr (KR) {
+      t.e = tile / (ymt * ntiles);
+      local = tile - t.e * ymt * ntiles;
+      mtn = ymt;
+    } else {
+      int lo = 0, hi = p.E - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_prefix[mid] <= tile) lo = mid; else hi = mid - 1;
+      }
+      t.e = uniform(lo);
+      local = tile - uniform(s_prefix[t.e]);
+      mtn = uniform(s_mtiles[t.e]);
+    }
+    // bands of 8 token tiles, walked across the columns, tokens fastest (as in the MX kernels)
+    const int nband = (mtn + 7) / 8;
+    const int band = min(local / (8 * ntiles), nband - 1);
+    const int within = local - band * 8 * ntiles;
+    const int gm = band == nband - 1 ? mtn - band * 8 : 8;
+    t.m0 = (band * 8 + within % gm) * FT;
+    t.n0 = (within / gm) * per;
+    t.off = p.sizes ? uniform(group_off(ld_uniform(p.offs, t.e))) : 0;
+    const int size = p.sizes ? uniform(group_size(ld_uniform(p.sizes, t.e), t.off)) : p.rows;
+    if constexpr (KR) {
+      // the group's tokens; its last 32 may hold padding, which is zero
+      const int span = group_size((size + 31) / 32 * 32, t.off);
+      t.m_valid = p.N;
+      t.kbase = t.off & ~127;
+      t.khi = t.off + span;
+      t.nkt = size > 0 ? (t.khi - t.kbase + 127) / 128 : 0;
+    } else {
+      t.m_valid = size;
+      t.khi = p.K;
+      t.nkt = (p.K + 127) / 128;
+    }
+    return t;
+  };
+
+  // LDS rows of a DMA instruction: 8, lane l row l / 8, chunk l % 8; the lane loads the chunk that the
+  // swizzle puts there: (l % 8) ^ (l / 16), that ^ 4 in odd instructions
+  const int lchunk = ((lane & 7) ^ (lane >> 4)) * 16;
+  const uint32_t ldw = KR ? uint32_t(p.rows) : uint32_t(p.K);   // bytes of an operand row
+
+  for (int item = vid; item < total; item += nwg) {
+    const FtTile t = decode(item);
+    rederive_lane();
+    const int tread = (wt * 64 + i16) * 128 + ((q ^ ((i16 >> 1) & 7)) << 4);
+    const int wread = FT_OP + (wn * 64 + i16) * 128 + ((q ^ ((i16 >> 1) & 7)) << 4);
+    // ---- the tile's operands
+    i32x4 rT, rW[2], rS;
+    uint32_t toff[4], soff, s_ld;
+    const float* wsc[3] = {nullptr, nullptr, nullptr};   // the weights' scales: rows rb 0..3, 4..5, 6..7
+    const int KB = KR ? 0 : (p.K + 127) / 128;
+    if constexpr (KR) {
+      auto left = [](int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); };
+      rT = make_rsrc_n(p.Y + int64_t(t.m0) * p.rows, uint32_t(left(p.N - t.m0, FT)) * ldw);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) toff[i] = uint32_t(wave * 32 + i * 8 + (lane >> 3)) * ldw + (lchunk ^ ((i & 1) * 64));
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        rW[h] = make_rsrc_n(p.X + int64_t(t.n0 + 128 * h) * p.rows, uint32_t(left(p.K - t.n0 - 128 * h, 128)) * ldw);
+      // waves 0..3 bring the scales of 64 rows of dY each, waves 4..7 those of X
+      const uint32_t nb = uint32_t((p.rows + 127) / 128);
+      const int n = wave < 4 ? p.N : p.K;
+      rS = make_rsrc_n(wave < 4 ? p.Yst : p.Xst, nb * uint32_t(n) * 4);
+      s_ld = uint32_t(n) * 4;
+      soff = uint32_t(t.kbase / 128) * s_ld + uint32_t((wave < 4 ? t.m0 : t.n0) + (wave & 3) * 64 + lane) * 4;
+    } else {
+      rT = make_rsrc_n(p.A, uint32_t(p.src_rows) * ldw);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = t.m0 + wave * 32 + i * 8 + (lane >> 3);
+        int src = t.off + m;
+        if (m < t.m_valid && p.map) src = p.map[src];
+        const bool in = m < t.m_valid && src >= 0 && src < p.src_rows;
+        toff[i] = in ? uint32_t(src) * ldw + (lchunk ^ ((i & 1) * 64)) : kInvalid;
+      }
+      const uint8_t* w = p.W ? ld_uniform(p.W, t.e) : p.Wv[t.e];
+      const float* ws = p.W ? ld_uniform(p.Ws, t.e) : p.Wsv[t.e];
+      const int nrows = SW ? p.F : p.N;
+      auto left = [](int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); };
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r0 = SW ? t.n0 : t.n0 + 128 * h;          // (SwiGLU: gate, then up rows of the same columns)
+        rW[h] = make_rsrc_n(w + (int64_t(r0) + (SW ? h * p.F : 0)) * p.K, uint32_t(left(nrows - r0, 128)) * ldw);
+      }
+      const int last = (SW ? 2 * p.F : p.N) - 1;
+      const int up = SW ? p.F + t.n0 + wn * 64 : t.n0 + 128;
+      wsc[0] = ws + int64_t(t.n0 / 128) * KB;
+      wsc[1] = ws + int64_t(min(up, last) / 128) * KB;
+      wsc[2] = ws + int64_t(min(SW ? up + 32 : up, last) / 128) * KB;
+      // (waves 4..7 bring the same scales as waves 0..3: every wave then has the same count to wait for)
+      rS = make_rsrc_n(p.Ast, uint32_t(KB) * uint32_t(p.ast_ld) * 4);
+      s_ld = uint32_t(p.ast_ld) * 4;
+      soff = uint32_t(t.off + t.m0 + (wave & 3) * 64 + lane) * 4;
+    }
+    // ---- DMA of one slice: the tokens, their scales and the first 128 weight rows; the other 128
+    // (offsets past the K range get the top bit and read zeros; so does a whole slice past the last)
+    const int kleft = t.khi - 1 - t.kbase - lchunk, kleft1 = t.khi - 1 - t.kbase - (lchunk ^ 64);
+    auto outside = [&](int kt, int i) { return uint32_t(((i & 1) ? kleft1 : kleft) - kt * 128) & kInvalid; };
+    const uint32_t woff = uint32_t(wave * 16 + (lane >> 3)) * ldw + uint32_t(lchunk);
+    const uint32_t woff1 = uint32_t(wave * 16 + 8 + (lane >> 3)) * ldw + uint32_t(lchunk ^ 64);
+    auto dma_t = [&](int kt, int i) {
+      dma16(rT, lds_base + (kt & 1) * FT_STAGE + (wave * 32 + i * 8) * 128, (toff[i] + uint32_t(t.kbase + kt * 128)) | outside(kt, i));
+    };
+    auto dma_w = [&](int kt, int h, int i) {
+      dma16(rW[h], lds_base + (kt & 1) * FT_STAGE + FT_OP + (h * 128 + wave * 16 + i * 8) * 128,
+            ((i ? woff1 : woff) + uint32_t(t.kbase + kt * 128)) | outside(kt, i));
+    };
+    auto dma_s = [&](int kt) {
+      dma4(rS, lds_base + FT_SCALES + (kt & 1) * (2 * FT * 4) + (KR ? wave : wave & 3) * 256,
+           (soff + uint32_t(kt) * s_ld) | (kt < t.nkt ? 0u : kInvalid));
+    };
+    // DMAs of a slice issued at mid-slice (dW reads the row operand's scales until the slice's end, so
+    // its scales come with the late ones)
+    constexpr int EARLY = KR ? 6 : 7;
+
+    f32x4 acc[8][4];
+#pragma unroll
+    for (int rb = 0; rb < 8; ++rb)
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) acc[rb][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if (t.nkt > 0) {
+      lds_barrier();   // every wave is done with the previous tile's slices
+      for (int k = 0; k < 2; ++k) {
+        for (int i = 0; i < 4; ++i) dma_t(k, i);
+        for (int i = 0; i < 2; ++i) dma_w(k, 0, i);
+        if (!KR || k == 0) dma_s(k);
+        if (k == 0)
+          for (int i = 0; i < 2; ++i) dma_w(0, 1, i);
+      }
+    }
+    float swv[3] = {0.f, 0.f, 0.f};     // lane l: the weight scale of slice (kt & ~63) + l
+    for (int kt = 0; kt < t.nkt; ++kt) {
+      if constexpr (!KR) {
+        if ((kt & 63) == 0) {
+          const int kb = min(kt + lane, KB - 1);
+#pragma unroll
+          for (int h = 0; h < (SW ? 3 : 2); ++h) swv[h] = wsc[h][kb];
+        }
+      }
+      vm_barrier<EARLY>();              // slice kt is resident
+      dma_w(kt + 1, 1, 0);
+      dma_w(kt + 1, 1, 1);
+      if constexpr (KR) dma_s(kt + 1);
+      const uint8_t* st = smem + (kt & 1) * FT_STAGE;
+      const float* sS = reinterpret_cast<const float*>(smem + FT_SCALES + (kt & 1) * (2 * FT * 4));
+      auto frag = [&](int at) {
+        const uint4 a = *reinterpret_cast<const uint4*>(st + at);
+        const uint4 b = *reinterpret_cast<const uint4*>(st + (at ^ 64));
+        return i32x8{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
+      };
+      i32x8 tf[4], wf[2];
+      float ts[4];
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) tf[tb] = frag(tread + tb * 2048);
+      wf[0] = frag(wread);
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) ts[tb] = sS[wt * 64 + tb * 16 + i16];
+      float sw[3] = {1.f, 1.f, 1.f};
+      if constexpr (!KR) {
+#pragma unroll
+        for (int h = 0; h < (SW ? 3 : 2); ++h) sw[h] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swv[h]), kt & 63));
+        if constexpr (!SW) sw[2] = sw[1];
+      }
+      f32x4 d[2][4];
+      f32x4 xs[2];
+      auto add = [&](auto rbc) {
+        constexpr int rb = decltype(rbc)::value;
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          if constexpr (KR) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[rb][tb][r] = fmaf(d[rb & 1][tb][r] * ts[tb], xs[rb & 1][r], acc[rb][tb][r]);
+          } else {
+            const float s = ts[tb] * sw[rb < 4 ? 0 : (rb < 6 ? 1 : 2)];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[rb][tb][r] = fmaf(d[rb & 1][tb][r], s, acc[rb][tb][r]);
+          }
+        }
+      };
+      static_for<0, 8>([&](auto rbc) {
+        constexpr int rb = decltype(rbc)::value;
+        if constexpr (rb < 7) wf[(rb + 1) & 1] = frag(wread + (rb + 1 < 4 ? (rb + 1) * 2048 : 128 * 128 + (rb + 1 - 4) * 2048));
+        if constexpr (KR) xs[rb & 1] = *reinterpret_cast<const f32x4*>(sS + FT + (rb < 4 ? 0 : 128) + wn * 64 + (rb & 3) * 16 + 4 * q);
+        if constexpr (rb == 4) {
+          lds_barrier();                // the tokens' half and the first 128 weight rows are read
+          if constexpr (!KR) dma_s(kt + 2);
+        }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+          d[rb & 1][tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[rb & 1], tf[tb], z, 0, 0, 0, 0, 0, 0);
+          if constexpr (rb >= 4 && rb < 6) {
+            if (tb == 0 || tb == 2) dma_t(kt + 2, (rb - 4) * 2 + tb / 2);
+          }
+          if constexpr (rb == 6) {
+            if (tb == 0 || tb == 2) dma_w(kt + 2, 0, tb / 2);
+          }
+        }
+        if constexpr (rb > 0) add(std::integral_constant<int, rb - 1>{});
+        __builtin_amdgcn_sched_barrier(0);   // one step at a time (registers)
+      });
+      add(std::integral_constant<int, 7>{});
+    }
+    __builtin_amdgcn_s_waitcnt(0);      // the slices past the end (zeros) have landed
+    rederive_lane();
+
+    // ---- epilogues.  acc[rb][tb][r]: column n0 + (rb < 4 ? 0 : 128) + wn * 64 + (rb % 4) * 16 + 4q + r,
+    // token m0 + wt * 64 + tb * 16 + i16
+    const int wrow0 = t.m0 + wt * 64;
+    int vr = t.m_valid - wrow0;
+    vr = uniform(vr < 0 ? 0 : (vr > 64 ? 64 : vr));
+    if constexpr (!SW) {
+      constexpr int ESZ = OUT == OUT_BF16 ? 2 : 4;
+      uint8_t* base;
+      if constexpr (KR) base = static_cast<uint8_t*>(p.D ? ld_uniform(p.D, t.e) : p.Dv[t.e]) + int64_t(wrow0) * ncols * ESZ;
+      else base = static_cast<uint8_t*>(p.C) + (int64_t(t.off) + wrow0) * ncols * ESZ;
+      const uint32_t rowb = uint32_t(ncols) * ESZ;
+      const __amdgpu_buffer_rsrc_t rC = __builtin_amdgcn_make_buffer_rsrc(base, 0, int(uint32_t(vr) * rowb), kRsrcFlags);
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      if (vr > 0) {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          const uint32_t row = uint32_t(tb * 16 + i16) * rowb;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c0 = t.n0 + h * 128 + wn * 64;
+            if constexpr (OUT == OUT_BF16) {
+              uint32_t lo[4], hi[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                lo[j] = bf16x2(acc[4 * h + j][tb][0], acc[4 * h + j][tb][1]);
+                hi[j] = bf16x2(acc[4 * h + j][tb][2], acc[4 * h + j][tb][3]);
+              }
+              transpose4(lo);
+              transpose4(hi);
+              const int c = c0 + q * 16;   // the lane has columns c .. c + 15 now
+              const uint32_t o = c < ncols ? row + uint32_t(c) * ESZ : kInvalid;
+              __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, rC, int(o), 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[2], hi[2], lo[3], hi[3]}, rC, int(o + 16), 0, 0);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int c = c0 + j * 16 + 4 * q;
+                const uint32_t o = c < ncols ? row + uint32_t(c) * ESZ : kInvalid;
+                f32x4 v = acc[4 * h + j][tb];
+                if constexpr (OUT == OUT_F32_ACC) {
+                  const u32x4 old = __builtin_amdgcn_raw_buffer_load_b128(rC, int(o), 0, 0);
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) v[r] += __uint_as_float(old[r]);
+                }
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rC, int(o), 0, 0);
+              }
+            }
+          }
+        }
+      }
+    } else {
+      // h = p silu(G) U of the tile's 128 columns, one block of 128 a token: its largest magnitude over
+      // the lane's 16 columns, the lanes 16 apart and the two waves of the columns' halves
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      const int64_t grow0 = int64_t(t.off) + wrow0;
+      uint32_t am[4];
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+        const bool in = tb * 16 + i16 < vr;
+        const float pr = p.prob == nullptr ? 1.f : (in ? p.prob[grow0 + tb * 16 + i16] : 0.f);
+        am[tb] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float G = acc[j][tb][r], U = acc[4 + j][tb][r];
+            const float h = pr * (G * __builtin_amdgcn_rcpf(1.f + __expf(-G))) * U;
+            acc[j][tb][r] = h;
+            am[tb] = umax(am[tb], __float_as_uint(h) & 0x7fffffffu);
+          }
+        const U32Pair a = permlane16_swap(am[tb], am[tb]);
+        am[tb] = umax(a.a, a.b);
+        const U32Pair b = permlane32_swap(am[tb], am[tb]);
+        am[tb] = umax(b.a, b.b);
+        if (q == 0) s_amax[wn * FT + wt * 64 + tb * 16 + i16] = am[tb];
+      }
+      lds_barrier();
+      const __amdgpu_buffer_rsrc_t rH =
+          __builtin_amdgcn_make_buffer_rsrc(p.h_codes + grow0 * p.F, 0, int(uint32_t(vr) * uint32_t(p.F)), kRsrcFlags);
+      if (vr > 0) {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          const int m = wt * 64 + tb * 16 + i16;
+          const FbScale sc = fb_scale(umax(s_amax[m], s_amax[FT + m]));
+          uint32_t v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[j] = e4m3x4(acc[j][tb][0] * sc.inv, acc[j][tb][1] * sc.inv, acc[j][tb][2] * sc.inv, acc[j][tb][3] * sc.inv);
+          transpose4(v);
+          const int c = t.n0 + wn * 64 + q * 16;
+          const uint32_t o = c < p.F ? uint32_t(tb * 16 + i16) * uint32_t(p.F) + uint32_t(c) : kInvalid;
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0], v[1], v[2], v[3]}, rH, int(o), 0, 0);
+          if (wn == 0 && q == 0 && tb * 16 + i16 < vr) p.h_scales[int64_t(t.n0 / 128) * p.ast_ld + grow0 + tb * 16 + i16] = sc.s;
+        }
+      }
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);   // no LDS DMA outlives the workgroup
+}
+
+#define FB_KERNEL(name, KR, SW, OUT, P) \
+  __global__ __launch_bounds__(FT_THREADS, 2) void name(P p) { fb_tile_body<KR, SW, OUT>(p); }
+FB_KERNEL(gemm_fb_store, false, false, OUT_BF16, FbGemm)
+FB_KERNEL(gemm_fb_store_f32, false, false, OUT_F32, FbGemm)
+FB_KERNEL(gemm_fb_swiglu, false, true, OUT_NONE, FbGemm)
+FB_KERNEL(gemm_fb_wgrad, true, false, OUT_BF16, FbWgrad)
+FB_KERNEL(gemm_fb_wgrad_f32, true, false, OUT_F32, FbWgrad)
+FB_KERNEL(gemm_fb_wgrad_f32_acc, true, false, OUT_F32_ACC, FbWgrad)
+#undef FB_KERNEL
+
+// One workgroup a CU (its LDS), fewer where there are fewer tiles
+template <typename Kern, typename P>
+static mge_status launch_fb(Kern kern, const char* name, const P& p, int64_t tiles, hipStream_t s) {
+  hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, FT_LDS);
+  int64_t grid = device_cus();
+  if (tiles < grid) grid = tiles;
+  if (grid <= 0) return MGE_OK;
+  ProfScope prof(s, name);
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(FT_THREADS), FT_LDS, s, p);
+  return hip_check(name);
+}
+
+mge_status launch_fb_tile(const FbGemm& p, bool swiglu, hipStream_t s) {
+  const int64_t mt = (int64_t(p.total) + FT - 1) / FT + (p.sizes ? p.E : 0);
+  if (swiglu) return launch_fb(gemm_fb_swiglu, "gemm_fp8_block_swiglu", p, mt * ((p.F + 127) / 128), s);
+  const int64_t tiles = mt * ((p.N + FT - 1) / FT);
+  return p.out_f32 ? launch_fb(gemm_fb_store_f32, "gemm_fp8_block", p, tiles, s) : launch_fb(gemm_fb_store, "gemm_fp8_block", p, tiles, s);
+}
+
+mge_status launch_fb_wgrad(const FbWgrad& p, hipStream_t s) {
+  const int64_t tiles = int64_t(p.E) * ((p.N + FT - 1) / FT) * ((p.K + FT - 1) / FT);
+  if (p.out == OUT_BF16) return launch_fb(gemm_fb_wgrad, "wgrad_fp8_block", p, tiles, s);
+  if (p.out == OUT_F32) return launch_fb(gemm_fb_wgrad_f32, "wgrad_fp8_block", p, tiles, s);
+  return launch_fb(gemm_fb_wgrad_f32_acc, "wgrad_fp8_block", p, tiles, s);
+}
+
+// Scales made block-major, 64 x 64 a workgroup through LDS; every matrix of the launch has its own range of workgroups
+struct FbScaleTArgs {
+  FbScaleT m[2];
+  int64_t first[2];
+  int n;
+};
+__global__ __launch_bounds__(256) void fb_scale_t_kernel(FbScaleTArgs a) {
+  __shared__ float tile[64][65];
+  const int which = a.n > 1 && int64_t(blockIdx.x) >= a.first[1] ? 1 : 0;
+  const FbScaleT& m = a.m[which];
+  const int nj = (m.kb + 63) / 64;
+  const int64_t blk = int64_t(blockIdx.x) - a.first[which];
+  const int64_t r0 = blk / nj * 64;
+  const int j0 = int(blk % nj) * 64;
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  for (int i = y; i < 64; i += 4) {
+    const int64_t r = r0 + i;
+    float v = 0.f;
+    if (r < m.rows && j0 + x < m.kb) {
+      const int64_t src = m.map ? int64_t(m.map[r]) : r;
+      if (src >= 0 && src < m.src_rows) v = m.in[src * m.kb + j0 + x];
+    }
+    tile[i][x] = v;
+  }
+  __syncthreads();
+  for (int i = y; i < 64; i += 4)
+    if (j0 + i < m.kb && r0 + x < m.rows) m.out[int64_t(j0 + i) * m.ld + r0 + x] = tile[x][i];
+}
+mge_status launch_fb_scale_t(const FbScaleT* list, int n, hipStream_t s) {
+  FbScaleTArgs a{};
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    a.m[i] = list[i];
+    a.first[i] = blocks;
+    blocks += (list[i].rows + 63) / 64 * ((list[i].kb + 63) / 64);
+  }
+  a.n = n;
+  if (blocks == 0) return MGE_OK;
+  ProfScope prof(s, "fp8_block_scales");
+  hipLaunchKernelGGL(fb_scale_t_kernel, dim3(unsigned(blocks)), dim3(256), 0, s, a);
+  return hip_check("fp8_block_scales");
+}
+
+}  // namespace mge

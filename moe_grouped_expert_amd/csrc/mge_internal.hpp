@@ -8,6 +8,22 @@
 
 namespace mge {
 
+// ------------------------------------------------------------ argument checks, workspaces
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+// Bump allocator over the caller's workspace.
+struct Carve {
+  uint8_t* base;
+  size_t used = 0;
+  explicit Carve(void* b) : base(static_cast<uint8_t*>(b)) {}
+  void* take(size_t bytes) {
+    void* p = base ? base + used : nullptr;
+    used += up256(bytes);
+    return p;
+  }
+};
+
 // ------------------------------------------------------------ per-kernel timing
 // While mge_profile_start() is in effect, a ProfScope records a HIP event on the
 // launch stream when it is constructed and another when it is destroyed, so each

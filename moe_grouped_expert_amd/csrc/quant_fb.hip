@@ -1,0 +1,229 @@
+// bf16 -> E4M3 with one fp32 scale per block of 128 (1 x 128 along the rows, or 128 x 128), in row
+// form and transposed, rows optionally gathered, and back.
+//
+// HBM-bound: one read of the input, one write of each form.  A workgroup takes a tile of 128 rows x
+// 128 columns (a block is never split), 8 columns of 2 x 4 consecutive rows a thread: a row's 128
+// values are in the 16 lanes of a DPP row, a column's 4 rows make one dword of the transposed form,
+// which goes through LDS so that it leaves in whole lines.
+#include "mge_common.hpp"
+
+#include "fp8b.hpp"
+
+namespace mge {
+
+constexpr int QF_LD = 132;   // bytes of a column in LDS: a dword of skew spreads the dword writes over the banks
+
+template <bool TILE, bool ROW, bool COL>
+__global__ __launch_bounds__(256) void quant_fb_kernel(QuantFbParams p, int64_t tiles, int nr, int nc) {
+  __shared__ __attribute__((aligned(16))) uint8_t s_col[COL ? FB * QF_LD : 4];
+  __shared__ uint32_t s_max[TILE ? 4 : (COL ? 4 * FB : 1)];
+  __shared__ float s_inv[!TILE && COL ? FB : 1];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int cl = (tid & 15) * 8;         // first of the thread's 8 columns
+  const int rg = tid >> 4;               // its rows: 64 i + 4 rg + j
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t b = tile / (int64_t(nr) * nc);
+    const int rem = int(tile - b * nr * nc);
+    const int tr = rem / nc, tc = rem - tr * nc;
+    const int64_t r0 = int64_t(tr) * FB;
+    const int c0 = tc * FB + cl;
+    const bool cin = c0 < p.C;
+    const uint16_t* src = p.in + b * p.in_bstride + c0;
+    uint4 x[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t r = r0 + 64 * i + 4 * rg + j;
+        x[i][j] = make_uint4(0, 0, 0, 0);
+        if (cin && r < p.R) {
+          int64_t sr = r;
+          if (p.map) {
+            sr = p.map[r];
+            if (sr < 0 || sr >= p.src_rows) sr = -1;
+          }
+          if (sr >= 0) x[i][j] = *reinterpret_cast<const uint4*>(src + sr * p.in_ld);
+        }
+      }
+    auto val = [&](int i, int j, int k) {
+      const uint32_t w = k < 4 ? (k < 2 ? x[i][j].x : x[i][j].y) : (k < 6 ? x[i][j].z : x[i][j].w);
+      return __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
+    };
+    // largest magnitudes, as bit patterns: of the thread's rows and columns
+    uint32_t rmax[2][4], cmax[8], all = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) cmax[k] = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        rmax[i][j] = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t m = __float_as_uint(val(i, j, k)) & 0x7fffffffu;
+          rmax[i][j] = umax(rmax[i][j], m);
+          cmax[k] = umax(cmax[k], m);
+        }
+        all = umax(all, rmax[i][j]);
+      }
+    auto store_row = [&](int i, int j, float inv) {
+      const int64_t r = r0 + 64 * i + 4 * rg + j;
+      if (cin && r < p.R)
+        *reinterpret_cast<uint2*>(p.row_codes + (b * p.R + r) * p.C + c0) =
+            make_uint2(e4m3x4(val(i, j, 0) * inv, val(i, j, 1) * inv, val(i, j, 2) * inv, val(i, j, 3) * inv),
+                       e4m3x4(val(i, j, 4) * inv, val(i, j, 5) * inv, val(i, j, 6) * inv, val(i, j, 7) * inv));
+    };
+    FbScale ts;
+    if constexpr (TILE) {
+      all = row16_umax(all);
+      const U32Pair a = permlane16_swap(all, all);
+      all = umax(a.a, a.b);
+      const U32Pair c = permlane32_swap(all, all);
+      all = umax(c.a, c.b);
+      if ((tid & 63) == 0) s_max[wave] = all;
+      __syncthreads();
+      ts = fb_scale(umax(umax(s_max[0], s_max[1]), umax(s_max[2], s_max[3])));
+      if (tid == 0) {
+        if constexpr (ROW) p.row_scales[(b * nr + tr) * nc + tc] = ts.s;
+        if constexpr (COL) p.col_scales[(b * nc + tc) * nr + tr] = ts.s;
+      }
+    }
+    if constexpr (ROW) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          FbScale sc = ts;
+          if constexpr (!TILE) {
+            sc = fb_scale(row16_umax(rmax[i][j]));
+            const int64_t r = r0 + 64 * i + 4 * rg + j;
+            if (cl == 0 && r < p.R) p.row_scales[(b * p.R + r) * nc + tc] = sc.s;
+          }
+          store_row(i, j, sc.inv);
+        }
+    }
+    if constexpr (COL) {
+      float inv[8];
+      if constexpr (TILE) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) inv[k] = ts.inv;
+      } else {
+        // over the wave's 4 row groups (lanes 16 and 32 apart), then the 4 waves
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const U32Pair a = permlane16_swap(cmax[k], cmax[k]);
+          const uint32_t m = umax(a.a, a.b);
+          const U32Pair c = permlane32_swap(m, m);
+          cmax[k] = umax(c.a, c.b);
+        }
+        if ((tid & 48) == 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s_max[wave * FB + cl + k] = cmax[k];
+        }
+        __syncthreads();
+        if (tid < FB) {
+          const FbScale sc = fb_scale(umax(umax(s_max[tid], s_max[FB + tid]), umax(s_max[2 * FB + tid], s_max[3 * FB + tid])));
+          s_inv[tid] = sc.inv;
+          const int c = tc * FB + tid;
+          if (c < p.C) p.col_scales[(b * p.C + c) * nr + tr] = sc.s;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) inv[k] = s_inv[cl + k];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<uint32_t*>(s_col + (cl + k) * QF_LD + 64 * i + 4 * rg) =
+              e4m3x4(val(i, 0, k) * inv[k], val(i, 1, k) * inv[k], val(i, 2, k) * inv[k], val(i, 3, k) * inv[k]);
+      __syncthreads();
+      // 16 bytes a thread: 8 threads a column
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = i * 32 + (tid >> 3), q = (tid & 7) * 16;
+        if (tc * FB + c < p.C && r0 + q < p.Rp) {
+          const uint32_t* s = reinterpret_cast<const uint32_t*>(s_col + c * QF_LD + q);
+          *reinterpret_cast<uint4*>(p.col_codes + (b * p.C + tc * FB + c) * p.Rp + r0 + q) = make_uint4(s[0], s[1], s[2], s[3]);
+        }
+      }
+    }
+    __syncthreads();   // the LDS is read before the next tile writes it
+  }
+}
+
+template <bool TILE>
+static void launch_q(const QuantFbParams& p, int64_t tiles, int nr, int nc, hipStream_t s) {
+  const unsigned grid = unsigned(tiles < (1 << 20) ? tiles : (1 << 20));
+  if (p.row_codes && p.col_codes) hipLaunchKernelGGL((quant_fb_kernel<TILE, true, true>), dim3(grid), dim3(256), 0, s, p, tiles, nr, nc);
+  else if (p.row_codes) hipLaunchKernelGGL((quant_fb_kernel<TILE, true, false>), dim3(grid), dim3(256), 0, s, p, tiles, nr, nc);
+  else hipLaunchKernelGGL((quant_fb_kernel<TILE, false, true>), dim3(grid), dim3(256), 0, s, p, tiles, nr, nc);
+}
+mge_status launch_quant_fb(const QuantFbParams& p, hipStream_t s) {
+  const int nr = int(fb_blocks(p.R)), nc = int(fb_blocks(p.C));
+  ProfScope prof(s, "fp8_block_quantize");
+  if (p.tile) launch_q<true>(p, int64_t(p.batch) * nr * nc, nr, nc, s);
+  else launch_q<false>(p, int64_t(p.batch) * nr * nc, nr, nc, s);
+  return hip_check("fp8_block_quantize");
+}
+
+// Values of 16 codes a thread.  A thread keeps its columns and goes over rows, so that the division
+// of its index happens once.
+template <bool F32>
+__global__ __launch_bounds__(256) void dequant_fb_kernel(int64_t rows, int R, int C, int tile, int per, int rpb, const uint8_t* codes,
+                                                         const float* scales, void* out) {
+  const int chunks = C / 16, kb = (C + FB - 1) / FB;
+  const int r = int(threadIdx.x) / per;
+  const int c = int(blockIdx.x) * per + int(threadIdx.x) - r * per;
+  if (r >= rpb || c >= chunks) return;
+  const int nr = (R + FB - 1) / FB;
+  for (int64_t row = int64_t(blockIdx.y) * rpb + r; row < rows; row += int64_t(gridDim.y) * rpb) {
+    const uint4 q = *reinterpret_cast<const uint4*>(codes + row * C + c * 16);
+    int64_t srow = row;
+    if (tile) {
+      const int64_t b = row / R;
+      srow = b * nr + (row - b * R) / FB;
+    }
+    const float s = scales[srow * kb + c / 8];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[i]), false);
+      const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[i]), true);
+      v[4 * i] = lo[0] * s; v[4 * i + 1] = lo[1] * s; v[4 * i + 2] = hi[0] * s; v[4 * i + 3] = hi[1] * s;
+    }
+    if constexpr (F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * C + c * 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * C + c * 16);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        o[i] = make_uint4(bf16x2(v[8 * i], v[8 * i + 1]), bf16x2(v[8 * i + 2], v[8 * i + 3]), bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                          bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    }
+  }
+}
+
+mge_status launch_dequant_fb(int64_t batch, int64_t R, int C, bool tile, const uint8_t* codes, const float* scales, int dtype,
+                             void* out, hipStream_t s) {
+  const int chunks = C / 16;
+  const int per = chunks < 256 ? chunks : 256, rpb = 256 / per;
+  const int64_t rows = batch * R;
+  const unsigned gx = unsigned((chunks + per - 1) / per);
+  int64_t gy = (rows + rpb - 1) / rpb;
+  const int64_t most = 16384 / gx + 1;
+  if (gy > most) gy = most;
+  ProfScope prof(s, "fp8_block_dequantize");
+  if (dtype == MGE_DTYPE_F32)
+    hipLaunchKernelGGL((dequant_fb_kernel<true>), dim3(gx, unsigned(gy)), dim3(256), 0, s, rows, int(R), C, tile ? 1 : 0, per, rpb,
+                       codes, scales, out);
+  else
+    hipLaunchKernelGGL((dequant_fb_kernel<false>), dim3(gx, unsigned(gy)), dim3(256), 0, s, rows, int(R), C, tile ? 1 : 0, per, rpb,
+                       codes, scales, out);
+  return hip_check("fp8_block_dequantize");
+}
+
+}  // namespace mge

@@ -1,0 +1,287 @@
+// Grouped products of FP8 operands with one fp32 scale per block of 128, for few rows per expert
+// (token-by-token serving): C[r][n] = sum over blocks b of sa[r][b] sw[n / 128][b] (sum over k in b of
+// A[r][k] W_e[n][k]).
+//
+// One read of the weights, so the kernels are built around that stream: a wave reads its rows' share of
+// the weights straight into registers (16 rows x 128 bytes an instruction pair, whole lines), as the
+// matrix unit's row operand, 16 tokens a block (MB = 1, 2 blocks) as its columns; more rows than that in
+// a group take further passes over the same weights.  As in the tile kernels a block's products are
+// summed from zero on the matrix unit (v_mfma_f32_16x16x128_f8f6f4: lane 16q + i feeds row / column i
+// with bytes 16q .. 16q + 15 and 64 + 16q .. of the block; result register r is row 4q + r, column i)
+// and added, scaled, to fp32 accumulators.  Rows past N, tokens past the group and bytes past K are
+// outside the buffer resources' bounds and read as zeros.
+#include "mge_common.hpp"
+
+#include "fp8b.hpp"
+
+namespace mge {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kSfOut = 0x80000000u;   // an offset past every bound
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t sf_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, int(bytes), 0x00020000);
+}
+__device__ __forceinline__ u32x4 sf_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, int(off), 0, 0);
+}
+__device__ __forceinline__ float sf_load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, int(off), 0, 0));
+}
+__device__ __forceinline__ i32x8 sf_frag(u32x4 a, u32x4 b) {
+  return i32x8{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
+}
+// a wave-uniform scale, by a scalar load
+__device__ __forceinline__ float sf_uniform(const float* p, int i) {
+  typedef const __attribute__((address_space(4))) float const_t;
+  return reinterpret_cast<const_t*>(reinterpret_cast<uintptr_t>(p))[i];
+}
+
+// The group of this workgroup: the blockIdx.y-th expert that has rows (at most min(E, rows) of them, which
+// is the grid); e < 0: none.  off, size: clamped into the rows of the groups.
+struct SfGroup {
+  int e, off, size;
+};
+__device__ __forceinline__ SfGroup sf_group(const FbGemm& p) {
+  __shared__ int32_t s_pick, s_cnt[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  SfGroup g{0, 0, p.rows};
+  if (p.sizes) {
+    if (tid == 0) s_pick = -1;
+    const bool some = tid < p.E && p.sizes[tid] > 0;
+    const uint64_t mask = __ballot(some);
+    if (lane == 0 && wave < 4) s_cnt[wave] = __popcll(mask);
+    __syncthreads();
+    int before = __popcll(mask & ((uint64_t(1) << lane) - 1));
+    for (int w = 0; w < wave && w < 4; ++w) before += s_cnt[w];
+    if (some && before == int(blockIdx.y)) s_pick = tid;
+    __syncthreads();
+    g.e = __builtin_amdgcn_readfirstlane(s_pick);
+    if (g.e < 0) return g;
+    g.off = p.offs[g.e];
+    g.size = p.sizes[g.e];
+    g.off = g.off < 0 ? 0 : (g.off > p.rows ? p.rows : g.off);
+    g.size = g.size > p.rows - g.off ? p.rows - g.off : g.size;
+    g.off = __builtin_amdgcn_readfirstlane(g.off);
+    g.size = __builtin_amdgcn_readfirstlane(g.size);
+  }
+  return g;
+}
+// Byte offset of a group's row m in A (through the map), past every bound where there is none; the row itself
+struct SfRow {
+  uint32_t a, s;
+};
+__device__ __forceinline__ SfRow sf_row(const FbGemm& p, const SfGroup& g, int m, int KB) {
+  if (m >= g.size) return SfRow{kSfOut, kSfOut};
+  int src = g.off + m;
+  if (p.map) src = p.map[src];
+  if (src < 0 || src >= p.src_rows) return SfRow{kSfOut, kSfOut};
+  return SfRow{uint32_t(src) * uint32_t(p.K), uint32_t(src) * uint32_t(KB) * 4};
+}
+
+// One step of U blocks: NB blocks of 16 weight rows times MB of 16 tokens.  w_off, rows: byte offsets of the
+// lane's row; sw(b, kb): the weight scale.
+template <int NB, int MB, int U, typename SW>
+__device__ __forceinline__ void sf_step(f32x4 (&acc)[NB][MB], __amdgpu_buffer_rsrc_t rW, __amdgpu_buffer_rsrc_t rA,
+                                        __amdgpu_buffer_rsrc_t rS, const uint32_t (&w_off)[NB], const SfRow (&rows)[MB], int kb0, int K,
+                                        int KB, int q, SW&& sw) {
+  u32x4 w[U][NB][2], a[U][MB][2];
+  float ts[U][MB];
+  const bool whole = (kb0 + U) * FB <= K;   // uniform
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t k = uint32_t(kb0 + u) * FB + 16 * q;
+    const uint32_t o0 = whole || k < uint32_t(K) ? 0u : kSfOut, o1 = whole || k + 64 < uint32_t(K) ? 0u : kSfOut;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      w[u][b][0] = sf_load16(rW, (w_off[b] + k) | o0 | (w_off[b] & kSfOut));
+      w[u][b][1] = sf_load16(rW, (w_off[b] + k + 64) | o1 | (w_off[b] & kSfOut));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t k = uint32_t(kb0 + u) * FB + 16 * q;
+    const uint32_t o0 = whole || k < uint32_t(K) ? 0u : kSfOut, o1 = whole || k + 64 < uint32_t(K) ? 0u : kSfOut;
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      a[u][m][0] = sf_load16(rA, (rows[m].a + k) | o0 | (rows[m].a & kSfOut));
+      a[u][m][1] = sf_load16(rA, (rows[m].a + k + 64) | o1 | (rows[m].a & kSfOut));
+      ts[u][m] = sf_load4(rS, (rows[m].s + uint32_t(kb0 + u) * 4) | (kb0 + u < KB ? 0u : kSfOut) | (rows[m].s & kSfOut));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const float s = sw(b, kb0 + u < KB ? kb0 + u : KB - 1);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(sf_frag(w[u][b][0], w[u][b][1]), sf_frag(a[u][m][0], a[u][m][1]),
+                                                                         z, 0, 0, 0, 0, 0, 0);
+        const float f = ts[u][m] * s;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[b][m][r] = fmaf(d[r], f, acc[b][m][r]);
+      }
+    }
+}
+
+// C: a workgroup owns NB blocks of 16 weight rows; its W waves split K (U blocks of 128 at a time, then the
+// next wave's follow) and add their partial sums through LDS in wave order.
+template <int W, int NB, int MB, int U, bool F32>
+__global__ __launch_bounds__(64 * W) void fb_stream_kernel(FbGemm p) {
+  static_assert(W >= 4, "a thread for each of up to 256 experts");
+  __shared__ __attribute__((aligned(16))) f32x4 red[W][NB * MB][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i16 = lane & 15, q = lane >> 4;
+  const SfGroup g = sf_group(p);
+  if (g.e < 0) return;
+  const int K = p.K, KB = (K + FB - 1) / FB;
+  const int chunks = (KB + U - 1) / U;
+  const __amdgpu_buffer_rsrc_t rW = sf_rsrc(p.W ? p.W[g.e] : p.Wv[g.e], uint32_t(p.N) * uint32_t(K));
+  const float* wsc = p.W ? p.Ws[g.e] : p.Wsv[g.e];
+  const __amdgpu_buffer_rsrc_t rA = sf_rsrc(p.A, uint32_t(p.src_rows) * uint32_t(K));
+  const __amdgpu_buffer_rsrc_t rS = sf_rsrc(p.As, uint32_t(p.src_rows) * uint32_t(KB) * 4);
+  const int n0 = int(blockIdx.x) * (NB * 16);
+  uint32_t w_off[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) w_off[b] = n0 + b * 16 + i16 < p.N ? uint32_t(n0 + b * 16 + i16) * uint32_t(K) : kSfOut;
+  auto sw = [&](int b, int kb) { return sf_uniform(wsc, min(n0 + b * 16, p.N - 1) / FB * KB + kb); };
+  for (int m0 = 0; m0 < g.size; m0 += 16 * MB) {
+    SfRow rows[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) rows[m] = sf_row(p, g, m0 + m * 16 + i16, KB);
+    f32x4 acc[NB][MB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) acc[b][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int c = wave; c < chunks; c += W) sf_step<NB, MB, U>(acc, rW, rA, rS, w_off, rows, c * U, K, KB, q, sw);
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) red[wave][b * MB + m][lane] = acc[b][m];
+    __syncthreads();
+    for (int j = wave; j < NB * MB; j += W) {
+      f32x4 c = red[0][j][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) {
+        const f32x4 x = red[w][j][lane];
+        c.x += x.x; c.y += x.y; c.z += x.z; c.w += x.w;
+      }
+      const int row = m0 + (j % MB) * 16 + i16;
+      const int n = n0 + (j / MB) * 16 + 4 * q;
+      if (row < g.size && n < p.N) {   // N is a multiple of 32
+        const int64_t o = (int64_t(g.off) + row) * p.N + n;
+        if constexpr (F32) *reinterpret_cast<float4*>(static_cast<float*>(p.C) + o) = make_float4(c.x, c.y, c.z, c.w);
+        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.C) + o) = make_uint2(bf16x2(c.x, c.y), bf16x2(c.z, c.w));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// h = p silu(G) U of one block of 128 columns a workgroup: wave w has the gate and up rows of 16 of them and
+// goes over all of K; the block's scale is the largest magnitude over the 8 waves.
+constexpr int SF_SW = 8;
+template <int MB, int U>
+__global__ __launch_bounds__(64 * SF_SW) void fb_stream_swiglu_kernel(FbGemm p) {
+  __shared__ uint32_t s_amax[SF_SW][16 * MB];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i16 = lane & 15, q = lane >> 4;
+  const SfGroup g = sf_group(p);
+  if (g.e < 0) return;
+  const int K = p.K, KB = (K + FB - 1) / FB, FBK = (p.F + FB - 1) / FB;
+  const __amdgpu_buffer_rsrc_t rW = sf_rsrc(p.W ? p.W[g.e] : p.Wv[g.e], 2u * uint32_t(p.F) * uint32_t(K));
+  const float* wsc = p.W ? p.Ws[g.e] : p.Wsv[g.e];
+  const __amdgpu_buffer_rsrc_t rA = sf_rsrc(p.A, uint32_t(p.src_rows) * uint32_t(K));
+  const __amdgpu_buffer_rsrc_t rS = sf_rsrc(p.As, uint32_t(p.src_rows) * uint32_t(KB) * 4);
+  const int f0 = int(blockIdx.x) * FB + wave * 16;   // the wave's first column (F is a multiple of 32)
+  const bool cols = f0 < p.F;
+  uint32_t w_off[2];
+  w_off[0] = cols ? uint32_t(f0 + i16) * uint32_t(K) : kSfOut;
+  w_off[1] = cols ? uint32_t(p.F + f0 + i16) * uint32_t(K) : kSfOut;
+  const int s0 = (cols ? f0 : 0) / FB * KB, s1 = (p.F + (cols ? f0 : 0)) / FB * KB;
+  auto sw = [&](int b, int kb) { return sf_uniform(wsc, (b ? s1 : s0) + kb); };
+  for (int m0 = 0; m0 < g.size; m0 += 16 * MB) {
+    SfRow rows[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) rows[m] = sf_row(p, g, m0 + m * 16 + i16, KB);
+    f32x4 acc[2][MB];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) acc[b][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (cols)
+      for (int kb = 0; kb < KB; kb += U) sf_step<2, MB, U>(acc, rW, rA, rS, w_off, rows, kb, K, KB, q, sw);
+    float h[MB][4];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      const int row = m0 + m * 16 + i16;
+      const float pr = !p.prob ? 1.f : (row < g.size ? p.prob[g.off + row] : 0.f);
+      uint32_t am = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        h[m][r] = pr * silu_f(acc[0][m][r]) * acc[1][m][r];
+        am = umax(am, __float_as_uint(h[m][r]) & 0x7fffffffu);
+      }
+      const U32Pair x = permlane16_swap(am, am);
+      am = umax(x.a, x.b);
+      const U32Pair y = permlane32_swap(am, am);
+      am = umax(y.a, y.b);
+      if (q == 0) s_amax[wave][m * 16 + i16] = am;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      const int row = m0 + m * 16 + i16;
+      uint32_t am = s_amax[0][m * 16 + i16];
+#pragma unroll
+      for (int w = 1; w < SF_SW; ++w) am = umax(am, s_amax[w][m * 16 + i16]);
+      const FbScale sc = fb_scale(am);
+      if (row < g.size && cols) {
+        const int64_t r = int64_t(g.off) + row;
+        *reinterpret_cast<uint32_t*>(p.h_codes + r * p.F + f0 + 4 * q) =
+            e4m3x4(h[m][0] * sc.inv, h[m][1] * sc.inv, h[m][2] * sc.inv, h[m][3] * sc.inv);
+        if (wave == 0 && q == 0) p.h_scales[r * FBK + blockIdx.x] = sc.s;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Groups that can have rows: the kernels' grid in y
+static unsigned groups_upper(const FbGemm& p) { return !p.sizes ? 1u : unsigned(p.E < p.total ? p.E : p.total); }
+
+template <int W, int NB, int MB, int U>
+static mge_status launch_store(const FbGemm& p, hipStream_t s) {
+  const dim3 grid(unsigned((p.N + NB * 16 - 1) / (NB * 16)), groups_upper(p));
+  ProfScope prof(s, "fp8_block_stream");
+  if (p.out_f32) hipLaunchKernelGGL((fb_stream_kernel<W, NB, MB, U, true>), grid, dim3(64 * W), 0, s, p);
+  else hipLaunchKernelGGL((fb_stream_kernel<W, NB, MB, U, false>), grid, dim3(64 * W), 0, s, p);
+  return hip_check("fp8_block_stream");
+}
+
+mge_status launch_fb_stream(const FbGemm& p, bool swiglu, hipStream_t s) {
+  if (p.total <= 0 || p.rows <= 0) return MGE_OK;
+  const bool two = p.total > 12 * int64_t(p.E);
+  if (swiglu) {
+    const dim3 grid(unsigned((p.F + FB - 1) / FB), groups_upper(p));
+    ProfScope prof(s, "fp8_block_stream_swiglu");
+    if (two) hipLaunchKernelGGL((fb_stream_swiglu_kernel<2, 2>), grid, dim3(64 * SF_SW), 0, s, p);
+    else hipLaunchKernelGGL((fb_stream_swiglu_kernel<1, 4>), grid, dim3(64 * SF_SW), 0, s, p);
+    return hip_check("fp8_block_stream_swiglu");
+  }
+  const int64_t blocks = int64_t((p.N + 15) / 16) * groups_upper(p);
+  if (two) return launch_store<8, 2, 2, 2>(p, s);
+  if (blocks < 1024) return launch_store<8, 1, 1, 4>(p, s);
+  return launch_store<8, 2, 1, 2>(p, s);
+}
+
+}  // namespace mge

@@ -28,8 +28,8 @@ constexpr int FT = 256;                       // rows of a tile on both sides
 constexpr int FT_THREADS = 512;
 constexpr int FT_OP = FT * 128;               // bytes of an operand in a stage
 constexpr int FT_STAGE = 2 * FT_OP;           // tokens, then weights
-constexpr int FT_SCALES = 2 * FT_STAGE;       // then, per stage, the tokens' scales and (dW) the row operand's
-constexpr int FT_LDS = FT_SCALES + 2 * 2 * FT * 4;
+constexpr int FT_SCALES = 2 * FT_STAGE;       // then a ring of 4 slices' scales: the tokens' and (dW) the row operand's
+constexpr int FT_LDS = FT_SCALES + 4 * 2 * FT * 4;
 
 // 4 x 4 transpose over the lanes 16 apart: lane 16q + i gives v[j] for j = 0..3 and gets v[q] of the
 // lanes 16p + i in v[p]
@@ -211,12 +211,21 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
             ((i ? woff1 : woff) + uint32_t(t.kbase + kt * 128)) | outside(kt, i));
     };
     auto dma_s = [&](int kt) {
-      dma4(rS, lds_base + FT_SCALES + (kt & 1) * (2 * FT * 4) + (KR ? wave : wave & 3) * 256,
+      dma4(rS, lds_base + FT_SCALES + (kt & 3) * (2 * FT * 4) + (KR ? wave : wave & 3) * 256,
            (soff + uint32_t(kt) * s_ld) | (kt < t.nkt ? 0u : kInvalid));
     };
-    // DMAs of a slice issued at mid-slice (dW reads the row operand's scales until the slice's end, so
-    // its scales come with the late ones)
-    constexpr int EARLY = KR ? 6 : 7;
+    // The early part of a slice (its tokens, scales and first 128 weight rows: 7 DMAs) and the late one
+    // (the other weight rows: 2).
+    constexpr int EARLY = 7, LATE = 2;
+    auto issue_late = [&](int kt) {
+      dma_w(kt, 1, 0);
+      dma_w(kt, 1, 1);
+    };
+    auto issue_early = [&](int kt) {
+      dma_s(kt);
+      for (int i = 0; i < 4; ++i) dma_t(kt, i);
+      for (int i = 0; i < 2; ++i) dma_w(kt, 0, i);
+    };
 
     f32x4 acc[8][4];
 #pragma unroll
@@ -225,87 +234,110 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       for (int tb = 0; tb < 4; ++tb) acc[rb][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     if (t.nkt > 0) {
-      lds_barrier();   // every wave is done with the previous tile's slices
-      for (int k = 0; k < 2; ++k) {
-        for (int i = 0; i < 4; ++i) dma_t(k, i);
-        for (int i = 0; i < 2; ++i) dma_w(k, 0, i);
-        if (!KR || k == 0) dma_s(k);
-        if (k == 0)
-          for (int i = 0; i < 2; ++i) dma_w(0, 1, i);
-      }
-    }
-    float swv[3] = {0.f, 0.f, 0.f};     // lane l: the weight scale of slice (kt & ~63) + l
-    for (int kt = 0; kt < t.nkt; ++kt) {
-      if constexpr (!KR) {
-        if ((kt & 63) == 0) {
-          const int kb = min(kt + lane, KB - 1);
+      // ---- K loop.  Step rb of a slice multiplies weight block rb by the 4 token blocks, adds the partial
+      // sums of the step before (so that no addition waits for its matrix instruction) and reads the next
+      // weight block; step 7 also reads the next slice's tokens, each as soon as its last product is issued,
+      // so that the matrix unit runs on across slices.  Two barriers a slice:
+      //   step 2   every wave has left slice kt - 1: the late part of kt + 1 is issued into its place; the
+      //            late part of kt, issued a slice ago, is resident (read from step 3 on)
+      //   step 5   every wave has read the early part of kt: that of kt + 2 is issued into its place; that of
+      //            kt + 1, issued a slice ago, is resident (read in step 7)
+      float swv[3] = {0.f, 0.f, 0.f};     // lane l: the weight scale of slice (kt & ~63) + l
+      auto load_swv = [&](int kt) {
+        const int kb = min(kt + lane, KB - 1);
 #pragma unroll
-          for (int h = 0; h < (SW ? 3 : 2); ++h) swv[h] = wsc[h][kb];
-        }
-      }
-      vm_barrier<EARLY>();              // slice kt is resident
-      dma_w(kt + 1, 1, 0);
-      dma_w(kt + 1, 1, 1);
-      if constexpr (KR) dma_s(kt + 1);
-      const uint8_t* st = smem + (kt & 1) * FT_STAGE;
-      const float* sS = reinterpret_cast<const float*>(smem + FT_SCALES + (kt & 1) * (2 * FT * 4));
-      auto frag = [&](int at) {
+        for (int h = 0; h < (SW ? 3 : 2); ++h) swv[h] = wsc[h][kb];
+        // (here, once in 64 slices: the compiler would otherwise wait for it, and with it for every
+        // DMA in flight, where the scales are used)
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+      };
+      if constexpr (!KR) load_swv(0);
+      lds_barrier();   // every wave is done with the previous tile's slices
+      issue_early(0);
+      issue_late(0);
+      issue_early(1);
+      vm_barrier<EARLY + LATE>();        // the early part of slice 0 is resident
+      auto frag = [&](const uint8_t* st, int at) {
         const uint4 a = *reinterpret_cast<const uint4*>(st + at);
         const uint4 b = *reinterpret_cast<const uint4*>(st + (at ^ 64));
         return i32x8{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
       };
+      auto scales_of = [&](int kt) { return reinterpret_cast<const float*>(smem + FT_SCALES + (kt & 3) * (2 * FT * 4)); };
       i32x8 tf[4], wf[2];
-      float ts[4];
+      float ts[4], tn[4], sc[4];          // token scales, those of the next slice, times the weights'
+      f32x4 d[2][4], xs[2];
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) tf[tb] = frag(tread + tb * 2048);
-      wf[0] = frag(wread);
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) ts[tb] = sS[wt * 64 + tb * 16 + i16];
-      float sw[3] = {1.f, 1.f, 1.f};
-      if constexpr (!KR) {
-#pragma unroll
-        for (int h = 0; h < (SW ? 3 : 2); ++h) sw[h] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swv[h]), kt & 63));
-        if constexpr (!SW) sw[2] = sw[1];
+      for (int tb = 0; tb < 4; ++tb) {
+        tf[tb] = frag(smem, tread + tb * 2048);
+        tn[tb] = scales_of(0)[wt * 64 + tb * 16 + i16];
+        ts[tb] = sc[tb] = 0.f;
+        d[1][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
-      f32x4 d[2][4];
-      f32x4 xs[2];
-      auto add = [&](auto rbc) {
-        constexpr int rb = decltype(rbc)::value;
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-          if constexpr (KR) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[rb][tb][r] = fmaf(d[rb & 1][tb][r] * ts[tb], xs[rb & 1][r], acc[rb][tb][r]);
-          } else {
-            const float s = ts[tb] * sw[rb < 4 ? 0 : (rb < 6 ? 1 : 2)];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[rb][tb][r] = fmaf(d[rb & 1][tb][r], s, acc[rb][tb][r]);
-          }
+      xs[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      wf[0] = frag(smem, wread);
+      for (int kt = 0; kt < t.nkt; ++kt) {
+        if constexpr (!KR) {
+          if ((kt & 63) == 0 && kt > 0) load_swv(kt);
         }
-      };
-      static_for<0, 8>([&](auto rbc) {
-        constexpr int rb = decltype(rbc)::value;
-        if constexpr (rb < 7) wf[(rb + 1) & 1] = frag(wread + (rb + 1 < 4 ? (rb + 1) * 2048 : 128 * 128 + (rb + 1 - 4) * 2048));
-        if constexpr (KR) xs[rb & 1] = *reinterpret_cast<const f32x4*>(sS + FT + (rb < 4 ? 0 : 128) + wn * 64 + (rb & 3) * 16 + 4 * q);
-        if constexpr (rb == 4) {
-          lds_barrier();                // the tokens' half and the first 128 weight rows are read
-          if constexpr (!KR) dma_s(kt + 2);
-        }
+        const uint8_t* st = smem + (kt & 1) * FT_STAGE;
+        const uint8_t* sn = smem + ((kt + 1) & 1) * FT_STAGE;
+        static_for<0, 8>([&](auto rbc) {
+          constexpr int rb = decltype(rbc)::value;
+          constexpr int pb = (rb + 7) & 7;   // the block whose sums are added
+          if constexpr (rb == 2) {
+            vm_barrier<EARLY>();
+            issue_late(kt + 1);
+          }
+          if constexpr (rb == 5) {
+            vm_barrier<LATE>();
+            dma_s(kt + 2);
+          }
+          if constexpr (rb < 7) wf[(rb + 1) & 1] = frag(st, wread + (rb + 1 < 4 ? (rb + 1) * 2048 : 128 * 128 + (rb + 1 - 4) * 2048));
+          else wf[0] = frag(sn, wread);
+          if constexpr (KR) xs[rb & 1] = *reinterpret_cast<const f32x4*>(scales_of(kt) + FT + (rb < 4 ? 0 : 128) + wn * 64 + (rb & 3) * 16 + 4 * q);
+          if constexpr (KR && rb == 1) {
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-          const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-          d[rb & 1][tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[rb & 1], tf[tb], z, 0, 0, 0, 0, 0, 0);
-          if constexpr (rb >= 4 && rb < 6) {
-            if (tb == 0 || tb == 2) dma_t(kt + 2, (rb - 4) * 2 + tb / 2);
+            for (int tb = 0; tb < 4; ++tb) ts[tb] = tn[tb];
           }
-          if constexpr (rb == 6) {
-            if (tb == 0 || tb == 2) dma_w(kt + 2, 0, tb / 2);
+          // the scales of the sums that this step adds
+          if constexpr (!KR && (rb == 1 || rb == 5 || (SW && rb == 7))) {
+            const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swv[rb == 1 ? 0 : (rb == 5 ? 1 : 2)]), kt & 63));
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+              if constexpr (rb == 1) ts[tb] = tn[tb];
+              sc[tb] = ts[tb] * w;
+            }
           }
+          __builtin_amdgcn_sched_barrier(0);
+          static_for<0, 4>([&](auto tbc) {
+            constexpr int tb = decltype(tbc)::value;
+            const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+            d[rb & 1][tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[rb & 1], tf[tb], z, 0, 0, 0, 0, 0, 0);
+            if constexpr (rb == 7) {
+              tf[tb] = frag(sn, tread + tb * 2048);
+              tn[tb] = scales_of(kt + 1)[wt * 64 + tb * 16 + i16];
+            }
+            if constexpr (rb == 5 || rb == 6) {
+              constexpr int i = (rb - 5) * 4 + tb;   // the early part of kt + 2, one DMA a matrix instruction
+              if constexpr (i < 4) dma_t(kt + 2, i);
+              else if constexpr (i < 6) dma_w(kt + 2, 0, i - 4);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if constexpr (KR) acc[pb][tb][r] = fmaf(d[(rb + 1) & 1][tb][r] * ts[tb], xs[(rb + 1) & 1][r], acc[pb][tb][r]);
+              else acc[pb][tb][r] = fmaf(d[(rb + 1) & 1][tb][r], sc[tb], acc[pb][tb][r]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          });
+        });
+      }
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (KR) acc[7][tb][r] = fmaf(d[1][tb][r] * ts[tb], xs[1][r], acc[7][tb][r]);
+          else acc[7][tb][r] = fmaf(d[1][tb][r], sc[tb], acc[7][tb][r]);
         }
-        if constexpr (rb > 0) add(std::integral_constant<int, rb - 1>{});
-        __builtin_amdgcn_sched_barrier(0);   // one step at a time (registers)
-      });
-      add(std::integral_constant<int, 7>{});
     }
     __builtin_amdgcn_s_waitcnt(0);      // the slices past the end (zeros) have landed
     rederive_lane();

@@ -39,9 +39,16 @@ __device__ __forceinline__ void transpose4(uint32_t* v) {
   v[0] = c.a; v[1] = c.b; v[2] = d.a; v[3] = d.b;
 }
 
-// 4 bytes per lane from buffer offset `voff` straight into LDS at lds_addr + 4 * lane
-__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds_addr), "v"(voff), "s"(rsrc)
+// 4 bytes per lane from buffer offset voff + soff (soff the same in every lane) straight into LDS at
+// lds_addr + 4 * lane
+__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
+               : "memory", "m0");
+}
+
+// 16 bytes per lane in the same way, at lds_addr + 16 * lane
+__device__ __forceinline__ void dma16s(i32x4 rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory", "m0");
 }
 
@@ -148,7 +155,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
     const FtTile t = decode(item);
     rederive_lane();
     const int tread = (wt * 64 + i16) * 128 + ((q ^ ((i16 >> 1) & 7)) << 4);
-    const int wread = FT_OP + (wn * 64 + i16) * 128 + ((q ^ ((i16 >> 1) & 7)) << 4);
+    const int wread = (wn * 64 + i16) * 128 + ((q ^ ((i16 >> 1) & 7)) << 4);
     // ---- the tile's operands
     i32x4 rT, rW[2], rS;
     uint32_t toff[4], soff, s_ld;
@@ -198,21 +205,28 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       soff = uint32_t(t.off + t.m0 + (wave & 3) * 64 + lane) * 4;
     }
     // ---- DMA of one slice: the tokens, their scales and the first 128 weight rows; the other 128
-    // (offsets past the K range get the top bit and read zeros; so does a whole slice past the last)
-    const int kleft = t.khi - 1 - t.kbase - lchunk, kleft1 = t.khi - 1 - t.kbase - (lchunk ^ 64);
-    auto outside = [&](int kt, int i) { return uint32_t(((i & 1) ? kleft1 : kleft) - kt * 128) & kInvalid; };
+    // The lane's offsets hold its row and chunk, the slice's place in K is the same in all lanes.  A slice
+    // past the last has a resource without records; in the last one, where it is not a whole 128 bytes, the
+    // chunks past its end get the top bit.  Both read zeros.
+    const int tail = (t.khi - t.kbase) & 127;      // bytes of the last slice, 0: whole
+    const uint32_t past0 = tail != 0 && lchunk >= tail ? kInvalid : 0u, past1 = tail != 0 && (lchunk ^ 64) >= tail ? kInvalid : 0u;
     const uint32_t woff = uint32_t(wave * 16 + (lane >> 3)) * ldw + uint32_t(lchunk);
     const uint32_t woff1 = uint32_t(wave * 16 + 8 + (lane >> 3)) * ldw + uint32_t(lchunk ^ 64);
+    auto at_slice = [&](i32x4 r, int kt) {
+      r[2] = kt < t.nkt ? r[2] : 0;
+      return r;
+    };
+    auto off_at = [&](uint32_t off, int kt, int odd) { return ((odd ? past1 : past0) & (kt == t.nkt - 1 ? kInvalid : 0u)) | off; };
     auto dma_t = [&](int kt, int i) {
-      dma16(rT, lds_base + (kt & 1) * FT_STAGE + (wave * 32 + i * 8) * 128, (toff[i] + uint32_t(t.kbase + kt * 128)) | outside(kt, i));
+      dma16s(at_slice(rT, kt), lds_base + (kt & 1) * FT_STAGE + (wave * 32 + i * 8) * 128, off_at(toff[i], kt, i & 1),
+             uint32_t(t.kbase + kt * 128));
     };
     auto dma_w = [&](int kt, int h, int i) {
-      dma16(rW[h], lds_base + (kt & 1) * FT_STAGE + FT_OP + (h * 128 + wave * 16 + i * 8) * 128,
-            ((i ? woff1 : woff) + uint32_t(t.kbase + kt * 128)) | outside(kt, i));
+      dma16s(at_slice(rW[h], kt), lds_base + (kt & 1) * FT_STAGE + FT_OP + (h * 128 + wave * 16 + i * 8) * 128,
+             off_at(i ? woff1 : woff, kt, i), uint32_t(t.kbase + kt * 128));
     };
     auto dma_s = [&](int kt) {
-      dma4(rS, lds_base + FT_SCALES + (kt & 3) * (2 * FT * 4) + (KR ? wave : wave & 3) * 256,
-           (soff + uint32_t(kt) * s_ld) | (kt < t.nkt ? 0u : kInvalid));
+      dma4(at_slice(rS, kt), lds_base + FT_SCALES + (kt & 3) * (2 * FT * 4) + (KR ? wave : wave & 3) * 256, soff, uint32_t(kt) * s_ld);
     };
     // The early part of a slice (its tokens, scales and first 128 weight rows: 7 DMAs) and the late one
     // (the other weight rows: 2).
@@ -257,9 +271,11 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       issue_late(0);
       issue_early(1);
       vm_barrier<EARLY + LATE>();        // the early part of slice 0 is resident
-      auto frag = [&](const uint8_t* st, int at) {
-        const uint4 a = *reinterpret_cast<const uint4*>(st + at);
-        const uint4 b = *reinterpret_cast<const uint4*>(st + (at ^ 64));
+      // (the two chunks of a fragment are 64 bytes apart in the row, either way round: a base each, so that the
+      // rows' distances fit the instructions' offsets)
+      auto frag = [&](const uint8_t* p0, const uint8_t* p1, int at) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p0 + at);
+        const uint4 b = *reinterpret_cast<const uint4*>(p1 + at);
         return i32x8{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
       };
       auto scales_of = [&](int kt) { return reinterpret_cast<const float*>(smem + FT_SCALES + (kt & 3) * (2 * FT * 4)); };
@@ -268,19 +284,19 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       f32x4 d[2][4], xs[2];
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
-        tf[tb] = frag(smem, tread + tb * 2048);
+        tf[tb] = frag(smem + tread, smem + (tread ^ 64), tb * 2048);
         tn[tb] = scales_of(0)[wt * 64 + tb * 16 + i16];
         ts[tb] = sc[tb] = 0.f;
         d[1][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
       xs[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      wf[0] = frag(smem, wread);
+      wf[0] = frag(smem + wread, smem + (wread ^ 64), FT_OP);
       for (int kt = 0; kt < t.nkt; ++kt) {
         if constexpr (!KR) {
           if ((kt & 63) == 0 && kt > 0) load_swv(kt);
         }
-        const uint8_t* st = smem + (kt & 1) * FT_STAGE;
-        const uint8_t* sn = smem + ((kt + 1) & 1) * FT_STAGE;
+        const int st = (kt & 1) * FT_STAGE, sn = FT_STAGE - st;   // this slice's stage, the next one's
+        const uint8_t *w0 = smem + st + wread, *w1 = smem + st + (wread ^ 64);
         static_for<0, 8>([&](auto rbc) {
           constexpr int rb = decltype(rbc)::value;
           constexpr int pb = (rb + 7) & 7;   // the block whose sums are added
@@ -292,8 +308,8 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
             vm_barrier<LATE>();
             dma_s(kt + 2);
           }
-          if constexpr (rb < 7) wf[(rb + 1) & 1] = frag(st, wread + (rb + 1 < 4 ? (rb + 1) * 2048 : 128 * 128 + (rb + 1 - 4) * 2048));
-          else wf[0] = frag(sn, wread);
+          if constexpr (rb < 7) wf[(rb + 1) & 1] = frag(w0, w1, FT_OP + (rb + 1 < 4 ? (rb + 1) * 2048 : 128 * 128 + (rb + 1 - 4) * 2048));
+          else wf[0] = frag(smem + sn + wread, smem + sn + (wread ^ 64), FT_OP);
           if constexpr (KR) xs[rb & 1] = *reinterpret_cast<const f32x4*>(scales_of(kt) + FT + (rb < 4 ? 0 : 128) + wn * 64 + (rb & 3) * 16 + 4 * q);
           if constexpr (KR && rb == 1) {
 #pragma unroll
@@ -314,7 +330,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
             const f32x4 z = {0.f, 0.f, 0.f, 0.f};
             d[rb & 1][tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[rb & 1], tf[tb], z, 0, 0, 0, 0, 0, 0);
             if constexpr (rb == 7) {
-              tf[tb] = frag(sn, tread + tb * 2048);
+              tf[tb] = frag(smem + sn + tread, smem + sn + (tread ^ 64), tb * 2048);
               tn[tb] = scales_of(kt + 1)[wt * 64 + tb * 16 + i16];
             }
             if constexpr (rb == 5 || rb == 6) {
@@ -493,16 +509,20 @@ __global__ __launch_bounds__(256) void fb_scale_t_kernel(FbScaleTArgs a) {
   const int64_t r0 = blk / nj * 64;
   const int j0 = int(blk % nj) * 64;
   const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < 64; i += 4) {
-    const int64_t r = r0 + i;
-    float v = 0.f;
-    if (r < m.rows && j0 + x < m.kb) {
-      const int64_t src = m.map ? int64_t(m.map[r]) : r;
-      if (src >= 0 && src < m.src_rows) v = m.in[src * m.kb + j0 + x];
-    }
-    tile[i][x] = v;
+  // (all 16 loads of a thread in flight, the map's first)
+  int64_t src[16];
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int64_t r = r0 + 4 * i + y;
+    src[i] = r >= m.rows ? -1 : (m.map ? int64_t(m.map[r]) : r);
   }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = src[i] >= 0 && src[i] < m.src_rows && j0 + x < m.kb ? m.in[src[i] * m.kb + j0 + x] : 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) tile[4 * i + y][x] = v[i];
   __syncthreads();
+#pragma unroll
   for (int i = y; i < 64; i += 4)
     if (j0 + i < m.kb && r0 + x < m.rows) m.out[int64_t(j0 + i) * m.ld + r0 + x] = tile[x][i];
 }

@@ -125,7 +125,7 @@ struct FbGemm {
   const float* prob;                // SwiGLU: [rows] or NULL (1)
   uint8_t* h_codes;                 // SwiGLU: [rows][F]
   float* h_scales;                  // SwiGLU: streaming [rows][ceil(F/128)], tiles [ceil(F/128)][ast_ld]
-  int tiles_upper;
+  int grid_main;                    // workgroups of the main launch's whole rounds (set by the launcher)
 };
 mge_status launch_fb_stream(const FbGemm& p, bool swiglu, hipStream_t s);
 mge_status launch_fb_tile(const FbGemm& p, bool swiglu, hipStream_t s);

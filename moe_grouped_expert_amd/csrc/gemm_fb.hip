@@ -20,16 +20,40 @@
 
 #include "fp8b.hpp"
 
+#include <algorithm>
+
 namespace mge {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int FT = 256;                       // rows of a tile on both sides
-constexpr int FT_THREADS = 512;
-constexpr int FT_OP = FT * 128;               // bytes of an operand in a stage
-constexpr int FT_STAGE = 2 * FT_OP;           // tokens, then weights
-constexpr int FT_SCALES = 2 * FT_STAGE;       // then a ring of 4 slices' scales: the tokens' and (dW) the row operand's
-constexpr int FT_LDS = FT_SCALES + 4 * 2 * FT * 4;
+// A kernel's tile: WN x WT waves of RB x TB blocks of 16 x 16 (weight rows x tokens), NST LDS stages
+template <int WN_, int WT_, int RB_, int TB_, int NST_>
+struct FbTile {
+  static constexpr int WN = WN_, WT = WT_, RB = RB_, TB = TB_, NST = NST_;
+  static constexpr int WAVES = WN * WT, THREADS = 64 * WAVES;
+  static constexpr int NR = WN * RB * 16, NT = WT * TB * 16;   // weight rows, tokens
+  static constexpr int H = RB / 2;                             // a wave's blocks in each half of the weight rows
+  static constexpr int OPT = NT * 128, OPW = NR * 128;         // bytes of the operands in a stage: tokens, then weights
+  static constexpr int STAGE = OPT + OPW;
+  static constexpr int SCALES = NST * STAGE;                   // then a ring of 2 NST slices' scales, 64 a wave:
+  static constexpr int RING = WAVES * 256;                     // the tokens' (first waves), then the row operand's
+  static constexpr int LDS = SCALES + 2 * NST * RING;
+  static constexpr int DT = NT / 8 / WAVES, DW = NR / 16 / WAVES;   // DMAs of a wave: tokens, each half of the weights
+  static_assert((NST & (NST - 1)) == 0 && RB % 2 == 0 && NT % (8 * WAVES) == 0 && NR % (16 * WAVES) == 0, "whole DMAs");
+  static_assert(NT / 64 + (NR + 63) / 64 <= WAVES && NT % 64 == 0, "64 scales a wave");
+};
+typedef FbTile<2, 4, 8, 4, 2> FbMain;    // 256 x 256
+typedef FbTile<2, 2, 4, 4, 4> FbQuad;    // 128 x 128
+
+// vm_barrier<A> where n > 0 (the same in every lane), else vm_barrier<B>.  The choice is made inside the asm: a
+// branch of the compiler's would cut the K loop's body into blocks, across which it moves the additions.
+template <int A, int B>
+__device__ __forceinline__ void vm_barrier_if(int n) {
+  asm volatile(
+      "s_cmp_gt_i32 %0, 0\n\ts_cbranch_scc0 .Lfb_b%=\n\ts_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_branch .Lfb_m%=\n"
+      ".Lfb_b%=:\n\ts_waitcnt vmcnt(%2) lgkmcnt(0)\n.Lfb_m%=:\n\ts_barrier" ::"s"(n), "n"(A), "n"(B)
+      : "memory", "scc");
+}
 
 // 4 x 4 transpose over the lanes 16 apart: lane 16q + i gives v[j] for j = 0..3 and gets v[q] of the
 // lanes 16p + i in v[p]
@@ -56,17 +80,27 @@ struct FtTile {
   int valid, e, off, m_valid, m0, n0, nkt, kbase, khi;
 };
 
-// KR: dW (FbWgrad), else C (FbGemm).  SW: the SwiGLU epilogue.
-template <bool KR, bool SW, int OUT, typename P>
+// What a tile's DMAs need
+struct FtOps {
+  i32x4 rT, rW[2], rS;
+  uint32_t toff[4], woff[2], soff, s_ld, past0, past1;
+};
+
+// KR: dW (FbWgrad), else C (FbGemm).  SW: the SwiGLU epilogue.  TAIL: the tiles past the main launch's last
+// whole round, in quarters (their 128 x 128 quadrants).
+template <typename TL, bool KR, bool SW, int OUT, bool TAIL, typename P>
 __device__ __forceinline__ void fb_tile_body(const P& p) {
+  constexpr int WN = TL::WN, RB = TL::RB, TB = TL::TB, H = TL::H, NST = TL::NST;
+  constexpr int HR = TL::NR / 2;               // weight rows of a half
+  static_assert(!SW || HR == FB, "a block of h is a tile's columns");
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int32_t s_prefix[G_MAXE + 1];
   __shared__ int32_t s_mtiles[G_MAXE];
-  __shared__ uint32_t s_amax[SW ? 2 * FT : 1];
+  __shared__ uint32_t s_amax[SW ? WN * TL::NT : 1];
   const uint32_t lds_base = uniform(int(uint32_t(reinterpret_cast<uintptr_t>(smem))));
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
-  const int wn = wave & 1, wt = wave >> 1;    // the wave's half of each 128 weight rows, its 64 tokens
+  const int wn = wave % WN, wt = wave / WN;    // the wave's share of each half of the weight rows, its tokens
   // derived again from an opaque copy of the lane at the top of every tile and after its K loop, so
   // that one phase's addresses are not kept in registers through the other
   int i16 = lane & 15, q = lane >> 4;
@@ -77,15 +111,16 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
     q = v >> 4;
   };
 
+  // tiles of 256 x 256 whatever the kernel's own (SwiGLU: 128 columns of gate and of up, the kernel's tokens)
+  constexpr int TM = SW ? TL::NT : 256, TN = SW ? FB : 256;
   int ncols = KR ? p.K : p.N;                              // columns of C
   if constexpr (SW) ncols = p.F;
-  const int per = SW ? FT / 2 : FT;
-  const int ntiles = (ncols + per - 1) / per;
+  const int ntiles = (ncols + TN - 1) / TN;
   auto group_off = [&](int off) { return off < 0 ? 0 : (off > p.rows ? p.rows : off); };
   auto group_size = [&](int size, int off) { return size < 0 ? 0 : (size > p.rows - off ? p.rows - off : size); };
   if constexpr (!KR) {
-    for (int e = tid; e < p.E; e += FT_THREADS)
-      s_mtiles[e] = ((p.sizes ? group_size(p.sizes[e], group_off(p.offs[e])) : p.rows) + FT - 1) / FT;
+    for (int e = tid; e < p.E; e += TL::THREADS)
+      s_mtiles[e] = ((p.sizes ? group_size(p.sizes[e], group_off(p.offs[e])) : p.rows) + TM - 1) / TM;
     __syncthreads();
     if (tid == 0) {
       int acc = 0;
@@ -97,16 +132,31 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
     }
     __syncthreads();
   }
-  const int ymt = KR ? (p.N + FT - 1) / FT : 0;
+  const int ymt = KR ? (p.N + TM - 1) / TM : 0;
   const int total = KR ? p.E * ymt * ntiles : uniform(s_prefix[p.E]);
   const int nwg = gridDim.x;
   int vid = blockIdx.x;
   if ((nwg & 7) == 0) vid = (blockIdx.x & 7) * (nwg >> 3) + (blockIdx.x >> 3);
+  // The tiles past the main launch's last whole round run as quadrants where those are at most two a
+  // workgroup; both launches decide from the same numbers.
+  int items = total, t_full = 0;
+  if constexpr (!KR && !SW) {
+    const int full = total / p.grid_main * p.grid_main, left = total - full;
+    const bool split = 2 * left <= p.grid_main;
+    t_full = uniform(full);
+    items = uniform(TAIL ? (split ? 4 * left : 0) : (split ? full : total));
+    if constexpr (TAIL) {
+      // an equal run of the items for each XCD (at most two a workgroup: the second ones at nwg on)
+      const int n = items < nwg ? items : nwg, run = (n + 7) >> 3;
+      if ((nwg & 7) == 0) vid = int(blockIdx.x >> 3) < run ? int(blockIdx.x & 7) * run + int(blockIdx.x >> 3) : items;
+    }
+  }
 
-  auto decode = [&](int tile) {
+  auto decode = [&](int item) {
     FtTile t{};
-    t.valid = tile < total;
+    t.valid = item < items;
     if (!t.valid) return t;
+    const int tile = TAIL ? t_full + item / 4 : item;
     int local, mtn;
     if constexpr (KR) {
       t.e = tile / (ymt * ntiles);
@@ -127,8 +177,12 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
     const int band = min(local / (8 * ntiles), nband - 1);
     const int within = local - band * 8 * ntiles;
     const int gm = band == nband - 1 ? mtn - band * 8 : 8;
-    t.m0 = (band * 8 + within % gm) * FT;
-    t.n0 = (within / gm) * per;
+    t.m0 = (band * 8 + within % gm) * TM;
+    t.n0 = (within / gm) * TN;
+    if constexpr (TAIL) {
+      t.m0 += (item & 2) ? 128 : 0;
+      t.n0 += (item & 1) ? 128 : 0;
+    }
     t.off = p.sizes ? uniform(group_off(ld_uniform(p.offs, t.e))) : 0;
     const int size = p.sizes ? uniform(group_size(ld_uniform(p.sizes, t.e), t.off)) : p.rows;
     if constexpr (KR) {
@@ -141,7 +195,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
     } else {
       t.m_valid = size;
       t.khi = p.K;
-      t.nkt = (p.K + 127) / 128;
+      t.nkt = TAIL && (t.m0 >= size || t.n0 >= ncols) ? 0 : (p.K + 127) / 128;   // (a quadrant of nothing)
     }
     return t;
   };
@@ -150,127 +204,168 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   // swizzle puts there: (l % 8) ^ (l / 16), that ^ 4 in odd instructions
   const int lchunk = ((lane & 7) ^ (lane >> 4)) * 16;
   const uint32_t ldw = KR ? uint32_t(p.rows) : uint32_t(p.K);   // bytes of an operand row
+  const int KB = KR ? 0 : (p.K + 127) / 128;
+  constexpr int DT = TL::DT, DW = TL::DW;
+  static_assert(DT <= 4 && DW <= 2, "offsets of a lane");
+  constexpr int SWV = TL::NT / 64;             // the first wave that brings the row operand's scales
 
-  for (int item = vid; item < total; item += nwg) {
-    const FtTile t = decode(item);
-    rederive_lane();
-    const int tread = (wt * 64 + i16) * 128 + ((q ^ ((i16 >> 1) & 7)) << 4);
-    const int wread = (wn * 64 + i16) * 128 + ((q ^ ((i16 >> 1) & 7)) << 4);
-    // ---- the tile's operands
-    i32x4 rT, rW[2], rS;
-    uint32_t toff[4], soff, s_ld;
-    const float* wsc[3] = {nullptr, nullptr, nullptr};   // the weights' scales: rows rb 0..3, 4..5, 6..7
-    const int KB = KR ? 0 : (p.K + 127) / 128;
-    if constexpr (KR) {
-      auto left = [](int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); };
-      rT = make_rsrc_n(p.Y + int64_t(t.m0) * p.rows, uint32_t(left(p.N - t.m0, FT)) * ldw);
+  // Rows of A of the lane's DMAs
+  auto rows_of = [&](const FtTile& t, int* src) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) toff[i] = uint32_t(wave * 32 + i * 8 + (lane >> 3)) * ldw + (lchunk ^ ((i & 1) * 64));
+    for (int i = 0; i < DT; ++i) {
+      const int m = t.m0 + wave * (DT * 8) + i * 8 + (lane >> 3);
+      src[i] = t.valid && m < t.m_valid ? t.off + m : -1;
+      if constexpr (!KR) {
+        if (src[i] >= 0 && p.map) src[i] = p.map[src[i]];
+      }
+    }
+  };
+  auto setup = [&](const FtTile& t, const int* src) {
+    FtOps o;
+    auto left = [](int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); };
+    if constexpr (KR) {
+      o.rT = make_rsrc_n(p.Y + int64_t(t.m0) * p.rows, uint32_t(left(p.N - t.m0, TL::NT)) * ldw);
+#pragma unroll
+      for (int i = 0; i < DT; ++i) o.toff[i] = uint32_t(wave * (DT * 8) + i * 8 + (lane >> 3)) * ldw + (lchunk ^ ((i & 1) * 64));
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        rW[h] = make_rsrc_n(p.X + int64_t(t.n0 + 128 * h) * p.rows, uint32_t(left(p.K - t.n0 - 128 * h, 128)) * ldw);
-      // waves 0..3 bring the scales of 64 rows of dY each, waves 4..7 those of X
+        o.rW[h] = make_rsrc_n(p.X + int64_t(t.n0 + HR * h) * p.rows, uint32_t(left(p.K - t.n0 - HR * h, HR)) * ldw);
       const uint32_t nb = uint32_t((p.rows + 127) / 128);
-      const int n = wave < 4 ? p.N : p.K;
-      rS = make_rsrc_n(wave < 4 ? p.Yst : p.Xst, nb * uint32_t(n) * 4);
-      s_ld = uint32_t(n) * 4;
-      soff = uint32_t(t.kbase / 128) * s_ld + uint32_t((wave < 4 ? t.m0 : t.n0) + (wave & 3) * 64 + lane) * 4;
+      const int n = wave < SWV ? p.N : p.K;
+      o.rS = make_rsrc_n(wave < SWV ? p.Yst : p.Xst, nb * uint32_t(n) * 4);
+      o.s_ld = uint32_t(n) * 4;
+      const int row = (wave < SWV ? t.m0 + wave * 64 : t.n0 + (wave - SWV) * 64) + lane;
+      o.soff = row < n ? uint32_t(t.kbase / 128) * o.s_ld + uint32_t(row) * 4 : kInvalid;
     } else {
-      rT = make_rsrc_n(p.A, uint32_t(p.src_rows) * ldw);
+      o.rT = make_rsrc_n(p.A, uint32_t(p.src_rows) * ldw);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int m = t.m0 + wave * 32 + i * 8 + (lane >> 3);
-        int src = t.off + m;
-        if (m < t.m_valid && p.map) src = p.map[src];
-        const bool in = m < t.m_valid && src >= 0 && src < p.src_rows;
-        toff[i] = in ? uint32_t(src) * ldw + (lchunk ^ ((i & 1) * 64)) : kInvalid;
-      }
+      for (int i = 0; i < DT; ++i)
+        o.toff[i] = src[i] >= 0 && src[i] < p.src_rows ? uint32_t(src[i]) * ldw + (lchunk ^ ((i & 1) * 64)) : kInvalid;
       const uint8_t* w = p.W ? ld_uniform(p.W, t.e) : p.Wv[t.e];
       const float* ws = p.W ? ld_uniform(p.Ws, t.e) : p.Wsv[t.e];
-      const int nrows = SW ? p.F : p.N;
-      auto left = [](int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); };
+      const int nrows = SW ? ncols : p.N;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r0 = SW ? t.n0 : t.n0 + 128 * h;          // (SwiGLU: gate, then up rows of the same columns)
-        rW[h] = make_rsrc_n(w + (int64_t(r0) + (SW ? h * p.F : 0)) * p.K, uint32_t(left(nrows - r0, 128)) * ldw);
+        const int r0 = SW ? t.n0 : t.n0 + HR * h;          // (SwiGLU: gate, then up rows of the same columns)
+        o.rW[h] = make_rsrc_n(w + (int64_t(r0) + (SW ? h * ncols : 0)) * p.K, uint32_t(left(nrows - r0, HR)) * ldw);
       }
-      const int last = (SW ? 2 * p.F : p.N) - 1;
-      const int up = SW ? p.F + t.n0 + wn * 64 : t.n0 + 128;
-      wsc[0] = ws + int64_t(t.n0 / 128) * KB;
-      wsc[1] = ws + int64_t(min(up, last) / 128) * KB;
-      wsc[2] = ws + int64_t(min(SW ? up + 32 : up, last) / 128) * KB;
-      // (waves 4..7 bring the same scales as waves 0..3: every wave then has the same count to wait for)
-      rS = make_rsrc_n(p.Ast, uint32_t(KB) * uint32_t(p.ast_ld) * 4);
-      s_ld = uint32_t(p.ast_ld) * 4;
-      soff = uint32_t(t.off + t.m0 + (wave & 3) * 64 + lane) * 4;
+      // the tokens' scales, 64 a wave; in the other waves' first lanes those of the weights: of the tile's
+      // halves, or with SwiGLU of the gate rows and of every 32 up rows
+      const int all = SW ? 2 * ncols : p.N;
+      if (wave < SWV) {
+        o.rS = make_rsrc_n(p.Ast, uint32_t(KB) * uint32_t(p.ast_ld) * 4);
+        o.s_ld = uint32_t(p.ast_ld) * 4;
+        const int m = t.m0 + wave * 64 + lane;
+        o.soff = m < t.m_valid ? uint32_t(t.off + m) * 4 : kInvalid;
+      } else {
+        const int row = lane == 0 ? t.n0 : (SW ? ncols + t.n0 + (lane - 1) * 32 : t.n0 + HR);
+        o.rS = make_rsrc_n(ws, uint32_t((all + FB - 1) / FB) * uint32_t(KB) * 4);
+        o.s_ld = 4;
+        o.soff = lane < (SW ? 5 : 2) && row < all ? uint32_t(row / FB) * uint32_t(KB) * 4 : kInvalid;
+      }
     }
-    // ---- DMA of one slice: the tokens, their scales and the first 128 weight rows; the other 128
     // The lane's offsets hold its row and chunk, the slice's place in K is the same in all lanes.  A slice
     // past the last has a resource without records; in the last one, where it is not a whole 128 bytes, the
     // chunks past its end get the top bit.  Both read zeros.
     const int tail = (t.khi - t.kbase) & 127;      // bytes of the last slice, 0: whole
-    const uint32_t past0 = tail != 0 && lchunk >= tail ? kInvalid : 0u, past1 = tail != 0 && (lchunk ^ 64) >= tail ? kInvalid : 0u;
-    const uint32_t woff = uint32_t(wave * 16 + (lane >> 3)) * ldw + uint32_t(lchunk);
-    const uint32_t woff1 = uint32_t(wave * 16 + 8 + (lane >> 3)) * ldw + uint32_t(lchunk ^ 64);
-    auto at_slice = [&](i32x4 r, int kt) {
-      r[2] = kt < t.nkt ? r[2] : 0;
-      return r;
-    };
-    auto off_at = [&](uint32_t off, int kt, int odd) { return ((odd ? past1 : past0) & (kt == t.nkt - 1 ? kInvalid : 0u)) | off; };
-    auto dma_t = [&](int kt, int i) {
-      dma16s(at_slice(rT, kt), lds_base + (kt & 1) * FT_STAGE + (wave * 32 + i * 8) * 128, off_at(toff[i], kt, i & 1),
-             uint32_t(t.kbase + kt * 128));
-    };
-    auto dma_w = [&](int kt, int h, int i) {
-      dma16s(at_slice(rW[h], kt), lds_base + (kt & 1) * FT_STAGE + FT_OP + (h * 128 + wave * 16 + i * 8) * 128,
-             off_at(i ? woff1 : woff, kt, i), uint32_t(t.kbase + kt * 128));
-    };
-    auto dma_s = [&](int kt) {
-      dma4(at_slice(rS, kt), lds_base + FT_SCALES + (kt & 3) * (2 * FT * 4) + (KR ? wave : wave & 3) * 256, soff, uint32_t(kt) * s_ld);
-    };
-    // The early part of a slice (its tokens, scales and first 128 weight rows: 7 DMAs) and the late one
-    // (the other weight rows: 2).
-    constexpr int EARLY = 7, LATE = 2;
-    auto issue_late = [&](int kt) {
-      dma_w(kt, 1, 0);
-      dma_w(kt, 1, 1);
-    };
-    auto issue_early = [&](int kt) {
-      dma_s(kt);
-      for (int i = 0; i < 4; ++i) dma_t(kt, i);
-      for (int i = 0; i < 2; ++i) dma_w(kt, 0, i);
-    };
+    o.past0 = tail != 0 && lchunk >= tail ? kInvalid : 0u;
+    o.past1 = tail != 0 && (lchunk ^ 64) >= tail ? kInvalid : 0u;
+    o.woff[0] = uint32_t(wave * (DW * 8) + (lane >> 3)) * ldw + uint32_t(lchunk);
+    o.woff[1] = uint32_t(wave * (DW * 8) + 8 + (lane >> 3)) * ldw + uint32_t(lchunk ^ 64);
+    return o;
+  };
+  // (a wave's first LDS row is a multiple of 16, so that its even and odd instructions are those of the swizzle)
+  static_assert(DT % 2 == 0 && DW % 2 == 0, "even instructions start at even groups of 8 rows");
+  auto at_slice = [](i32x4 r, const FtTile& t, int kt) {
+    r[2] = kt < t.nkt ? r[2] : 0;
+    return r;
+  };
+  // (no offset beside a resource without records, so that no form of the range check takes one from the other)
+  auto place = [](const i32x4& r, uint32_t k) { return r[2] != 0 ? k : 0u; };
+  auto off_at = [](const FtOps& o, const FtTile& t, uint32_t off, int kt, int odd) {
+    return ((odd ? o.past1 : o.past0) & (kt == t.nkt - 1 ? kInvalid : 0u)) | off;
+  };
+  auto dma_t = [&](const FtOps& o, const FtTile& t, int kt, int i) {
+    const i32x4 r = at_slice(o.rT, t, kt);
+    dma16s(r, lds_base + (kt & (NST - 1)) * TL::STAGE + (wave * (DT * 8) + i * 8) * 128, off_at(o, t, o.toff[i], kt, i & 1),
+           place(r, uint32_t(t.kbase + kt * 128)));
+  };
+  auto dma_w = [&](const FtOps& o, const FtTile& t, int kt, int h, int i) {
+    const i32x4 r = at_slice(o.rW[h], t, kt);
+    dma16s(r, lds_base + (kt & (NST - 1)) * TL::STAGE + TL::OPT + (h * HR + wave * (DW * 8) + i * 8) * 128, off_at(o, t, o.woff[i], kt, i),
+           place(r, uint32_t(t.kbase + kt * 128)));
+  };
+  auto dma_s = [&](const FtOps& o, const FtTile& t, int kt) {
+    const i32x4 r = at_slice(o.rS, t, kt);
+    dma4(r, lds_base + TL::SCALES + (kt & (2 * NST - 1)) * TL::RING + wave * 256, o.soff, place(r, uint32_t(kt) * o.s_ld));
+  };
+  // The early part of a slice (its tokens, scales and the first half of the weight rows) and the late one
+  constexpr int EARLY = 1 + DT + DW, LATE = DW;
+  auto issue_late = [&](const FtOps& o, const FtTile& t, int kt) {
+#pragma unroll
+    for (int i = 0; i < DW; ++i) dma_w(o, t, kt, 1, i);
+  };
+  auto issue_early = [&](const FtOps& o, const FtTile& t, int kt) {
+    dma_s(o, t, kt);
+#pragma unroll
+    for (int i = 0; i < DT; ++i) dma_t(o, t, kt, i);
+#pragma unroll
+    for (int i = 0; i < DW; ++i) dma_w(o, t, kt, 0, i);
+  };
+  auto prologue = [&](const FtOps& o, const FtTile& t) {
+#pragma unroll
+    for (int k = 0; k < NST; ++k) {
+      issue_early(o, t, k);
+      issue_late(o, t, k);
+    }
+  };
+  // Stores that every wave's epilogue issues at least: the next tile's first DMAs are issued before
+  // them, and its first waits leave them in flight
+  constexpr int STORES = OUT == OUT_BF16 ? TB * H / 4 * 2 * 2 : (OUT == OUT_F32 ? TB * RB : (SW ? TB : 0));
+  static_assert(NST * (EARLY + LATE) + STORES < 64, "vmcnt");
 
-    f32x4 acc[8][4];
+  FtTile t = decode(vid);
+  FtOps o{};
+  int stores = 0;   // 1: the wave has stores in flight that are newer than this tile's first DMAs
+  int src[DT];
+  rows_of(t, src);
+  if (t.valid) {
+    o = setup(t, src);
+    if (t.nkt > 0) prologue(o, t);
+  }
+  for (int item = vid; item < items; item += nwg) {
+    rederive_lane();
+    // loads whose latency the K loop hides: the next tile's rows, the probabilities of this one's
+    const FtTile nxt = decode(item + nwg);
+    rows_of(nxt, src);
+    float pr[TB];
+    if constexpr (SW) {
 #pragma unroll
-    for (int rb = 0; rb < 8; ++rb)
+      for (int tb = 0; tb < TB; ++tb) {
+        const int m = t.m0 + wt * (TB * 16) + tb * 16 + i16;
+        pr[tb] = p.prob == nullptr ? 1.f : (m < t.m_valid ? p.prob[int64_t(t.off) + m] : 0.f);
+      }
+    }
+    const int tread = (wt * (TB * 16) + i16) * 128 + ((q ^ ((i16 >> 1) & 7)) << 4);
+    const int wread = (wn * (H * 16) + i16) * 128 + ((q ^ ((i16 >> 1) & 7)) << 4);
+    f32x4 acc[RB][TB];
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) acc[rb][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) acc[rb][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     if (t.nkt > 0) {
-      // ---- K loop.  Step rb of a slice multiplies weight block rb by the 4 token blocks, adds the partial
+      // ---- K loop.  Step rb of a slice multiplies weight block rb by the token blocks, adds the partial
       // sums of the step before (so that no addition waits for its matrix instruction) and reads the next
-      // weight block; step 7 also reads the next slice's tokens, each as soon as its last product is issued,
-      // so that the matrix unit runs on across slices.  Two barriers a slice:
-      //   step 2   every wave has left slice kt - 1: the late part of kt + 1 is issued into its place; the
-      //            late part of kt, issued a slice ago, is resident (read from step 3 on)
-      //   step 5   every wave has read the early part of kt: that of kt + 2 is issued into its place; that of
-      //            kt + 1, issued a slice ago, is resident (read in step 7)
-      float swv[3] = {0.f, 0.f, 0.f};     // lane l: the weight scale of slice (kt & ~63) + l
-      auto load_swv = [&](int kt) {
-        const int kb = min(kt + lane, KB - 1);
-#pragma unroll
-        for (int h = 0; h < (SW ? 3 : 2); ++h) swv[h] = wsc[h][kb];
-        // (here, once in 64 slices: the compiler would otherwise wait for it, and with it for every
-        // DMA in flight, where the scales are used)
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
-      };
-      if constexpr (!KR) load_swv(0);
-      lds_barrier();   // every wave is done with the previous tile's slices
-      issue_early(0);
-      issue_late(0);
-      issue_early(1);
-      vm_barrier<EARLY + LATE>();        // the early part of slice 0 is resident
+      // weight block; the last step also reads the next slice's tokens, each as soon as its last product is
+      // issued, so that the matrix unit runs on across slices.  Two barriers a slice, at each of which one
+      // part of the stage has been read by every wave and is filled again with slice kt + NST, and the part
+      // read next, issued NST - 1/2 slices ago, is resident:
+      //   before step H - 1 (which reads the late part)   the early part is free
+      //   before the last step (which reads the early part of kt + 1)   the late part is free
+      constexpr int BP = H - 1, BQ = RB - 1;
+      constexpr int FLY = (NST - 1) * (EARLY + LATE);   // DMAs newer than the part waited for, at both
+      vm_barrier_if<FLY + LATE + STORES, FLY + LATE>(stores);   // the early part of slice 0 is resident
       // (the two chunks of a fragment are 64 bytes apart in the row, either way round: a base each, so that the
       // rows' distances fit the instructions' offsets)
       auto frag = [&](const uint8_t* p0, const uint8_t* p1, int at) {
@@ -278,66 +373,71 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
         const uint4 b = *reinterpret_cast<const uint4*>(p1 + at);
         return i32x8{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
       };
-      auto scales_of = [&](int kt) { return reinterpret_cast<const float*>(smem + FT_SCALES + (kt & 3) * (2 * FT * 4)); };
-      i32x8 tf[4], wf[2];
-      float ts[4], tn[4], sc[4];          // token scales, those of the next slice, times the weights'
-      f32x4 d[2][4], xs[2];
+      auto scales_of = [&](int kt) { return reinterpret_cast<const float*>(smem + TL::SCALES + (kt & (2 * NST - 1)) * TL::RING); };
+      constexpr int RS = SWV * 64;        // the row operand's scales in a slice's ring entry
+      i32x8 tf[TB], wf[2];
+      float ts[TB], tn[TB], sc[TB];       // token scales, those of the next slice, times the weights'
+      f32x4 d[2][TB], xs[2];
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
+      for (int tb = 0; tb < TB; ++tb) {
         tf[tb] = frag(smem + tread, smem + (tread ^ 64), tb * 2048);
-        tn[tb] = scales_of(0)[wt * 64 + tb * 16 + i16];
+        tn[tb] = scales_of(0)[wt * (TB * 16) + tb * 16 + i16];
         ts[tb] = sc[tb] = 0.f;
         d[1][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
       xs[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      wf[0] = frag(smem + wread, smem + (wread ^ 64), FT_OP);
+      wf[0] = frag(smem + wread, smem + (wread ^ 64), TL::OPT);
+      int fresh = stores ? NST : 0;       // slices whose parts are older than the stores
+#pragma clang loop unroll(disable)
       for (int kt = 0; kt < t.nkt; ++kt) {
-        if constexpr (!KR) {
-          if ((kt & 63) == 0 && kt > 0) load_swv(kt);
-        }
-        const int st = (kt & 1) * FT_STAGE, sn = FT_STAGE - st;   // this slice's stage, the next one's
+        const int st = (kt & (NST - 1)) * TL::STAGE, sn = ((kt + 1) & (NST - 1)) * TL::STAGE;   // this slice's stage, the next one's
         const uint8_t *w0 = smem + st + wread, *w1 = smem + st + (wread ^ 64);
-        static_for<0, 8>([&](auto rbc) {
+        const float* sS = scales_of(kt) + RS;
+        static_for<0, RB>([&](auto rbc) {
           constexpr int rb = decltype(rbc)::value;
-          constexpr int pb = (rb + 7) & 7;   // the block whose sums are added
-          if constexpr (rb == 2) {
-            vm_barrier<EARLY>();
-            issue_late(kt + 1);
+          constexpr int pb = (rb + RB - 1) % RB;   // the block whose sums are added
+          if constexpr (rb == BP) {
+            vm_barrier_if<FLY + STORES, FLY>(fresh);
+            dma_s(o, t, kt + NST);
           }
-          if constexpr (rb == 5) {
-            vm_barrier<LATE>();
-            dma_s(kt + 2);
+          if constexpr (rb == BQ) {
+            --fresh;
+            vm_barrier_if<FLY + STORES, FLY>(fresh);
           }
-          if constexpr (rb < 7) wf[(rb + 1) & 1] = frag(w0, w1, FT_OP + (rb + 1 < 4 ? (rb + 1) * 2048 : 128 * 128 + (rb + 1 - 4) * 2048));
-          else wf[0] = frag(smem + sn + wread, smem + sn + (wread ^ 64), FT_OP);
-          if constexpr (KR) xs[rb & 1] = *reinterpret_cast<const f32x4*>(scales_of(kt) + FT + (rb < 4 ? 0 : 128) + wn * 64 + (rb & 3) * 16 + 4 * q);
+          if constexpr (rb < RB - 1) wf[(rb + 1) & 1] = frag(w0, w1, TL::OPT + (rb + 1 < H ? (rb + 1) * 2048 : HR * 128 + (rb + 1 - H) * 2048));
+          else wf[0] = frag(smem + sn + wread, smem + sn + (wread ^ 64), TL::OPT);
+          if constexpr (KR) xs[rb & 1] = *reinterpret_cast<const f32x4*>(sS + (rb < H ? 0 : HR) + wn * (H * 16) + (rb % H) * 16 + 4 * q);
           if constexpr (KR && rb == 1) {
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) ts[tb] = tn[tb];
+            for (int tb = 0; tb < TB; ++tb) ts[tb] = tn[tb];
           }
-          // the scales of the sums that this step adds
-          if constexpr (!KR && (rb == 1 || rb == 5 || (SW && rb == 7))) {
-            const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swv[rb == 1 ? 0 : (rb == 5 ? 1 : 2)]), kt & 63));
+          // the scales of the sums that this step adds (SwiGLU: an up half's rows are in one or two scales' rows)
+          if constexpr (!KR && (rb == 1 || rb == H + 1 || (SW && rb > H && (rb - 1 - H) * 16 % 32 == 0))) {
+            const float w = sS[rb == 1 ? 0 : (SW ? 1 + (wn * H + rb - 1 - H) / 2 : 1)];
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
+            for (int tb = 0; tb < TB; ++tb) {
               if constexpr (rb == 1) ts[tb] = tn[tb];
               sc[tb] = ts[tb] * w;
             }
           }
           __builtin_amdgcn_sched_barrier(0);
-          static_for<0, 4>([&](auto tbc) {
+          static_for<0, TB>([&](auto tbc) {
             constexpr int tb = decltype(tbc)::value;
             const f32x4 z = {0.f, 0.f, 0.f, 0.f};
             d[rb & 1][tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[rb & 1], tf[tb], z, 0, 0, 0, 0, 0, 0);
-            if constexpr (rb == 7) {
+            if constexpr (rb == RB - 1) {
               tf[tb] = frag(smem + sn + tread, smem + sn + (tread ^ 64), tb * 2048);
-              tn[tb] = scales_of(kt + 1)[wt * 64 + tb * 16 + i16];
+              tn[tb] = scales_of(kt + 1)[wt * (TB * 16) + tb * 16 + i16];
             }
-            if constexpr (rb == 5 || rb == 6) {
-              constexpr int i = (rb - 5) * 4 + tb;   // the early part of kt + 2, one DMA a matrix instruction
-              if constexpr (i < 4) dma_t(kt + 2, i);
-              else if constexpr (i < 6) dma_w(kt + 2, 0, i - 4);
+            // the parts of kt + NST, at most one DMA a matrix instruction
+            if constexpr (rb >= BP && rb < BQ) {
+              constexpr int n = (BQ - BP) * TB, i = (rb - BP) * TB + tb, k0 = (DT + DW) * i / n, k1 = (DT + DW) * (i + 1) / n;
+              if constexpr (k1 > k0) {
+                if constexpr (k0 < DT) dma_t(o, t, kt + NST, k0);
+                else dma_w(o, t, kt + NST, 0, k0 - DT);
+              }
             }
+            if constexpr (rb == BQ && tb < DW) dma_w(o, t, kt + NST, 1, tb);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               if constexpr (KR) acc[pb][tb][r] = fmaf(d[(rb + 1) & 1][tb][r] * ts[tb], xs[(rb + 1) & 1][r], acc[pb][tb][r]);
@@ -345,153 +445,176 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
             }
             __builtin_amdgcn_sched_barrier(0);
           });
+          static_assert((BQ - BP) * TB >= DT + DW && TB >= DW, "a part is issued before the next barrier");
         });
       }
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb)
+      for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          if constexpr (KR) acc[7][tb][r] = fmaf(d[1][tb][r] * ts[tb], xs[1][r], acc[7][tb][r]);
-          else acc[7][tb][r] = fmaf(d[1][tb][r], sc[tb], acc[7][tb][r]);
+          if constexpr (KR) acc[RB - 1][tb][r] = fmaf(d[1][tb][r] * ts[tb], xs[1][r], acc[RB - 1][tb][r]);
+          else acc[RB - 1][tb][r] = fmaf(d[1][tb][r], sc[tb], acc[RB - 1][tb][r]);
         }
     }
+    const FtTile cur = t;
     __builtin_amdgcn_s_waitcnt(0);      // the slices past the end (zeros) have landed
+    t = nxt;
+    if (t.valid) o = setup(t, src);
+    lds_barrier();                      // every wave is done with the stages
+    if (t.valid && t.nkt > 0) prologue(o, t);
+    stores = STORES > 0 ? 1 : 0;
     rederive_lane();
 
-    // ---- epilogues.  acc[rb][tb][r]: column n0 + (rb < 4 ? 0 : 128) + wn * 64 + (rb % 4) * 16 + 4q + r,
-    // token m0 + wt * 64 + tb * 16 + i16
-    const int wrow0 = t.m0 + wt * 64;
-    int vr = t.m_valid - wrow0;
-    vr = uniform(vr < 0 ? 0 : (vr > 64 ? 64 : vr));
+    // ---- epilogues.  acc[rb][tb][r]: column n0 + (rb < H ? 0 : HR) + wn * 16 H + (rb % H) * 16 + 4q + r,
+    // token m0 + wt * 16 TB + tb * 16 + i16.  Stores go through resources that end at the last valid row.
+    const int wrow0 = cur.m0 + wt * (TB * 16);
+    int vr = cur.m_valid - wrow0;
+    vr = uniform(vr < 0 ? 0 : (vr > TB * 16 ? TB * 16 : vr));
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     if constexpr (!SW) {
       constexpr int ESZ = OUT == OUT_BF16 ? 2 : 4;
       uint8_t* base;
-      if constexpr (KR) base = static_cast<uint8_t*>(p.D ? ld_uniform(p.D, t.e) : p.Dv[t.e]) + int64_t(wrow0) * ncols * ESZ;
-      else base = static_cast<uint8_t*>(p.C) + (int64_t(t.off) + wrow0) * ncols * ESZ;
+      if constexpr (KR) base = static_cast<uint8_t*>(p.D ? ld_uniform(p.D, cur.e) : p.Dv[cur.e]) + int64_t(wrow0) * ncols * ESZ;
+      else base = static_cast<uint8_t*>(p.C) + (int64_t(cur.off) + wrow0) * ncols * ESZ;
       const uint32_t rowb = uint32_t(ncols) * ESZ;
       const __amdgpu_buffer_rsrc_t rC = __builtin_amdgcn_make_buffer_rsrc(base, 0, int(uint32_t(vr) * rowb), kRsrcFlags);
-      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-      if (vr > 0) {
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-          const uint32_t row = uint32_t(tb * 16 + i16) * rowb;
+      for (int tb = 0; tb < TB; ++tb) {
+        const uint32_t row = uint32_t(tb * 16 + i16) * rowb;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c0 = t.n0 + h * 128 + wn * 64;
-            if constexpr (OUT == OUT_BF16) {
-              uint32_t lo[4], hi[4];
+        for (int h = 0; h < 2; ++h) {
+          const int c0 = cur.n0 + h * HR + wn * (H * 16);
+          if constexpr (OUT == OUT_BF16) {
+            constexpr int L = H;            // 4 blocks: 64 columns; 2: 32 columns, the lanes' halves in turn
+            static_assert(L == 4 || L == 2, "blocks of a half");
+            uint32_t lo[4], hi[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                lo[j] = bf16x2(acc[4 * h + j][tb][0], acc[4 * h + j][tb][1]);
-                hi[j] = bf16x2(acc[4 * h + j][tb][2], acc[4 * h + j][tb][3]);
-              }
-              transpose4(lo);
-              transpose4(hi);
-              const int c = c0 + q * 16;   // the lane has columns c .. c + 15 now
-              const uint32_t o = c < ncols ? row + uint32_t(c) * ESZ : kInvalid;
-              __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, rC, int(o), 0, 0);
-              __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[2], hi[2], lo[3], hi[3]}, rC, int(o + 16), 0, 0);
+            for (int j = 0; j < 4; ++j) {
+              const f32x4 v = acc[L * h + j % L][tb];
+              lo[j] = bf16x2(v[0], v[1]);
+              hi[j] = bf16x2(v[2], v[3]);
+            }
+            transpose4(lo);
+            transpose4(hi);
+            // the lane has columns c .. c + 15 of block q now (two blocks: q and q + 2 hold the same, and
+            // store half of it each)
+            const int c = c0 + (q % L) * 16;
+            const uint32_t off = c < ncols ? row + uint32_t(c) * ESZ : kInvalid;
+            if constexpr (L == 4) {
+              __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, rC, int(off), 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[2], hi[2], lo[3], hi[3]}, rC, int(off + 16), 0, 0);
             } else {
+              const u32x4 v = q < 2 ? u32x4{lo[0], hi[0], lo[1], hi[1]} : u32x4{lo[2], hi[2], lo[3], hi[3]};
+              __builtin_amdgcn_raw_buffer_store_b128(v, rC, int(off + (q < 2 ? 0 : 16)), 0, 0);
+            }
+          } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int c = c0 + j * 16 + 4 * q;
-                const uint32_t o = c < ncols ? row + uint32_t(c) * ESZ : kInvalid;
-                f32x4 v = acc[4 * h + j][tb];
-                if constexpr (OUT == OUT_F32_ACC) {
-                  const u32x4 old = __builtin_amdgcn_raw_buffer_load_b128(rC, int(o), 0, 0);
+            for (int j = 0; j < H; ++j) {
+              const int c = c0 + j * 16 + 4 * q;
+              const uint32_t off = c < ncols ? row + uint32_t(c) * ESZ : kInvalid;
+              f32x4 v = acc[H * h + j][tb];
+              if constexpr (OUT == OUT_F32_ACC) {
+                const u32x4 old = __builtin_amdgcn_raw_buffer_load_b128(rC, int(off), 0, 0);
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) v[r] += __uint_as_float(old[r]);
-                }
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rC, int(o), 0, 0);
+                for (int r = 0; r < 4; ++r) v[r] += __uint_as_float(old[r]);
               }
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rC, int(off), 0, 0);
             }
           }
         }
       }
     } else {
       // h = p silu(G) U of the tile's 128 columns, one block of 128 a token: its largest magnitude over
-      // the lane's 16 columns, the lanes 16 apart and the two waves of the columns' halves
-      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-      const int64_t grow0 = int64_t(t.off) + wrow0;
-      uint32_t am[4];
+      // the lane's columns, the lanes 16 apart and the waves that share the tokens
+      const int64_t grow0 = int64_t(cur.off) + wrow0;
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        const bool in = tb * 16 + i16 < vr;
-        const float pr = p.prob == nullptr ? 1.f : (in ? p.prob[grow0 + tb * 16 + i16] : 0.f);
-        am[tb] = 0;
+      for (int tb = 0; tb < TB; ++tb) {
+        uint32_t am = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < H; ++j)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float G = acc[j][tb][r], U = acc[4 + j][tb][r];
-            const float h = pr * (G * __builtin_amdgcn_rcpf(1.f + __expf(-G))) * U;
+            const float G = acc[j][tb][r], U = acc[H + j][tb][r];
+            const float h = pr[tb] * (G * __builtin_amdgcn_rcpf(1.f + __expf(-G))) * U;
             acc[j][tb][r] = h;
-            am[tb] = umax(am[tb], __float_as_uint(h) & 0x7fffffffu);
+            am = umax(am, __float_as_uint(h) & 0x7fffffffu);
           }
-        const U32Pair a = permlane16_swap(am[tb], am[tb]);
-        am[tb] = umax(a.a, a.b);
-        const U32Pair b = permlane32_swap(am[tb], am[tb]);
-        am[tb] = umax(b.a, b.b);
-        if (q == 0) s_amax[wn * FT + wt * 64 + tb * 16 + i16] = am[tb];
+        const U32Pair a = permlane16_swap(am, am);
+        am = umax(a.a, a.b);
+        const U32Pair b = permlane32_swap(am, am);
+        am = umax(b.a, b.b);
+        if (q == 0) s_amax[wn * TL::NT + wt * (TB * 16) + tb * 16 + i16] = am;
       }
       lds_barrier();
       const __amdgpu_buffer_rsrc_t rH =
           __builtin_amdgcn_make_buffer_rsrc(p.h_codes + grow0 * p.F, 0, int(uint32_t(vr) * uint32_t(p.F)), kRsrcFlags);
-      if (vr > 0) {
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-          const int m = wt * 64 + tb * 16 + i16;
-          const FbScale sc = fb_scale(umax(s_amax[m], s_amax[FT + m]));
-          uint32_t v[4];
+      for (int tb = 0; tb < TB; ++tb) {
+        const int m = wt * (TB * 16) + tb * 16 + i16;
+        uint32_t am = s_amax[m];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[j] = e4m3x4(acc[j][tb][0] * sc.inv, acc[j][tb][1] * sc.inv, acc[j][tb][2] * sc.inv, acc[j][tb][3] * sc.inv);
-          transpose4(v);
-          const int c = t.n0 + wn * 64 + q * 16;
-          const uint32_t o = c < p.F ? uint32_t(tb * 16 + i16) * uint32_t(p.F) + uint32_t(c) : kInvalid;
-          __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0], v[1], v[2], v[3]}, rH, int(o), 0, 0);
-          if (wn == 0 && q == 0 && tb * 16 + i16 < vr) p.h_scales[int64_t(t.n0 / 128) * p.ast_ld + grow0 + tb * 16 + i16] = sc.s;
+        for (int w = 1; w < WN; ++w) am = umax(am, s_amax[w * TL::NT + m]);
+        const FbScale sc = fb_scale(am);
+        const int c0 = cur.n0 + wn * (H * 16);
+        uint32_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4 x = acc[j % H][tb];
+          v[j] = e4m3x4(x[0] * sc.inv, x[1] * sc.inv, x[2] * sc.inv, x[3] * sc.inv);
         }
+        transpose4(v);
+        const int c = c0 + (q % H) * 16;
+        const uint32_t off = c < p.F && q < H ? uint32_t(tb * 16 + i16) * uint32_t(p.F) + uint32_t(c) : kInvalid;
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0], v[1], v[2], v[3]}, rH, int(off), 0, 0);
+        if (wn == 0 && q == 0 && tb * 16 + i16 < vr) p.h_scales[int64_t(cur.n0 / FB) * p.ast_ld + grow0 + tb * 16 + i16] = sc.s;
       }
     }
   }
   __builtin_amdgcn_s_waitcnt(0);   // no LDS DMA outlives the workgroup
 }
 
-#define FB_KERNEL(name, KR, SW, OUT, P) \
-  __global__ __launch_bounds__(FT_THREADS, 2) void name(P p) { fb_tile_body<KR, SW, OUT>(p); }
-FB_KERNEL(gemm_fb_store, false, false, OUT_BF16, FbGemm)
-FB_KERNEL(gemm_fb_store_f32, false, false, OUT_F32, FbGemm)
-FB_KERNEL(gemm_fb_swiglu, false, true, OUT_NONE, FbGemm)
-FB_KERNEL(gemm_fb_wgrad, true, false, OUT_BF16, FbWgrad)
-FB_KERNEL(gemm_fb_wgrad_f32, true, false, OUT_F32, FbWgrad)
-FB_KERNEL(gemm_fb_wgrad_f32_acc, true, false, OUT_F32_ACC, FbWgrad)
+#define FB_KERNEL(name, TL, PER_SIMD, KR, SW, OUT, TAIL, P) \
+  __global__ __launch_bounds__(TL::THREADS, PER_SIMD) void name(P p) { fb_tile_body<TL, KR, SW, OUT, TAIL>(p); }
+FB_KERNEL(gemm_fb_store, FbMain, 2, false, false, OUT_BF16, false, FbGemm)
+FB_KERNEL(gemm_fb_store_f32, FbMain, 2, false, false, OUT_F32, false, FbGemm)
+FB_KERNEL(gemm_fb_store_tail, FbQuad, 1, false, false, OUT_BF16, true, FbGemm)
+FB_KERNEL(gemm_fb_store_f32_tail, FbQuad, 1, false, false, OUT_F32, true, FbGemm)
+FB_KERNEL(gemm_fb_swiglu, FbMain, 2, false, true, OUT_NONE, false, FbGemm)
+FB_KERNEL(gemm_fb_wgrad, FbMain, 2, true, false, OUT_BF16, false, FbWgrad)
+FB_KERNEL(gemm_fb_wgrad_f32, FbMain, 2, true, false, OUT_F32, false, FbWgrad)
+FB_KERNEL(gemm_fb_wgrad_f32_acc, FbMain, 2, true, false, OUT_F32_ACC, false, FbWgrad)
 #undef FB_KERNEL
 
-// One workgroup a CU (its LDS), fewer where there are fewer tiles
-template <typename Kern, typename P>
-static mge_status launch_fb(Kern kern, const char* name, const P& p, int64_t tiles, hipStream_t s) {
-  hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, FT_LDS);
-  int64_t grid = device_cus();
-  if (tiles < grid) grid = tiles;
+// A persistent launch of at most `grid` workgroups
+template <typename TL, typename Kern, typename P>
+static mge_status launch_fb(Kern kern, const char* name, const P& p, int64_t grid, hipStream_t s) {
+  hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, TL::LDS);
   if (grid <= 0) return MGE_OK;
   ProfScope prof(s, name);
-  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(FT_THREADS), FT_LDS, s, p);
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(TL::THREADS), TL::LDS, s, p);
   return hip_check(name);
 }
 
-mge_status launch_fb_tile(const FbGemm& p, bool swiglu, hipStream_t s) {
-  const int64_t mt = (int64_t(p.total) + FT - 1) / FT + (p.sizes ? p.E : 0);
-  if (swiglu) return launch_fb(gemm_fb_swiglu, "gemm_fp8_block_swiglu", p, mt * ((p.F + 127) / 128), s);
-  const int64_t tiles = mt * ((p.N + FT - 1) / FT);
-  return p.out_f32 ? launch_fb(gemm_fb_store_f32, "gemm_fp8_block", p, tiles, s) : launch_fb(gemm_fb_store, "gemm_fp8_block", p, tiles, s);
+mge_status launch_fb_tile(const FbGemm& p0, bool swiglu, hipStream_t s) {
+  FbGemm p = p0;
+  const int64_t mt = (int64_t(p.total) + 255) / 256 + (p.sizes ? p.E : 0);
+  const int cus = device_cus();
+  if (swiglu) return launch_fb<FbMain>(gemm_fb_swiglu, "gemm_fp8_block_swiglu", p, std::min<int64_t>(cus, mt * ((p.F + 127) / 128)), s);
+  const int64_t tiles = mt * ((p.N + 255) / 256);
+  p.grid_main = cus;
+  const int64_t grid = std::min<int64_t>(cus, tiles), tail = std::min<int64_t>(cus, 4 * tiles);
+  mge_status st = p.out_f32 ? launch_fb<FbMain>(gemm_fb_store_f32, "gemm_fp8_block", p, grid, s)
+                            : launch_fb<FbMain>(gemm_fb_store, "gemm_fp8_block", p, grid, s);
+  if (st != MGE_OK) return st;
+  return p.out_f32 ? launch_fb<FbQuad>(gemm_fb_store_f32_tail, "gemm_fp8_block_tail", p, tail, s)
+                   : launch_fb<FbQuad>(gemm_fb_store_tail, "gemm_fp8_block_tail", p, tail, s);
 }
 
 mge_status launch_fb_wgrad(const FbWgrad& p, hipStream_t s) {
-  const int64_t tiles = int64_t(p.E) * ((p.N + FT - 1) / FT) * ((p.K + FT - 1) / FT);
-  if (p.out == OUT_BF16) return launch_fb(gemm_fb_wgrad, "wgrad_fp8_block", p, tiles, s);
-  if (p.out == OUT_F32) return launch_fb(gemm_fb_wgrad_f32, "wgrad_fp8_block", p, tiles, s);
-  return launch_fb(gemm_fb_wgrad_f32_acc, "wgrad_fp8_block", p, tiles, s);
+  const int64_t grid = std::min<int64_t>(device_cus(), int64_t(p.E) * ((p.N + 255) / 256) * ((p.K + 255) / 256));
+  if (p.out == OUT_BF16) return launch_fb<FbMain>(gemm_fb_wgrad, "wgrad_fp8_block", p, grid, s);
+  if (p.out == OUT_F32) return launch_fb<FbMain>(gemm_fb_wgrad_f32, "wgrad_fp8_block", p, grid, s);
+  return launch_fb<FbMain>(gemm_fb_wgrad_f32_acc, "wgrad_fp8_block", p, grid, s);
 }
 
 // Scales made block-major, 64 x 64 a workgroup through LDS; every matrix of the launch has its own range of workgroups

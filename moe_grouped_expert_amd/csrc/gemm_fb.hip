@@ -25,6 +25,7 @@
 namespace mge {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // A kernel's tile: WN x WT waves of RB x TB blocks of 16 x 16 (weight rows x tokens), NST LDS stages
 template <int WN_, int WT_, int RB_, int TB_, int NST_>
@@ -44,6 +45,19 @@ struct FbTile {
 };
 typedef FbTile<2, 4, 8, 4, 2> FbMain;    // 256 x 256
 typedef FbTile<2, 2, 4, 4, 4> FbQuad;    // 128 x 128
+
+// Lanes 2j and 2j + 1 trade their b and a: the even lane then has its own a and the odd lane's a, the odd one
+// the even lane's b and its own b.  Where a lane's a and b are neighbouring 16 bytes of its row of the output,
+// stores of `a` then write the even lanes' rows and those of `b` the odd lanes', in twice as long runs.
+__device__ __forceinline__ void pair_rows(u32x4& a, u32x4& b, bool odd) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t got = dpp_u<0xB1>(odd ? a[k] : b[k]);
+    const uint32_t x = a[k];
+    a[k] = odd ? got : x;
+    b[k] = odd ? b[k] : got;
+  }
+}
 
 // vm_barrier<A> where n > 0 (the same in every lane), else vm_barrier<B>.  The choice is made inside the asm: a
 // branch of the compiler's would cut the K loop's body into blocks, across which it moves the additions.
@@ -321,7 +335,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   };
   // Stores that every wave's epilogue issues at least: the next tile's first DMAs are issued before
   // them, and its first waits leave them in flight
-  constexpr int STORES = OUT == OUT_BF16 ? TB * H / 4 * 2 * 2 : (OUT == OUT_F32 ? TB * RB : (SW ? TB : 0));
+  constexpr int STORES = OUT == OUT_BF16 ? TB * 2 * 2 : (OUT == OUT_F32 ? TB * RB : (SW ? TB : 0));
   static_assert(NST * (EARLY + LATE) + STORES < 64, "vmcnt");
 
   FtTile t = decode(vid);
@@ -470,7 +484,6 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
     const int wrow0 = cur.m0 + wt * (TB * 16);
     int vr = cur.m_valid - wrow0;
     vr = uniform(vr < 0 ? 0 : (vr > TB * 16 ? TB * 16 : vr));
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     if constexpr (!SW) {
       constexpr int ESZ = OUT == OUT_BF16 ? 2 : 4;
       uint8_t* base;
@@ -478,47 +491,52 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       else base = static_cast<uint8_t*>(p.C) + (int64_t(cur.off) + wrow0) * ncols * ESZ;
       const uint32_t rowb = uint32_t(ncols) * ESZ;
       const __amdgpu_buffer_rsrc_t rC = __builtin_amdgcn_make_buffer_rsrc(base, 0, int(uint32_t(vr) * rowb), kRsrcFlags);
+      // whole lines of 128 bytes: lanes 2j and 2j + 1 store row 2j, then row 2j + 1, 16 bytes each
+      constexpr int pol = KR ? kNonTemporal : 0;   // gradients: written once, read by no workgroup
+      const bool odd = (i16 & 1) != 0;
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) {
-        const uint32_t row = uint32_t(tb * 16 + i16) * rowb;
+        const uint32_t row = uint32_t(tb * 16 + (i16 & ~1)) * rowb;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int c0 = cur.n0 + h * HR + wn * (H * 16);
           if constexpr (OUT == OUT_BF16) {
-            constexpr int L = H;            // 4 blocks: 64 columns; 2: 32 columns, the lanes' halves in turn
-            static_assert(L == 4 || L == 2, "blocks of a half");
+            static_assert(H == 4 || H == 2, "blocks of a half");
             uint32_t lo[4], hi[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const f32x4 v = acc[L * h + j % L][tb];
+              const f32x4 v = acc[H * h + j % H][tb];
               lo[j] = bf16x2(v[0], v[1]);
               hi[j] = bf16x2(v[2], v[3]);
             }
             transpose4(lo);
             transpose4(hi);
-            // the lane has columns c .. c + 15 of block q now (two blocks: q and q + 2 hold the same, and
-            // store half of it each)
-            const int c = c0 + (q % L) * 16;
-            const uint32_t off = c < ncols ? row + uint32_t(c) * ESZ : kInvalid;
-            if constexpr (L == 4) {
-              __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, rC, int(off), 0, 0);
-              __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[2], hi[2], lo[3], hi[3]}, rC, int(off + 16), 0, 0);
-            } else {
-              const u32x4 v = q < 2 ? u32x4{lo[0], hi[0], lo[1], hi[1]} : u32x4{lo[2], hi[2], lo[3], hi[3]};
-              __builtin_amdgcn_raw_buffer_store_b128(v, rC, int(off + (q < 2 ? 0 : 16)), 0, 0);
-            }
+            // the lane has columns c .. c + 15 of block q now (two blocks: q and q + 2 have the same one,
+            // and the lanes q >= 2 store nothing)
+            u32x4 a = {lo[0], hi[0], lo[1], hi[1]}, b = {lo[2], hi[2], lo[3], hi[3]};
+            pair_rows(a, b, odd);
+            const int c = c0 + q * 16;
+            const uint32_t off = c < ncols && q < H ? row + uint32_t(c) * ESZ + (odd ? 16 : 0) : kInvalid;
+            __builtin_amdgcn_raw_buffer_store_b128(a, rC, int(off), 0, pol);
+            __builtin_amdgcn_raw_buffer_store_b128(b, rC, int(off + rowb), 0, pol);
           } else {
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
-              const int c = c0 + j * 16 + 4 * q;
+            for (int j = 0; j < H; j += 2) {
+              u32x4 a = __builtin_bit_cast(u32x4, acc[H * h + j][tb]), b = __builtin_bit_cast(u32x4, acc[H * h + j + 1][tb]);
+              pair_rows(a, b, odd);
+              const int c = c0 + (j + (odd ? 1 : 0)) * 16 + 4 * q;
               const uint32_t off = c < ncols ? row + uint32_t(c) * ESZ : kInvalid;
-              f32x4 v = acc[H * h + j][tb];
               if constexpr (OUT == OUT_F32_ACC) {
-                const u32x4 old = __builtin_amdgcn_raw_buffer_load_b128(rC, int(off), 0, 0);
+                const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rC, int(off), 0, pol);
+                const u32x4 y = __builtin_amdgcn_raw_buffer_load_b128(rC, int(off + rowb), 0, pol);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] += __uint_as_float(old[r]);
+                for (int r = 0; r < 4; ++r) {
+                  a[r] = __float_as_uint(__uint_as_float(a[r]) + __uint_as_float(x[r]));
+                  b[r] = __float_as_uint(__uint_as_float(b[r]) + __uint_as_float(y[r]));
+                }
               }
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rC, int(off), 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b128(a, rC, int(off), 0, pol);
+              __builtin_amdgcn_raw_buffer_store_b128(b, rC, int(off + rowb), 0, pol);
             }
           }
         }

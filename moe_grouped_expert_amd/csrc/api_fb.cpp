@@ -26,9 +26,38 @@ static mge_status check_norm(int T, int H, int x_dtype, int w_dtype, int y_dtype
   return MGE_OK;
 }
 
-// rows from which a product runs on the tile kernels: the streaming kernels read an expert's weights
-// again for every 16 or 32 of its rows
-static bool fb_tile(int E, int64_t total) { return total > 64 * int64_t(E); }
+// Streaming or tile kernels: estimates of a product's time in microseconds from what both measured on
+// MI355X (whole calls, rows an expert of E x [N][K]: streamed, tiled).
+//   8 x [4096][14336]: 8 rows 100, 130; 24 rows 129, 131; 32 rows 142, 132; 64 rows 218, 140
+//   8 x [2048][4096]: 8 rows 17, 26; 32 rows 24, 27; 48 rows 33, 27; 64 rows 38, 27
+//   16 x [1024][2048]: 8 rows 9, 20; 48 rows 20.4, 20.9; 128 rows 40, 22
+//   [8192][8192]: 8 rows 18, 38; 64 rows 34, 39; 128 rows 64, 41
+//   [4096][4096]: 8 rows 6.6, 24; 64 rows 19, 25; 128 rows 34, 25
+// Streaming reads the weights at about 5 TB/s for every 64 rows, and a row past 8 adds 1/57 of that;
+// the tile kernels take a fixed 14 us, 0.75 us for every 256 of K of a round of 128 x 128 tiles, and no less than
+// their weights at 3.6 TB/s.
+static double stream_us(int64_t E, int64_t N, int64_t K, int64_t total) {
+  const double rows = double(total) / double(E), bytes = double(std::min(E, total)) * double(N) * double(K);
+  return (4 + bytes / 5.0e6) * (1 + std::max(0.0, rows - 8) / 57) * std::max(1.0, ceil(rows / 64));
+}
+static double tile_us(int64_t E, int64_t N, int64_t K, int64_t total) {
+  const double rows = double(total) / double(E), bytes = double(std::min(E, total)) * double(N) * double(K);
+  const double tiles = double(std::min(E, total)) * std::max(1.0, ceil(rows / 128)) * double((N + 127) / 128);
+  return 14 + std::max(0.75 * double((K + 255) / 256) * ceil(tiles / 256), bytes / 3.6e6);
+}
+static bool fb_tile(int64_t E, int64_t N, int64_t K, int64_t total) { return tile_us(E, N, K, total) < stream_us(E, N, K, total); }
+static bool fb_tile_mlp(int64_t E, int64_t H, int64_t F, int64_t total) {
+  return tile_us(E, 2 * F, H, total) + tile_us(E, H, F, total) < stream_us(E, 2 * F, H, total) + stream_us(E, H, F, total);
+}
+// SwiGLU in the gate-up product's epilogue needs all of a block of 128 columns, gate and up, in a workgroup: tiles of
+// 256 weight rows, of which there are few for few columns.  Then the product in the plain form, which fills more
+// CUs, and SwiGLU on its own.  Whole MLP, fused and not, us: 250 tokens, one expert 4096 x 4096 (32 tiles) 80, 58;
+// 144 tokens, top-2 of 3 experts 512 x 768 (18) 30, 28; 64 tokens, top-2 of 8 experts 2048 x 1408 (88) 50, 50, 500
+// tokens 66, 75; 250 tokens, one expert 4096 x 14336 (112) 123, 122; two experts (224) 139, 155.
+constexpr int64_t kFusedTiles = 64;
+static bool fb_fused(int64_t E, int64_t F, int64_t total, bool tile) {
+  return tile && ((total + 255) / 256 + std::min(E, total) - 1) * fb_blocks(F) > kFusedTiles;
+}
 
 static int64_t fb_total(int64_t total, int64_t rows) { return total > 0 && total < rows ? total : rows; }
 
@@ -144,10 +173,10 @@ mge_status fp8_block_dequantize(const mge_dequant_fb_args* a, void* stream) {
 }
 
 size_t mge_gemm_fb_workspace_bytes(const mge_gemm_fb_args* a) {
-  if (!a || a->struct_size != sizeof(mge_gemm_fb_args) || a->E < 1 || a->E > 256 || a->K < 32 || a->rows < 0 || a->rows >= kTwoGiB / a->K)
+  if (!a || a->struct_size != sizeof(mge_gemm_fb_args) || a->E < 1 || a->E > 256 || a->N < 32 || a->K < 32 || a->rows < 0 || a->rows >= kTwoGiB / a->K)
     return 0;
   return (fb_table(a->E) ? up256(2 * size_t(a->E) * sizeof(void*)) : 0) +
-         (fb_tile(a->E, fb_total(a->total_rows, a->rows)) ? fb_scales_t(a->rows, a->K) : 0);
+         (fb_tile(a->E, a->N, a->K, fb_total(a->total_rows, a->rows)) ? fb_scales_t(a->rows, a->K) : 0);
 }
 
 mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
@@ -203,7 +232,7 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
       p.Wsv[e] = a->w_scale[e];
     }
   }
-  if (!fb_tile(a->E, p.total)) return launch_fb_stream(p, false, s);
+  if (!fb_tile(p.E, p.N, p.K, p.total)) return launch_fb_stream(p, s);
   float* ast = static_cast<float*>(ws.take(fb_scales_t(a->rows, a->K)));
   p.Ast = ast; p.ast_ld = a->rows;
   const FbScaleT t{a->a_scale, a->a_rows, a->src_rows, a->rows, int(fb_blocks(a->K)), ast, a->rows};
@@ -272,8 +301,9 @@ size_t mge_fwd_fb_workspace_bytes(const mge_fwd_fb_args* a) {
   if (!a || a->struct_size != sizeof(mge_fwd_fb_args) || a->E < 1 || a->E > 256 || a->H < 32 || a->F < 32 || a->rows < 0 ||
       a->rows >= kTwoGiB / std::max(a->H, a->F))
     return 0;
-  const bool tile = fb_tile(a->E, fb_total(a->total_rows, a->rows));
-  return (fb_table(a->E) ? up256(4 * size_t(a->E) * sizeof(void*)) : 0) + up256(size_t(a->rows) * a->F) + fb_scales_t(a->rows, a->F) +
+  const int64_t total = fb_total(a->total_rows, a->rows);
+  const bool tile = fb_tile_mlp(a->E, a->H, a->F, total);
+  return (fb_fused(a->E, a->F, total, tile) ? 0 : up256(size_t(a->rows) * a->F * 8)) + (fb_table(a->E) ? up256(4 * size_t(a->E) * sizeof(void*)) : 0) + up256(size_t(a->rows) * a->F) + fb_scales_t(a->rows, a->F) +
          (tile ? fb_scales_t(a->rows, a->H) : 0);
 }
 
@@ -346,16 +376,25 @@ mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
   g.h_codes = static_cast<uint8_t*>(ws.take(size_t(a->rows) * F));
   g.h_scales = static_cast<float*>(ws.take(fb_scales_t(a->rows, F)));
   d.A = g.h_codes; d.As = g.h_scales; d.Ast = g.h_scales; d.ast_ld = a->rows;
-  if (!fb_tile(E, g.total)) {
-    st = launch_fb_stream(g, true, s);
-    return st != MGE_OK ? st : launch_fb_stream(d, false, s);
+  const bool tile = fb_tile_mlp(E, H, F, g.total);
+  if (tile) {
+    float* xst = static_cast<float*>(ws.take(fb_scales_t(a->rows, H)));
+    g.Ast = xst; g.ast_ld = a->rows;
+    const FbScaleT t{a->x_scale, a->perm_src, a->x_rows, a->rows, int(fb_blocks(H)), xst, a->rows};
+    st = launch_fb_scale_t(&t, 1, s);
+    if (st != MGE_OK) return st;
   }
-  float* xst = static_cast<float*>(ws.take(fb_scales_t(a->rows, H)));
-  g.Ast = xst; g.ast_ld = a->rows;
-  const FbScaleT t{a->x_scale, a->perm_src, a->x_rows, a->rows, int(fb_blocks(H)), xst, a->rows};
-  st = launch_fb_scale_t(&t, 1, s);
-  if (st == MGE_OK) st = launch_fb_tile(g, true, s);
-  return st != MGE_OK ? st : launch_fb_tile(d, false, s);
+  if (fb_fused(E, F, g.total, tile)) {
+    st = launch_fb_tile(g, true, s);
+  } else {
+    float* gu = static_cast<float*>(ws.take(size_t(a->rows) * F * 8));
+    g.C = gu;
+    g.out_f32 = 1;
+    st = tile ? launch_fb_tile(g, false, s) : launch_fb_stream(g, s);
+    if (st == MGE_OK) st = launch_fb_swiglu(g.rows, F, gu, g.prob, g.map, g.h_codes, g.h_scales, tile ? a->rows : 0, s);
+  }
+  if (st != MGE_OK) return st;
+  return tile ? launch_fb_tile(d, false, s) : launch_fb_stream(d, s);
 }
 
 }  // extern "C"

@@ -124,11 +124,16 @@ struct FbGemm {
   int out_f32;
   const float* prob;                // SwiGLU: [rows] or NULL (1)
   uint8_t* h_codes;                 // SwiGLU: [rows][F]
-  float* h_scales;                  // SwiGLU: streaming [rows][ceil(F/128)], tiles [ceil(F/128)][ast_ld]
+  float* h_scales;                  // SwiGLU: [ceil(F/128)][ast_ld]
   int grid_main;                    // workgroups of the main launch's whole rounds (set by the launcher)
 };
-mge_status launch_fb_stream(const FbGemm& p, bool swiglu, hipStream_t s);
+mge_status launch_fb_stream(const FbGemm& p, hipStream_t s);
 mge_status launch_fb_tile(const FbGemm& p, bool swiglu, hipStream_t s);
+
+// h = p silu(G) U of fp32 rows [G U], quantized 1 x 128; scales [rows][ceil(F/128)], or with ld > 0 [ceil(F/128)][ld];
+// rows r with map[r] < 0 are left out
+mge_status launch_fb_swiglu(int rows, int F, const float* gu, const float* prob, const int32_t* map, uint8_t* codes, float* scales,
+                            int64_t ld, hipStream_t s);
 
 // dw_e[n][k] = sum over the tokens of expert e: columns [offs[e], offs[e] + sizes[e]) of both
 struct FbWgrad {

@@ -27,24 +27,25 @@ namespace mge {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// A kernel's tile: WN x WT waves of RB x TB blocks of 16 x 16 (weight rows x tokens), NST LDS stages
-template <int WN_, int WT_, int RB_, int TB_, int NST_>
+// A kernel's tile: WN x WT waves of RB x TB blocks of 16 x 16 (weight rows x tokens), NST LDS stages.  KG groups of
+// such waves take the slices in turn, each through stages of its own, and add their sums at the tile's end.
+template <int WN_, int WT_, int RB_, int TB_, int NST_, int KG_>
 struct FbTile {
-  static constexpr int WN = WN_, WT = WT_, RB = RB_, TB = TB_, NST = NST_;
-  static constexpr int WAVES = WN * WT, THREADS = 64 * WAVES;
+  static constexpr int WN = WN_, WT = WT_, RB = RB_, TB = TB_, NST = NST_, KG = KG_;
+  static constexpr int WAVES = WN * WT, THREADS = 64 * WAVES * KG;   // WAVES: of a group
   static constexpr int NR = WN * RB * 16, NT = WT * TB * 16;   // weight rows, tokens
   static constexpr int H = RB / 2;                             // a wave's blocks in each half of the weight rows
   static constexpr int OPT = NT * 128, OPW = NR * 128;         // bytes of the operands in a stage: tokens, then weights
   static constexpr int STAGE = OPT + OPW;
   static constexpr int SCALES = NST * STAGE;                   // then a ring of 2 NST slices' scales, 64 a wave:
   static constexpr int RING = WAVES * 256;                     // the tokens' (first waves), then the row operand's
-  static constexpr int LDS = SCALES + 2 * NST * RING;
+  static constexpr int GROUP = SCALES + 2 * NST * RING, LDS = KG * GROUP;
   static constexpr int DT = NT / 8 / WAVES, DW = NR / 16 / WAVES;   // DMAs of a wave: tokens, each half of the weights
   static_assert((NST & (NST - 1)) == 0 && RB % 2 == 0 && NT % (8 * WAVES) == 0 && NR % (16 * WAVES) == 0, "whole DMAs");
   static_assert(NT / 64 + (NR + 63) / 64 <= WAVES && NT % 64 == 0, "64 scales a wave");
 };
-typedef FbTile<2, 4, 8, 4, 2> FbMain;    // 256 x 256
-typedef FbTile<2, 2, 4, 4, 4> FbQuad;    // 128 x 128
+typedef FbTile<2, 4, 8, 4, 2, 1> FbMain;   // 256 x 256
+typedef FbTile<2, 2, 4, 4, 2, 2> FbQuad;   // 128 x 128
 
 // Lanes 2j and 2j + 1 trade their b and a: the even lane then has its own a and the odd lane's a, the odd one
 // the even lane's b and its own b.  Where a lane's a and b are neighbouring 16 bytes of its row of the output,
@@ -104,16 +105,18 @@ struct FtOps {
 // whole round, in quarters (their 128 x 128 quadrants).
 template <typename TL, bool KR, bool SW, int OUT, bool TAIL, typename P>
 __device__ __forceinline__ void fb_tile_body(const P& p) {
-  constexpr int WN = TL::WN, RB = TL::RB, TB = TL::TB, H = TL::H, NST = TL::NST;
+  constexpr int WN = TL::WN, RB = TL::RB, TB = TL::TB, H = TL::H, NST = TL::NST, KG = TL::KG;
   constexpr int HR = TL::NR / 2;               // weight rows of a half
   static_assert(!SW || HR == FB, "a block of h is a tile's columns");
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int32_t s_prefix[G_MAXE + 1];
   __shared__ int32_t s_mtiles[G_MAXE];
   __shared__ uint32_t s_amax[SW ? WN * TL::NT : 1];
-  const uint32_t lds_base = uniform(int(uint32_t(reinterpret_cast<uintptr_t>(smem))));
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = uniform(tid >> 6);
+  const int wave = KG == 1 ? uniform(tid >> 6) : uniform((tid >> 6) % TL::WAVES);   // of the group
+  const int kg = KG == 1 ? 0 : uniform((tid >> 6) / TL::WAVES);
+  uint8_t* const gmem = smem + kg * TL::GROUP;                                      // the group's stages
+  const uint32_t lds_base = uniform(int(uint32_t(reinterpret_cast<uintptr_t>(gmem))));
   const int wn = wave % WN, wt = wave / WN;    // the wave's share of each half of the weight rows, its tokens
   // derived again from an opaque copy of the lane at the top of every tile and after its K loop, so
   // that one phase's addresses are not kept in registers through the other
@@ -290,28 +293,29 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   };
   // (a wave's first LDS row is a multiple of 16, so that its even and odd instructions are those of the swizzle)
   static_assert(DT % 2 == 0 && DW % 2 == 0, "even instructions start at even groups of 8 rows");
-  auto at_slice = [](i32x4 r, const FtTile& t, int kt) {
-    r[2] = kt < t.nkt ? r[2] : 0;
+  // (from here on kt counts the group's own slices: slice KG kt + kg of the tile)
+  auto at_slice = [&](i32x4 r, const FtTile& t, int kt) {
+    r[2] = KG * kt + kg < t.nkt ? r[2] : 0;
     return r;
   };
   // (no offset beside a resource without records, so that no form of the range check takes one from the other)
   auto place = [](const i32x4& r, uint32_t k) { return r[2] != 0 ? k : 0u; };
-  auto off_at = [](const FtOps& o, const FtTile& t, uint32_t off, int kt, int odd) {
-    return ((odd ? o.past1 : o.past0) & (kt == t.nkt - 1 ? kInvalid : 0u)) | off;
+  auto off_at = [&](const FtOps& o, const FtTile& t, uint32_t off, int kt, int odd) {
+    return ((odd ? o.past1 : o.past0) & (KG * kt + kg == t.nkt - 1 ? kInvalid : 0u)) | off;
   };
   auto dma_t = [&](const FtOps& o, const FtTile& t, int kt, int i) {
     const i32x4 r = at_slice(o.rT, t, kt);
     dma16s(r, lds_base + (kt & (NST - 1)) * TL::STAGE + (wave * (DT * 8) + i * 8) * 128, off_at(o, t, o.toff[i], kt, i & 1),
-           place(r, uint32_t(t.kbase + kt * 128)));
+           place(r, uint32_t(t.kbase + (KG * kt + kg) * 128)));
   };
   auto dma_w = [&](const FtOps& o, const FtTile& t, int kt, int h, int i) {
     const i32x4 r = at_slice(o.rW[h], t, kt);
-    dma16s(r, lds_base + (kt & (NST - 1)) * TL::STAGE + TL::OPT + (h * HR + wave * (DW * 8) + i * 8) * 128, off_at(o, t, o.woff[i], kt, i),
-           place(r, uint32_t(t.kbase + kt * 128)));
+    dma16s(r, lds_base + (kt & (NST - 1)) * TL::STAGE + TL::OPT + (h * HR + wave * (DW * 8) + i * 8) * 128,
+           off_at(o, t, o.woff[i], kt, i), place(r, uint32_t(t.kbase + (KG * kt + kg) * 128)));
   };
   auto dma_s = [&](const FtOps& o, const FtTile& t, int kt) {
     const i32x4 r = at_slice(o.rS, t, kt);
-    dma4(r, lds_base + TL::SCALES + (kt & (2 * NST - 1)) * TL::RING + wave * 256, o.soff, place(r, uint32_t(kt) * o.s_ld));
+    dma4(r, lds_base + TL::SCALES + (kt & (2 * NST - 1)) * TL::RING + wave * 256, o.soff, place(r, uint32_t(KG * kt + kg) * o.s_ld));
   };
   // The early part of a slice (its tokens, scales and the first half of the weight rows) and the late one
   constexpr int EARLY = 1 + DT + DW, LATE = DW;
@@ -387,25 +391,26 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
         const uint4 b = *reinterpret_cast<const uint4*>(p1 + at);
         return i32x8{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
       };
-      auto scales_of = [&](int kt) { return reinterpret_cast<const float*>(smem + TL::SCALES + (kt & (2 * NST - 1)) * TL::RING); };
+      auto scales_of = [&](int kt) { return reinterpret_cast<const float*>(gmem + TL::SCALES + (kt & (2 * NST - 1)) * TL::RING); };
       constexpr int RS = SWV * 64;        // the row operand's scales in a slice's ring entry
       i32x8 tf[TB], wf[2];
       float ts[TB], tn[TB], sc[TB];       // token scales, those of the next slice, times the weights'
       f32x4 d[2][TB], xs[2];
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) {
-        tf[tb] = frag(smem + tread, smem + (tread ^ 64), tb * 2048);
+        tf[tb] = frag(gmem + tread, gmem + (tread ^ 64), tb * 2048);
         tn[tb] = scales_of(0)[wt * (TB * 16) + tb * 16 + i16];
         ts[tb] = sc[tb] = 0.f;
         d[1][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
       xs[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      wf[0] = frag(smem + wread, smem + (wread ^ 64), TL::OPT);
+      wf[0] = frag(gmem + wread, gmem + (wread ^ 64), TL::OPT);
+      const int nit = KG == 1 ? t.nkt : (t.nkt + KG - 1) / KG;
       int fresh = stores ? NST : 0;       // slices whose parts are older than the stores
 #pragma clang loop unroll(disable)
-      for (int kt = 0; kt < t.nkt; ++kt) {
+      for (int kt = 0; kt < nit; ++kt) {
         const int st = (kt & (NST - 1)) * TL::STAGE, sn = ((kt + 1) & (NST - 1)) * TL::STAGE;   // this slice's stage, the next one's
-        const uint8_t *w0 = smem + st + wread, *w1 = smem + st + (wread ^ 64);
+        const uint8_t *w0 = gmem + st + wread, *w1 = gmem + st + (wread ^ 64);
         const float* sS = scales_of(kt) + RS;
         static_for<0, RB>([&](auto rbc) {
           constexpr int rb = decltype(rbc)::value;
@@ -419,7 +424,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
             vm_barrier_if<FLY + STORES, FLY>(fresh);
           }
           if constexpr (rb < RB - 1) wf[(rb + 1) & 1] = frag(w0, w1, TL::OPT + (rb + 1 < H ? (rb + 1) * 2048 : HR * 128 + (rb + 1 - H) * 2048));
-          else wf[0] = frag(smem + sn + wread, smem + sn + (wread ^ 64), TL::OPT);
+          else wf[0] = frag(gmem + sn + wread, gmem + sn + (wread ^ 64), TL::OPT);
           if constexpr (KR) xs[rb & 1] = *reinterpret_cast<const f32x4*>(sS + (rb < H ? 0 : HR) + wn * (H * 16) + (rb % H) * 16 + 4 * q);
           if constexpr (KR && rb == 1) {
 #pragma unroll
@@ -440,7 +445,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
             const f32x4 z = {0.f, 0.f, 0.f, 0.f};
             d[rb & 1][tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[rb & 1], tf[tb], z, 0, 0, 0, 0, 0, 0);
             if constexpr (rb == RB - 1) {
-              tf[tb] = frag(smem + sn + tread, smem + sn + (tread ^ 64), tb * 2048);
+              tf[tb] = frag(gmem + sn + tread, gmem + sn + (tread ^ 64), tb * 2048);
               tn[tb] = scales_of(kt + 1)[wt * (TB * 16) + tb * 16 + i16];
             }
             // the parts of kt + NST, at most one DMA a matrix instruction
@@ -475,7 +480,27 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
     t = nxt;
     if (t.valid) o = setup(t, src);
     lds_barrier();                      // every wave is done with the stages
+    if constexpr (KG > 1) {
+      // the second group's sums through LDS (16 bytes a lane and block, whole wave after wave)
+      static_assert(KG == 2 && TL::WAVES * 64 * RB * TB * 16 <= TL::LDS, "sums of a group");
+      f32x4* sum = reinterpret_cast<f32x4*>(smem) + wave * (RB * TB * 64) + lane;
+      if (kg == 1) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int tb = 0; tb < TB; ++tb) sum[(rb * TB + tb) * 64] = acc[rb][tb];
+      }
+      lds_barrier();
+      if (kg == 0) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int tb = 0; tb < TB; ++tb) acc[rb][tb] += sum[(rb * TB + tb) * 64];
+      }
+      lds_barrier();
+    }
     if (t.valid && t.nkt > 0) prologue(o, t);
+    if (KG > 1 && kg > 0) continue;     // (no stores)
     stores = STORES > 0 ? 1 : 0;
     rederive_lane();
 
@@ -595,8 +620,8 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   __global__ __launch_bounds__(TL::THREADS, PER_SIMD) void name(P p) { fb_tile_body<TL, KR, SW, OUT, TAIL>(p); }
 FB_KERNEL(gemm_fb_store, FbMain, 2, false, false, OUT_BF16, false, FbGemm)
 FB_KERNEL(gemm_fb_store_f32, FbMain, 2, false, false, OUT_F32, false, FbGemm)
-FB_KERNEL(gemm_fb_store_tail, FbQuad, 1, false, false, OUT_BF16, true, FbGemm)
-FB_KERNEL(gemm_fb_store_f32_tail, FbQuad, 1, false, false, OUT_F32, true, FbGemm)
+FB_KERNEL(gemm_fb_store_tail, FbQuad, 2, false, false, OUT_BF16, true, FbGemm)
+FB_KERNEL(gemm_fb_store_f32_tail, FbQuad, 2, false, false, OUT_F32, true, FbGemm)
 FB_KERNEL(gemm_fb_swiglu, FbMain, 2, false, true, OUT_NONE, false, FbGemm)
 FB_KERNEL(gemm_fb_wgrad, FbMain, 2, true, false, OUT_BF16, false, FbWgrad)
 FB_KERNEL(gemm_fb_wgrad_f32, FbMain, 2, true, false, OUT_F32, false, FbWgrad)
@@ -620,10 +645,15 @@ mge_status launch_fb_tile(const FbGemm& p0, bool swiglu, hipStream_t s) {
   if (swiglu) return launch_fb<FbMain>(gemm_fb_swiglu, "gemm_fp8_block_swiglu", p, std::min<int64_t>(cus, mt * ((p.F + 127) / 128)), s);
   const int64_t tiles = mt * ((p.N + 255) / 256);
   p.grid_main = cus;
-  const int64_t grid = std::min<int64_t>(cus, tiles), tail = std::min<int64_t>(cus, 4 * tiles);
-  mge_status st = p.out_f32 ? launch_fb<FbMain>(gemm_fb_store_f32, "gemm_fp8_block", p, grid, s)
-                            : launch_fb<FbMain>(gemm_fb_store, "gemm_fp8_block", p, grid, s);
-  if (st != MGE_OK) return st;
+  // (with tiles for half a round at most, all of them are the tail's)
+  mge_status st = MGE_OK;
+  if (2 * tiles > cus) {
+    const int64_t grid = std::min<int64_t>(cus, tiles);
+    st = p.out_f32 ? launch_fb<FbMain>(gemm_fb_store_f32, "gemm_fp8_block", p, grid, s)
+                   : launch_fb<FbMain>(gemm_fb_store, "gemm_fp8_block", p, grid, s);
+    if (st != MGE_OK) return st;
+  }
+  const int64_t tail = std::min<int64_t>(cus, 4 * tiles);
   return p.out_f32 ? launch_fb<FbQuad>(gemm_fb_store_f32_tail, "gemm_fp8_block_tail", p, tail, s)
                    : launch_fb<FbQuad>(gemm_fb_store_tail, "gemm_fp8_block_tail", p, tail, s);
 }

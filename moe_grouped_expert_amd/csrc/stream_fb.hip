@@ -186,74 +186,49 @@ __global__ __launch_bounds__(64 * W) void fb_stream_kernel(FbGemm p) {
   }
 }
 
-// h = p silu(G) U of one block of 128 columns a workgroup: wave w has the gate and up rows of 16 of them and
-// goes over all of K; the block's scale is the largest magnitude over the 8 waves.
-constexpr int SF_SW = 8;
-template <int MB, int U>
-__global__ __launch_bounds__(64 * SF_SW) void fb_stream_swiglu_kernel(FbGemm p) {
-  __shared__ uint32_t s_amax[SF_SW][16 * MB];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int i16 = lane & 15, q = lane >> 4;
-  const SfGroup g = sf_group(p);
-  if (g.e < 0) return;
-  const int K = p.K, KB = (K + FB - 1) / FB, FBK = (p.F + FB - 1) / FB;
-  const __amdgpu_buffer_rsrc_t rW = sf_rsrc(p.W ? p.W[g.e] : p.Wv[g.e], 2u * uint32_t(p.F) * uint32_t(K));
-  const float* wsc = p.W ? p.Ws[g.e] : p.Wsv[g.e];
-  const __amdgpu_buffer_rsrc_t rA = sf_rsrc(p.A, uint32_t(p.src_rows) * uint32_t(K));
-  const __amdgpu_buffer_rsrc_t rS = sf_rsrc(p.As, uint32_t(p.src_rows) * uint32_t(KB) * 4);
-  const int f0 = int(blockIdx.x) * FB + wave * 16;   // the wave's first column (F is a multiple of 32)
-  const bool cols = f0 < p.F;
-  uint32_t w_off[2];
-  w_off[0] = cols ? uint32_t(f0 + i16) * uint32_t(K) : kSfOut;
-  w_off[1] = cols ? uint32_t(p.F + f0 + i16) * uint32_t(K) : kSfOut;
-  const int s0 = (cols ? f0 : 0) / FB * KB, s1 = (p.F + (cols ? f0 : 0)) / FB * KB;
-  auto sw = [&](int b, int kb) { return sf_uniform(wsc, (b ? s1 : s0) + kb); };
-  for (int m0 = 0; m0 < g.size; m0 += 16 * MB) {
-    SfRow rows[MB];
+// h = p silu(G) U of fp32 rows [G U], one block of 128 for 16 lanes, 8 columns each.  A launch of its own: with the
+// epilogue of the product above a workgroup would need all 256 weight rows of a block, and however its waves
+// share them it reads slower and fills fewer CUs (whole MLP, fused and not: 16 tokens, top-2 of 8 experts
+// 4096 x 14336 283 and 251 us; one token, 4096 x 4096 47 and 19 us).
+__global__ __launch_bounds__(256) void fb_swiglu_kernel(int rows, int F, const float* gu, const float* prob, const int32_t* map, uint8_t* codes,
+                                                        float* scales, int64_t ld) {
+  const int nb = (F + FB - 1) / FB;
+  const int64_t blk = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (blk >= int64_t(rows) * nb) return;
+  const int r = int(blk / nb), b = int(blk - int64_t(r) * nb);
+  if (map && map[r] < 0) return;   // padding between the groups (the same for the 16 lanes)
+  const int f = b * FB + (threadIdx.x & 15) * 8;
+  const bool in = f < F;
+  float h[8];
+  uint32_t am = 0;
+  const float pr = prob ? prob[r] : 1.f;
 #pragma unroll
-    for (int m = 0; m < MB; ++m) rows[m] = sf_row(p, g, m0 + m * 16 + i16, KB);
-    f32x4 acc[2][MB];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int m = 0; m < MB; ++m) acc[b][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (cols)
-      for (int kb = 0; kb < KB; kb += U) sf_step<2, MB, U>(acc, rW, rA, rS, w_off, rows, kb, K, KB, q, sw);
-    float h[MB][4];
-#pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      const int row = m0 + m * 16 + i16;
-      const float pr = !p.prob ? 1.f : (row < g.size ? p.prob[g.off + row] : 0.f);
-      uint32_t am = 0;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        h[m][r] = pr * silu_f(acc[0][m][r]) * acc[1][m][r];
-        am = umax(am, __float_as_uint(h[m][r]) & 0x7fffffffu);
-      }
-      const U32Pair x = permlane16_swap(am, am);
-      am = umax(x.a, x.b);
-      const U32Pair y = permlane32_swap(am, am);
-      am = umax(y.a, y.b);
-      if (q == 0) s_amax[wave][m * 16 + i16] = am;
+  for (int i = 0; i < 8; i += 4) {
+    float4 g = make_float4(0, 0, 0, 0), u = g;
+    if (in) {
+      g = *reinterpret_cast<const float4*>(gu + int64_t(r) * 2 * F + f + i);
+      u = *reinterpret_cast<const float4*>(gu + int64_t(r) * 2 * F + F + f + i);
     }
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      const int row = m0 + m * 16 + i16;
-      uint32_t am = s_amax[0][m * 16 + i16];
-#pragma unroll
-      for (int w = 1; w < SF_SW; ++w) am = umax(am, s_amax[w][m * 16 + i16]);
-      const FbScale sc = fb_scale(am);
-      if (row < g.size && cols) {
-        const int64_t r = int64_t(g.off) + row;
-        *reinterpret_cast<uint32_t*>(p.h_codes + r * p.F + f0 + 4 * q) =
-            e4m3x4(h[m][0] * sc.inv, h[m][1] * sc.inv, h[m][2] * sc.inv, h[m][3] * sc.inv);
-        if (wave == 0 && q == 0) p.h_scales[r * FBK + blockIdx.x] = sc.s;
-      }
-    }
-    __syncthreads();
+    h[i] = pr * silu_f(g.x) * u.x;
+    h[i + 1] = pr * silu_f(g.y) * u.y;
+    h[i + 2] = pr * silu_f(g.z) * u.z;
+    h[i + 3] = pr * silu_f(g.w) * u.w;
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) am = umax(am, __float_as_uint(h[i]) & 0x7fffffffu);
+  const FbScale sc = fb_scale(row16_umax(am));
+  if (!in) return;
+  *reinterpret_cast<uint2*>(codes + int64_t(r) * F + f) =
+      make_uint2(e4m3x4(h[0] * sc.inv, h[1] * sc.inv, h[2] * sc.inv, h[3] * sc.inv),
+                 e4m3x4(h[4] * sc.inv, h[5] * sc.inv, h[6] * sc.inv, h[7] * sc.inv));
+  if ((threadIdx.x & 15) == 0) scales[ld > 0 ? int64_t(b) * ld + r : int64_t(r) * nb + b] = sc.s;
+}
+mge_status launch_fb_swiglu(int rows, int F, const float* gu, const float* prob, const int32_t* map, uint8_t* codes, float* scales,
+                            int64_t ld, hipStream_t s) {
+  const int64_t blocks = int64_t(rows) * ((F + FB - 1) / FB);
+  ProfScope prof(s, "fp8_block_swiglu");
+  hipLaunchKernelGGL(fb_swiglu_kernel, dim3(unsigned((blocks + 15) / 16)), dim3(256), 0, s, rows, F, gu, prob, map, codes, scales, ld);
+  return hip_check("fp8_block_swiglu");
 }
 
 // Groups that can have rows: the kernels' grid in y
@@ -268,18 +243,11 @@ static mge_status launch_store(const FbGemm& p, hipStream_t s) {
   return hip_check("fp8_block_stream");
 }
 
-mge_status launch_fb_stream(const FbGemm& p, bool swiglu, hipStream_t s) {
+mge_status launch_fb_stream(const FbGemm& p, hipStream_t s) {
   if (p.total <= 0 || p.rows <= 0) return MGE_OK;
-  const bool two = p.total > 12 * int64_t(p.E);
-  if (swiglu) {
-    const dim3 grid(unsigned((p.F + FB - 1) / FB), groups_upper(p));
-    ProfScope prof(s, "fp8_block_stream_swiglu");
-    if (two) hipLaunchKernelGGL((fb_stream_swiglu_kernel<2, 2>), grid, dim3(64 * SF_SW), 0, s, p);
-    else hipLaunchKernelGGL((fb_stream_swiglu_kernel<1, 4>), grid, dim3(64 * SF_SW), 0, s, p);
-    return hip_check("fp8_block_stream_swiglu");
-  }
   const int64_t blocks = int64_t((p.N + 15) / 16) * groups_upper(p);
-  if (two) return launch_store<8, 2, 2, 2>(p, s);
+  if (p.total > 32 * int64_t(p.E)) return launch_store<8, 2, 4, 2>(p, s);
+  if (p.total > 12 * int64_t(p.E)) return launch_store<8, 2, 2, 2>(p, s);
   if (blocks < 1024) return launch_store<8, 1, 1, 4>(p, s);
   return launch_store<8, 2, 1, 2>(p, s);
 }

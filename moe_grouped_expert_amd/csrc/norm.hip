@@ -170,7 +170,7 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_kernel(NormParams p) {
 
 // The backward.  A thread's columns are the same in every row, so dw's share of a workgroup
 // accumulates in registers; the workgroups' shares (in `part`) are summed by rmsnorm_dw_kernel in
-// their order.
+// their order.  The next row's x and dy are on their way while a row is reduced.
 template <bool F32, int NT, int NV>
 __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams p) {
   constexpr int RPW = kNormThreads / NT;
@@ -183,25 +183,53 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-  int par = 0;
-  for (int64_t row0 = int64_t(blockIdx.x) * RPW; row0 < p.T; row0 += int64_t(gridDim.x) * RPW) {
-    const int64_t row = row0 + threadIdx.x / NT;
+  // x and dy as they are in memory (dy: 16 bytes more where it is fp32)
+  Vec8<F32> xv[NV];
+  Vec8<true> yv[NV];
+  float rstd = 0.f;
+  auto fetch = [&](int64_t row) {
     const bool live = row < p.T;
-    float xh[NV][8], g[NV][8];
-    float dot = 0.f;
-    const float rstd = live ? p.rstd[row] : 0.f;
+    rstd = live ? p.rstd[row] : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * NT + t;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) xh[i][j] = g[i][j] = 0.f;
+      xv[i].zero();
+      yv[i].zero();
       if (live && c < chunks) {
-        Vec8<F32> x;
-        x.load(p.x, row * p.x_ld + c * 8);
-        x.get(xh[i]);
-        get8(p.dy, row * p.dy_ld + c * 8, p.dy_f32, g[i]);
+        xv[i].load(p.x, row * p.x_ld + c * 8);
+        if (p.dy_f32) yv[i].load(p.dy, row * p.dy_ld + c * 8);
+        else yv[i].a = *reinterpret_cast<const float4*>(static_cast<const uint16_t*>(p.dy) + row * p.dy_ld + c * 8);
       }
     }
+  };
+  int par = 0;
+  const int64_t step = int64_t(gridDim.x) * RPW;
+  fetch(int64_t(blockIdx.x) * RPW + threadIdx.x / NT);
+  for (int64_t row0 = int64_t(blockIdx.x) * RPW; row0 < p.T; row0 += step) {
+    const int64_t row = row0 + threadIdx.x / NT;
+    const bool live = row < p.T;
+    float xh[NV][8], g[NV][8];
+    const float rs = rstd;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      xv[i].get(xh[i]);
+      if (p.dy_f32) {
+        yv[i].get(g[i]);
+      } else {
+        Vec8<false> y;
+        y.v = make_uint4(__float_as_uint(yv[i].a.x), __float_as_uint(yv[i].a.y), __float_as_uint(yv[i].a.z), __float_as_uint(yv[i].a.w));
+        y.get(g[i]);
+      }
+    }
+    Vec8<F32> res[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * NT + t;
+      res[i].zero();
+      if (p.d_res && live && c < chunks) res[i].load(p.d_res, row * p.H + c * 8);
+    }
+    fetch(row + step);
+    float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * NT + t;
@@ -211,7 +239,7 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams
       if (c < chunks) get8(p.weight, c * 8, p.w_f32, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        xh[i][j] *= rstd;
+        xh[i][j] *= rs;
         dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
         g[i][j] *= w[j];
         dot = fmaf(g[i][j], xh[i][j], dot);
@@ -223,17 +251,10 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams
     for (int i = 0; i < NV; ++i) {
       const int c = i * NT + t;
       if (live && c < chunks) {
-        float d[8];
+        float d[8], f[8];
+        res[i].get(f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = rstd * fmaf(-xh[i][j], dot, g[i][j]);
-        if (p.d_res) {
-          Vec8<F32> r;
-          float f[8];
-          r.load(p.d_res, row * p.H + c * 8);
-          r.get(f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] += f[j];
-        }
+        for (int j = 0; j < 8; ++j) d[j] = rs * fmaf(-xh[i][j], dot, g[i][j]) + f[j];
         Vec8<F32> o;
         o.set(d);
         o.store(p.dx, row * p.H + c * 8);
@@ -275,24 +296,29 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams
   }
 }
 
-// dw[h] = sum over n rows of part[.][h], in a fixed order: 16 column groups of 4, 16 slices of rows
-__global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* part, int n, int H, float* dw) {
-  __shared__ float4 s[16][16];
-  const int c = int(blockIdx.x) * 16 + (threadIdx.x & 15), k = threadIdx.x >> 4;
+// dw[h] = sum over n rows of part[.][h], in a fixed order: 16 column groups of 4, 64 slices of rows
+__global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* part, int n, int H, float* dw) {
+  __shared__ float4 s[64][16];
+  const int x = threadIdx.x & 15, k = threadIdx.x >> 4;
+  const int c = int(blockIdx.x) * 16 + x;
   float4 a = make_float4(0, 0, 0, 0);
-  if (c * 4 < H)
-    for (int r = k; r < n; r += 16) {
+  if (c * 4 < H) {
+#pragma unroll 4
+    for (int r = k; r < n; r += 64) {
       const float4 v = *reinterpret_cast<const float4*>(part + int64_t(r) * H + c * 4);
       a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
     }
-  s[k][threadIdx.x & 15] = a;
-  __syncthreads();
-  if (k > 0 || c * 4 >= H) return;
-  for (int i = 1; i < 16; ++i) {
-    const float4 v = s[i][threadIdx.x];
-    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
   }
-  *reinterpret_cast<float4*>(dw + c * 4) = a;
+  s[k][x] = a;
+  for (int o = 32; o > 0; o >>= 1) {
+    __syncthreads();
+    if (k < o) {
+      const float4 v = s[k + o][x];
+      a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+      s[k][x] = a;
+    }
+  }
+  if (k == 0 && c * 4 < H) *reinterpret_cast<float4*>(dw + c * 4) = a;
 }
 
 // A wave a row where a row fits its registers and there are rows for every CU, else a workgroup
@@ -324,8 +350,10 @@ mge_status launch_rmsnorm(const NormParams& p, bool x_f32, hipStream_t s) {
   return x_f32 ? fwd_by_size<true>(p, s) : fwd_by_size<false>(p, s);
 }
 
+// (the backward keeps a row's xhat, g and dw: a wave has the registers for 1024 values)
+static bool wave_rows_bwd(int64_t T, int H) { return H <= 1024 && (T >= 2048 || H <= 512); }
 int rmsnorm_bwd_parts(int64_t T, int H) {
-  const int64_t n = wave_rows(T, H) ? (T + 3) / 4 : T;
+  const int64_t n = wave_rows_bwd(T, H) ? (T + 3) / 4 : T;
   return int(n < 512 ? n : 512);
 }
 template <bool F32, int NT, int NV>
@@ -339,23 +367,18 @@ static mge_status launch_bwd(const NormBwdParams& p, hipStream_t s) {
   mge_status st = hip_check("rmsnorm_bwd");
   if (st != MGE_OK || !p.dw) return st;
   ProfScope prof(s, "rmsnorm_dw");
-  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3(unsigned((p.H / 4 + 15) / 16)), dim3(256), 0, s, p.part, n, p.H, p.dw);
+  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3(unsigned((p.H / 4 + 15) / 16)), dim3(1024), 0, s, p.part, n, p.H, p.dw);
   return hip_check("rmsnorm_dw");
 }
 mge_status launch_rmsnorm_dw_zero(int H, float* dw, hipStream_t s) {
   ProfScope prof(s, "rmsnorm_dw");
-  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3(unsigned((H / 4 + 15) / 16)), dim3(256), 0, s, nullptr, 0, H, dw);
+  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3(unsigned((H / 4 + 15) / 16)), dim3(1024), 0, s, nullptr, 0, H, dw);
   return hip_check("rmsnorm_dw");
 }
 template <bool F32>
 static mge_status bwd_by_size(const NormBwdParams& p, hipStream_t s) {
   const int ch = p.H / 8;
-  if (wave_rows(p.T, p.H)) {
-    if (ch <= 64) return launch_bwd<F32, 64, 1>(p, s);
-    if (ch <= 128) return launch_bwd<F32, 64, 2>(p, s);
-    if (ch <= 256) return launch_bwd<F32, 64, 4>(p, s);
-    return launch_bwd<F32, 64, 8>(p, s);
-  }
+  if (wave_rows_bwd(p.T, p.H)) return ch <= 64 ? launch_bwd<F32, 64, 1>(p, s) : launch_bwd<F32, 64, 2>(p, s);
   if (ch <= 256) return launch_bwd<F32, 256, 1>(p, s);
   if (ch <= 512) return launch_bwd<F32, 256, 2>(p, s);
   if (ch <= 1024) return launch_bwd<F32, 256, 4>(p, s);

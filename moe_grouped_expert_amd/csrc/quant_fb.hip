@@ -2,7 +2,7 @@
 // form and transposed, rows optionally gathered, and back.
 //
 // HBM-bound: one read of the input, one write of each form.  A workgroup takes a tile of 128 rows x
-// 128 columns (a block is never split), 8 columns of 2 x 4 consecutive rows a thread: a row's 128
+// 128 columns (a block is never split), 8 columns of 4 consecutive rows a thread: a row's 128
 // values are in the 16 lanes of a DPP row, a column's 4 rows make one dword of the transposed form,
 // which goes through LDS so that it leaves in whole lines.
 #include "mge_common.hpp"
@@ -13,14 +13,15 @@ namespace mge {
 
 constexpr int QF_LD = 132;   // bytes of a column in LDS: a dword of skew spreads the dword writes over the banks
 
+constexpr int QF_THREADS = 512;
 template <bool TILE, bool ROW, bool COL>
-__global__ __launch_bounds__(256) void quant_fb_kernel(QuantFbParams p, int64_t tiles, int nr, int nc) {
+__global__ __launch_bounds__(QF_THREADS) void quant_fb_kernel(QuantFbParams p, int64_t tiles, int nr, int nc) {
   __shared__ __attribute__((aligned(16))) uint8_t s_col[COL ? FB * QF_LD : 4];
-  __shared__ uint32_t s_max[TILE ? 4 : (COL ? 4 * FB : 1)];
+  __shared__ uint32_t s_max[TILE ? 8 : (COL ? 8 * FB : 1)];
   __shared__ float s_inv[!TILE && COL ? FB : 1];
   const int tid = threadIdx.x, wave = tid >> 6;
   const int cl = (tid & 15) * 8;         // first of the thread's 8 columns
-  const int rg = tid >> 4;               // its rows: 64 i + 4 rg + j
+  const int rg = tid >> 4;               // its rows: 4 rg + j
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t b = tile / (int64_t(nr) * nc);
     const int rem = int(tile - b * nr * nc);
@@ -29,50 +30,39 @@ __global__ __launch_bounds__(256) void quant_fb_kernel(QuantFbParams p, int64_t 
     const int c0 = tc * FB + cl;
     const bool cin = c0 < p.C;
     const uint16_t* src = p.in + b * p.in_bstride + c0;
-    uint4 x[2][4];
+    const int64_t rt = r0 + 4 * rg;
+    uint4 x[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t r = r0 + 64 * i + 4 * rg + j;
-        x[i][j] = make_uint4(0, 0, 0, 0);
-        if (cin && r < p.R) {
-          int64_t sr = r;
-          if (p.map) {
-            sr = p.map[r];
-            if (sr < 0 || sr >= p.src_rows) sr = -1;
-          }
-          if (sr >= 0) x[i][j] = *reinterpret_cast<const uint4*>(src + sr * p.in_ld);
+    for (int j = 0; j < 4; ++j) {
+      x[j] = make_uint4(0, 0, 0, 0);
+      if (cin && rt + j < p.R) {
+        int64_t sr = rt + j;
+        if (p.map) {
+          sr = p.map[sr];
+          if (sr < 0 || sr >= p.src_rows) sr = -1;
         }
+        if (sr >= 0) x[j] = *reinterpret_cast<const uint4*>(src + sr * p.in_ld);
       }
-    auto val = [&](int i, int j, int k) {
-      const uint32_t w = k < 4 ? (k < 2 ? x[i][j].x : x[i][j].y) : (k < 6 ? x[i][j].z : x[i][j].w);
+    }
+    auto val = [&](int j, int k) {
+      const uint32_t w = k < 4 ? (k < 2 ? x[j].x : x[j].y) : (k < 6 ? x[j].z : x[j].w);
       return __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
     };
     // largest magnitudes, as bit patterns: of the thread's rows and columns
-    uint32_t rmax[2][4], cmax[8], all = 0;
+    uint32_t rmax[4], cmax[8], all = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) cmax[k] = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 4; ++j) {
+      rmax[j] = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        rmax[i][j] = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t m = __float_as_uint(val(i, j, k)) & 0x7fffffffu;
-          rmax[i][j] = umax(rmax[i][j], m);
-          cmax[k] = umax(cmax[k], m);
-        }
-        all = umax(all, rmax[i][j]);
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t m = __float_as_uint(val(j, k)) & 0x7fffffffu;
+        rmax[j] = umax(rmax[j], m);
+        cmax[k] = umax(cmax[k], m);
       }
-    auto store_row = [&](int i, int j, float inv) {
-      const int64_t r = r0 + 64 * i + 4 * rg + j;
-      if (cin && r < p.R)
-        *reinterpret_cast<uint2*>(p.row_codes + (b * p.R + r) * p.C + c0) =
-            make_uint2(e4m3x4(val(i, j, 0) * inv, val(i, j, 1) * inv, val(i, j, 2) * inv, val(i, j, 3) * inv),
-                       e4m3x4(val(i, j, 4) * inv, val(i, j, 5) * inv, val(i, j, 6) * inv, val(i, j, 7) * inv));
-    };
+      all = umax(all, rmax[j]);
+    }
     FbScale ts;
     if constexpr (TILE) {
       all = row16_umax(all);
@@ -82,7 +72,9 @@ __global__ __launch_bounds__(256) void quant_fb_kernel(QuantFbParams p, int64_t 
       all = umax(c.a, c.b);
       if ((tid & 63) == 0) s_max[wave] = all;
       __syncthreads();
-      ts = fb_scale(umax(umax(s_max[0], s_max[1]), umax(s_max[2], s_max[3])));
+#pragma unroll
+      for (int w = 0; w < 8; ++w) all = umax(all, s_max[w]);
+      ts = fb_scale(all);
       if (tid == 0) {
         if constexpr (ROW) p.row_scales[(b * nr + tr) * nc + tc] = ts.s;
         if constexpr (COL) p.col_scales[(b * nc + tc) * nr + tr] = ts.s;
@@ -90,17 +82,18 @@ __global__ __launch_bounds__(256) void quant_fb_kernel(QuantFbParams p, int64_t 
     }
     if constexpr (ROW) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          FbScale sc = ts;
-          if constexpr (!TILE) {
-            sc = fb_scale(row16_umax(rmax[i][j]));
-            const int64_t r = r0 + 64 * i + 4 * rg + j;
-            if (cl == 0 && r < p.R) p.row_scales[(b * p.R + r) * nc + tc] = sc.s;
-          }
-          store_row(i, j, sc.inv);
+      for (int j = 0; j < 4; ++j) {
+        FbScale sc = ts;
+        const int64_t r = rt + j;
+        if constexpr (!TILE) {
+          sc = fb_scale(row16_umax(rmax[j]));
+          if (cl == 0 && r < p.R) p.row_scales[(b * p.R + r) * nc + tc] = sc.s;
         }
+        if (cin && r < p.R)
+          *reinterpret_cast<uint2*>(p.row_codes + (b * p.R + r) * p.C + c0) =
+              make_uint2(e4m3x4(val(j, 0) * sc.inv, val(j, 1) * sc.inv, val(j, 2) * sc.inv, val(j, 3) * sc.inv),
+                         e4m3x4(val(j, 4) * sc.inv, val(j, 5) * sc.inv, val(j, 6) * sc.inv, val(j, 7) * sc.inv));
+      }
     }
     if constexpr (COL) {
       float inv[8];
@@ -108,7 +101,7 @@ __global__ __launch_bounds__(256) void quant_fb_kernel(QuantFbParams p, int64_t 
 #pragma unroll
         for (int k = 0; k < 8; ++k) inv[k] = ts.inv;
       } else {
-        // over the wave's 4 row groups (lanes 16 and 32 apart), then the 4 waves
+        // over the wave's 4 row groups (lanes 16 and 32 apart), then the 8 waves
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const U32Pair a = permlane16_swap(cmax[k], cmax[k]);
@@ -122,7 +115,10 @@ __global__ __launch_bounds__(256) void quant_fb_kernel(QuantFbParams p, int64_t 
         }
         __syncthreads();
         if (tid < FB) {
-          const FbScale sc = fb_scale(umax(umax(s_max[tid], s_max[FB + tid]), umax(s_max[2 * FB + tid], s_max[3 * FB + tid])));
+          uint32_t m = s_max[tid];
+#pragma unroll
+          for (int w = 1; w < 8; ++w) m = umax(m, s_max[w * FB + tid]);
+          const FbScale sc = fb_scale(m);
           s_inv[tid] = sc.inv;
           const int c = tc * FB + tid;
           if (c < p.C) p.col_scales[(b * p.C + c) * nr + tr] = sc.s;
@@ -133,15 +129,13 @@ __global__ __launch_bounds__(256) void quant_fb_kernel(QuantFbParams p, int64_t 
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<uint32_t*>(s_col + (cl + k) * QF_LD + 64 * i + 4 * rg) =
-              e4m3x4(val(i, 0, k) * inv[k], val(i, 1, k) * inv[k], val(i, 2, k) * inv[k], val(i, 3, k) * inv[k]);
+        *reinterpret_cast<uint32_t*>(s_col + (cl + k) * QF_LD + 4 * rg) =
+            e4m3x4(val(0, k) * inv[k], val(1, k) * inv[k], val(2, k) * inv[k], val(3, k) * inv[k]);
       __syncthreads();
       // 16 bytes a thread: 8 threads a column
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = i * 32 + (tid >> 3), q = (tid & 7) * 16;
+      for (int i = 0; i < 2; ++i) {
+        const int c = i * 64 + (tid >> 3), q = (tid & 7) * 16;
         if (tc * FB + c < p.C && r0 + q < p.Rp) {
           const uint32_t* s = reinterpret_cast<const uint32_t*>(s_col + c * QF_LD + q);
           *reinterpret_cast<uint4*>(p.col_codes + (b * p.C + tc * FB + c) * p.Rp + r0 + q) = make_uint4(s[0], s[1], s[2], s[3]);
@@ -155,9 +149,9 @@ __global__ __launch_bounds__(256) void quant_fb_kernel(QuantFbParams p, int64_t 
 template <bool TILE>
 static void launch_q(const QuantFbParams& p, int64_t tiles, int nr, int nc, hipStream_t s) {
   const unsigned grid = unsigned(tiles < (1 << 20) ? tiles : (1 << 20));
-  if (p.row_codes && p.col_codes) hipLaunchKernelGGL((quant_fb_kernel<TILE, true, true>), dim3(grid), dim3(256), 0, s, p, tiles, nr, nc);
-  else if (p.row_codes) hipLaunchKernelGGL((quant_fb_kernel<TILE, true, false>), dim3(grid), dim3(256), 0, s, p, tiles, nr, nc);
-  else hipLaunchKernelGGL((quant_fb_kernel<TILE, false, true>), dim3(grid), dim3(256), 0, s, p, tiles, nr, nc);
+  if (p.row_codes && p.col_codes) hipLaunchKernelGGL((quant_fb_kernel<TILE, true, true>), dim3(grid), dim3(QF_THREADS), 0, s, p, tiles, nr, nc);
+  else if (p.row_codes) hipLaunchKernelGGL((quant_fb_kernel<TILE, true, false>), dim3(grid), dim3(QF_THREADS), 0, s, p, tiles, nr, nc);
+  else hipLaunchKernelGGL((quant_fb_kernel<TILE, false, true>), dim3(grid), dim3(QF_THREADS), 0, s, p, tiles, nr, nc);
 }
 mge_status launch_quant_fb(const QuantFbParams& p, hipStream_t s) {
   const int nr = int(fb_blocks(p.R)), nc = int(fb_blocks(p.C));

@@ -776,8 +776,8 @@ mge_status rmsnorm_bwd(const mge_rmsnorm_bwd_args* args, void* stream);
  * rows[r] is outside [0, src_rows) (perm_src of moe_route_permute: the tokens are permuted
  * as they are quantized).
  * Errors: MGE_ERR_INVALID_ARG for an unknown block or orientation, negative sizes, C not a
- * multiple of 32, C or R above 2^31 - 256, a map with batch > 1 or 128X128, strides too small
- * or not multiples of 8, NULL or misaligned pointers (16 bytes; scales and rows 4).
+ * multiple of 32 or above 2^24, R above 2^31 - 256, a map with batch > 1 or 128X128, strides too
+ * small or not multiples of 8, NULL or misaligned pointers (16 bytes; scales and rows 4).
  * batch, R or C = 0 is a no-op.
  * ---------------------------------------------------------------------------- */
 enum { MGE_BLOCK_1X128 = 0, MGE_BLOCK_128X128 = 1 };
@@ -836,7 +836,7 @@ mge_status fp8_block_dequantize(const mge_dequant_fb_args* args, void* stream);
  * Workspace: mge_gemm_fb_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for
  * few rows over at most 64 experts.
  * Errors: MGE_ERR_INVALID_ARG for E outside [1, 256], N or K not a positive multiple of 32,
- * N above 2^22, rows or src_rows < 0 or >= 2^31 / K, src_rows other than rows without a map,
+ * or above 2^22, rows or src_rows < 0 or >= 2^31 / K, src_rows other than rows without a map,
  * an expert's weight of 2^31 bytes or more, an unknown dtype, NULL or misaligned pointers
  * (codes, out, workspace 16 bytes, scales and a_rows 4), one of split_sizes / group_offsets
  * without the other or E > 1 without both; MGE_ERR_WORKSPACE.
@@ -878,7 +878,7 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* args, void* stream);
  * Sums, NaN: as fp8_block_grouped_gemm.
  * Workspace: mge_wgrad_fb_workspace_bytes(args) bytes, 16-byte aligned.
  * Errors: as fp8_block_grouped_gemm, N and K at most 2^22, rows a multiple of 32 in
- * [0, 2^31 / max(N, K)), accumulate with bf16; MGE_ERR_WORKSPACE.
+ * [0, 2^31 / max(N, K, 256)), accumulate with bf16; MGE_ERR_WORKSPACE.
  * ---------------------------------------------------------------------------- */
 typedef struct mge_wgrad_fb_args {
   uint32_t struct_size;
@@ -914,7 +914,8 @@ mge_status fp8_block_grouped_wgrad(const mge_wgrad_fb_args* args, void* stream);
  * total_rows: an upper bound of the groups' row count the caller knows (T*k), or 0.  Rows
  * outside the groups are untouched.
  * Workspace: mge_fwd_fb_workspace_bytes(args) bytes, 16-byte aligned.
- * Errors: as fp8_block_grouped_gemm for both products; MGE_ERR_WORKSPACE.
+ * Errors: as fp8_block_grouped_gemm for both products (2F is the first one's N);
+ * MGE_ERR_WORKSPACE.
  * ---------------------------------------------------------------------------- */
 typedef struct mge_fwd_fb_args {
   uint32_t struct_size;

@@ -1244,11 +1244,14 @@ def fp8_block_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, w, w_scale, s
     src, K = _codes_rows(a, a_scale, "a")
     dev = a.device
     _on(dev, a_scale, out, split_sizes, group_offsets, a_rows, workspace)
-    E = len(w)
-    stacked = isinstance(w, torch.Tensor)
-    if E < 1 or len(w_scale) != E or (w.dim() != 3 if stacked else w[0].dim() != 2):
-        raise ValueError("w must be [E, N, K] with w_scale [E, ceil(N/128), ceil(K/128)]")
-    N = w.shape[1] if stacked else w[0].shape[0]
+    if isinstance(w, torch.Tensor):
+        shape = w.shape
+        _need(len(shape) == 3 and shape[0] > 0, "w must be [E, N, K]")
+        E, N = shape[0], shape[1]
+    else:
+        E = len(w)
+        _need(E > 0 and w[0].dim() == 2, "w must be E matrices [N, K]")
+        N = w[0].shape[0]
     rows = src
     if a_rows is not None:
         _need(a_rows.dim() == 1 and a_rows.dtype == torch.int32 and a_rows.is_contiguous(), "a_rows must be contiguous int32 [rows]")

@@ -16,7 +16,10 @@ namespace mge {
 
 static bool is_dtype(int d) { return d == MGE_DTYPE_BF16 || d == MGE_DTYPE_F32; }
 constexpr int64_t kTwoGiB = int64_t(1) << 31;
-constexpr int kMaxCols = 1 << 22;   // columns of a product: 64 rows of them stay within a buffer's 31-bit offsets
+// Columns of a product and lengths of its sums: 64 rows of fp32 results and a tile's 256 rows of operands stay within a
+// buffer's 31-bit offsets
+constexpr int kMaxCols = 1 << 22;
+constexpr int kTileRows = 256;
 
 static mge_status check_norm(int T, int H, int x_dtype, int w_dtype, int y_dtype, int64_t ld) {
   MGE_REQUIRE(T >= 0, "T must be >= 0 (got %d)", T);
@@ -59,7 +62,8 @@ static bool fb_fused(int64_t E, int64_t F, int64_t total, bool tile) {
   return tile && ((total + 255) / 256 + std::min(E, total) - 1) * fb_blocks(F) > kFusedTiles;
 }
 
-static int64_t fb_total(int64_t total, int64_t rows) { return total > 0 && total < rows ? total : rows; }
+// Rows of all groups at most (without groups: all rows)
+static int64_t fb_total(const void* sizes, int64_t total, int64_t rows) { return sizes && total > 0 && total < rows ? total : rows; }
 
 // Few experts' pointers travel in the kernels' arguments, more through a table in the workspace
 static bool fb_table(int E) { return E > kFbInline; }
@@ -131,7 +135,7 @@ mge_status fp8_block_quantize(const mge_quant_fb_args* a, void* stream) {
   MGE_REQUIRE(a->struct_size == sizeof(mge_quant_fb_args), "struct_size mismatch");
   MGE_REQUIRE(a->block == MGE_BLOCK_1X128 || a->block == MGE_BLOCK_128X128, "block must be 1X128 or 128X128 (got %d)", a->block);
   MGE_REQUIRE(a->batch >= 0 && a->R >= 0 && a->C >= 0, "negative size");
-  MGE_REQUIRE(a->C % 32 == 0 && a->C <= 0x7fffff00 && a->R <= 0x7fffff00, "C must be a multiple of 32, C and R at most %d (got %d, %d)",
+  MGE_REQUIRE(a->C % 32 == 0 && a->C <= 1 << 24 && a->R <= 0x7fffff00, "C must be a multiple of 32 and at most 2^24, R at most %d (got %d, %d)",
               0x7fffff00, a->C, a->R);
   MGE_REQUIRE(a->orient != 0 && (a->orient & ~3u) == 0, "orient must be ROW, COL or ROW|COL");
   MGE_REQUIRE(!a->rows || (a->batch <= 1 && a->block == MGE_BLOCK_1X128 && a->src_rows >= 0 && aligned4(a->rows)),
@@ -176,7 +180,7 @@ size_t mge_gemm_fb_workspace_bytes(const mge_gemm_fb_args* a) {
   if (!a || a->struct_size != sizeof(mge_gemm_fb_args) || a->E < 1 || a->E > 256 || a->N < 32 || a->K < 32 || a->rows < 0 || a->rows >= kTwoGiB / a->K)
     return 0;
   return (fb_table(a->E) ? up256(2 * size_t(a->E) * sizeof(void*)) : 0) +
-         (fb_tile(a->E, a->N, a->K, fb_total(a->total_rows, a->rows)) ? fb_scales_t(a->rows, a->K) : 0);
+         (fb_tile(a->E, a->N, a->K, fb_total(a->split_sizes, a->total_rows, a->rows)) ? fb_scales_t(a->rows, a->K) : 0);
 }
 
 mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
@@ -184,8 +188,8 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
   MGE_REQUIRE(a != nullptr, "args is NULL");
   MGE_REQUIRE(a->struct_size == sizeof(mge_gemm_fb_args), "struct_size mismatch");
   MGE_REQUIRE(a->E >= 1 && a->E <= 256, "E must be in [1, 256] (got %d)", a->E);
-  MGE_REQUIRE(a->N >= 32 && a->N % 32 == 0 && a->N <= kMaxCols && a->K >= 32 && a->K % 32 == 0,
-              "N and K must be positive multiples of 32, N at most %d (got N=%d, K=%d)", kMaxCols, a->N, a->K);
+  MGE_REQUIRE(a->N >= 32 && a->N % 32 == 0 && a->N <= kMaxCols && a->K >= 32 && a->K % 32 == 0 && a->K <= kMaxCols,
+              "N and K must be positive multiples of 32, at most %d (got N=%d, K=%d)", kMaxCols, a->N, a->K);
   MGE_REQUIRE(a->rows >= 0 && a->rows < kTwoGiB / a->K && a->src_rows >= 0 && a->src_rows < kTwoGiB / a->K,
               "rows and src_rows must be in [0, 2^31 / K) (got %lld, %lld)", static_cast<long long>(a->rows),
               static_cast<long long>(a->src_rows));
@@ -214,7 +218,7 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
   Carve ws(a->workspace);
   FbGemm p{};
   p.E = a->E; p.N = a->N; p.K = a->K;
-  p.rows = int(a->rows); p.total = int(fb_total(a->total_rows, a->rows));
+  p.rows = int(a->rows); p.total = int(fb_total(a->split_sizes, a->total_rows, a->rows));
   p.sizes = a->split_sizes; p.offs = a->group_offsets;
   p.map = a->a_rows; p.src_rows = int(a->src_rows);
   p.A = a->a; p.As = a->a_scale;
@@ -242,7 +246,7 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
 
 size_t mge_wgrad_fb_workspace_bytes(const mge_wgrad_fb_args* a) {
   if (!a || a->struct_size != sizeof(mge_wgrad_fb_args) || a->E < 1 || a->E > 256 || a->N < 32 || a->K < 32 || a->rows < 0 ||
-      a->rows >= kTwoGiB / std::max(a->N, a->K))
+      a->rows >= kTwoGiB / std::max({a->N, a->K, kTileRows}))
     return 0;
   const size_t nb = size_t(fb_blocks(a->rows));
   return (fb_table(a->E) ? up256(size_t(a->E) * sizeof(void*)) : 0) + up256(nb * a->N * 4) + up256(nb * a->K * 4);
@@ -255,8 +259,8 @@ mge_status fp8_block_grouped_wgrad(const mge_wgrad_fb_args* a, void* stream) {
   MGE_REQUIRE(a->E >= 1 && a->E <= 256, "E must be in [1, 256] (got %d)", a->E);
   MGE_REQUIRE(a->N >= 32 && a->N % 32 == 0 && a->K >= 32 && a->K % 32 == 0 && a->N <= kMaxCols && a->K <= kMaxCols,
               "N and K must be positive multiples of 32, at most %d (got N=%d, K=%d)", kMaxCols, a->N, a->K);
-  MGE_REQUIRE(a->rows >= 0 && a->rows % 32 == 0 && a->rows < kTwoGiB / std::max(a->N, a->K),
-              "rows must be a multiple of 32 in [0, 2^31 / max(N, K)) (got %lld)", static_cast<long long>(a->rows));
+  MGE_REQUIRE(a->rows >= 0 && a->rows % 32 == 0 && a->rows < kTwoGiB / std::max({a->N, a->K, kTileRows}),
+              "rows must be a multiple of 32 in [0, 2^31 / max(N, K, 256)) (got %lld)", static_cast<long long>(a->rows));
   MGE_REQUIRE((a->split_sizes != nullptr) == (a->group_offsets != nullptr) && (a->split_sizes || a->E == 1),
               "split_sizes and group_offsets go together, and E > 1 needs both");
   MGE_REQUIRE(is_dtype(a->out_dtype) && (!a->accumulate || a->out_dtype == MGE_DTYPE_F32), "out_dtype must be BF16 or F32, F32 to accumulate");
@@ -301,10 +305,10 @@ size_t mge_fwd_fb_workspace_bytes(const mge_fwd_fb_args* a) {
   if (!a || a->struct_size != sizeof(mge_fwd_fb_args) || a->E < 1 || a->E > 256 || a->H < 32 || a->F < 32 || a->rows < 0 ||
       a->rows >= kTwoGiB / std::max(a->H, a->F))
     return 0;
-  const int64_t total = fb_total(a->total_rows, a->rows);
+  const int64_t total = fb_total(a->split_sizes, a->total_rows, a->rows);
   const bool tile = fb_tile_mlp(a->E, a->H, a->F, total);
-  return (fb_fused(a->E, a->F, total, tile) ? 0 : up256(size_t(a->rows) * a->F * 8)) + (fb_table(a->E) ? up256(4 * size_t(a->E) * sizeof(void*)) : 0) + up256(size_t(a->rows) * a->F) + fb_scales_t(a->rows, a->F) +
-         (tile ? fb_scales_t(a->rows, a->H) : 0);
+  return (fb_table(a->E) ? up256(4 * size_t(a->E) * sizeof(void*)) : 0) + up256(size_t(a->rows) * a->F) + fb_scales_t(a->rows, a->F) +
+         (tile ? fb_scales_t(a->rows, a->H) : 0) + (fb_fused(a->E, a->F, total, tile) ? 0 : up256(size_t(a->rows) * a->F * 8));
 }
 
 mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
@@ -312,8 +316,8 @@ mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
   MGE_REQUIRE(a != nullptr, "args is NULL");
   MGE_REQUIRE(a->struct_size == sizeof(mge_fwd_fb_args), "struct_size mismatch");
   MGE_REQUIRE(a->E >= 1 && a->E <= 256, "E must be in [1, 256] (got %d)", a->E);
-  MGE_REQUIRE(a->H >= 32 && a->H % 32 == 0 && a->F >= 32 && a->F % 32 == 0 && a->H <= kMaxCols && a->F <= kMaxCols,
-              "H and F must be positive multiples of 32, at most %d (got H=%d, F=%d)", kMaxCols, a->H, a->F);
+  MGE_REQUIRE(a->H >= 32 && a->H % 32 == 0 && a->F >= 32 && a->F % 32 == 0 && a->H <= kMaxCols && a->F <= kMaxCols / 2,
+              "H and F must be positive multiples of 32, at most %d and %d (got H=%d, F=%d)", kMaxCols, kMaxCols / 2, a->H, a->F);
   MGE_REQUIRE(a->rows >= 0 && a->rows < kTwoGiB / std::max(a->H, a->F) && a->x_rows >= 0 && a->x_rows < kTwoGiB / a->H,
               "rows must be in [0, 2^31 / max(H, F)) and x_rows in [0, 2^31 / H) (got %lld, %lld)", static_cast<long long>(a->rows),
               static_cast<long long>(a->x_rows));
@@ -346,7 +350,7 @@ mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
   const int E = a->E, H = a->H, F = a->F;
   FbGemm g{};
   g.E = E; g.N = 2 * F; g.K = H; g.F = F;
-  g.rows = int(a->rows); g.total = int(fb_total(a->total_rows, a->rows));
+  g.rows = int(a->rows); g.total = int(fb_total(a->split_sizes, a->total_rows, a->rows));
   g.sizes = a->split_sizes; g.offs = a->group_offsets;
   g.map = a->perm_src; g.src_rows = int(a->x_rows);
   g.A = a->x; g.As = a->x_scale; g.prob = a->prob_perm;
@@ -391,7 +395,7 @@ mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
     g.C = gu;
     g.out_f32 = 1;
     st = tile ? launch_fb_tile(g, false, s) : launch_fb_stream(g, s);
-    if (st == MGE_OK) st = launch_fb_swiglu(g.rows, F, gu, g.prob, g.map, g.h_codes, g.h_scales, tile ? a->rows : 0, s);
+    if (st == MGE_OK) st = launch_fb_swiglu(g, gu, tile ? a->rows : 0, s);
   }
   if (st != MGE_OK) return st;
   return tile ? launch_fb_tile(d, false, s) : launch_fb_stream(d, s);

@@ -130,10 +130,9 @@ struct FbGemm {
 mge_status launch_fb_stream(const FbGemm& p, hipStream_t s);
 mge_status launch_fb_tile(const FbGemm& p, bool swiglu, hipStream_t s);
 
-// h = p silu(G) U of fp32 rows [G U], quantized 1 x 128; scales [rows][ceil(F/128)], or with ld > 0 [ceil(F/128)][ld];
-// rows r with map[r] < 0 are left out
-mge_status launch_fb_swiglu(int rows, int F, const float* gu, const float* prob, const int32_t* map, uint8_t* codes, float* scales,
-                            int64_t ld, hipStream_t s);
+// h_codes, h_scales of fp32 rows gu = [G U] (rows behind and between the groups may be left out); scales
+// [rows][ceil(F/128)], or with ld > 0 [ceil(F/128)][ld]
+mge_status launch_fb_swiglu(const FbGemm& p, const float* gu, int64_t ld, hipStream_t s);
 
 // dw_e[n][k] = sum over the tokens of expert e: columns [offs[e], offs[e] + sizes[e]) of both
 struct FbWgrad {

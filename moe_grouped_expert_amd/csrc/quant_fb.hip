@@ -15,7 +15,7 @@ constexpr int QF_LD = 132;   // bytes of a column in LDS: a dword of skew spread
 
 constexpr int QF_THREADS = 512;
 template <bool TILE, bool ROW, bool COL>
-__global__ __launch_bounds__(QF_THREADS) void quant_fb_kernel(QuantFbParams p, int64_t tiles, int nr, int nc) {
+__global__ __launch_bounds__(QF_THREADS, 8) void quant_fb_kernel(QuantFbParams p, int64_t tiles, int nr, int nc) {
   __shared__ __attribute__((aligned(16))) uint8_t s_col[COL ? FB * QF_LD : 4];
   __shared__ uint32_t s_max[TILE ? 8 : (COL ? 8 * FB : 1)];
   __shared__ float s_inv[!TILE && COL ? FB : 1];
@@ -44,24 +44,26 @@ __global__ __launch_bounds__(QF_THREADS) void quant_fb_kernel(QuantFbParams p, i
         if (sr >= 0) x[j] = *reinterpret_cast<const uint4*>(src + sr * p.in_ld);
       }
     }
+    // (between the phases the values are unpacked again: kept as floats they would halve the waves)
+    auto repack = [&]() {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(x[j].x), "+v"(x[j].y), "+v"(x[j].z), "+v"(x[j].w));
+    };
     auto val = [&](int j, int k) {
       const uint32_t w = k < 4 ? (k < 2 ? x[j].x : x[j].y) : (k < 6 ? x[j].z : x[j].w);
       return __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
     };
-    // largest magnitudes, as bit patterns: of the thread's rows and columns
-    uint32_t rmax[4], cmax[8], all = 0;
+    // largest magnitudes, as bit patterns
+    auto row_max = [&](int j) {
+      uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) cmax[k] = 0;
+      for (int k = 0; k < 8; ++k) m = umax(m, __float_as_uint(val(j, k)) & 0x7fffffffu);
+      return m;
+    };
+    uint32_t all = 0;
+    if constexpr (TILE) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      rmax[j] = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t m = __float_as_uint(val(j, k)) & 0x7fffffffu;
-        rmax[j] = umax(rmax[j], m);
-        cmax[k] = umax(cmax[k], m);
-      }
-      all = umax(all, rmax[j]);
+      for (int j = 0; j < 4; ++j) all = umax(all, row_max(j));
     }
     FbScale ts;
     if constexpr (TILE) {
@@ -81,21 +83,24 @@ __global__ __launch_bounds__(QF_THREADS) void quant_fb_kernel(QuantFbParams p, i
       }
     }
     if constexpr (ROW) {
+      uint8_t* rbase = p.row_codes + (b * p.R + r0) * p.C;   // (the same in every lane; 128 rows are below 2^32 bytes)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        if constexpr (!TILE && COL) __builtin_amdgcn_sched_barrier(0);   // a row at a time
         FbScale sc = ts;
         const int64_t r = rt + j;
         if constexpr (!TILE) {
-          sc = fb_scale(row16_umax(rmax[j]));
+          sc = fb_scale(row16_umax(row_max(j)));
           if (cl == 0 && r < p.R) p.row_scales[(b * p.R + r) * nc + tc] = sc.s;
         }
         if (cin && r < p.R)
-          *reinterpret_cast<uint2*>(p.row_codes + (b * p.R + r) * p.C + c0) =
+          *reinterpret_cast<uint2*>(rbase + (uint32_t(4 * rg + j) * uint32_t(p.C) + uint32_t(c0))) =
               make_uint2(e4m3x4(val(j, 0) * sc.inv, val(j, 1) * sc.inv, val(j, 2) * sc.inv, val(j, 3) * sc.inv),
                          e4m3x4(val(j, 4) * sc.inv, val(j, 5) * sc.inv, val(j, 6) * sc.inv, val(j, 7) * sc.inv));
       }
     }
     if constexpr (COL) {
+      if constexpr (!TILE && ROW) repack();
       float inv[8];
       if constexpr (TILE) {
 #pragma unroll
@@ -104,14 +109,14 @@ __global__ __launch_bounds__(QF_THREADS) void quant_fb_kernel(QuantFbParams p, i
         // over the wave's 4 row groups (lanes 16 and 32 apart), then the 8 waves
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const U32Pair a = permlane16_swap(cmax[k], cmax[k]);
-          const uint32_t m = umax(a.a, a.b);
-          const U32Pair c = permlane32_swap(m, m);
-          cmax[k] = umax(c.a, c.b);
-        }
-        if ((tid & 48) == 0) {
+          uint32_t m = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s_max[wave * FB + cl + k] = cmax[k];
+          for (int j = 0; j < 4; ++j) m = umax(m, __float_as_uint(val(j, k)) & 0x7fffffffu);
+          const U32Pair a = permlane16_swap(m, m);
+          m = umax(a.a, a.b);
+          const U32Pair c = permlane32_swap(m, m);
+          m = umax(c.a, c.b);
+          if ((tid & 48) == 0) s_max[wave * FB + cl + k] = m;
         }
         __syncthreads();
         if (tid < FB) {

@@ -186,22 +186,34 @@ __global__ __launch_bounds__(64 * W) void fb_stream_kernel(FbGemm p) {
   }
 }
 
+struct SwigluArgs {
+  int rows, F, E;
+  const float* prob;
+  const int32_t *map, *sizes, *offs;
+  uint8_t* codes;
+  float* scales;
+};
+
 // h = p silu(G) U of fp32 rows [G U], one block of 128 for 16 lanes, 8 columns each.  A launch of its own: with the
 // epilogue of the product above a workgroup would need all 256 weight rows of a block, and however its waves
 // share them it reads slower and fills fewer CUs (whole MLP, fused and not: 16 tokens, top-2 of 8 experts
 // 4096 x 14336 283 and 251 us; one token, 4096 x 4096 47 and 19 us).
-__global__ __launch_bounds__(256) void fb_swiglu_kernel(int rows, int F, const float* gu, const float* prob, const int32_t* map, uint8_t* codes,
-                                                        float* scales, int64_t ld) {
-  const int nb = (F + FB - 1) / FB;
+__global__ __launch_bounds__(256) void fb_swiglu_kernel(SwigluArgs p, const float* gu, int64_t ld) {
+  const int F = p.F, nb = (F + FB - 1) / FB;
   const int64_t blk = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
-  if (blk >= int64_t(rows) * nb) return;
+  if (blk >= int64_t(p.rows) * nb) return;
   const int r = int(blk / nb), b = int(blk - int64_t(r) * nb);
-  if (map && map[r] < 0) return;   // padding between the groups (the same for the 16 lanes)
+  if (p.map && p.map[r] < 0 && p.sizes) {   // (the same for the 16 lanes)
+    // without a token: padding between the groups, whose G U nobody wrote, or a group's row of zeros
+    bool mine = false;
+    for (int e = threadIdx.x & 15; e < p.E; e += 16) mine |= r >= p.offs[e] && r - p.offs[e] < p.sizes[e];
+    if (row16_umax(mine ? 1u : 0u) == 0) return;
+  }
   const int f = b * FB + (threadIdx.x & 15) * 8;
   const bool in = f < F;
   float h[8];
   uint32_t am = 0;
-  const float pr = prob ? prob[r] : 1.f;
+  const float pr = p.prob ? p.prob[r] : 1.f;
 #pragma unroll
   for (int i = 0; i < 8; i += 4) {
     float4 g = make_float4(0, 0, 0, 0), u = g;
@@ -218,16 +230,16 @@ __global__ __launch_bounds__(256) void fb_swiglu_kernel(int rows, int F, const f
   for (int i = 0; i < 8; ++i) am = umax(am, __float_as_uint(h[i]) & 0x7fffffffu);
   const FbScale sc = fb_scale(row16_umax(am));
   if (!in) return;
-  *reinterpret_cast<uint2*>(codes + int64_t(r) * F + f) =
+  *reinterpret_cast<uint2*>(p.codes + int64_t(r) * F + f) =
       make_uint2(e4m3x4(h[0] * sc.inv, h[1] * sc.inv, h[2] * sc.inv, h[3] * sc.inv),
                  e4m3x4(h[4] * sc.inv, h[5] * sc.inv, h[6] * sc.inv, h[7] * sc.inv));
-  if ((threadIdx.x & 15) == 0) scales[ld > 0 ? int64_t(b) * ld + r : int64_t(r) * nb + b] = sc.s;
+  if ((threadIdx.x & 15) == 0) p.scales[ld > 0 ? int64_t(b) * ld + r : int64_t(r) * nb + b] = sc.s;
 }
-mge_status launch_fb_swiglu(int rows, int F, const float* gu, const float* prob, const int32_t* map, uint8_t* codes, float* scales,
-                            int64_t ld, hipStream_t s) {
-  const int64_t blocks = int64_t(rows) * ((F + FB - 1) / FB);
+mge_status launch_fb_swiglu(const FbGemm& g, const float* gu, int64_t ld, hipStream_t s) {
+  const int64_t blocks = int64_t(g.rows) * ((g.F + FB - 1) / FB);
+  const SwigluArgs p{g.rows, g.F, g.E, g.prob, g.map, g.sizes, g.offs, g.h_codes, g.h_scales};
   ProfScope prof(s, "fp8_block_swiglu");
-  hipLaunchKernelGGL(fb_swiglu_kernel, dim3(unsigned((blocks + 15) / 16)), dim3(256), 0, s, rows, F, gu, prob, map, codes, scales, ld);
+  hipLaunchKernelGGL(fb_swiglu_kernel, dim3(unsigned((blocks + 15) / 16)), dim3(256), 0, s, p, gu, ld);
   return hip_check("fp8_block_swiglu");
 }
 

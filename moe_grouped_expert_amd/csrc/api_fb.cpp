@@ -68,7 +68,8 @@ static int64_t fb_total(const void* sizes, int64_t total, int64_t rows) { return
 // Few experts' pointers travel in the kernels' arguments, more through a table in the workspace
 static bool fb_table(int E) { return E > kFbInline; }
 
-static size_t fb_scales_t(int64_t rows, int K) { return up256(size_t(rows) * size_t(fb_blocks(K)) * 4); }
+// Scales by blocks of 128 (a wave reads 64 of a block's at a time, past the last ones too)
+static size_t fb_scales_t(int64_t rows, int64_t K) { return up256(size_t(rows) * size_t(fb_blocks(K)) * 4) + 256; }
 
 }  // namespace mge
 
@@ -248,8 +249,7 @@ size_t mge_wgrad_fb_workspace_bytes(const mge_wgrad_fb_args* a) {
   if (!a || a->struct_size != sizeof(mge_wgrad_fb_args) || a->E < 1 || a->E > 256 || a->N < 32 || a->K < 32 || a->rows < 0 ||
       a->rows >= kTwoGiB / std::max({a->N, a->K, kTileRows}))
     return 0;
-  const size_t nb = size_t(fb_blocks(a->rows));
-  return (fb_table(a->E) ? up256(size_t(a->E) * sizeof(void*)) : 0) + up256(nb * a->N * 4) + up256(nb * a->K * 4);
+  return (fb_table(a->E) ? up256(size_t(a->E) * sizeof(void*)) : 0) + fb_scales_t(a->N, a->rows) + fb_scales_t(a->K, a->rows);
 }
 
 mge_status fp8_block_grouped_wgrad(const mge_wgrad_fb_args* a, void* stream) {
@@ -292,8 +292,8 @@ mge_status fp8_block_grouped_wgrad(const mge_wgrad_fb_args* a, void* stream) {
     for (int e = 0; e < a->E; ++e) p.Dv[e] = a->dw[e];
   }
   const int nb = int(fb_blocks(a->rows));
-  float* yst = static_cast<float*>(ws.take(size_t(nb) * a->N * 4));
-  float* xst = static_cast<float*>(ws.take(size_t(nb) * a->K * 4));
+  float* yst = static_cast<float*>(ws.take(fb_scales_t(a->N, a->rows)));
+  float* xst = static_cast<float*>(ws.take(fb_scales_t(a->K, a->rows)));
   p.Yst = yst; p.Xst = xst;
   p.out = a->accumulate ? OUT_F32_ACC : (a->out_dtype == MGE_DTYPE_F32 ? OUT_F32 : OUT_BF16);
   const FbScaleT t[2] = {{a->dy_scale, nullptr, a->N, a->N, nb, yst, a->N}, {a->x_scale, nullptr, a->K, a->K, nb, xst, a->K}};

@@ -95,10 +95,10 @@ struct FtTile {
   int valid, e, off, m_valid, m0, n0, nkt, kbase, khi;
 };
 
-// What a tile's DMAs need
+// What a tile's DMAs need beside offsets that all tiles share
 struct FtOps {
   i32x4 rT, rW[2], rS;
-  uint32_t toff[4], woff[2], soff, s_ld, past0, past1;
+  uint32_t toff[4];   // C (the rows of A may be gathered)
 };
 
 // KR: dW (FbWgrad), else C (FbGemm).  SW: the SwiGLU epilogue.  TAIL: the tiles past the main launch's last
@@ -237,22 +237,36 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       }
     }
   };
+  // The lane's offsets hold its row and chunk, the slice's place in K is the same in all lanes.
+  uint32_t krow[4], woff[2];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) krow[i] = uint32_t(wave * (DT * 8) + i * 8 + (lane >> 3)) * ldw + (lchunk ^ ((i & 1) * 64));   // (dW: rows of dY)
+  woff[0] = uint32_t(wave * (DW * 8) + (lane >> 3)) * ldw + uint32_t(lchunk);
+  woff[1] = uint32_t(wave * (DW * 8) + 8 + (lane >> 3)) * ldw + uint32_t(lchunk ^ 64);
+  // Scales: the tokens' (dW: of dY), 64 a wave; in the other waves for dW those of X, for C in the first lanes those of
+  // the weights, of the tile's halves or with SwiGLU of the gate rows and of every 32 up rows.  (Lanes past the rows or
+  // the group read other rows' scales or zeros; what they scale is zero or not stored.)
+  const bool of_t = wave < SWV;
+  uint32_t s_ld, soff = uint32_t(lane) * 4;   // bytes of a slice; the lane's
+  if constexpr (KR) {
+    s_ld = uint32_t(of_t ? p.N : p.K) * 4;
+  } else {
+    s_ld = of_t ? uint32_t(p.ast_ld) * 4 : 4u;
+    const int blk = SW ? (lane == 0 ? 0 : (p.F + (lane - 1) * 32) / FB) : lane * HR / FB;
+    if (!of_t) soff = lane < (SW ? 5 : 2) ? uint32_t(blk * KB) * 4 : kInvalid;
+  }
   auto setup = [&](const FtTile& t, const int* src) {
     FtOps o;
     auto left = [](int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); };
     if constexpr (KR) {
       o.rT = make_rsrc_n(p.Y + int64_t(t.m0) * p.rows, uint32_t(left(p.N - t.m0, TL::NT)) * ldw);
 #pragma unroll
-      for (int i = 0; i < DT; ++i) o.toff[i] = uint32_t(wave * (DT * 8) + i * 8 + (lane >> 3)) * ldw + (lchunk ^ ((i & 1) * 64));
-#pragma unroll
       for (int h = 0; h < 2; ++h)
         o.rW[h] = make_rsrc_n(p.X + int64_t(t.n0 + HR * h) * p.rows, uint32_t(left(p.K - t.n0 - HR * h, HR)) * ldw);
-      const uint32_t nb = uint32_t((p.rows + 127) / 128);
-      const int n = wave < SWV ? p.N : p.K;
-      o.rS = make_rsrc_n(wave < SWV ? p.Yst : p.Xst, nb * uint32_t(n) * 4);
-      o.s_ld = uint32_t(n) * 4;
-      const int row = (wave < SWV ? t.m0 + wave * 64 : t.n0 + (wave - SWV) * 64) + lane;
-      o.soff = row < n ? uint32_t(t.kbase / 128) * o.s_ld + uint32_t(row) * 4 : kInvalid;
+      const int n = of_t ? p.N : p.K;
+      const int64_t at = int64_t(t.kbase / 128) * n + (of_t ? t.m0 + wave * 64 : t.n0 + (wave - SWV) * 64);
+      const int64_t all = int64_t((p.rows + 127) / 128) * n;
+      o.rS = make_rsrc_n((of_t ? p.Yst : p.Xst) + at, at < all ? uint32_t(all - at) * 4 : 0);
     } else {
       o.rT = make_rsrc_n(p.A, uint32_t(p.src_rows) * ldw);
 #pragma unroll
@@ -266,29 +280,10 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
         const int r0 = SW ? t.n0 : t.n0 + HR * h;          // (SwiGLU: gate, then up rows of the same columns)
         o.rW[h] = make_rsrc_n(w + (int64_t(r0) + (SW ? h * ncols : 0)) * p.K, uint32_t(left(nrows - r0, HR)) * ldw);
       }
-      // the tokens' scales, 64 a wave; in the other waves' first lanes those of the weights: of the tile's
-      // halves, or with SwiGLU of the gate rows and of every 32 up rows
-      const int all = SW ? 2 * ncols : p.N;
-      if (wave < SWV) {
-        o.rS = make_rsrc_n(p.Ast, uint32_t(KB) * uint32_t(p.ast_ld) * 4);
-        o.s_ld = uint32_t(p.ast_ld) * 4;
-        const int m = t.m0 + wave * 64 + lane;
-        o.soff = m < t.m_valid ? uint32_t(t.off + m) * 4 : kInvalid;
-      } else {
-        const int row = lane == 0 ? t.n0 : (SW ? ncols + t.n0 + (lane - 1) * 32 : t.n0 + HR);
-        o.rS = make_rsrc_n(ws, uint32_t((all + FB - 1) / FB) * uint32_t(KB) * 4);
-        o.s_ld = 4;
-        o.soff = lane < (SW ? 5 : 2) && row < all ? uint32_t(row / FB) * uint32_t(KB) * 4 : kInvalid;
-      }
+      const int64_t at = of_t ? int64_t(t.off) + t.m0 + wave * 64 : int64_t(t.n0 / FB) * KB;
+      const int64_t all = of_t ? int64_t(KB) * p.ast_ld : int64_t(((SW ? 2 * ncols : p.N) + FB - 1) / FB) * KB;
+      o.rS = make_rsrc_n((of_t ? p.Ast : ws) + at, at < all ? uint32_t(all - at) * 4 : 0);
     }
-    // The lane's offsets hold its row and chunk, the slice's place in K is the same in all lanes.  A slice
-    // past the last has a resource without records; in the last one, where it is not a whole 128 bytes, the
-    // chunks past its end get the top bit.  Both read zeros.
-    const int tail = (t.khi - t.kbase) & 127;      // bytes of the last slice, 0: whole
-    o.past0 = tail != 0 && lchunk >= tail ? kInvalid : 0u;
-    o.past1 = tail != 0 && (lchunk ^ 64) >= tail ? kInvalid : 0u;
-    o.woff[0] = uint32_t(wave * (DW * 8) + (lane >> 3)) * ldw + uint32_t(lchunk);
-    o.woff[1] = uint32_t(wave * (DW * 8) + 8 + (lane >> 3)) * ldw + uint32_t(lchunk ^ 64);
     return o;
   };
   // (a wave's first LDS row is a multiple of 16, so that its even and odd instructions are those of the swizzle)
@@ -300,22 +295,30 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   };
   // (no offset beside a resource without records, so that no form of the range check takes one from the other)
   auto place = [](const i32x4& r, uint32_t k) { return r[2] != 0 ? k : 0u; };
-  auto off_at = [&](const FtOps& o, const FtTile& t, uint32_t off, int kt, int odd) {
-    return ((odd ? o.past1 : o.past0) & (KG * kt + kg == t.nkt - 1 ? kInvalid : 0u)) | off;
+  // A slice past the last has a resource without records; in the last one, where it is not a whole 128 bytes, the
+  // chunks past its end get the top bit.  Both read zeros.
+  auto off_at = [&](const FtTile& t, uint32_t off, int kt, int odd) {
+    const int tail = (t.khi - t.kbase) & 127;      // bytes of the last slice, 0: whole
+    const int end = tail != 0 && KG * kt + kg == t.nkt - 1 ? tail : 128;
+    return (lchunk ^ (odd * 64)) < end ? off : kInvalid;
   };
+  // AHEAD: the last NST slices of a tile bring the first NST of the next one, so that operands arrive without a
+  // pause; the stages are taken in turn over all tiles (gd: slices before those of the tile that is brought in).
+  constexpr bool AHEAD = KR && KG == 1;
+  int gd = 0;
   auto dma_t = [&](const FtOps& o, const FtTile& t, int kt, int i) {
     const i32x4 r = at_slice(o.rT, t, kt);
-    dma16s(r, lds_base + (kt & (NST - 1)) * TL::STAGE + (wave * (DT * 8) + i * 8) * 128, off_at(o, t, o.toff[i], kt, i & 1),
+    dma16s(r, lds_base + ((gd + kt) & (NST - 1)) * TL::STAGE + (wave * (DT * 8) + i * 8) * 128, off_at(t, KR ? krow[i] : o.toff[i], kt, i & 1),
            place(r, uint32_t(t.kbase + (KG * kt + kg) * 128)));
   };
   auto dma_w = [&](const FtOps& o, const FtTile& t, int kt, int h, int i) {
     const i32x4 r = at_slice(o.rW[h], t, kt);
-    dma16s(r, lds_base + (kt & (NST - 1)) * TL::STAGE + TL::OPT + (h * HR + wave * (DW * 8) + i * 8) * 128,
-           off_at(o, t, o.woff[i], kt, i), place(r, uint32_t(t.kbase + (KG * kt + kg) * 128)));
+    dma16s(r, lds_base + ((gd + kt) & (NST - 1)) * TL::STAGE + TL::OPT + (h * HR + wave * (DW * 8) + i * 8) * 128,
+           off_at(t, woff[i], kt, i), place(r, uint32_t(t.kbase + (KG * kt + kg) * 128)));
   };
   auto dma_s = [&](const FtOps& o, const FtTile& t, int kt) {
     const i32x4 r = at_slice(o.rS, t, kt);
-    dma4(r, lds_base + TL::SCALES + (kt & (2 * NST - 1)) * TL::RING + wave * 256, o.soff, place(r, uint32_t(KG * kt + kg) * o.s_ld));
+    dma4(r, lds_base + TL::SCALES + ((gd + kt) & (2 * NST - 1)) * TL::RING + wave * 256, soff, place(r, uint32_t(KG * kt + kg) * s_ld));
   };
   // The early part of a slice (its tokens, scales and the first half of the weight rows) and the late one
   constexpr int EARLY = 1 + DT + DW, LATE = DW;
@@ -345,6 +348,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   FtTile t = decode(vid);
   FtOps o{};
   int stores = 0;   // 1: the wave has stores in flight that are newer than this tile's first DMAs
+  bool ahead = false;   // the tile's first slices came with the tile before
   int src[DT];
   rows_of(t, src);
   if (t.valid) {
@@ -383,7 +387,9 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       //   before the last step (which reads the early part of kt + 1)   the late part is free
       constexpr int BP = H - 1, BQ = RB - 1;
       constexpr int FLY = (NST - 1) * (EARLY + LATE);   // DMAs newer than the part waited for, at both
-      vm_barrier_if<FLY + LATE + STORES, FLY + LATE>(stores);   // the early part of slice 0 is resident
+      // the early part of slice 0 is resident (ahead: since the last barrier of the tile before)
+      if (!AHEAD || !ahead) vm_barrier_if<FLY + LATE + STORES, FLY + LATE>(stores);
+      const int g0 = gd;
       // (the two chunks of a fragment are 64 bytes apart in the row, either way round: a base each, so that the
       // rows' distances fit the instructions' offsets)
       auto frag = [&](const uint8_t* p0, const uint8_t* p1, int at) {
@@ -391,25 +397,31 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
         const uint4 b = *reinterpret_cast<const uint4*>(p1 + at);
         return i32x8{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
       };
-      auto scales_of = [&](int kt) { return reinterpret_cast<const float*>(gmem + TL::SCALES + (kt & (2 * NST - 1)) * TL::RING); };
+      auto scales_of = [&](int kt) { return reinterpret_cast<const float*>(gmem + TL::SCALES + ((g0 + kt) & (2 * NST - 1)) * TL::RING); };
       constexpr int RS = SWV * 64;        // the row operand's scales in a slice's ring entry
+      const int s0 = (g0 & (NST - 1)) * TL::STAGE;
       i32x8 tf[TB], wf[2];
       float ts[TB], tn[TB], sc[TB];       // token scales, those of the next slice, times the weights'
       f32x4 d[2][TB], xs[2];
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) {
-        tf[tb] = frag(gmem + tread, gmem + (tread ^ 64), tb * 2048);
+        tf[tb] = frag(gmem + s0 + tread, gmem + s0 + (tread ^ 64), tb * 2048);
         tn[tb] = scales_of(0)[wt * (TB * 16) + tb * 16 + i16];
         ts[tb] = sc[tb] = 0.f;
         d[1][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
       xs[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      wf[0] = frag(gmem + wread, gmem + (wread ^ 64), TL::OPT);
-      const int nit = KG == 1 ? t.nkt : (t.nkt + KG - 1) / KG;
+      wf[0] = frag(gmem + s0 + wread, gmem + s0 + (wread ^ 64), TL::OPT);
+      // (AHEAD: at least NST slices, those past the end are zeros)
+      const int nit = AHEAD ? max(t.nkt, NST) : (t.nkt + KG - 1) / KG;
       int fresh = stores ? NST : 0;       // slices whose parts are older than the stores
+      FtTile in = t;                      // the tile that is brought in, and its slice beside slice kt: kt + di
+      int kt = 0, di = NST;
 #pragma clang loop unroll(disable)
-      for (int kt = 0; kt < nit; ++kt) {
-        const int st = (kt & (NST - 1)) * TL::STAGE, sn = ((kt + 1) & (NST - 1)) * TL::STAGE;   // this slice's stage, the next one's
+      for (int end = AHEAD ? nit - NST : nit;; end = nit) {
+#pragma clang loop unroll(disable)
+      for (; kt < end; ++kt) {
+        const int st = ((g0 + kt) & (NST - 1)) * TL::STAGE, sn = ((g0 + kt + 1) & (NST - 1)) * TL::STAGE;   // this slice's stage, the next one's
         const uint8_t *w0 = gmem + st + wread, *w1 = gmem + st + (wread ^ 64);
         const float* sS = scales_of(kt) + RS;
         static_for<0, RB>([&](auto rbc) {
@@ -417,7 +429,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
           constexpr int pb = (rb + RB - 1) % RB;   // the block whose sums are added
           if constexpr (rb == BP) {
             vm_barrier_if<FLY + STORES, FLY>(fresh);
-            dma_s(o, t, kt + NST);
+            dma_s(o, in, kt + di);
           }
           if constexpr (rb == BQ) {
             --fresh;
@@ -452,11 +464,11 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
             if constexpr (rb >= BP && rb < BQ) {
               constexpr int n = (BQ - BP) * TB, i = (rb - BP) * TB + tb, k0 = (DT + DW) * i / n, k1 = (DT + DW) * (i + 1) / n;
               if constexpr (k1 > k0) {
-                if constexpr (k0 < DT) dma_t(o, t, kt + NST, k0);
-                else dma_w(o, t, kt + NST, 0, k0 - DT);
+                if constexpr (k0 < DT) dma_t(o, in, kt + di, k0);
+                else dma_w(o, in, kt + di, 0, k0 - DT);
               }
             }
-            if constexpr (rb == BQ && tb < DW) dma_w(o, t, kt + NST, 1, tb);
+            if constexpr (rb == BQ && tb < DW) dma_w(o, in, kt + di, 1, tb);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               if constexpr (KR) acc[pb][tb][r] = fmaf(d[(rb + 1) & 1][tb][r] * ts[tb], xs[(rb + 1) & 1][r], acc[pb][tb][r]);
@@ -467,6 +479,12 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
           static_assert((BQ - BP) * TB >= DT + DW && TB >= DW, "a part is issued before the next barrier");
         });
       }
+        if (end == nit) break;
+        o = setup(nxt, src);
+        in = nxt;
+        gd = g0 + nit;
+        di = NST - nit;
+      }
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
@@ -476,10 +494,13 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
         }
     }
     const FtTile cur = t;
-    __builtin_amdgcn_s_waitcnt(0);      // the slices past the end (zeros) have landed
     t = nxt;
-    if (t.valid) o = setup(t, src);
-    lds_barrier();                      // every wave is done with the stages
+    ahead = AHEAD && cur.nkt > 0 && t.nkt > 0;
+    if (!ahead) {
+      __builtin_amdgcn_s_waitcnt(0);    // the slices past the end (zeros) have landed
+      if (t.valid) o = setup(t, src);
+      lds_barrier();                    // every wave is done with the stages
+    }
     if constexpr (KG > 1) {
       // the second group's sums through LDS (16 bytes a lane and block, whole wave after wave)
       static_assert(KG == 2 && TL::WAVES * 64 * RB * TB * 16 <= TL::LDS, "sums of a group");
@@ -499,7 +520,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       }
       lds_barrier();
     }
-    if (t.valid && t.nkt > 0) prologue(o, t);
+    if (!ahead && t.valid && t.nkt > 0) prologue(o, t);
     if (KG > 1 && kg > 0) continue;     // (no stores)
     stores = STORES > 0 ? 1 : 0;
     rederive_lane();

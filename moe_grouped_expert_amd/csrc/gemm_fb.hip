@@ -402,6 +402,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       const int s0 = (g0 & (NST - 1)) * TL::STAGE;
       i32x8 tf[TB], wf[2];
       float ts[TB], tn[TB], sc[TB];       // token scales, those of the next slice, times the weights'
+      float ws = 0.f;
       f32x4 d[2][TB], xs[2];
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) {
@@ -442,15 +443,17 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) ts[tb] = tn[tb];
           }
-          // the scales of the sums that this step adds (SwiGLU: an up half's rows are in one or two scales' rows)
-          if constexpr (!KR && (rb == 1 || rb == H + 1 || (SW && rb > H && (rb - 1 - H) * 16 % 32 == 0))) {
-            const float w = sS[rb == 1 ? 0 : (SW ? 1 + (wn * H + rb - 1 - H) / 2 : 1)];
+          // the scales of the sums that this step adds (SwiGLU: an up half's rows are in one or two scales' rows), the
+          // weights' read a step before
+          constexpr auto fresh_scale = [](int b) { return b == 1 || b == H + 1 || (SW && b > H && (b - 1 - H) * 16 % 32 == 0); };
+          if constexpr (!KR && fresh_scale(rb)) {
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) {
               if constexpr (rb == 1) ts[tb] = tn[tb];
-              sc[tb] = ts[tb] * w;
+              sc[tb] = ts[tb] * ws;
             }
           }
+          if constexpr (!KR && fresh_scale(rb + 1)) ws = sS[rb == 0 ? 0 : (SW ? 1 + (wn * H + rb - H) / 2 : 1)];
           __builtin_amdgcn_sched_barrier(0);
           static_for<0, TB>([&](auto tbc) {
             constexpr int tb = decltype(tbc)::value;

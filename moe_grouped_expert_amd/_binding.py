@@ -1032,6 +1032,11 @@ def _like(t, shape, dtype, what: str):
         raise ValueError(f"{what} must be contiguous {dtype} {list(shape)}")
 
 
+def _new_like(x, dtype):
+    """A new contiguous tensor of x's shape (empty_like is the quickest way there is, where it gives that)."""
+    return torch.empty_like(x, dtype=dtype) if x.is_contiguous() else x.new_empty(x.shape, dtype=dtype)
+
+
 def _fblocks(n: int) -> int:
     return (n + 127) // 128
 
@@ -1060,10 +1065,10 @@ def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     if out is None:
         _need(want_y or form is not None, "no output asked for (want_y or form)")
         f32 = torch.float32
-        out = RmsnormOut(y=x.new_empty(x.shape, dtype=ydt) if want_y else None,
-                         residual=None if residual is None else x.new_empty(x.shape), rstd=x.new_empty(lead, dtype=f32))
+        out = RmsnormOut(y=_new_like(x, ydt) if want_y else None,
+                         residual=None if residual is None else _new_like(x, x.dtype), rstd=x.new_empty(lead, dtype=f32))
         if form is not None:
-            out.codes, out.scales = x.new_empty(x.shape, dtype=torch.uint8), x.new_empty(lead + (_fblocks(H),), dtype=f32)
+            out.codes, out.scales = _new_like(x, torch.uint8), x.new_empty(lead + (_fblocks(H),), dtype=f32)
     else:
         _on(dev, out.y, out.codes, out.scales, out.residual, out.rstd)
         _need((residual is None) == (out.residual is None), "out.residual goes with residual")
@@ -1095,7 +1100,7 @@ def rmsnorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: t
     if d_residual is not None:
         _like(d_residual, x.shape, x.dtype, "d_residual")
     if out is None:
-        dx, dw = x.new_empty(x.shape), x.new_empty(H, dtype=torch.float32) if want_dw else None
+        dx, dw = _new_like(x, x.dtype), x.new_empty(H, dtype=torch.float32) if want_dw else None
     else:
         dx, dw = out
         _on(dev, dx, dw)
@@ -1184,7 +1189,7 @@ def fp8_block_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype: s
     dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
     _on(dev, scales, out)
     if out is None:
-        out = codes.new_empty(codes.shape, dtype=dt)
+        out = _new_like(codes, dt)
     else:
         _like(out, codes.shape, dt, "out")
     batch = 1

@@ -69,7 +69,10 @@ static int64_t fb_total(const void* sizes, int64_t total, int64_t rows) { return
 static bool fb_table(int E) { return E > kFbInline; }
 
 // Scales by blocks of 128 (a wave reads 64 of a block's at a time, past the last ones too)
-static size_t fb_scales_t(int64_t rows, int64_t K) { return up256(size_t(rows) * size_t(fb_blocks(K)) * 4) + 256; }
+static size_t fb_scales_t(int64_t rows, int64_t K) {
+  const size_t n = size_t(rows) * size_t(fb_blocks(K)) * 4;
+  return n ? up256(n) + 256 : 0;
+}
 
 }  // namespace mge
 

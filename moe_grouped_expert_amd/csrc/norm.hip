@@ -7,9 +7,11 @@
 //   dx = rstd (g - xhat mean(g xhat)) + d_residual,  dw = sum over the rows of dy xhat
 // Everything in between is fp32; y, the codes and dx are rounded once from it.
 //
-// Both are one pass over HBM.  A row stays in the registers of NT threads (64: a wave, no barrier;
-// 256: a workgroup), 8 consecutive values a thread and step, so that 16 neighbouring lanes hold one
-// block of 128 and its scale is a maximum over a DPP row.
+// Both are one pass over HBM, which bounds them.  A row stays in the registers of NT threads (64: a wave, no
+// barrier; 256, 512: a workgroup), 8 consecutive values a thread and step, so that 16 neighbouring lanes hold one
+// block of 128 and its scale is a maximum over a DPP row.  Measured on MI355X: forward of 16384 x 4096 bf16 with a
+// residual, bf16 and 8-bit output 118 us (4.9 TB/s, a copy's rate is 5.1), of 8 rows 3 us; backward of 16384 x 4096
+// with a residual's gradient 95 us, of 2048 x 16384 45 us.
 #include "mge_common.hpp"
 
 #include "fp8b.hpp"
@@ -72,7 +74,7 @@ __device__ __forceinline__ void get8(const void* p, int64_t i, int f32, float* f
   }
 }
 
-// Sum of v over the NT threads of a row; slot: LDS of 4 floats per use (NT = 256)
+// Sum of v over the NT threads of a row; slot: LDS of NT / 64 floats (of the row's workgroup)
 template <int NT>
 __device__ __forceinline__ float row_sum(float v, float* slot) {
   v = wave_sum64(v);
@@ -80,15 +82,20 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
   if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
   __syncthreads();
   const float4 q = *reinterpret_cast<const float4*>(slot);
-  return (q.x + q.y) + (q.z + q.w);
+  v = (q.x + q.y) + (q.z + q.w);
+  if constexpr (NT == 512) {
+    const float4 u = *reinterpret_cast<const float4*>(slot + 4);
+    v += (u.x + u.y) + (u.z + u.w);
+  }
+  return v;
 }
 
-constexpr int kNormThreads = 256;
+constexpr int norm_threads(int nt) { return nt > 256 ? nt : 256; }
 
 template <bool F32, int NT, int NV>
-__global__ __launch_bounds__(kNormThreads) void rmsnorm_kernel(NormParams p) {
-  __shared__ __attribute__((aligned(16))) float s_part[2][4];
-  constexpr int RPW = kNormThreads / NT;   // rows of a workgroup at a time
+__global__ __launch_bounds__(norm_threads(NT)) void rmsnorm_kernel(NormParams p) {
+  __shared__ __attribute__((aligned(16))) float s_part[2][NT == 512 ? 8 : 4];
+  constexpr int RPW = norm_threads(NT) / NT;   // rows of a workgroup at a time
   const int t = threadIdx.x % NT;
   const int chunks = p.H / 8;
   const int kb = (p.H + FB - 1) / FB;
@@ -172,9 +179,9 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_kernel(NormParams p) {
 // accumulates in registers; the workgroups' shares (in `part`) are summed by rmsnorm_dw_kernel in
 // their order.  The next row's x and dy are on their way while a row is reduced.
 template <bool F32, int NT, int NV>
-__global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams p) {
-  constexpr int RPW = kNormThreads / NT;
-  __shared__ __attribute__((aligned(16))) float s_part[2][4];
+__global__ __launch_bounds__(norm_threads(NT)) void rmsnorm_bwd_kernel(NormBwdParams p) {
+  constexpr int RPW = norm_threads(NT) / NT;
+  __shared__ __attribute__((aligned(16))) float s_part[2][NT == 512 ? 8 : 4];
   const int t = threadIdx.x % NT;
   const int chunks = p.H / 8;
   const float inv_h = 1.f / float(p.H);
@@ -204,10 +211,12 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams
   };
   int par = 0;
   const int64_t step = int64_t(gridDim.x) * RPW;
-  fetch(int64_t(blockIdx.x) * RPW + threadIdx.x / NT);
+  constexpr bool NEXT = NT < 512 || NV < 4;   // (the longest rows leave no registers for it)
+  if constexpr (NEXT) fetch(int64_t(blockIdx.x) * RPW + threadIdx.x / NT);
   for (int64_t row0 = int64_t(blockIdx.x) * RPW; row0 < p.T; row0 += step) {
     const int64_t row = row0 + threadIdx.x / NT;
     const bool live = row < p.T;
+    if constexpr (!NEXT) fetch(row);
     float xh[NV][8], g[NV][8];
     const float rs = rstd;
 #pragma unroll
@@ -228,7 +237,7 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams
       res[i].zero();
       if (p.d_res && live && c < chunks) res[i].load(p.d_res, row * p.H + c * 8);
     }
-    fetch(row + step);
+    if constexpr (NEXT) fetch(row + step);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -321,26 +330,25 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* part, int
   if (k == 0 && c * 4 < H) *reinterpret_cast<float4*>(dw + c * 4) = a;
 }
 
-// A wave a row where a row fits its registers and there are rows for every CU, else a workgroup
-static bool wave_rows(int64_t T, int H) { return H <= 64 * 8 * 8 && (T >= 2048 || H <= 512); }
-constexpr int kNormGrid = 2048;   // workgroups of a launch at most (8 for each of 256 CUs)
+// A wave a row for short rows, else a workgroup (us, a wave and a workgroup a row, bf16 with a residual and 8-bit
+// output: 8192 x 512 7.7, 14.6; 8192 x 1024 13.8, 16.5; 1024 x 1024 4.1, 4.4; 16 x 1024 3.4, 2.9; 8192 x 2048 24.5,
+// 24.2; 16384 x 4096 122, 118; 256 x 4096 8.1, 4.3).
+static bool wave_rows(int64_t T, int H) { return H <= 512 || (H <= 1024 && T >= 1024); }
+// Workgroups of a launch at most, 8 for each CU (16384 x 4096: 512 workgroups 126 us, 2048 120, 16384 122)
+constexpr int kNormGrid = 2048;
 
 template <bool F32, int NT, int NV>
 static mge_status launch_fwd(const NormParams& p, hipStream_t s) {
-  const int64_t n = (p.T * NT + kNormThreads - 1) / kNormThreads;
+  constexpr int threads = norm_threads(NT);
+  const int64_t n = (p.T * NT + threads - 1) / threads;
   ProfScope prof(s, "rmsnorm_fwd");
-  hipLaunchKernelGGL((rmsnorm_kernel<F32, NT, NV>), dim3(unsigned(n < kNormGrid ? n : kNormGrid)), dim3(kNormThreads), 0, s, p);
+  hipLaunchKernelGGL((rmsnorm_kernel<F32, NT, NV>), dim3(unsigned(n < kNormGrid ? n : kNormGrid)), dim3(threads), 0, s, p);
   return hip_check("rmsnorm_fwd");
 }
 template <bool F32>
 static mge_status fwd_by_size(const NormParams& p, hipStream_t s) {
   const int ch = p.H / 8;
-  if (wave_rows(p.T, p.H)) {
-    if (ch <= 64) return launch_fwd<F32, 64, 1>(p, s);
-    if (ch <= 128) return launch_fwd<F32, 64, 2>(p, s);
-    if (ch <= 256) return launch_fwd<F32, 64, 4>(p, s);
-    return launch_fwd<F32, 64, 8>(p, s);
-  }
+  if (wave_rows(p.T, p.H)) return ch <= 64 ? launch_fwd<F32, 64, 1>(p, s) : launch_fwd<F32, 64, 2>(p, s);
   if (ch <= 256) return launch_fwd<F32, 256, 1>(p, s);
   if (ch <= 512) return launch_fwd<F32, 256, 2>(p, s);
   if (ch <= 1024) return launch_fwd<F32, 256, 4>(p, s);
@@ -350,11 +358,18 @@ mge_status launch_rmsnorm(const NormParams& p, bool x_f32, hipStream_t s) {
   return x_f32 ? fwd_by_size<true>(p, s) : fwd_by_size<false>(p, s);
 }
 
-// (the backward keeps a row's xhat, g and dw: a wave has the registers for 1024 values)
-static bool wave_rows_bwd(int64_t T, int H) { return H <= 1024 && (T >= 2048 || H <= 512); }
+// The backward, in the same way (8192 x 512 10.1, 18.8; 8192 x 1024 16.7, 22.2; 1024 x 1024 7.3, 8.3; 256 x 1024 6.1,
+// 6.0).  It keeps a row's xhat and g, the next row and dw: about 17 registers a value and thread, so that longer rows go
+// to 512 threads before they would spill.
+static bool wave_rows_bwd(int64_t T, int H) { return H <= 512 || (H <= 1024 && T >= 1024); }
+// As many workgroups as the 256 CUs hold at once (bf16, 8192 x 4096: 512 workgroups 46 us, 768 39, 1024 48; 2048 x 8192:
+// 512 31, 768 35; 8192 x 2048: 512 26.3, 1280 25.7; fp32 8192 x 4096: 512 74, 768 79); of the shortest rows fewer, since
+// each costs a share of dw (8192 x 512: 512 10.0, 1280 12.5)
 int rmsnorm_bwd_parts(int64_t T, int H) {
-  const int64_t n = wave_rows_bwd(T, H) ? (T + 3) / 4 : T;
-  return int(n < 512 ? n : 512);
+  const bool wave = wave_rows_bwd(T, H);
+  const int64_t n = wave ? (T + 3) / 4 : T;
+  const int most = H <= 512 ? 512 : (H <= 2048 && !wave ? 1280 : (H <= 4096 ? 768 : (H <= 8192 ? 512 : 256)));
+  return int(n < most ? n : most);
 }
 template <bool F32, int NT, int NV>
 static mge_status launch_bwd(const NormBwdParams& p, hipStream_t s) {
@@ -362,7 +377,7 @@ static mge_status launch_bwd(const NormBwdParams& p, hipStream_t s) {
   const int lds = NT == 64 && p.dw ? 3 * p.H * 4 : 0;
   {
     ProfScope prof(s, "rmsnorm_bwd");
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<F32, NT, NV>), dim3(unsigned(n)), dim3(kNormThreads), lds, s, p);
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<F32, NT, NV>), dim3(unsigned(n)), dim3(norm_threads(NT)), lds, s, p);
   }
   mge_status st = hip_check("rmsnorm_bwd");
   if (st != MGE_OK || !p.dw) return st;
@@ -381,8 +396,8 @@ static mge_status bwd_by_size(const NormBwdParams& p, hipStream_t s) {
   if (wave_rows_bwd(p.T, p.H)) return ch <= 64 ? launch_bwd<F32, 64, 1>(p, s) : launch_bwd<F32, 64, 2>(p, s);
   if (ch <= 256) return launch_bwd<F32, 256, 1>(p, s);
   if (ch <= 512) return launch_bwd<F32, 256, 2>(p, s);
-  if (ch <= 1024) return launch_bwd<F32, 256, 4>(p, s);
-  return launch_bwd<F32, 256, 8>(p, s);
+  if (ch <= 1024) return launch_bwd<F32, F32 ? 512 : 256, F32 ? 2 : 4>(p, s);
+  return launch_bwd<F32, 512, 4>(p, s);
 }
 mge_status launch_rmsnorm_bwd(const NormBwdParams& p, bool x_f32, hipStream_t s) {
   return x_f32 ? bwd_by_size<true>(p, s) : bwd_by_size<false>(p, s);

@@ -15,7 +15,20 @@
 // Operands come HBM -> LDS directly in slices of 128 bytes, two stages of 64 KB.  The tokens' fragments
 // of a slice (32 registers) are read first and the weights' streamed behind the matrix instructions, so
 // the tokens' half of a stage and the first half of the weights' are free at mid-slice and refilled from
-// there on (one and a half slices to arrive), the rest at the slice's end.
+// there on (one and a half slices to arrive), the rest at the slice's end.  The next tile's first slices
+// are issued before the epilogue (C) or with the last slices of the tile (dW).
+//
+// What bounds it, on MI355X: a slice of a CU takes 1.8 us (C; 2.4 PFLOP/s) and 1.9 - 2.1 us (dW), where the
+// matrix unit needs 1.1 at the 1.7 - 1.9 GHz that the power leaves.  An f8 instruction holds the vector unit's
+// port for 16 of its 32 cycles (its 16 operand registers), which leaves room for 4 additions; dW's second
+// multiply makes a step 50 cycles.  Without the operands' arrival a slice takes 1.6 and 1.5 us, so a CU's
+// intake (33 - 36 bytes a ns) is the rest.  A tile's start and epilogue, 600 vector instructions a wave, is 3 - 5 us.
+// Measured: 8191 uneven rows over 8 x [4096][14336] 475 us (2.0 PFLOP/s), its weight gradient in bf16 620 us,
+// the gate-up product with SwiGLU of 16384 rows over 8 x [28672][4096] 1.8 ms (2.1 PFLOP/s).
+//
+// C's tiles past the last whole round of the CUs run as quadrants of 128 x 128, whose 8 waves are two groups
+// that take the slices in turn and add their sums at the end: 64 tiles left of 8191 rows take 100 us that way,
+// one 256 x 256 tile more 200.
 #include "gemm_impl.hpp"
 
 #include "fp8b.hpp"

@@ -142,3 +142,52 @@ def test_extreme_sizes_of_the_norm(m, T, H):
     assert dx.shape == (T, H) and dw.shape == (H,)
     if T == 0:
         assert not dw.any()
+
+
+def test_nothing_to_read(m):
+    """Rows that a map sends to an operand without rows are zeros; a gated MLP of no tokens does nothing."""
+    dev = "cuda"
+    w, w_s = torch.full((2, 96, 160), 56, dtype=torch.uint8, device=dev), torch.ones(2, 1, 2, device=dev)
+    none, none_s = torch.empty(0, 160, dtype=torch.uint8, device=dev), torch.empty(0, 2, device=dev)
+    for sizes in ([3, 4], [300, 200]):
+        n = sum(sizes)
+        rows = gpu(np.arange(n), np.int32)
+        got = m.fp8_block_grouped_gemm(none, none_s, w, w_s, gpu(sizes, np.int32), gpu([0, sizes[0]], np.int32), rows, out_dtype="f32")
+        assert got.shape == (n, 96) and not got.any()
+    wd, wd_s = torch.full((1, 160, 96), 56, dtype=torch.uint8, device=dev), torch.ones(1, 2, 1, device=dev)
+    wg, wg_s = torch.full((1, 192, 160), 56, dtype=torch.uint8, device=dev), torch.ones(1, 2, 2, device=dev)
+    assert m.grouped_mlp_fwd_fp8_block(None, none, none_s, wg, wd, wg_s, wd_s).y_perm.shape == (0, 160)
+
+
+def test_two_graphs_and_eager_calls_between(m):
+    """Two captured graphs and eager calls of other sizes share no workspace: every replay gives the eager bits."""
+    rng = np.random.default_rng(41)
+    w, w_s, _ = zip(*(operand(rng, 288, 416, False, True) for _ in range(3)))
+    w, w_s = gpu(np.stack(w)), gpu(np.stack(w_s))
+    calls = []
+    for n in (9, 500):
+        a, a_s, _ = operand(rng, n, 416, False)
+        sizes = [n // 2, 0, n - n // 2]
+        calls.append((gpu(a), gpu(a_s), w, w_s, gpu(sizes, np.int32), gpu(np.cumsum([0] + sizes[:2]), np.int32)))
+    ref = [m.fp8_block_grouped_gemm(*c) for c in calls]
+    x, nw = torch.randn(700, 416, device="cuda").to(torch.bfloat16), torch.randn(416, device="cuda")
+    rs = m.rmsnorm_fwd(x, nw).rstd
+    grad = m.rmsnorm_bwd(x, x, nw, rs, x)
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((m.fp8_block_grouped_gemm(*c), *m.rmsnorm_bwd(x, x, nw, rs, x)))
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        for g in graphs:
+            g.replay()
+        again = [m.fp8_block_grouped_gemm(*c) for c in calls]
+        torch.cuda.synchronize()
+        for o, r, e in zip(outs, ref, again):
+            assert torch.equal(o[0], r) and torch.equal(e, r)
+            assert torch.equal(o[1], grad[0]) and torch.equal(o[2], grad[1])
+    graphs.clear()

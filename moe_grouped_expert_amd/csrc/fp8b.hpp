@@ -25,6 +25,12 @@ __device__ __forceinline__ FbScale fb_scale(uint32_t bits) {
   const bool fin = bits < 0x7f800000u;
   return FbScale{fin ? m / 448.f : __uint_as_float(0x7fc00000u), fin ? 448.f / m : 0.f};
 }
+// Codes of four values of a block times its factor.  Such a product is at most 448 (1 + 2^-23), which rounds to E4M3's
+// largest value: no clamp.  (In a block with an infinity or NaN they have no meaning.)
+__device__ __forceinline__ uint32_t fb_codes4(float a, float b, float c, float d) {
+  const int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, __float_as_int(a), false);
+  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
+}
 // max of the bit patterns over the 16 lanes of a DPP row (every lane gets it)
 __device__ __forceinline__ uint32_t row16_umax(uint32_t v) {
   v = umax(v, dpp_u<0xB1>(v));    // lane ^ 1

@@ -640,7 +640,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const f32x4 x = acc[j % H][tb];
-          v[j] = e4m3x4(x[0] * sc.inv, x[1] * sc.inv, x[2] * sc.inv, x[3] * sc.inv);
+          v[j] = fb_codes4(x[0] * sc.inv, x[1] * sc.inv, x[2] * sc.inv, x[3] * sc.inv);
         }
         transpose4(v);
         const int c = c0 + (q % H) * 16;

@@ -166,8 +166,8 @@ __global__ __launch_bounds__(norm_threads(NT)) void rmsnorm_kernel(NormParams p)
         const FbScale sc = fb_scale(row16_umax(m));
         if (in) {
           *reinterpret_cast<uint2*>(p.codes + row * p.H + c * 8) =
-              make_uint2(e4m3x4(y[0] * sc.inv, y[1] * sc.inv, y[2] * sc.inv, y[3] * sc.inv),
-                         e4m3x4(y[4] * sc.inv, y[5] * sc.inv, y[6] * sc.inv, y[7] * sc.inv));
+              make_uint2(fb_codes4(y[0] * sc.inv, y[1] * sc.inv, y[2] * sc.inv, y[3] * sc.inv),
+                         fb_codes4(y[4] * sc.inv, y[5] * sc.inv, y[6] * sc.inv, y[7] * sc.inv));
           if ((t & 15) == 0) p.scales[row * kb + c / 16] = sc.s;
         }
       }

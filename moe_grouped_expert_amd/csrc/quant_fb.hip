@@ -17,10 +17,19 @@ namespace mge {
 constexpr int QF_LD = 132;   // bytes of a column in LDS: a dword of skew spreads the dword writes over the banks
 
 constexpr int QF_THREADS = 512;
+
+// larger of each 16-bit half; magnitudes of two bf16 values in that form; the larger half as the bits of an fp32 value
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ uint32_t pk_abs(uint32_t v) { return v & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t pk_fold(uint32_t v) { return umax(v << 16, v & 0xffff0000u); }
+
 template <bool TILE, bool ROW, bool COL>
 __global__ __launch_bounds__(QF_THREADS, 8) void quant_fb_kernel(QuantFbParams p, int64_t tiles, int nr, int nc) {
   __shared__ __attribute__((aligned(16))) uint8_t s_col[COL ? FB * QF_LD : 4];
-  __shared__ uint32_t s_max[TILE ? 8 : (COL ? 8 * FB : 1)];
+  __shared__ __attribute__((aligned(16))) uint32_t s_max[TILE ? 8 : (COL ? 8 * FB / 2 : 4)];   // (columns: 16 bits each)
   __shared__ float s_inv[!TILE && COL ? FB : 1];
   const int tid = threadIdx.x, wave = tid >> 6;
   const int cl = (tid & 15) * 8;         // first of the thread's 8 columns
@@ -56,13 +65,8 @@ __global__ __launch_bounds__(QF_THREADS, 8) void quant_fb_kernel(QuantFbParams p
       const uint32_t w = k < 4 ? (k < 2 ? x[j].x : x[j].y) : (k < 6 ? x[j].z : x[j].w);
       return __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
     };
-    // largest magnitudes, as bit patterns
-    auto row_max = [&](int j) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) m = umax(m, __float_as_uint(val(j, k)) & 0x7fffffffu);
-      return m;
-    };
+    // largest magnitudes, as bit patterns, two values at a time
+    auto row_max = [&](int j) { return pk_fold(pk_max(pk_max(pk_abs(x[j].x), pk_abs(x[j].y)), pk_max(pk_abs(x[j].z), pk_abs(x[j].w)))); };
     uint32_t all = 0;
     if constexpr (TILE) {
 #pragma unroll
@@ -98,8 +102,8 @@ __global__ __launch_bounds__(QF_THREADS, 8) void quant_fb_kernel(QuantFbParams p
         }
         if (cin && r < p.R)
           *reinterpret_cast<uint2*>(rbase + (uint32_t(4 * rg + j) * uint32_t(p.C) + uint32_t(c0))) =
-              make_uint2(e4m3x4(val(j, 0) * sc.inv, val(j, 1) * sc.inv, val(j, 2) * sc.inv, val(j, 3) * sc.inv),
-                         e4m3x4(val(j, 4) * sc.inv, val(j, 5) * sc.inv, val(j, 6) * sc.inv, val(j, 7) * sc.inv));
+              make_uint2(fb_codes4(val(j, 0) * sc.inv, val(j, 1) * sc.inv, val(j, 2) * sc.inv, val(j, 3) * sc.inv),
+                         fb_codes4(val(j, 4) * sc.inv, val(j, 5) * sc.inv, val(j, 6) * sc.inv, val(j, 7) * sc.inv));
       }
     }
     if constexpr (COL) {
@@ -110,23 +114,24 @@ __global__ __launch_bounds__(QF_THREADS, 8) void quant_fb_kernel(QuantFbParams p
         for (int k = 0; k < 8; ++k) inv[k] = ts.inv;
       } else {
         // over the wave's 4 row groups (lanes 16 and 32 apart), then the 8 waves
+        uint32_t cm[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) m = umax(m, __float_as_uint(val(j, k)) & 0x7fffffffu);
-          const U32Pair a = permlane16_swap(m, m);
-          m = umax(a.a, a.b);
-          const U32Pair c = permlane32_swap(m, m);
-          m = umax(c.a, c.b);
-          if ((tid & 48) == 0) s_max[wave * FB + cl + k] = m;
+        for (int k = 0; k < 4; ++k) {
+          auto at = [&](int j) { return pk_abs(k < 2 ? (k < 1 ? x[j].x : x[j].y) : (k < 3 ? x[j].z : x[j].w)); };
+          cm[k] = pk_max(pk_max(at(0), at(1)), pk_max(at(2), at(3)));
+          const U32Pair a = permlane16_swap(cm[k], cm[k]);
+          cm[k] = pk_max(a.a, a.b);
+          const U32Pair c = permlane32_swap(cm[k], cm[k]);
+          cm[k] = pk_max(c.a, c.b);
         }
+        if ((tid & 48) == 0) *reinterpret_cast<uint4*>(s_max + (wave * FB + cl) / 2) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
         __syncthreads();
         if (tid < FB) {
-          uint32_t m = s_max[tid];
+          const uint16_t* s = reinterpret_cast<const uint16_t*>(s_max) + tid;
+          uint32_t m = s[0];
 #pragma unroll
-          for (int w = 1; w < 8; ++w) m = umax(m, s_max[w * FB + tid]);
-          const FbScale sc = fb_scale(m);
+          for (int w = 1; w < 8; ++w) m = umax(m, s[w * FB]);
+          const FbScale sc = fb_scale(m << 16);
           s_inv[tid] = sc.inv;
           const int c = tc * FB + tid;
           if (c < p.C) p.col_scales[(b * p.C + c) * nr + tr] = sc.s;
@@ -138,7 +143,7 @@ __global__ __launch_bounds__(QF_THREADS, 8) void quant_fb_kernel(QuantFbParams p
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         *reinterpret_cast<uint32_t*>(s_col + (cl + k) * QF_LD + 4 * rg) =
-            e4m3x4(val(0, k) * inv[k], val(1, k) * inv[k], val(2, k) * inv[k], val(3, k) * inv[k]);
+            fb_codes4(val(0, k) * inv[k], val(1, k) * inv[k], val(2, k) * inv[k], val(3, k) * inv[k]);
       __syncthreads();
       // 16 bytes a thread: 8 threads a column
 #pragma unroll

@@ -232,8 +232,8 @@ __global__ __launch_bounds__(256) void fb_swiglu_kernel(SwigluArgs p, const floa
   const FbScale sc = fb_scale(row16_umax(am));
   if (!in) return;
   *reinterpret_cast<uint2*>(p.codes + int64_t(r) * F + f) =
-      make_uint2(e4m3x4(h[0] * sc.inv, h[1] * sc.inv, h[2] * sc.inv, h[3] * sc.inv),
-                 e4m3x4(h[4] * sc.inv, h[5] * sc.inv, h[6] * sc.inv, h[7] * sc.inv));
+      make_uint2(fb_codes4(h[0] * sc.inv, h[1] * sc.inv, h[2] * sc.inv, h[3] * sc.inv),
+                 fb_codes4(h[4] * sc.inv, h[5] * sc.inv, h[6] * sc.inv, h[7] * sc.inv));
   if ((threadIdx.x & 15) == 0) p.scales[ld > 0 ? int64_t(b) * ld + r : int64_t(r) * nb + b] = sc.s;
 }
 mge_status launch_fb_swiglu(const FbGemm& g, const float* gu, int64_t ld, hipStream_t s) {

@@ -191,3 +191,27 @@ def test_two_graphs_and_eager_calls_between(m):
             assert torch.equal(o[0], r) and torch.equal(e, r)
             assert torch.equal(o[1], grad[0]) and torch.equal(o[2], grad[1])
     graphs.clear()
+
+
+def test_largest_value_of_a_block_is_the_largest_code(m):
+    """Every mantissa of a block's largest value, at small, ordinary and the largest exponents: 448 / m rounded up or down,
+    its code is E4M3's largest; in both orientations and in the norm, whose values are fp32."""
+    bits = np.array([e * 128 + k for e in (0, 1, 20, 26, 27, 28, 64, 126, 127, 128, 200, 254) for k in range(128)], np.uint16)
+    bits = bits[bits > 0]
+    x = torch.from_numpy(bits.view(np.int16).copy()).cuda().view(torch.bfloat16)
+    x = torch.stack([x, -x], 1).repeat_interleave(16, 1).contiguous()                # [n, 32]: m and -m
+    for orient, t in (("row", x), ("col", x.t().contiguous())):
+        t = t if orient == "row" else torch.nn.functional.pad(t, (0, -t.shape[1] % 32)).contiguous()
+        got = m.fp8_block_quantize(t, orient)
+        codes, scales = (got[0], got[1]) if orient == "row" else (got[2][:len(bits)], got[3][:len(bits)])
+        q, s = fb.quantize(x.float().cpu().numpy())
+        np.testing.assert_array_equal(npy(codes)[:, :32], q)
+        np.testing.assert_array_equal(npy(scales), s)
+    big = bits >= 28 * 128
+    assert (q[big] & 127 == 126).all()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    v = torch.rand(4096, 128, device="cuda", generator=g) + 0.5
+    o = m.rmsnorm_fwd(v, torch.ones(128, device="cuda"), form="fp8_block", y_dtype="f32")
+    q, s = fb.quantize(npy(o.y))
+    np.testing.assert_array_equal(npy(o.codes), q)
+    np.testing.assert_array_equal(npy(o.scales), s)

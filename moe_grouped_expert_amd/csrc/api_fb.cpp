@@ -297,8 +297,9 @@ mge_status fp8_block_grouped_wgrad(const mge_wgrad_fb_args* a, void* stream) {
   const int nb = int(fb_blocks(a->rows));
   float* yst = static_cast<float*>(ws.take(fb_scales_t(a->N, a->rows)));
   float* xst = static_cast<float*>(ws.take(fb_scales_t(a->K, a->rows)));
-  p.Yst = yst; p.Xst = xst;
+  p.Ys = a->dy_scale; p.Xs = a->x_scale; p.Yst = yst; p.Xst = xst;
   p.out = a->accumulate ? OUT_F32_ACC : (a->out_dtype == MGE_DTYPE_F32 ? OUT_F32 : OUT_BF16);
+  if (fb_wgrad_small(p)) return launch_fb_wgrad(p, s);
   const FbScaleT t[2] = {{a->dy_scale, nullptr, a->N, a->N, nb, yst, a->N}, {a->x_scale, nullptr, a->K, a->K, nb, xst, a->K}};
   const mge_status st = launch_fb_scale_t(t, 2, s);
   return st != MGE_OK ? st : launch_fb_wgrad(p, s);

@@ -148,12 +148,15 @@ struct FbWgrad {
   const int32_t* offs;
   const uint8_t* Y;                 // [N][rows]
   const uint8_t* X;                 // [K][rows]
-  const float* Yst;                 // [ceil(rows/128)][N]
+  const float* Ys;                  // [N][ceil(rows/128)]
+  const float* Xs;                  // [K][ceil(rows/128)]
+  const float* Yst;                 // [ceil(rows/128)][N], unless fb_wgrad_small
   const float* Xst;                 // [ceil(rows/128)][K]
   void* const* D;                   // device table (NULL: Dv): [N][K] of each expert
   void* Dv[kFbInline];
   int out;                          // OutForm
 };
+bool fb_wgrad_small(const FbWgrad& p);
 mge_status launch_fb_wgrad(const FbWgrad& p, hipStream_t s);
 
 // out[j][r] = in[row(r)][j]: fp32 scales, block-major; row(r) = map ? map[r] : r, 0 where outside [0, src_rows)

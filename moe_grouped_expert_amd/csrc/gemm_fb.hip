@@ -59,6 +59,7 @@ struct FbTile {
 };
 typedef FbTile<2, 4, 8, 4, 2, 1> FbMain;   // 256 x 256
 typedef FbTile<2, 2, 4, 4, 2, 2> FbQuad;   // 128 x 128
+typedef FbTile<2, 2, 4, 4, 2, 1> FbSmall;  // 128 x 128, two workgroups a CU (dW)
 
 // Lanes 2j and 2j + 1 trade their b and a: the even lane then has its own a and the odd lane's a, the odd one
 // the even lane's b and its own b.  Where a lane's a and b are neighbouring 16 bytes of its row of the output,
@@ -141,8 +142,8 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
     q = v >> 4;
   };
 
-  // tiles of 256 x 256 whatever the kernel's own (SwiGLU: 128 columns of gate and of up, the kernel's tokens)
-  constexpr int TM = SW ? TL::NT : 256, TN = SW ? FB : 256;
+  // tiles of 256 x 256 for C whatever the kernel's own (SwiGLU: 128 columns of gate and of up, the kernel's tokens)
+  constexpr int TM = SW || KR ? TL::NT : 256, TN = SW ? FB : (KR ? TL::NR : 256);
   int ncols = KR ? p.K : p.N;                              // columns of C
   if constexpr (SW) ncols = p.F;
   const int ntiles = (ncols + TN - 1) / TN;
@@ -261,7 +262,11 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   // the group read other rows' scales or zeros; what they scale is zero or not stored.)
   const bool of_t = wave < SWV;
   uint32_t s_ld, soff = uint32_t(lane) * 4;   // bytes of a slice; the lane's
-  if constexpr (KR) {
+  constexpr bool ROWS = KR && TL::NR < 256;    // dW's small tiles: the scales as they come, a line a row
+  if constexpr (ROWS) {
+    s_ld = 4;
+    soff *= uint32_t((p.rows + 127) / 128);
+  } else if constexpr (KR) {
     s_ld = uint32_t(of_t ? p.N : p.K) * 4;
   } else {
     s_ld = of_t ? uint32_t(p.ast_ld) * 4 : 4u;
@@ -277,9 +282,9 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       for (int h = 0; h < 2; ++h)
         o.rW[h] = make_rsrc_n(p.X + int64_t(t.n0 + HR * h) * p.rows, uint32_t(left(p.K - t.n0 - HR * h, HR)) * ldw);
       const int n = of_t ? p.N : p.K;
-      const int64_t at = int64_t(t.kbase / 128) * n + (of_t ? t.m0 + wave * 64 : t.n0 + (wave - SWV) * 64);
-      const int64_t all = int64_t((p.rows + 127) / 128) * n;
-      o.rS = make_rsrc_n((of_t ? p.Yst : p.Xst) + at, at < all ? uint32_t(all - at) * 4 : 0);
+      const int64_t nb = (p.rows + 127) / 128, row = of_t ? t.m0 + wave * 64 : t.n0 + (wave - SWV) * 64, all = nb * n;
+      const int64_t at = ROWS ? row * nb + t.kbase / 128 : t.kbase / 128 * int64_t(n) + row;
+      o.rS = make_rsrc_n((ROWS ? (of_t ? p.Ys : p.Xs) : (of_t ? p.Yst : p.Xst)) + at, at < all ? uint32_t(all - at) * 4 : 0);
     } else {
       o.rT = make_rsrc_n(p.A, uint32_t(p.src_rows) * ldw);
 #pragma unroll
@@ -663,6 +668,9 @@ FB_KERNEL(gemm_fb_swiglu, FbMain, 2, false, true, OUT_NONE, false, FbGemm)
 FB_KERNEL(gemm_fb_wgrad, FbMain, 2, true, false, OUT_BF16, false, FbWgrad)
 FB_KERNEL(gemm_fb_wgrad_f32, FbMain, 2, true, false, OUT_F32, false, FbWgrad)
 FB_KERNEL(gemm_fb_wgrad_f32_acc, FbMain, 2, true, false, OUT_F32_ACC, false, FbWgrad)
+FB_KERNEL(gemm_fb_wgrad_small, FbSmall, 2, true, false, OUT_BF16, false, FbWgrad)
+FB_KERNEL(gemm_fb_wgrad_f32_small, FbSmall, 2, true, false, OUT_F32, false, FbWgrad)
+FB_KERNEL(gemm_fb_wgrad_f32_acc_small, FbSmall, 2, true, false, OUT_F32_ACC, false, FbWgrad)
 #undef FB_KERNEL
 
 // A persistent launch of at most `grid` workgroups
@@ -695,11 +703,32 @@ mge_status launch_fb_tile(const FbGemm& p0, bool swiglu, hipStream_t s) {
                    : launch_fb<FbQuad>(gemm_fb_store_tail, "gemm_fp8_block_tail", p, tail, s);
 }
 
+// dW's tiles: 256 x 256, or 128 x 128 with two workgroups a CU, which take in twice the bytes, but fill the CUs with
+// few tiles, overlap one's epilogue with the other's slices and read the scales as they come (the pass that makes them
+// block-major is a launch of its own).  By estimates of the time in us from what both measured on MI355X (bf16, 256 and
+// 128; slices: an expert's tokens / 128): 8 x [1024][1024], 1 slice 16.4, 9.6, 8 26.9, 17.5, 32 66, 49; [4096][4096], 3
+// slices 21.9, 17.8, 8 31.9, 28.5, 32 78, 94; 8 x [2048][2048], 1 slice 27.9, 25.1, 8 52, 56; 8 x [4096][14336] (scales
+// block-major for both), 1 slice 219, 293, 8 556, 709.
+bool fb_wgrad_small(const FbWgrad& p) {
+  const int64_t cus = device_cus();
+  const double slices = std::max(1.0, double(p.rows) / 128 / p.E);
+  auto rounds = [&](int n, int64_t per) { return double((int64_t(p.E) * ((p.N + n - 1) / n) * ((p.K + n - 1) / n) + per - 1) / per); };
+  return 5 + rounds(128, 2 * cus) * (3 + 1.3 * slices) < 11 + rounds(256, cus) * (5.5 + 1.85 * slices);
+}
+template <typename TL, typename Kern>
+static mge_status launch_wgrad(Kern kern, int per_cu, const FbWgrad& p, hipStream_t s) {
+  const int64_t tiles = int64_t(p.E) * ((p.N + TL::NT - 1) / TL::NT) * ((p.K + TL::NR - 1) / TL::NR);
+  return launch_fb<TL>(kern, "wgrad_fp8_block", p, std::min<int64_t>(int64_t(per_cu) * device_cus(), tiles), s);
+}
 mge_status launch_fb_wgrad(const FbWgrad& p, hipStream_t s) {
-  const int64_t grid = std::min<int64_t>(device_cus(), int64_t(p.E) * ((p.N + 255) / 256) * ((p.K + 255) / 256));
-  if (p.out == OUT_BF16) return launch_fb<FbMain>(gemm_fb_wgrad, "wgrad_fp8_block", p, grid, s);
-  if (p.out == OUT_F32) return launch_fb<FbMain>(gemm_fb_wgrad_f32, "wgrad_fp8_block", p, grid, s);
-  return launch_fb<FbMain>(gemm_fb_wgrad_f32_acc, "wgrad_fp8_block", p, grid, s);
+  if (fb_wgrad_small(p)) {
+    if (p.out == OUT_BF16) return launch_wgrad<FbSmall>(gemm_fb_wgrad_small, 2, p, s);
+    if (p.out == OUT_F32) return launch_wgrad<FbSmall>(gemm_fb_wgrad_f32_small, 2, p, s);
+    return launch_wgrad<FbSmall>(gemm_fb_wgrad_f32_acc_small, 2, p, s);
+  }
+  if (p.out == OUT_BF16) return launch_wgrad<FbMain>(gemm_fb_wgrad, 1, p, s);
+  if (p.out == OUT_F32) return launch_wgrad<FbMain>(gemm_fb_wgrad_f32, 1, p, s);
+  return launch_wgrad<FbMain>(gemm_fb_wgrad_f32_acc, 1, p, s);
 }
 
 // Scales made block-major, 64 x 64 a workgroup through LDS; every matrix of the launch has its own range of workgroups

@@ -31,14 +31,14 @@ static mge_status check_norm(int T, int H, int x_dtype, int w_dtype, int y_dtype
 
 // Streaming or tile kernels: estimates of a product's time in microseconds from what both measured on
 // MI355X (whole calls, rows an expert of E x [N][K]: streamed, tiled).
-//   8 x [4096][14336]: 8 rows 100, 130; 24 rows 129, 131; 32 rows 142, 132; 64 rows 218, 140
-//   8 x [2048][4096]: 8 rows 17, 26; 32 rows 24, 27; 48 rows 33, 27; 64 rows 38, 27
-//   16 x [1024][2048]: 8 rows 9, 20; 48 rows 20.4, 20.9; 128 rows 40, 22
-//   [8192][8192]: 8 rows 18, 38; 64 rows 34, 39; 128 rows 64, 41
-//   [4096][4096]: 8 rows 6.6, 24; 64 rows 19, 25; 128 rows 34, 25
+//   8 x [4096][14336]: 8 rows 100, 122; 16 rows 118, 123; 32 rows 142, 127; 64 rows 217, 143
+//   8 x [2048][4096]: 8 rows 17, 22; 16 rows 20, 22; 32 rows 24, 22; 64 rows 38, 22
+//   16 x [1024][2048]: 8 rows 9, 15; 32 rows 13.5, 15.4; 48 rows 20, 16; 128 rows 40, 17
+//   [8192][8192]: 8 rows 18, 33; 48 rows 30, 33; 64 rows 34, 33; 128 rows 64, 35
+//   [4096][4096]: 8 rows 6.7, 20; 64 rows 19, 20; 128 rows 34, 20
 // Streaming reads the weights at about 5 TB/s for every 64 rows, and a row past 8 adds 1/57 of that;
-// the tile kernels take a fixed 14 us, 0.75 us for every 256 of K of a round of 128 x 128 tiles, and no less than
-// their weights at 3.6 TB/s.
+// the tile kernels take a fixed 8 us, 0.75 us for every 256 of K of a round of 128 x 128 tiles, and no less than
+// their weights at 4.2 TB/s.
 static double stream_us(int64_t E, int64_t N, int64_t K, int64_t total) {
   const double rows = double(total) / double(E), bytes = double(std::min(E, total)) * double(N) * double(K);
   return (4 + bytes / 5.0e6) * (1 + std::max(0.0, rows - 8) / 57) * std::max(1.0, ceil(rows / 64));
@@ -46,7 +46,7 @@ static double stream_us(int64_t E, int64_t N, int64_t K, int64_t total) {
 static double tile_us(int64_t E, int64_t N, int64_t K, int64_t total) {
   const double rows = double(total) / double(E), bytes = double(std::min(E, total)) * double(N) * double(K);
   const double tiles = double(std::min(E, total)) * std::max(1.0, ceil(rows / 128)) * double((N + 127) / 128);
-  return 14 + std::max(0.75 * double((K + 255) / 256) * ceil(tiles / 256), bytes / 3.6e6);
+  return 8 + std::max(0.75 * double((K + 255) / 256) * ceil(tiles / 256), bytes / 4.2e6);
 }
 static bool fb_tile(int64_t E, int64_t N, int64_t K, int64_t total) { return tile_us(E, N, K, total) < stream_us(E, N, K, total); }
 static bool fb_tile_mlp(int64_t E, int64_t H, int64_t F, int64_t total) {
@@ -241,6 +241,7 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
     }
   }
   if (!fb_tile(p.E, p.N, p.K, p.total)) return launch_fb_stream(p, s);
+  if (fb_tail_only(p)) return launch_fb_tile(p, false, s);
   float* ast = static_cast<float*>(ws.take(fb_scales_t(a->rows, a->K)));
   p.Ast = ast; p.ast_ld = a->rows;
   const FbScaleT t{a->a_scale, a->a_rows, a->src_rows, a->rows, int(fb_blocks(a->K)), ast, a->rows};
@@ -385,14 +386,15 @@ mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
   g.h_scales = static_cast<float*>(ws.take(fb_scales_t(a->rows, F)));
   d.A = g.h_codes; d.As = g.h_scales; d.Ast = g.h_scales; d.ast_ld = a->rows;
   const bool tile = fb_tile_mlp(E, H, F, g.total);
-  if (tile) {
+  const bool fused = fb_fused(E, F, g.total, tile);
+  if (tile && (fused || !fb_tail_only(g))) {
     float* xst = static_cast<float*>(ws.take(fb_scales_t(a->rows, H)));
     g.Ast = xst; g.ast_ld = a->rows;
     const FbScaleT t{a->x_scale, a->perm_src, a->x_rows, a->rows, int(fb_blocks(H)), xst, a->rows};
     st = launch_fb_scale_t(&t, 1, s);
     if (st != MGE_OK) return st;
   }
-  if (fb_fused(E, F, g.total, tile)) {
+  if (fused) {
     st = launch_fb_tile(g, true, s);
   } else {
     float* gu = static_cast<float*>(ws.take(size_t(a->rows) * F * 8));

@@ -119,8 +119,8 @@ struct FbGemm {
   const int32_t* map;               // optional: row of A of each row (outside [0, src_rows): zeros)
   int src_rows;
   const uint8_t* A;                 // [src_rows][K]
-  const float* As;                  // streaming: [src_rows][ceil(K/128)]
-  const float* Ast;                 // tiles: [ceil(K/128)][ast_ld], by row of the groups
+  const float* As;                  // [src_rows][ceil(K/128)]
+  const float* Ast;                 // tiles: [ceil(K/128)][ast_ld], by row of the groups (NULL: As, where fb_tail_only)
   int64_t ast_ld;
   const uint8_t* const* W;          // device tables (NULL: Wv, Wsv): [N][K] codes of each expert
   const float* const* Ws;           // [ceil(N/128)][ceil(K/128)]
@@ -134,6 +134,7 @@ struct FbGemm {
   int grid_main;                    // workgroups of the main launch's whole rounds (set by the launcher)
 };
 mge_status launch_fb_stream(const FbGemm& p, hipStream_t s);
+bool fb_tail_only(const FbGemm& p);
 mge_status launch_fb_tile(const FbGemm& p, bool swiglu, hipStream_t s);
 
 // h_codes, h_scales of fp32 rows gu = [G U] (rows behind and between the groups may be left out); scales

@@ -113,6 +113,7 @@ struct FtTile {
 struct FtOps {
   i32x4 rT, rW[2], rS;
   uint32_t toff[4];   // C (the rows of A may be gathered)
+  uint32_t soff;      // TAIL
 };
 
 // KR: dW (FbWgrad), else C (FbGemm).  SW: the SwiGLU epilogue.  TAIL: the tiles past the main launch's last
@@ -169,7 +170,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   int vid = blockIdx.x;
   if ((nwg & 7) == 0) vid = (blockIdx.x & 7) * (nwg >> 3) + (blockIdx.x >> 3);
   // The tiles past the main launch's last whole round run as quadrants where those are at most two a
-  // workgroup; both launches decide from the same numbers.
+  // workgroup; both launches decide from the same numbers.  (Without a main launch a round has no end.)
   int items = total, t_full = 0;
   if constexpr (!KR && !SW) {
     const int full = total / p.grid_main * p.grid_main, left = total - full;
@@ -177,7 +178,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
     t_full = uniform(full);
     items = uniform(TAIL ? (split ? 4 * left : 0) : (split ? full : total));
     if constexpr (TAIL) {
-      // an equal run of the items for each XCD (at most two a workgroup: the second ones at nwg on)
+      // an equal run of the items for each XCD (further ones at nwg on)
       const int n = items < nwg ? items : nwg, run = (n + 7) >> 3;
       if ((nwg & 7) == 0) vid = int(blockIdx.x >> 3) < run ? int(blockIdx.x & 7) * run + int(blockIdx.x >> 3) : items;
     }
@@ -240,8 +241,17 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   static_assert(DT <= 4 && DW <= 2, "offsets of a lane");
   constexpr int SWV = TL::NT / 64;             // the first wave that brings the row operand's scales
 
-  // Rows of A of the lane's DMAs
+  const bool of_t = wave < SWV;                // (the wave brings the tokens' scales)
+  bool direct = false;                         // C's quadrants without a main launch read the tokens' scales as they come
+  if constexpr (TAIL) direct = p.Ast == nullptr;
+
+  // Rows of A of the lane's DMAs (TAIL: and of its scale)
   auto rows_of = [&](const FtTile& t, int* src) {
+    if constexpr (TAIL) {
+      const int m = t.m0 + wave * 64 + lane;
+      src[DT] = direct && of_t && t.valid && m < t.m_valid ? t.off + m : -1;
+      if (src[DT] >= 0 && p.map) src[DT] = p.map[src[DT]];
+    }
 #pragma unroll
     for (int i = 0; i < DT; ++i) {
       const int m = t.m0 + wave * (DT * 8) + i * 8 + (lane >> 3);
@@ -260,7 +270,6 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   // Scales: the tokens' (dW: of dY), 64 a wave; in the other waves for dW those of X, for C in the first lanes those of
   // the weights, of the tile's halves or with SwiGLU of the gate rows and of every 32 up rows.  (Lanes past the rows or
   // the group read other rows' scales or zeros; what they scale is zero or not stored.)
-  const bool of_t = wave < SWV;
   uint32_t s_ld, soff = uint32_t(lane) * 4;   // bytes of a slice; the lane's
   constexpr bool ROWS = KR && TL::NR < 256;    // dW's small tiles: the scales as they come, a line a row
   if constexpr (ROWS) {
@@ -269,7 +278,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   } else if constexpr (KR) {
     s_ld = uint32_t(of_t ? p.N : p.K) * 4;
   } else {
-    s_ld = of_t ? uint32_t(p.ast_ld) * 4 : 4u;
+    s_ld = of_t && !direct ? uint32_t(p.ast_ld) * 4 : 4u;
     const int blk = SW ? (lane == 0 ? 0 : (p.F + (lane - 1) * 32) / FB) : lane * HR / FB;
     if (!of_t) soff = lane < (SW ? 5 : 2) ? uint32_t(blk * KB) * 4 : kInvalid;
   }
@@ -301,6 +310,13 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
       const int64_t at = of_t ? int64_t(t.off) + t.m0 + wave * 64 : int64_t(t.n0 / FB) * KB;
       const int64_t all = of_t ? int64_t(KB) * p.ast_ld : int64_t(((SW ? 2 * ncols : p.N) + FB - 1) / FB) * KB;
       o.rS = make_rsrc_n((of_t ? p.Ast : ws) + at, at < all ? uint32_t(all - at) * 4 : 0);
+      o.soff = soff;
+      if constexpr (TAIL) {
+        if (direct && of_t) {
+          o.rS = make_rsrc_n(p.As, uint32_t(p.src_rows) * uint32_t(KB) * 4);
+          o.soff = src[DT] >= 0 && src[DT] < p.src_rows ? uint32_t(src[DT]) * uint32_t(KB) * 4 : kInvalid;
+        }
+      }
     }
     return o;
   };
@@ -336,7 +352,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   };
   auto dma_s = [&](const FtOps& o, const FtTile& t, int kt) {
     const i32x4 r = at_slice(o.rS, t, kt);
-    dma4(r, lds_base + TL::SCALES + ((gd + kt) & (2 * NST - 1)) * TL::RING + wave * 256, soff, place(r, uint32_t(KG * kt + kg) * s_ld));
+    dma4(r, lds_base + TL::SCALES + ((gd + kt) & (2 * NST - 1)) * TL::RING + wave * 256, TAIL ? o.soff : soff, place(r, uint32_t(KG * kt + kg) * s_ld));
   };
   // The early part of a slice (its tokens, scales and the first half of the weight rows) and the late one
   constexpr int EARLY = 1 + DT + DW, LATE = DW;
@@ -367,7 +383,7 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
   FtOps o{};
   int stores = 0;   // 1: the wave has stores in flight that are newer than this tile's first DMAs
   bool ahead = false;   // the tile's first slices came with the tile before
-  int src[DT];
+  int src[DT + (TAIL ? 1 : 0)];
   rows_of(t, src);
   if (t.valid) {
     o = setup(t, src);
@@ -683,16 +699,23 @@ static mge_status launch_fb(Kern kern, const char* name, const P& p, int64_t gri
   return hip_check(name);
 }
 
+static int64_t fb_token_tiles(const FbGemm& p) { return (int64_t(p.total) + 255) / 256 + (p.sizes ? p.E : 0); }
+// With tiles for half a round at most, were the groups even, all tiles are the tail's, however many there are; it takes
+// the tokens' scales in either form, which saves the launch that makes them block-major
+bool fb_tail_only(const FbGemm& p) {
+  const int64_t groups = std::max(1, p.sizes ? std::min(p.E, p.total) : 1), each = (p.total + groups - 1) / groups;
+  return 2 * groups * ((each + 255) / 256) * ((p.N + 255) / 256) <= device_cus();
+}
 mge_status launch_fb_tile(const FbGemm& p0, bool swiglu, hipStream_t s) {
   FbGemm p = p0;
-  const int64_t mt = (int64_t(p.total) + 255) / 256 + (p.sizes ? p.E : 0);
+  const int64_t mt = fb_token_tiles(p);
   const int cus = device_cus();
   if (swiglu) return launch_fb<FbMain>(gemm_fb_swiglu, "gemm_fp8_block_swiglu", p, std::min<int64_t>(cus, mt * ((p.F + 127) / 128)), s);
   const int64_t tiles = mt * ((p.N + 255) / 256);
-  p.grid_main = cus;
-  // (with tiles for half a round at most, all of them are the tail's)
+  const bool only = fb_tail_only(p);
+  p.grid_main = only ? 1 << 30 : cus;
   mge_status st = MGE_OK;
-  if (2 * tiles > cus) {
+  if (!only) {
     const int64_t grid = std::min<int64_t>(cus, tiles);
     st = p.out_f32 ? launch_fb<FbMain>(gemm_fb_store_f32, "gemm_fp8_block", p, grid, s)
                    : launch_fb<FbMain>(gemm_fb_store, "gemm_fp8_block", p, grid, s);

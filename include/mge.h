@@ -834,7 +834,7 @@ mge_status fp8_block_dequantize(const mge_dequant_fb_args* args, void* stream);
  * A NaN (scale, E4M3 code 0x7f) reaches its row of out (a), or its column or the 128 columns
  * of its scale, in its expert's rows (w), and no other element.
  * Workspace: mge_gemm_fb_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for
- * few rows over at most 64 experts.
+ * few rows or few tiles over at most 64 experts.
  * Errors: MGE_ERR_INVALID_ARG for E outside [1, 256], N or K not a positive multiple of 32,
  * or above 2^22, rows or src_rows < 0 or >= 2^31 / K, src_rows other than rows without a map,
  * an expert's weight of 2^31 bytes or more, an unknown dtype, NULL or misaligned pointers

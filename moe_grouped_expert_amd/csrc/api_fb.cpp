@@ -53,14 +53,12 @@ static bool fb_tile_mlp(int64_t E, int64_t H, int64_t F, int64_t total) {
   return tile_us(E, 2 * F, H, total) + tile_us(E, H, F, total) < stream_us(E, 2 * F, H, total) + stream_us(E, H, F, total);
 }
 // SwiGLU in the gate-up product's epilogue needs all of a block of 128 columns, gate and up, in a workgroup: tiles of
-// 256 weight rows, of which there are few for few columns.  Then the product in the plain form, which fills more
-// CUs, and SwiGLU on its own.  Whole MLP, fused and not, us: 250 tokens, one expert 4096 x 4096 (32 tiles) 80, 58;
-// 144 tokens, top-2 of 3 experts 512 x 768 (18) 30, 28; 64 tokens, top-2 of 8 experts 2048 x 1408 (88) 50, 50, 500
-// tokens 66, 75; 250 tokens, one expert 4096 x 14336 (112) 123, 122; two experts (224) 139, 155.
-constexpr int64_t kFusedTiles = 64;
-static bool fb_fused(int64_t E, int64_t F, int64_t total, bool tile) {
-  return tile && ((total + 255) / 256 + std::min(E, total) - 1) * fb_blocks(F) > kFusedTiles;
-}
+// 256 weight rows.  Where those are half a round at most, the product in the plain form, by quadrants, fills more CUs,
+// and SwiGLU follows on its own.  Whole MLP, fused and not, us: 250 tokens, one expert 4096 x 4096 (32 tiles) 78, 52;
+// 250 tokens, top-2 of 8 experts 2048 x 1408 (88) 51, 47, 1000 tokens 65, 65; 256 tokens, top-2 of 4 experts 4096 x
+// 4096 (128) 84, 78; 500 tokens, one expert 4096 x 14336 (224) 128, 147; 128 tokens, top-4 of 16 experts 1024 x 2048
+// (256) 44, 51.
+static bool fb_fused(int64_t E, int64_t F, int64_t total, bool tile) { return tile && !fb_tail_only(E, 2 * F, total); }
 
 // Rows of all groups at most (without groups: all rows)
 static int64_t fb_total(const void* sizes, int64_t total, int64_t rows) { return sizes && total > 0 && total < rows ? total : rows; }
@@ -183,8 +181,10 @@ mge_status fp8_block_dequantize(const mge_dequant_fb_args* a, void* stream) {
 size_t mge_gemm_fb_workspace_bytes(const mge_gemm_fb_args* a) {
   if (!a || a->struct_size != sizeof(mge_gemm_fb_args) || a->E < 1 || a->E > 256 || a->N < 32 || a->K < 32 || a->rows < 0 || a->rows >= kTwoGiB / a->K)
     return 0;
+  const int64_t total = fb_total(a->split_sizes, a->total_rows, a->rows);
+  const bool tile = fb_tile(a->E, a->N, a->K, total);
   return (fb_table(a->E) ? up256(2 * size_t(a->E) * sizeof(void*)) : 0) +
-         (fb_tile(a->E, a->N, a->K, fb_total(a->split_sizes, a->total_rows, a->rows)) ? fb_scales_t(a->rows, a->K) : 0);
+         (tile && !fb_tail_only(a->E, a->N, total) ? fb_scales_t(a->rows, a->K) : 0);
 }
 
 mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
@@ -241,8 +241,8 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
     }
   }
   if (!fb_tile(p.E, p.N, p.K, p.total)) return launch_fb_stream(p, s);
-  if (fb_tail_only(p)) return launch_fb_tile(p, false, s);
-  float* ast = static_cast<float*>(ws.take(fb_scales_t(a->rows, a->K)));
+  if (fb_tail_only(p.E, p.N, p.total)) return launch_fb_tile(p, false, s);
+  float* ast = static_cast<float*>(ws.take(fb_scales_t(a->rows, a->K)));   // (block-major, by row of the groups)
   p.Ast = ast; p.ast_ld = a->rows;
   const FbScaleT t{a->a_scale, a->a_rows, a->src_rows, a->rows, int(fb_blocks(a->K)), ast, a->rows};
   const mge_status st = launch_fb_scale_t(&t, 1, s);
@@ -313,7 +313,7 @@ size_t mge_fwd_fb_workspace_bytes(const mge_fwd_fb_args* a) {
   const int64_t total = fb_total(a->split_sizes, a->total_rows, a->rows);
   const bool tile = fb_tile_mlp(a->E, a->H, a->F, total);
   return (fb_table(a->E) ? up256(4 * size_t(a->E) * sizeof(void*)) : 0) + up256(size_t(a->rows) * a->F) + fb_scales_t(a->rows, a->F) +
-         (tile ? fb_scales_t(a->rows, a->H) : 0) + (fb_fused(a->E, a->F, total, tile) ? 0 : up256(size_t(a->rows) * a->F * 8));
+         (fb_fused(a->E, a->F, total, tile) ? fb_scales_t(a->rows, a->H) : up256(size_t(a->rows) * a->F * 8));
 }
 
 mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
@@ -387,7 +387,7 @@ mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
   d.A = g.h_codes; d.As = g.h_scales; d.Ast = g.h_scales; d.ast_ld = a->rows;
   const bool tile = fb_tile_mlp(E, H, F, g.total);
   const bool fused = fb_fused(E, F, g.total, tile);
-  if (tile && (fused || !fb_tail_only(g))) {
+  if (fused) {   // (the quadrants take the tokens' scales as they come)
     float* xst = static_cast<float*>(ws.take(fb_scales_t(a->rows, H)));
     g.Ast = xst; g.ast_ld = a->rows;
     const FbScaleT t{a->x_scale, a->perm_src, a->x_rows, a->rows, int(fb_blocks(H)), xst, a->rows};

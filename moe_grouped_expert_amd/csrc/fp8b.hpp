@@ -134,7 +134,7 @@ struct FbGemm {
   int grid_main;                    // workgroups of the main launch's whole rounds (set by the launcher)
 };
 mge_status launch_fb_stream(const FbGemm& p, hipStream_t s);
-bool fb_tail_only(const FbGemm& p);
+bool fb_tail_only(int64_t E, int64_t N, int64_t total);
 mge_status launch_fb_tile(const FbGemm& p, bool swiglu, hipStream_t s);
 
 // h_codes, h_scales of fp32 rows gu = [G U] (rows behind and between the groups may be left out); scales

@@ -702,9 +702,9 @@ static mge_status launch_fb(Kern kern, const char* name, const P& p, int64_t gri
 static int64_t fb_token_tiles(const FbGemm& p) { return (int64_t(p.total) + 255) / 256 + (p.sizes ? p.E : 0); }
 // With tiles for half a round at most, were the groups even, all tiles are the tail's, however many there are; it takes
 // the tokens' scales in either form, which saves the launch that makes them block-major
-bool fb_tail_only(const FbGemm& p) {
-  const int64_t groups = std::max(1, p.sizes ? std::min(p.E, p.total) : 1), each = (p.total + groups - 1) / groups;
-  return 2 * groups * ((each + 255) / 256) * ((p.N + 255) / 256) <= device_cus();
+bool fb_tail_only(int64_t E, int64_t N, int64_t total) {
+  const int64_t groups = std::max<int64_t>(1, std::min(E, total)), each = (total + groups - 1) / groups;
+  return 2 * groups * ((each + 255) / 256) * ((N + 255) / 256) <= 256;   // (CUs of a whole chip: workspaces go by it)
 }
 mge_status launch_fb_tile(const FbGemm& p0, bool swiglu, hipStream_t s) {
   FbGemm p = p0;
@@ -712,7 +712,7 @@ mge_status launch_fb_tile(const FbGemm& p0, bool swiglu, hipStream_t s) {
   const int cus = device_cus();
   if (swiglu) return launch_fb<FbMain>(gemm_fb_swiglu, "gemm_fp8_block_swiglu", p, std::min<int64_t>(cus, mt * ((p.F + 127) / 128)), s);
   const int64_t tiles = mt * ((p.N + 255) / 256);
-  const bool only = fb_tail_only(p);
+  const bool only = fb_tail_only(p.E, p.N, p.total);
   p.grid_main = only ? 1 << 30 : cus;
   mge_status st = MGE_OK;
   if (!only) {

@@ -154,7 +154,7 @@ def test_mlp(kw, word):
 
 
 def test_workspaces_and_empty():
-    assert gemm(rows=2000, src_rows=2000, workspace=None)[0] == b.MGE_ERR_WORKSPACE
+    assert gemm(N=8192, rows=2000, src_rows=2000, workspace=None)[0] == b.MGE_ERR_WORKSPACE
     assert gemm(rows=0, src_rows=0, workspace=None, a=None, a_scale=None, out=None)[0] == b.MGE_OK
     assert wgrad(workspace_bytes=64)[0] == b.MGE_ERR_WORKSPACE
     assert mlp(workspace=None)[0] == b.MGE_ERR_WORKSPACE

@@ -4,9 +4,9 @@
 // HBM-bound: one read of the input, one write of each form.  A workgroup takes a tile of 128 rows x
 // 128 columns (a block is never split), 8 columns of 4 consecutive rows a thread: a row's 128
 // values are in the 16 lanes of a DPP row, a column's 4 rows make one dword of the transposed form,
-// which goes through LDS so that it leaves in whole lines.  64 registers, so that a CU holds 32 waves
+// which goes through LDS so that it leaves in whole lines.  At most 64 registers, so that a CU holds 32 waves
 // (128 registers: 80 us for the first figure).  Measured on MI355X: 8192 x 4096 gathered to 16384 rows, both forms
-// 65 us, the bytes at a copy's rate 40; [28672][4096] in 128 x 128 blocks, both forms and each read back, 229 us, the bytes
+// 63 us, the bytes at a copy's rate 41; [28672][4096] in 128 x 128 blocks, both forms and each read back, 229 us, the bytes
 // at that rate 230.
 #include "mge_common.hpp"
 

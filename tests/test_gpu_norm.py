@@ -224,3 +224,19 @@ def test_captured_and_deterministic(m):
         assert all(torch.equal(a, b) for a, b in zip(ref, out)), rep
         assert all(torch.equal(a, b) for a, b in zip(ref, step())), ("eager", rep)
     del graph
+
+
+@pytest.mark.parametrize("T,H", [(700, 16384), (1500, 8192), (1700, 4096), (3000, 1056), (3001, 512), (3500, 1024)])
+@pytest.mark.parametrize("xd", ["bf16", "f32"])
+def test_bwd_several_rows_a_workgroup(m, T, H, xd):
+    """More rows than workgroups: the next row on its way while one is reduced, and over a gradient in place."""
+    check_bwd(m, T, H, xd, "bf16", "bf16")
+    rng = np.random.default_rng(T)
+    x, dy, dres, w = rand(rng, (T, H), xd), rand(rng, (T, H), xd), rand(rng, (T, H), xd), rand(rng, H, "f32")
+    rstd = m.rmsnorm_fwd(x, w, y_dtype="f32").rstd
+    dx, dw = m.rmsnorm_bwd(dy, x, w, rstd, dres)
+    for i in range(3):
+        args = [dy.clone(), x.clone(), w, rstd, dres.clone()]
+        o = args[(0, 1, 4)[i]]
+        got = m.rmsnorm_bwd(*args, out=(o, torch.empty_like(dw)))
+        assert got[0] is o and torch.equal(o, dx) and torch.equal(got[1], dw), i

@@ -66,12 +66,6 @@ static int64_t fb_total(const void* sizes, int64_t total, int64_t rows) { return
 // Few experts' pointers travel in the kernels' arguments, more through a table in the workspace
 static bool fb_table(int E) { return E > kFbInline; }
 
-// Scales by blocks of 128 (a wave reads 64 of a block's at a time, past the last ones too)
-static size_t fb_scales_t(int64_t rows, int64_t K) {
-  const size_t n = size_t(rows) * size_t(fb_blocks(K)) * 4;
-  return n ? up256(n) + 256 : 0;
-}
-
 }  // namespace mge
 
 extern "C" {
@@ -184,7 +178,7 @@ size_t mge_gemm_fb_workspace_bytes(const mge_gemm_fb_args* a) {
   const int64_t total = fb_total(a->split_sizes, a->total_rows, a->rows);
   const bool tile = fb_tile(a->E, a->N, a->K, total);
   return (fb_table(a->E) ? up256(2 * size_t(a->E) * sizeof(void*)) : 0) +
-         (tile && !fb_tail_only(a->E, a->N, total) ? fb_scales_t(a->rows, a->K) : 0);
+         (tile && !fb_tail_only(a->E, a->N, total) ? fb_scales_bytes(a->rows, a->K) : 0);
 }
 
 mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
@@ -242,7 +236,7 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
   }
   if (!fb_tile(p.E, p.N, p.K, p.total)) return launch_fb_stream(p, s);
   if (fb_tail_only(p.E, p.N, p.total)) return launch_fb_tile(p, false, s);
-  float* ast = static_cast<float*>(ws.take(fb_scales_t(a->rows, a->K)));   // (block-major, by row of the groups)
+  float* ast = static_cast<float*>(ws.take(fb_scales_bytes(a->rows, a->K)));   // (block-major, by row of the groups)
   p.Ast = ast; p.ast_ld = a->rows;
   const FbScaleT t{a->a_scale, a->a_rows, a->src_rows, a->rows, int(fb_blocks(a->K)), ast, a->rows};
   const mge_status st = launch_fb_scale_t(&t, 1, s);
@@ -253,7 +247,7 @@ size_t mge_wgrad_fb_workspace_bytes(const mge_wgrad_fb_args* a) {
   if (!a || a->struct_size != sizeof(mge_wgrad_fb_args) || a->E < 1 || a->E > 256 || a->N < 32 || a->K < 32 || a->rows < 0 ||
       a->rows >= kTwoGiB / std::max({a->N, a->K, kTileRows}))
     return 0;
-  return (fb_table(a->E) ? up256(size_t(a->E) * sizeof(void*)) : 0) + fb_scales_t(a->N, a->rows) + fb_scales_t(a->K, a->rows);
+  return (fb_table(a->E) ? up256(size_t(a->E) * sizeof(void*)) : 0) + fb_scales_bytes(a->N, a->rows) + fb_scales_bytes(a->K, a->rows);
 }
 
 mge_status fp8_block_grouped_wgrad(const mge_wgrad_fb_args* a, void* stream) {
@@ -296,8 +290,8 @@ mge_status fp8_block_grouped_wgrad(const mge_wgrad_fb_args* a, void* stream) {
     for (int e = 0; e < a->E; ++e) p.Dv[e] = a->dw[e];
   }
   const int nb = int(fb_blocks(a->rows));
-  float* yst = static_cast<float*>(ws.take(fb_scales_t(a->N, a->rows)));
-  float* xst = static_cast<float*>(ws.take(fb_scales_t(a->K, a->rows)));
+  float* yst = static_cast<float*>(ws.take(fb_scales_bytes(a->N, a->rows)));
+  float* xst = static_cast<float*>(ws.take(fb_scales_bytes(a->K, a->rows)));
   p.Ys = a->dy_scale; p.Xs = a->x_scale; p.Yst = yst; p.Xst = xst;
   p.out = a->accumulate ? OUT_F32_ACC : (a->out_dtype == MGE_DTYPE_F32 ? OUT_F32 : OUT_BF16);
   if (fb_wgrad_small(p)) return launch_fb_wgrad(p, s);
@@ -312,8 +306,8 @@ size_t mge_fwd_fb_workspace_bytes(const mge_fwd_fb_args* a) {
     return 0;
   const int64_t total = fb_total(a->split_sizes, a->total_rows, a->rows);
   const bool tile = fb_tile_mlp(a->E, a->H, a->F, total);
-  return (fb_table(a->E) ? up256(4 * size_t(a->E) * sizeof(void*)) : 0) + up256(size_t(a->rows) * a->F) + fb_scales_t(a->rows, a->F) +
-         (fb_fused(a->E, a->F, total, tile) ? fb_scales_t(a->rows, a->H) : up256(size_t(a->rows) * a->F * 8));
+  return (fb_table(a->E) ? up256(4 * size_t(a->E) * sizeof(void*)) : 0) + up256(size_t(a->rows) * a->F) + fb_scales_bytes(a->rows, a->F) +
+         (fb_fused(a->E, a->F, total, tile) ? fb_scales_bytes(a->rows, a->H) : up256(size_t(a->rows) * a->F * 8));
 }
 
 mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
@@ -383,12 +377,12 @@ mge_status grouped_mlp_fwd_fp8_block(const mge_fwd_fb_args* a, void* stream) {
     }
   }
   g.h_codes = static_cast<uint8_t*>(ws.take(size_t(a->rows) * F));
-  g.h_scales = static_cast<float*>(ws.take(fb_scales_t(a->rows, F)));
+  g.h_scales = static_cast<float*>(ws.take(fb_scales_bytes(a->rows, F)));
   d.A = g.h_codes; d.As = g.h_scales; d.Ast = g.h_scales; d.ast_ld = a->rows;
   const bool tile = fb_tile_mlp(E, H, F, g.total);
   const bool fused = fb_fused(E, F, g.total, tile);
   if (fused) {   // (the quadrants take the tokens' scales as they come)
-    float* xst = static_cast<float*>(ws.take(fb_scales_t(a->rows, H)));
+    float* xst = static_cast<float*>(ws.take(fb_scales_bytes(a->rows, H)));
     g.Ast = xst; g.ast_ld = a->rows;
     const FbScaleT t{a->x_scale, a->perm_src, a->x_rows, a->rows, int(fb_blocks(H)), xst, a->rows};
     st = launch_fb_scale_t(&t, 1, s);

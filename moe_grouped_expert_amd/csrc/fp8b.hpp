@@ -15,6 +15,25 @@ namespace mge {
 constexpr int FB = 128;   // values of a block along an axis
 inline int64_t fb_blocks(int64_t n) { return (n + FB - 1) / FB; }
 
+// What a wave of the tile kernels reads of a matrix's scales, 64 rows from `row` on and block `blk` first: where that
+// begins (elements) and the bytes that its buffer resource covers.  by_row: [rows][nb], else block-major [nb][rows].
+// A slice's place goes into the scalar offset, which a resource does not bound in every form of its range check, so the
+// resource of a wave that starts past the last row is empty: past the last block's row `rows` it would read behind the
+// table.  What starts before it ends at most 63 elements behind (fb_scales_bytes has them).
+struct FbSpan {
+  int64_t at;
+  uint32_t bytes;
+};
+constexpr FbSpan fb_scale_span(int64_t row, int64_t rows, int64_t blk, int64_t nb, bool by_row) {
+  const int64_t at = by_row ? row * nb + blk : blk * rows + row;
+  return FbSpan{at, row < rows && blk < nb ? uint32_t(rows * nb - at) * 4 : 0};
+}
+// Workspace of block-major scales [ceil(K/128)][rows], and what the last wave of a row reads behind them
+inline size_t fb_scales_bytes(int64_t rows, int64_t K) {
+  const size_t n = size_t(rows) * size_t(fb_blocks(K)) * 4;
+  return n ? up256(n) + 256 : 0;
+}
+
 #ifdef __HIPCC__
 // Scale and factor of a block from the largest of its values' bit patterns without signs
 struct FbScale {

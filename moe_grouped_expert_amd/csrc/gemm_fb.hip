@@ -290,10 +290,8 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         o.rW[h] = make_rsrc_n(p.X + int64_t(t.n0 + HR * h) * p.rows, uint32_t(left(p.K - t.n0 - HR * h, HR)) * ldw);
-      const int n = of_t ? p.N : p.K;
-      const int64_t nb = (p.rows + 127) / 128, row = of_t ? t.m0 + wave * 64 : t.n0 + (wave - SWV) * 64, all = nb * n;
-      const int64_t at = ROWS ? row * nb + t.kbase / 128 : t.kbase / 128 * int64_t(n) + row;
-      o.rS = make_rsrc_n((ROWS ? (of_t ? p.Ys : p.Xs) : (of_t ? p.Yst : p.Xst)) + at, at < all ? uint32_t(all - at) * 4 : 0);
+      const FbSpan sp = fb_scale_span(of_t ? t.m0 + wave * 64 : t.n0 + (wave - SWV) * 64, of_t ? p.N : p.K, t.kbase / 128, (p.rows + 127) / 128, ROWS);
+      o.rS = make_rsrc_n((ROWS ? (of_t ? p.Ys : p.Xs) : (of_t ? p.Yst : p.Xst)) + sp.at, sp.bytes);
     } else {
       o.rT = make_rsrc_n(p.A, uint32_t(p.src_rows) * ldw);
 #pragma unroll
@@ -307,9 +305,9 @@ __device__ __forceinline__ void fb_tile_body(const P& p) {
         const int r0 = SW ? t.n0 : t.n0 + HR * h;          // (SwiGLU: gate, then up rows of the same columns)
         o.rW[h] = make_rsrc_n(w + (int64_t(r0) + (SW ? h * ncols : 0)) * p.K, uint32_t(left(nrows - r0, HR)) * ldw);
       }
-      const int64_t at = of_t ? int64_t(t.off) + t.m0 + wave * 64 : int64_t(t.n0 / FB) * KB;
-      const int64_t all = of_t ? int64_t(KB) * p.ast_ld : int64_t(((SW ? 2 * ncols : p.N) + FB - 1) / FB) * KB;
-      o.rS = make_rsrc_n((of_t ? p.Ast : ws) + at, at < all ? uint32_t(all - at) * 4 : 0);
+      const FbSpan sp = of_t ? fb_scale_span(int64_t(t.off) + t.m0 + wave * 64, p.ast_ld, 0, KB, false)
+                             : fb_scale_span(t.n0 / FB, ((SW ? 2 * ncols : p.N) + FB - 1) / FB, 0, KB, true);
+      o.rS = make_rsrc_n((of_t ? p.Ast : ws) + sp.at, sp.bytes);
       o.soff = soff;
       if constexpr (TAIL) {
         if (direct && of_t) {

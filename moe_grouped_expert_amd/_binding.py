@@ -1015,16 +1015,26 @@ class RmsnormOut:
     rstd: Optional[torch.Tensor] = None
 
 
+def _int32(sizes: int, what: str):
+    """Refuses sizes (or-ed together) that the argument blocks' 32-bit fields would cut off."""
+    if sizes >> 31:
+        raise ValueError(f"{what} must be below 2^31")
+
+
 def _rows_of(t: torch.Tensor, what: str):
     """[..., H] as rows: (T, H, row stride) of a contiguous tensor, or of a matrix of contiguous rows."""
     if t.dim() < 1 or t.dtype not in _TORCH_DTYPE:
         raise ValueError(f"{what} must be [..., H], float32 or bfloat16")
     H = t.shape[-1]
     if t.is_contiguous():
-        return (t.numel() // H if H else 0), H, H
-    if t.dim() != 2 or t.stride(1) != 1:
+        T, ld = (t.numel() // H if H else 0), H
+    elif t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{what} must be contiguous, or a matrix of contiguous rows")
-    return t.shape[0], H, t.stride(0) if t.shape[0] > 1 else H
+    else:
+        T = t.shape[0]
+        ld = t.stride(0) if T > 1 else H
+    _int32(T | H, f"the rows and columns of {what}")
+    return T, H, ld
 
 
 def _like(t, shape, dtype, what: str):
@@ -1147,12 +1157,13 @@ def fp8_block_quantize(x: torch.Tensor, orient: str = "row", block: str = "1x128
     for d in lead:
         batch *= d
     dev = x.device
-    _on(dev, rows)
     R = src
     if rows is not None:
         _need(rows.dim() == 1 and rows.dtype == torch.int32 and rows.is_contiguous(), "rows must be contiguous int32 [R]")
         _need(len(shape) == 2 and block == "1x128", "rows needs a matrix and block='1x128'")
         R = rows.shape[0]
+    _int32(batch | R | Cc, "batch, rows and columns")
+    _on(dev, rows)
     Rp, nr, nc = (R + 31) // 32 * 32, _fblocks(R), _fblocks(Cc)
     want_row, want_col = orient != "col", orient != "row"
     tile = block == "128x128"
@@ -1185,6 +1196,10 @@ def fp8_block_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype: s
     rowwise = tuple(scales.shape) == lead + (R, _fblocks(Cc))
     if not rowwise and tuple(scales.shape) != lead + (_fblocks(R), _fblocks(Cc)):
         raise ValueError("scales must be [..., R, ceil(C/128)] or [..., ceil(R/128), ceil(C/128)]")
+    batch = 1
+    for d in lead:
+        batch *= d
+    _int32(batch | R | Cc, "batch, rows and columns")
     dev = codes.device
     dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
     _on(dev, scales, out)
@@ -1192,9 +1207,6 @@ def fp8_block_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype: s
         out = _new_like(codes, dt)
     else:
         _like(out, codes.shape, dt, "out")
-    batch = 1
-    for d in lead:
-        batch *= d
     a = DequantFbArgs(C.sizeof(DequantFbArgs), BLOCK["1x128" if rowwise else "128x128"], batch, R, Cc, DTYPE[out_dtype],
                       codes.data_ptr(), scales.data_ptr(), out.data_ptr())
     _call("fp8_block_dequantize", a, dev)
@@ -1223,6 +1235,7 @@ def _check_groups(split_sizes, group_offsets, E: int):
 def _codes_rows(a, a_scale, what: str):
     if a.dim() != 2 or not _is_u8(a) or not _is_f32(a_scale) or tuple(a_scale.shape) != (a.shape[0], _fblocks(a.shape[1])):
         raise ValueError(f"{what} must be contiguous uint8 [rows, K] with float32 scales [rows, ceil(K/128)]")
+    _int32(a.shape[0] | a.shape[1], f"the rows and columns of {what}")
     return a.shape
 
 
@@ -1257,6 +1270,7 @@ def fp8_block_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, w, w_scale, s
         E = len(w)
         _need(E > 0 and w[0].dim() == 2, "w must be E matrices [N, K]")
         N = w[0].shape[0]
+    _int32(N, "N")
     rows = src
     if a_rows is not None:
         _need(a_rows.dim() == 1 and a_rows.dtype == torch.int32 and a_rows.is_contiguous(), "a_rows must be contiguous int32 [rows]")
@@ -1326,6 +1340,7 @@ def grouped_mlp_fwd_fp8_block(rt: Optional[RouteOut], x: torch.Tensor, x_scale: 
     _need(rt is None or rt.T == T, "x must have a row for each of the route's tokens")
     R = T if rt is None else rt.R
     F = (w_gate_up.shape[1] if isinstance(w_gate_up, torch.Tensor) else w_gate_up[0].shape[0]) // 2
+    _int32(F, "F")
     dt = torch.bfloat16 if y_dtype == "bf16" else torch.float32
     _on(dev, x_scale)
     if rt is not None:

@@ -831,6 +831,10 @@ mge_status fp8_block_dequantize(const mge_dequant_fb_args* args, void* stream);
  * Groups, total_rows: as mxfp4_grouped_gemm.  Rows outside the groups are untouched.
  * A block's 128 products are added on the matrix unit, in eights of which what lies 2^-13
  * below the largest product is cut off; the blocks are added in fp32.
+ * A block's two scales are multiplied first, in fp32, so their product has to be within fp32's
+ * range: past it (blocks whose largest values multiply to 6.8e43 or more) the elements that add
+ * these two blocks become infinite or NaN, no others; below its normal numbers it loses bits, an
+ * absolute error of at most 2^-125 for each block.
  * A NaN (scale, E4M3 code 0x7f) reaches its row of out (a), or its column or the 128 columns
  * of its scale, in its expert's rows (w), and no other element.
  * Workspace: mge_gemm_fb_workspace_bytes(args) bytes, 16-byte aligned; 0 (NULL allowed) for
@@ -875,7 +879,9 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* args, void* stream);
  * wrong results, but no access outside the buffers.
  * dw: [host] array of E device pointers, [N][K] fp32 or bf16, overwritten (an expert without
  * rows: zeros), or fp32 with accumulate != 0: added to.
- * Sums, NaN: as fp8_block_grouped_gemm.
+ * Sums, NaN: as fp8_block_grouped_gemm, but a block's sum is multiplied by dy_scale, then by
+ * x_scale, so that a dy_scale from 2^-108 to 2^103 (dy up to 4.5e33) goes with every x_scale; past
+ * it elements of its row may become infinite, no others.
  * Workspace: mge_wgrad_fb_workspace_bytes(args) bytes, 16-byte aligned.
  * Errors: as fp8_block_grouped_gemm, N and K at most 2^22, rows a multiple of 32 in
  * [0, 2^31 / max(N, K, 256)), accumulate with bf16; MGE_ERR_WORKSPACE.

@@ -1256,7 +1256,8 @@ def fp8_block_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, w, w_scale, s
     ceil(K/128)] (stacked, or sequences of E matrices).  a_rows: int32 [rows of out], row r then reads a[a_rows[r]]
     (zeros where that is outside a): a route's perm_src.  split_sizes, group_offsets, total_rows: as
     mxfp4_grouped_gemm.  Rows outside the groups are left as they were.  For the input gradient pass the transposed
-    form of the weight."""
+    form of the weight.  A block's two scales are multiplied in fp32: past its range the elements that add the two
+    blocks are infinite or NaN."""
     if out_dtype not in DTYPE:
         raise ValueError(f"out_dtype must be 'bf16' or 'f32', not {out_dtype!r}")
     src, K = _codes_rows(a, a_scale, "a")

@@ -701,8 +701,8 @@ mge_status mxfp4_grouped_gemm(const mge_gemm4_args* args, void* stream);
  * y and codes are optional, one is needed; rstd is optional (the backward takes it).
  * residual_out may be residual or, with x_row_stride = H, x itself; y, codes and scales may
  * not overlap an input.  x: row stride x_row_stride elements; everything else contiguous.
- * A row whose sum of squares is past fp32's range gives rstd 0.  NaN and infinities stay in
- * their row.
+ * A row whose sum of squares is past fp32's range gives rstd 0, one whose sum is below it with
+ * eps = 0 an infinite rstd.  NaN and infinities stay in their row.
  * Errors: MGE_ERR_INVALID_ARG for T < 0, H not a multiple of 32 in [32, 16384], unknown
  * dtypes, an x_row_stride below H or not a multiple of 8, eps negative or not finite, one of
  * residual / residual_out or of codes / scales without the other, no output, NULL or
@@ -802,8 +802,8 @@ mge_status fp8_block_quantize(const mge_quant_fb_args* args, void* stream);
 /* ------------------------------------------------------------------------------
  * fp8_block_dequantize — the values element * scale of `batch` matrices of contiguous codes
  * [R][C] with scales [R][ceil(C/128)] (1X128) or [ceil(R/128)][ceil(C/128)] (128X128) -> out
- * [batch][R][C] bf16 or fp32 (one rounding).  E4M3's NaN codes (0x7f, 0xff) and NaN scales
- * give NaN.
+ * [batch][R][C] fp32 (the product rounded to it) or bf16 (that rounded again).  E4M3's NaN codes
+ * (0x7f, 0xff) and NaN scales give NaN.
  * Errors: MGE_ERR_INVALID_ARG for negative sizes, C not a multiple of 32, C or R above
  * 2^31 - 256, an unknown block or dtype, NULL or misaligned (16-byte; scales 4) pointers.
  * ---------------------------------------------------------------------------- */
@@ -911,9 +911,11 @@ mge_status fp8_block_grouped_wgrad(const mge_wgrad_fb_args* args, void* stream);
  * fp32 scale per block of 128: per row r of expert e's group, with s = perm_src[r] (s = r
  * without it; zeros where outside [0, x_rows)) and p = prob_perm[r] (1 without it),
  *   [G U] = x[s] W_gate_up[e]^T,  h = p * silu(G) * U,  y_perm[r] = h W_down[e]^T
- * as two fp8_block_grouped_gemm products; h is quantized (1 x 128) in the first one's
- * epilogue and stays in the workspace.  x: codes [x_rows][H], scales [x_rows][ceil(H/128)],
- * one row a token (rmsnorm_fwd, fp8_block_quantize).  Weights: [2F][H] (gate rows first) with
+ * as two fp8_block_grouped_gemm products; h is quantized (1 x 128) in between and stays in
+ * the workspace: in the first one's epilogue, or, with few rows or few tiles, by a kernel of its
+ * own, for which the workspace holds [G U] in fp32 too (8 F bytes for each of `rows`).  x: codes
+ * [x_rows][H], scales [x_rows][ceil(H/128)], one row a token (rmsnorm_fwd, fp8_block_quantize).
+ * Weights: [2F][H] (gate rows first) with
  * scales [ceil(2F/128)][ceil(H/128)], [H][F] with [ceil(H/128)][ceil(F/128)].  split_sizes,
  * group_offsets, perm_src, prob_perm: as moe_route_permute writes them (rows =
  * mge_perm_rows); with none of them and E = 1 it is a dense gated MLP (a shared expert).

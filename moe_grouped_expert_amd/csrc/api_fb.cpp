@@ -243,6 +243,7 @@ mge_status fp8_block_grouped_gemm(const mge_gemm_fb_args* a, void* stream) {
   return st != MGE_OK ? st : launch_fb_tile(p, false, s);
 }
 
+// (with block-major scales whatever the tiles: their choice goes by the device's CUs, a size asked for beforehand does not)
 size_t mge_wgrad_fb_workspace_bytes(const mge_wgrad_fb_args* a) {
   if (!a || a->struct_size != sizeof(mge_wgrad_fb_args) || a->E < 1 || a->E > 256 || a->N < 32 || a->K < 32 || a->rows < 0 ||
       a->rows >= kTwoGiB / std::max({a->N, a->K, kTileRows}))

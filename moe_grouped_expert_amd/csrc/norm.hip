@@ -10,7 +10,7 @@
 // Both are one pass over HBM, which bounds them.  A row stays in the registers of NT threads (64: a wave, no
 // barrier; 256, 512: a workgroup), 8 consecutive values a thread and step, so that 16 neighbouring lanes hold one
 // block of 128 and its scale is a maximum over a DPP row.  Measured on MI355X: forward of 16384 x 4096 bf16 with a
-// residual, bf16 and 8-bit output 118 us (4.9 TB/s, a copy's rate is 5.1), of 8 rows 3 us; backward of 16384 x 4096
+// residual, bf16 and 8-bit output 118 us (606 MB, 5.1 TB/s, a copy's rate), of 8 rows 3 us; backward of 16384 x 4096
 // with a residual's gradient 95 us, of 2048 x 16384 45 us.
 #include "mge_common.hpp"
 
